@@ -78,8 +78,9 @@ extern "C" {
  * 5: ce_fwd_bwd_fused_noalloc
  * 6: ce_linear.gemm (was reserved): the chunked head's GEMM engine; the head's
  *    logits stride in the workspace rounded up to a multiple of 8
- * 7: ce_stream_reference */
-#define CE_ABI_VERSION 7
+ * 7: ce_stream_reference
+ * 8: ce_logits_process(_backward), ce_embedding(_backward), ce_rms_norm, _quant and _backward */
+#define CE_ABI_VERSION 8
 
 typedef enum ce_status {
   CE_OK = 0,
@@ -418,6 +419,151 @@ int32_t ce_linear_gemm_plan(const ce_linear* lin);
 ce_status ce_linear_tune(const ce_linear* lin, const ce_params* p, void* dh, int64_t dh_ld, float* dw,
                          int64_t dw_ld, int64_t chunk_rows, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Logit processing: what is done to the logits before a distribution is read
+ * off them -- penalties for repeated tokens, a bias, a grammar's mask and the
+ * temperature -- in one pass, ahead of sampling, or of the loss calls above
+ * where a sampled policy's log-probabilities are trained.  For row r, column j
+ * (global column vocab_start + j of a shard), with c the occurrences of j among
+ * the row's output tokens and `seen` its presence among prompt or output:
+ *   v = seen ? (x > 0 ? x / repetition : x repetition) : x
+ *   z = ((v - frequency c - presence [c > 0]) + bias_j) / temperature,
+ *   z = -inf where the mask's bit is 0, whatever x holds there (NaN too).
+ * The arithmetic is FP32, with 1 / temperature rounded once; z is rounded once
+ * to the logits' dtype.  -inf and NaN logits stay so where allowed.  A row whose
+ * mask allows nothing is all -inf.
+ *
+ * Every pointer is device memory and may be NULL: that step is then left out.
+ */
+typedef struct ce_process {
+  const int64_t* history; /* row (i0, i1)'s tokens start at i0 * history_s0 + i1 * history_s1 and are contiguous;
+                             rows may share them (stride 0: the prefixes of one sequence).  Tokens are global
+                             vocabulary indices; any outside this buffer's columns (padding, another shard's)
+                             count nowhere */
+  int64_t history_s0, history_s1;
+  int64_t history_max;    /* tokens of the longest row (the width of `history`), below 2^31 */
+  const int32_t* history_len; /* [N] tokens of row r, taken into [0, history_max]; NULL: history_max */
+  const int32_t* prompt_len;  /* [N] how many of them, the first ones, are the prompt's; NULL: 0 */
+  const float* repetition;    /* [N], > 0; penalties need a history (CE_EINVAL) */
+  const float* frequency;     /* [N] */
+  const float* presence;      /* [N] */
+  const float* temperature;   /* [N], > 0 and at least 2^-126 */
+  const float* bias;      /* row (i0, i1)'s v_local values at i0 * bias_s0 + i1 * bias_s1 (stride 0: shared) */
+  int64_t bias_s0, bias_s1;
+  const uint32_t* mask;   /* row (i0, i1)'s ceil(v_local / 32) words, strides in words (0: shared); bit j % 32 of
+                             word j / 32 is 1 where local column j is allowed */
+  int64_t mask_s0, mask_s1;
+  uint8_t* signs;         /* row r's ceil(v_local / 8) bytes at r * signs_ld: bit j % 8 of byte j / 8 is [x_rj > 0].
+                             Written by ce_logits_process, read by the gradient of a repetition penalty */
+  int64_t signs_ld;       /* >= ceil(v_local / 8) */
+} ce_process;
+
+/* z into `out`, which has x's dtype and shape and its own strides; out->data ==
+ * x->data with the same strides works in place, any other overlap does not.
+ * One kernel launch; sums of counts are whole numbers, so repeats are equal
+ * bit for bit. */
+ce_status ce_logits_process(const ce_logits* x, const ce_logits* out, const ce_process* p, hipStream_t stream);
+
+/* The gradient with respect to x (history, mask, temperature and the
+ * penalties are constants):
+ *   dx = dz (seen ? (x > 0 ? 1 / repetition : repetition) : 1) / temperature, +0.0 where masked,
+ * whatever dz holds there.  `p` as for the forward call, whose `signs` stand
+ * for x (required with `repetition`); frequency, presence and bias are not
+ * read.  In place or not, as above. */
+ce_status ce_logits_process_backward(const ce_logits* dz, const ce_logits* out, const ce_process* p,
+                                     hipStream_t stream);
+
+/*
+ * Embedding: out_n = scale W[id_n], for the whole table or the rows
+ * [vocab_start, vocab_start + v_local) that a vocabulary shard holds.  An id of
+ * another shard gives a row of zeros (the shards' outputs add up); an id outside
+ * [0, vocab_total) violates the precondition: nothing is read out of bounds and
+ * the row is NaN.
+ */
+typedef struct ce_embedding_desc {
+  const int64_t* ids;  /* device, id n at ids[n * id_stride] */
+  int64_t id_stride;   /* >= 0 */
+  int64_t N, D;        /* tokens (at most 2^26) and columns */
+  const void* weight;  /* device [v_local, D], row stride w_ld elements (not read by the gradient) */
+  int64_t w_ld;
+  int32_t dtype;       /* CE_BF16 or CE_F32, for weight, out and dout */
+  int32_t reserved;    /* must be 0 */
+  int64_t v_local, vocab_start, vocab_total;
+  float scale;
+} ce_embedding_desc;
+
+/* out: device [N, D] in the weight's dtype, row stride out_ld, one rounding of scale W. */
+ce_status ce_embedding(const ce_embedding_desc* m, void* out, int64_t out_ld, hipStream_t stream);
+
+/* Workspace bytes of ce_embedding_backward; 0 if the sizes are refused. */
+size_t ce_embedding_workspace_bytes(int64_t N, int64_t D, int64_t v_local);
+
+/*
+ * dw[v] (+)= scale * sum over the tokens n with id_n = vocab_start + v of dout_n:
+ *   dout         device [N, D], row stride dout_ld
+ *   padding_idx  tokens of this id add nothing (negative: none); nor do other shards' ids, or ids outside the
+ *                vocabulary
+ *   dw           device FP32 [v_local, D], row stride dw_ld; accumulate = 0 writes every row (zeros where no
+ *                token names it), 1 adds to the rows that tokens name and touches no other: with a table tied
+ *                to the head, ce_linear_cross_entropy's dw
+ *   ws           ce_embedding_workspace_bytes bytes, 256-byte aligned, needing no preparation; two calls must
+ *                not use one workspace concurrently
+ * Sums are FP32 over each id's tokens in an order fixed by their positions, so
+ * repeats are equal bit for bit.
+ */
+ce_status ce_embedding_backward(const ce_embedding_desc* m, const void* dout, int64_t dout_ld, int64_t padding_idx,
+                                float* dw, int64_t dw_ld, int32_t accumulate, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/*
+ * RMS norm with the residual's addition:
+ *   s = x + residual,  y = s (mean_j s_j^2 + eps)^(-1/2) weight
+ * in FP32, y and the written s rounded once each (y is formed from s before
+ * its rounding).  Squares are FP32: a row whose mean square exceeds FP32 comes
+ * out 0, and a row holding a NaN comes out NaN.  Rows of at most 32768 columns
+ * (CE_ELAYOUT).
+ */
+typedef struct ce_norm {
+  const void* x;        /* device [N, D], row stride x_ld */
+  const void* residual; /* device [N, D], row stride residual_ld, or NULL */
+  const void* weight;   /* device [D] */
+  int32_t dtype;        /* CE_BF16 or CE_F32: x, residual and the outputs */
+  int32_t weight_dtype; /* CE_BF16 or CE_F32 */
+  int64_t N, D, x_ld, residual_ld;
+  float eps;            /* finite, >= 0 */
+} ce_norm;
+
+/* y: device [N, D], row stride y_ld; sum: s, device [N, D], row stride sum_ld, or NULL.  Either may be the
+ * same buffer as x or residual (same row stride), for an update in place; not one another. */
+ce_status ce_rms_norm(const ce_norm* n, void* y, int64_t y_ld, void* sum, int64_t sum_ld, hipStream_t stream);
+
+/*
+ * The same with the output in 8 bits, for each group of `group` columns (0: the
+ * row; else 32, 64 or 128, the last of a row possibly short):
+ *   scale = max(max |y| / 448, 2^-126),  q = e4m3(y / scale)   (OCP e4m3, round to nearest even)
+ *   q       device bytes [N, D], row stride q_ld
+ *   scales  device FP32 [N, ceil(D / group)] ([N, 1] for group 0), contiguous
+ * A NaN in a row makes all its q NaN, with scale 2^-126.
+ */
+ce_status ce_rms_norm_quant(const ce_norm* n, void* q, int64_t q_ld, int32_t group, float* scales, void* sum,
+                            int64_t sum_ld, hipStream_t stream);
+
+/* Workspace bytes of ce_rms_norm_backward; 0 if the sizes are refused. */
+size_t ce_rms_norm_workspace_bytes(int64_t N, int64_t D);
+
+/*
+ * The gradient, from the forward's written sum s as n->x (n->residual NULL):
+ *   dx = rstd (dy weight) - s rstd^3 mean_j(dy weight s) + dsum     (also the residual's gradient)
+ *   dweight (+)= sum over rows of dy s rstd
+ *   dsum     device [N, D], the gradient that reaches s by the residual stream, or NULL
+ *   dx       device [N, D] in x's dtype, or NULL; may be dy's or dsum's buffer (same row stride)
+ *   dweight  device FP32 [D], or NULL; accumulate = 1 adds to it
+ *   ws       ce_rms_norm_workspace_bytes bytes, 256-byte aligned (needed with dweight), no preparation
+ */
+ce_status ce_rms_norm_backward(const ce_norm* n, const void* dy, int64_t dy_ld, const void* dsum, int64_t dsum_ld,
+                               void* dx, int64_t dx_ld, float* dweight, int32_t accumulate, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
 /* Waits for `stream` and reports whether any call that used `ws` since it was
  * prepared or last checked gave up waiting in a split-row exchange or count
  * (CE_EDEADLOCK; its results were NaN) or found the workspace unprepared
@@ -444,7 +590,8 @@ ce_status ce_stream_reference(const void* src, void* dst, int64_t bytes, hipStre
  * Kernel timing for benchmarks.  After ce_profile_start(capacity), each of
  * the next `capacity` calls of ce_forward(_ex), ce_backward_inplace(_ex),
  * ce_fwd_bwd_fused(_noalloc), ce_shards_fwd_bwd_fused, ce_shard_partial_stats,
- * ce_scale_grad_inplace or ce_stream_reference that launch work records a pair
+ * ce_scale_grad_inplace, ce_logits_process(_backward) or ce_stream_reference
+ * that launch work records a pair
  * of HIP events on its stream around its main (bandwidth-dominant) kernel.
  * ce_profile_stop(ms, cap, count) waits for those events, writes up to `cap`
  * durations in milliseconds to host array `ms`, the number recorded to

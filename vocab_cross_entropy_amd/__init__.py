@@ -15,6 +15,9 @@ and the interface of the TransformerEngineNPU issue #29 page (section 1):
     parallel_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False,
                            dist_process_group=None, ignore_idx=-100)
 
+and, beside the loss (``_ops.py``): logit processing (process_logits,
+processed_cross_entropy), embedding and RMS norm (norm_linear_cross_entropy).
+
 ``reduce_loss`` is False / True (the page's flag: per-row losses / their mean
 over non-ignored rows) or one of "none", "mean", "sum".  ``smoothing`` (a
 keyword) is "all" (a / V on every class, torch's convention) or "others"
@@ -767,3 +770,10 @@ class Profiler:
         _check(lib.ce_profile_stop(buf, self.capacity, ctypes.byref(n)))
         self.ms = [buf[i] for i in range(n.value)]
         return False
+
+
+# the operators around the loss (they build on the helpers above)
+from . import _ops  # noqa: E402
+from ._ops import *  # noqa: E402,F401,F403
+
+__all__ += _ops.__all__

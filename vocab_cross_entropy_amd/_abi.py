@@ -19,7 +19,7 @@ CE_F32, CE_BF16 = 0, 1
 CE_REDUCE_NONE, CE_REDUCE_MEAN, CE_REDUCE_SUM = 0, 1, 2
 CE_SMOOTH_ALL, CE_SMOOTH_OTHERS = 0, 1
 CE_GEMM_AUTO, CE_GEMM_NATIVE, CE_GEMM_LIBRARY = 0, 1, 2
-CE_ABI_VERSION = 7
+CE_ABI_VERSION = 8
 
 
 class CeLogits(ctypes.Structure):
@@ -65,6 +65,27 @@ class CeLinear(ctypes.Structure):
     ]
 
 
+def _fields(spec: str):
+    """"name:type ..." pairs: p pointer, q int64, i int32, f float."""
+    types = {"p": ctypes.c_void_p, "q": ctypes.c_int64, "i": ctypes.c_int32, "f": ctypes.c_float}
+    return [(name, types[code]) for name, code in (item.split(":") for item in spec.split())]
+
+
+class CeProcess(ctypes.Structure):
+    _fields_ = _fields("history:p history_s0:q history_s1:q history_max:q history_len:p prompt_len:p repetition:p "
+                       "frequency:p presence:p temperature:p bias:p bias_s0:q bias_s1:q mask:p mask_s0:q mask_s1:q "
+                       "signs:p signs_ld:q")
+
+
+class CeEmbeddingDesc(ctypes.Structure):
+    _fields_ = _fields("ids:p id_stride:q N:q D:q weight:p w_ld:q dtype:i reserved:i v_local:q vocab_start:q "
+                       "vocab_total:q scale:f")
+
+
+class CeNorm(ctypes.Structure):
+    _fields_ = _fields("x:p residual:p weight:p dtype:i weight_dtype:i N:q D:q x_ld:q residual_ld:q eps:f")
+
+
 # Every symbol include/ce.h declares, with its ctypes signature.
 _P = ctypes.POINTER
 _vp = ctypes.c_void_p
@@ -101,6 +122,18 @@ SIGNATURES = {
     "ce_linear_cross_entropy": (ctypes.c_int, [_P(CeLinear), _vp, ctypes.c_int64, _P(CeParams), _vp, _vp, _vp, _vp,
                                                ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
                                                _vp, ctypes.c_size_t, _vp]),
+    "ce_logits_process": (ctypes.c_int, [_P(CeLogits), _P(CeLogits), _P(CeProcess), _vp]),
+    "ce_logits_process_backward": (ctypes.c_int, [_P(CeLogits), _P(CeLogits), _P(CeProcess), _vp]),
+    "ce_embedding": (ctypes.c_int, [_P(CeEmbeddingDesc), _vp, ctypes.c_int64, _vp]),
+    "ce_embedding_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "ce_embedding_backward": (ctypes.c_int, [_P(CeEmbeddingDesc), _vp, ctypes.c_int64, ctypes.c_int64, _vp,
+                                             ctypes.c_int64, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]),
+    "ce_rms_norm": (ctypes.c_int, [_P(CeNorm), _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp]),
+    "ce_rms_norm_quant": (ctypes.c_int, [_P(CeNorm), _vp, ctypes.c_int64, ctypes.c_int32, _vp, _vp, ctypes.c_int64,
+                                         _vp]),
+    "ce_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "ce_rms_norm_backward": (ctypes.c_int, [_P(CeNorm), _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp,
+                                            ctypes.c_int64, _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]),
     "ce_workspace_check": (ctypes.c_int, [_vp, _vp]),
     "ce_profile_start": (ctypes.c_int, [ctypes.c_int32]),
     "ce_profile_stop": (ctypes.c_int, [_vp, ctypes.c_int32, _P(ctypes.c_int32)]),

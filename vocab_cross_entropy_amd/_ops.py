@@ -1,0 +1,476 @@
+"""The operators around the loss: logit processing, embedding and RMS norm.
+
+Like the rest of the binding, the ``ce_*`` functions marshal torch device
+tensors into the C ABI's descriptors (``include/ce.h`` defines each operator)
+and run on torch's current stream of the tensors' device; ``process_logits``,
+``processed_cross_entropy``, ``embedding``, ``rms_norm`` and
+``norm_linear_cross_entropy`` are their autograd forms.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi
+from . import (CeArgumentError, _check, _device_of, _dtype_code, _need, _ptr, _stream, _workspace,
+               ce_fwd_bwd_fused, ce_scale_grad_inplace, lib, linear_cross_entropy, logits_desc, reduction_code)
+
+__all__ = [
+    "ce_logits_process", "ce_logits_process_backward", "logits_signs", "process_logits", "processed_cross_entropy",
+    "ce_embedding", "ce_embedding_backward", "ce_embedding_workspace_bytes", "embedding",
+    "ce_rms_norm", "ce_rms_norm_quant", "ce_rms_norm_backward", "ce_rms_norm_workspace_bytes", "rms_norm",
+    "norm_linear_cross_entropy",
+]
+
+
+def _call(dev: torch.device, fn, *args):
+    """Run an entry point on torch's current stream of ``dev``, with ``dev`` the current device (kernels are
+    looked up per device)."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)))
+
+
+def _einval(msg: str):
+    raise CeArgumentError(_abi.CE_EINVAL, msg)
+
+
+def _elayout(msg: str):
+    raise CeArgumentError(_abi.CE_ELAYOUT, msg)
+
+
+def _rows(dev, what, t, shape, dtype):
+    """``t`` is a [rows, columns] matrix on ``dev`` with contiguous columns; its row stride."""
+    if t is None:
+        _einval(f"{what} is missing")
+    _need(dev, what, t, dtype, contiguous=False)
+    if tuple(t.shape) != tuple(shape):
+        _einval(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        _elayout(f"{what} needs contiguous columns")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+# ---- logit processing ------------------------------------------------------------------------------------
+
+
+def _side(dev, what, t, x, width, dtype):
+    """A (d0, d1, >= width) companion of the logits, any row strides: (pointer, s0, s1)."""
+    if t is None:
+        return None, 0, 0
+    _need(dev, what, t, dtype, contiguous=False)
+    if t.dim() != 3 or t.shape[:2] != x.shape[:2] or t.shape[2] < width:
+        _einval(f"{what} must be ({x.shape[0]}, {x.shape[1]}, {width}), got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        _elayout(f"{what} needs a contiguous last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _process_desc(dev, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask,
+                  temperature, signs):
+    N, V = x.shape[0] * x.shape[1], x.shape[2]
+    p = _abi.CeProcess()
+    p.history, p.history_s0, p.history_s1 = _side(dev, "history", history, x, 0, torch.int64)
+    p.history_max = 0 if history is None else history.shape[2]
+    for what, t, dtype in (("history_len", history_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
+                           ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
+                           ("presence", presence, torch.float32), ("temperature", temperature, torch.float32)):
+        if t is not None:
+            _need(dev, what, t, dtype, N)
+            setattr(p, what, t.data_ptr())
+    if history is not None and history.numel() == 0:
+        # no row has a token, so nothing is counted; an empty tensor has no address
+        p.history_max = 0
+        p.history = p.history_len = p.prompt_len = p.repetition = p.frequency = p.presence = None
+    p.bias, p.bias_s0, p.bias_s1 = _side(dev, "bias", bias, x, V, torch.float32)
+    p.mask, p.mask_s0, p.mask_s1 = _side(dev, "mask", mask, x, (V + 31) // 32, torch.int32)
+    if signs is not None:
+        if signs.dim() != 2 or signs.shape[1] < (V + 7) // 8:
+            _einval(f"signs must be ({N}, {(V + 7) // 8}), see logits_signs")
+        p.signs_ld = _rows(dev, "signs", signs, (N, signs.shape[1]), torch.uint8)
+        p.signs = signs.data_ptr()
+    return p
+
+
+def _process(fn, x, out, vocab_start, vocab_total, **steps):
+    dev = _device_of(x)
+    out = x if out is None else out
+    xd = logits_desc(x, vocab_start, vocab_total)
+    if out is not x:
+        _need(dev, "out", out, x.dtype, contiguous=False)
+        if out.shape != x.shape:
+            _einval(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
+    zd = xd if out is x else logits_desc(out, vocab_start, vocab_total)
+    p = _process_desc(dev, x, **steps)
+    _call(dev, fn, ctypes.byref(xd), ctypes.byref(zd), ctypes.byref(p))
+    return out
+
+
+def logits_signs(x: torch.Tensor) -> torch.Tensor:
+    """An empty ``signs`` buffer for (d0, d1, V) logits: one bit per logit, [N, ceil(V / 8)] bytes."""
+    return torch.empty((x.shape[0] * x.shape[1], (x.shape[2] + 7) // 8), dtype=torch.uint8, device=x.device)
+
+
+def ce_logits_process(x, *, out=None, history=None, history_len=None, prompt_len=None, repetition=None,
+                      presence=None, frequency=None, bias=None, mask=None, temperature=None, signs=None,
+                      vocab_start=0, vocab_total=None):
+    """Penalties, bias, grammar mask and temperature over (d0, d1, V) logits, in place or into ``out``.
+
+    ``history`` (d0, d1, L) int64 tokens (rows may share storage, ``expand``), ``history_len`` and
+    ``prompt_len`` [N] int32; ``repetition``, ``frequency``, ``presence`` and ``temperature`` [N] FP32;
+    ``bias`` (d0, d1, V) FP32 and ``mask`` (d0, d1, ceil(V / 32)) int32 words of allowed columns, both any row
+    strides.  ``signs`` (see logits_signs) is written for the gradient.  Each is optional.  Returns the
+    processed logits."""
+    return _process(lib.ce_logits_process, x, out, vocab_start, vocab_total, history=history,
+                    history_len=history_len, prompt_len=prompt_len, repetition=repetition, presence=presence,
+                    frequency=frequency, bias=bias, mask=mask, temperature=temperature, signs=signs)
+
+
+def ce_logits_process_backward(dz, *, out=None, signs=None, history=None, history_len=None, prompt_len=None,
+                               repetition=None, mask=None, temperature=None, vocab_start=0, vocab_total=None):
+    """The gradient of ce_logits_process with respect to the logits, in place over ``dz`` or into ``out``.
+    ``signs`` are the forward's, needed with ``repetition``."""
+    return _process(lib.ce_logits_process_backward, dz, out, vocab_start, vocab_total, history=history,
+                    history_len=history_len, prompt_len=prompt_len, repetition=repetition, presence=None,
+                    frequency=None, bias=None, mask=mask, temperature=temperature, signs=signs)
+
+
+def _constants(**steps):
+    for name, t in steps.items():
+        if t is not None and t.requires_grad:
+            _einval(f"{name} is a constant of the processing and gets no gradient (it requires one)")
+
+
+def _grad_rows(g: torch.Tensor) -> torch.Tensor:
+    """An incoming gradient the kernels can read: contiguous columns, rows of their own."""
+    ok = g.stride(-1) == 1 and all(n <= 1 or s >= g.shape[-1] for n, s in zip(g.shape[:-1], g.stride()[:-1]))
+    return g if ok and g.shape[-1] > 0 else g.contiguous()
+
+
+class ProcessLogits(torch.autograd.Function):
+    """Autograd form of ce_logits_process, out of place: the logits are left as they are and not kept (the
+    backward needs their signs alone, one bit each, and those only with a repetition penalty)."""
+
+    @staticmethod
+    def forward(ctx, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask, temperature):
+        signs = logits_signs(x) if repetition is not None and ctx.needs_input_grad[0] else None
+        z = ce_logits_process(x.detach(), out=torch.empty_like(x), history=history, history_len=history_len,
+                              prompt_len=prompt_len, repetition=repetition, presence=presence, frequency=frequency,
+                              bias=bias, mask=mask, temperature=temperature, signs=signs)
+        ctx.save_for_backward(signs, history, history_len, prompt_len, repetition, mask, temperature)
+        return z
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dz):
+        signs, history, history_len, prompt_len, repetition, mask, temperature = ctx.saved_tensors
+        if repetition is None:
+            history = history_len = prompt_len = None
+        dz = _grad_rows(dz)
+        dx = ce_logits_process_backward(dz, out=torch.empty_like(dz), signs=signs, history=history,
+                                        history_len=history_len, prompt_len=prompt_len, repetition=repetition,
+                                        mask=mask, temperature=temperature)
+        return dx, None, None, None, None, None, None, None, None, None
+
+
+def process_logits(logits, *, history=None, history_len=None, prompt_len=None, repetition=None, presence=None,
+                   frequency=None, bias=None, mask=None, temperature=None):
+    """Processed logits (a new tensor, in the logits' dtype) with the options of ce_logits_process; the
+    gradient reaches ``logits``, everything else is a constant."""
+    _constants(repetition=repetition, presence=presence, frequency=frequency, bias=bias, temperature=temperature)
+    return ProcessLogits.apply(logits, history, history_len, prompt_len, repetition, presence, frequency, bias, mask,
+                               temperature)
+
+
+class ProcessedCrossEntropy(torch.autograd.Function):
+    """ce_logits_process, the fused loss and the processing's gradient, all in place over the logits' storage
+    (TENPU #29 section 6 stages the gradient there): the forward leaves in ``inp`` the gradient for an upstream
+    gradient of 1, the backward scales it (ce_scale_grad_inplace)."""
+
+    @staticmethod
+    def forward(ctx, inp, target, label_smoothing, reduce_loss, ignore_idx, smoothing, history, history_len,
+                prompt_len, repetition, presence, frequency, bias, mask, temperature):
+        buf = inp.detach()
+        signs = logits_signs(buf) if repetition is not None else None
+        ce_logits_process(buf, history=history, history_len=history_len, prompt_len=prompt_len,
+                          repetition=repetition, presence=presence, frequency=frequency, bias=bias, mask=mask,
+                          temperature=temperature, signs=signs)
+        loss, _ = ce_fwd_bwd_fused(buf, target, label_smoothing, reduce_loss, ignore_idx, smoothing=smoothing)
+        if repetition is None:
+            history = history_len = prompt_len = None
+        if repetition is not None or mask is not None or temperature is not None:
+            ce_logits_process_backward(buf, signs=signs, history=history, history_len=history_len,
+                                       prompt_len=prompt_len, repetition=repetition, mask=mask,
+                                       temperature=temperature)
+        ctx.reduced = reduction_code(reduce_loss) != _abi.CE_REDUCE_NONE
+        ctx.save_for_backward(buf)
+        return loss[0] if ctx.reduced else loss.view(target.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss):
+        (buf,) = ctx.saved_tensors
+        ce_scale_grad_inplace(buf, grad_loss, per_row=not ctx.reduced)
+        return (buf,) + (None,) * 14
+
+
+def processed_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False, ignore_idx=-100, *, smoothing="all",
+                            history=None, history_len=None, prompt_len=None, repetition=None, presence=None,
+                            frequency=None, bias=None, mask=None, temperature=None):
+    """Cross-entropy (the negative log-probability) under the distribution that sampling drew from:
+    parallel_cross_entropy of the processed logits, with both options' arguments.  As there, the gradient is
+    staged in place in ``inp``."""
+    _constants(repetition=repetition, presence=presence, frequency=frequency, bias=bias, temperature=temperature)
+    return ProcessedCrossEntropy.apply(inp, target, label_smoothing, reduce_loss, ignore_idx, smoothing, history,
+                                       history_len, prompt_len, repetition, presence, frequency, bias, mask,
+                                       temperature)
+
+
+# ---- embedding -------------------------------------------------------------------------------------------
+
+
+def _embedding_desc(ids, dtype_of, D, v_local, scale, vocab_start, vocab_total):
+    m = _abi.CeEmbeddingDesc()
+    N = ids.shape[0]
+    m.ids, m.id_stride, m.N, m.D = ids.data_ptr() if N else None, ids.stride(0) if N > 1 else 1, N, D
+    m.dtype, m.v_local, m.vocab_start = _dtype_code(dtype_of), v_local, int(vocab_start)
+    m.vocab_total = v_local if vocab_total is None else int(vocab_total)
+    m.scale = float(scale)
+    return m
+
+
+def _need_ids(dev, ids):
+    _need(dev, "ids", ids, torch.int64, contiguous=False)
+    if ids is None or ids.dim() != 1:
+        _einval("ids must be a 1-d int64 tensor")
+
+
+def ce_embedding(ids, weight, scale=1.0, *, out=None, vocab_start=0, vocab_total=None):
+    """``scale * weight[ids]`` for [N] int64 ``ids`` and a [V, D] table, or the rows from ``vocab_start`` on of a
+    vocabulary of ``vocab_total`` (other shards' ids give zeros).  Returns [N, D]."""
+    dev = _device_of(weight, "weight")
+    if weight.dim() != 2:
+        _einval("weight must be [V, D]")
+    _need_ids(dev, ids)
+    V, D = weight.shape
+    m = _embedding_desc(ids, weight, D, V, scale, vocab_start, vocab_total)
+    m.weight, m.w_ld = weight.data_ptr(), _rows(dev, "weight", weight, (V, D), None)
+    if out is None:
+        out = torch.empty((m.N, D), dtype=weight.dtype, device=dev)
+    _call(dev, lib.ce_embedding, ctypes.byref(m), _ptr(out), _rows(dev, "out", out, (m.N, D), weight.dtype))
+    return out
+
+
+def ce_embedding_workspace_bytes(tokens: int, D: int, v_local: int) -> int:
+    n = lib.ce_embedding_workspace_bytes(int(tokens), int(D), int(v_local))
+    if n == 0:
+        _check(_abi.CE_EINVAL)
+    return int(n)
+
+
+def ce_embedding_backward(dout, ids, v_local, scale=1.0, *, padding_idx=None, dw=None, accumulate=False, ws=None,
+                          vocab_start=0, vocab_total=None):
+    """The table's FP32 [v_local, D] gradient from ``dout`` [N, D], written to ``dw`` or added to it
+    (``accumulate``; a tied head's ce_linear_cross_entropy gradient).  Tokens equal to ``padding_idx`` add
+    nothing.  Returns dw."""
+    dev = _device_of(dout, "dout")
+    if dout.dim() != 2:
+        _einval("dout must be [N, D]")
+    _need_ids(dev, ids)
+    N, D = dout.shape
+    if ids.shape[0] != N:
+        _einval(f"{ids.shape[0]} ids for {N} rows of dout")
+    if padding_idx is not None and padding_idx < 0:
+        _einval("padding_idx must be a vocabulary index")
+    m = _embedding_desc(ids, dout, D, int(v_local), scale, vocab_start, vocab_total)
+    if accumulate and dw is None:
+        _einval("accumulate needs dw")
+    need = ce_embedding_workspace_bytes(N, D, v_local)
+    dw = torch.empty((v_local, D), dtype=torch.float32, device=dev) if dw is None else dw
+    ws = _workspace(need, dev) if ws is None else ws
+    _need(dev, "workspace", ws, torch.uint8)
+    _call(dev, lib.ce_embedding_backward, ctypes.byref(m), _ptr(dout), _rows(dev, "dout", dout, (N, D), None),
+          -1 if padding_idx is None else int(padding_idx), _ptr(dw),
+          _rows(dev, "dw", dw, (v_local, D), torch.float32), int(bool(accumulate)), _ptr(ws), ws.numel())
+    return dw
+
+
+class Embedding(torch.autograd.Function):
+    """Autograd form of ce_embedding; the gradient by ce_embedding_backward."""
+
+    @staticmethod
+    def forward(ctx, weight, ids, scale, padding_idx, grad_buffer, vocab_start, vocab_total):
+        flat = ids.reshape(-1)
+        out = ce_embedding(flat, weight.detach(), scale, vocab_start=vocab_start, vocab_total=vocab_total)
+        ctx.args = (scale, padding_idx, vocab_start, vocab_total, weight.shape)
+        ctx.grad_buffer = grad_buffer
+        ctx.save_for_backward(flat)
+        return out.view(*ids.shape, weight.shape[1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        (flat,) = ctx.saved_tensors
+        scale, padding_idx, vocab_start, vocab_total, (V, D) = ctx.args
+        dw = ce_embedding_backward(dout.reshape(-1, D).contiguous(), flat, V, scale, padding_idx=padding_idx,
+                                   dw=ctx.grad_buffer, accumulate=ctx.grad_buffer is not None,
+                                   vocab_start=vocab_start, vocab_total=vocab_total)
+        return dw if ctx.grad_buffer is None else None, None, None, None, None, None, None
+
+
+def embedding(ids, weight, scale=1.0, *, padding_idx=None, grad_buffer=None, vocab_start=0, vocab_total=None):
+    """``scale * weight[ids]`` for int64 ``ids`` of any shape; reaches autograd through Embedding (the FP32
+    gradient, which autograd casts to the weight's dtype).  With ``grad_buffer``, an FP32 [V, D] tensor, the
+    backward adds the gradient to it instead and ``weight.grad`` stays as it is: with a tied head, the buffer that
+    ce_linear_cross_entropy adds its dw to."""
+    if grad_buffer is not None:
+        _rows(_device_of(weight, "weight"), "grad_buffer", grad_buffer, weight.shape, torch.float32)
+    return Embedding.apply(weight, ids, scale, padding_idx, grad_buffer, vocab_start, vocab_total)
+
+
+# ---- RMS norm --------------------------------------------------------------------------------------------
+
+
+def _norm_desc(dev, x, weight, residual, eps):
+    if x.dim() != 2:
+        _einval("x must be [N, D]")
+    N, D = x.shape
+    _need(dev, "weight", weight, None, D)
+    if weight is None or tuple(weight.shape) != (D,):
+        _einval(f"weight must be [{D}]")
+    n = _abi.CeNorm()
+    n.x, n.x_ld, n.N, n.D = x.data_ptr(), _rows(dev, "x", x, (N, D), None), N, D
+    n.weight, n.dtype, n.weight_dtype, n.eps = weight.data_ptr(), _dtype_code(x), _dtype_code(weight), float(eps)
+    if residual is not None:
+        n.residual, n.residual_ld = residual.data_ptr(), _rows(dev, "residual", residual, (N, D), x.dtype)
+        if N == 0:
+            n.residual = None
+    return n
+
+
+def _sum_arg(dev, x, residual, sum_out):
+    """The buffer the sum goes to (None without a residual unless one is given) and its arguments."""
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if sum_out is None:
+        return None, 0
+    return sum_out, _rows(dev, "sum_out", sum_out, x.shape, x.dtype)
+
+
+def ce_rms_norm(x, weight, residual=None, eps=1e-6, *, out=None, sum_out=None):
+    """RMS norm of ``x + residual`` ([N, D]); returns (y, sum), the sum None without a residual (unless
+    ``sum_out`` asks for it).  ``out`` and ``sum_out`` may be x or residual themselves."""
+    dev = _device_of(x, "x")
+    n = _norm_desc(dev, x, weight, residual, eps)
+    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    total, total_ld = _sum_arg(dev, x, residual, sum_out)
+    _call(dev, lib.ce_rms_norm, ctypes.byref(n), _ptr(out), _rows(dev, "out", out, x.shape, x.dtype), _ptr(total),
+          total_ld)
+    return out, total
+
+
+def ce_rms_norm_quant(x, weight, residual=None, eps=1e-6, *, group=0, out=None, scales=None, sum_out=None):
+    """ce_rms_norm with its output in e4m3 (torch.float8_e4m3fn) and FP32 scales, one for each ``group`` columns
+    (32, 64 or 128; 0: one for the row).  Returns (q, scales [N, groups], sum or None)."""
+    dev = _device_of(x, "x")
+    n = _norm_desc(dev, x, weight, residual, eps)
+    N, D = x.shape
+    groups = -(-D // group) if group > 0 else 1
+    out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=dev) if out is None else out
+    scales = torch.empty((N, groups), dtype=torch.float32, device=dev) if scales is None else scales
+    _need(dev, "scales", scales, torch.float32, N * groups)
+    total, total_ld = _sum_arg(dev, x, residual, sum_out)
+    _call(dev, lib.ce_rms_norm_quant, ctypes.byref(n), _ptr(out),
+          _rows(dev, "out", out, (N, D), torch.float8_e4m3fn), int(group), _ptr(scales), _ptr(total), total_ld)
+    return out, scales, total
+
+
+def ce_rms_norm_workspace_bytes(rows: int, D: int) -> int:
+    n = lib.ce_rms_norm_workspace_bytes(int(rows), int(D))
+    if n == 0:
+        _check(_abi.CE_EINVAL)
+    return int(n)
+
+
+def ce_rms_norm_backward(dy, s, weight, eps=1e-6, *, dsum=None, dx=None, dweight=None, accumulate=False, ws=None,
+                         want_dx=True, want_dweight=True):
+    """The gradient from the forward's sum ``s`` ([N, D]): (dx, the gradient of x and of the residual, in s's
+    dtype; dweight, FP32 [D]).  ``dsum`` is the gradient that reaches the sum by the residual stream; ``dx`` may
+    be dy or dsum itself; ``accumulate`` adds to ``dweight``."""
+    dev = _device_of(s, "s")
+    n = _norm_desc(dev, s, weight, None, eps)
+    N, D = s.shape
+    dy_ld = _rows(dev, "dy", dy, (N, D), s.dtype)
+    dsum_ld = _rows(dev, "dsum", dsum, (N, D), s.dtype) if dsum is not None and N else 0
+    if accumulate and dweight is None:
+        _einval("accumulate needs dweight")
+    if dx is None and want_dx:
+        dx = torch.empty((N, D), dtype=s.dtype, device=dev)
+    if dweight is None and want_dweight:
+        dweight = torch.empty(D, dtype=torch.float32, device=dev)
+    _need(dev, "dweight", dweight, torch.float32, D)
+    if dweight is not None and ws is None:
+        ws = _workspace(ce_rms_norm_workspace_bytes(N, D), dev)
+    _need(dev, "workspace", ws, torch.uint8)
+    _call(dev, lib.ce_rms_norm_backward, ctypes.byref(n), _ptr(dy), dy_ld, _ptr(dsum) if N else None, dsum_ld,
+          _ptr(dx), _rows(dev, "dx", dx, (N, D), s.dtype) if dx is not None else 0, _ptr(dweight),
+          int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0)
+    return dx, dweight
+
+
+class RmsNorm(torch.autograd.Function):
+    """Autograd form of ce_rms_norm and ce_rms_norm_backward over (..., D) tensors.  Only the sum (or x itself)
+    and the weight are kept; the backward recomputes the row's scale from them."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        D = x.shape[-1]
+        flat = x.reshape(-1, D)
+        y, total = ce_rms_norm(flat, weight, None if residual is None else residual.reshape(-1, D), eps)
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        if residual is None:
+            ctx.save_for_backward(x, weight)
+            return y.view(x.shape)
+        total = total.view(x.shape)
+        ctx.save_for_backward(total, weight)
+        return y.view(x.shape), total
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum=None):
+        s, weight = ctx.saved_tensors
+        if dy is None:  # only the sum was used
+            return dsum, None, dsum if ctx.needs_input_grad[2] else None, None
+        D = s.shape[-1]
+
+        def flat(t):
+            return None if t is None else _grad_rows(t.reshape(-1, D))
+
+        dx, dweight = ce_rms_norm_backward(flat(dy), s.reshape(-1, D), weight, ctx.eps, dsum=flat(dsum),
+                                           want_dx=ctx.needs_input_grad[0] or ctx.needs_input_grad[2],
+                                           want_dweight=ctx.needs_input_grad[1])
+        dx = None if dx is None else dx.view(s.shape)
+        return (dx if ctx.needs_input_grad[0] else None, dweight, dx if ctx.needs_input_grad[2] else None, None)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6):
+    """RMS norm over the last dimension; with ``residual`` of ``x + residual``, returning (y, sum).  Reaches
+    autograd through RmsNorm: x, residual and weight (an FP32 gradient, cast to the weight's dtype)."""
+    if residual is not None and residual.shape != x.shape:
+        _einval(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
+    return RmsNorm.apply(x, weight, residual, eps)
+
+
+def norm_linear_cross_entropy(h, norm_weight, weight, target, label_smoothing=0.0, reduce_loss="mean",
+                              ignore_idx=-100, *, residual=None, eps=1e-6, smoothing="all", chunk_rows=0,
+                              gemm="auto"):
+    """The end of a language model: the final RMS norm (of ``h``, or of ``h + residual``), the head and the loss,
+    by rms_norm and linear_cross_entropy.  ``h`` and ``residual`` [N, D]."""
+    y = rms_norm(h, norm_weight, residual, eps)
+    return linear_cross_entropy(y if residual is None else y[0], weight, target, label_smoothing, reduce_loss,
+                                ignore_idx, smoothing=smoothing, chunk_rows=chunk_rows, gemm=gemm)

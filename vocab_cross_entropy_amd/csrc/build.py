@@ -34,6 +34,9 @@ COMMON = ["-std=c++17", "-fPIC", "-O3", f"-I{INCLUDE}", f"-I{CSRC}", "-Wall"]
 DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-ffp-contract=on"]
 
+SOURCES = ["ce_kernels.hip", "ce_gemm.hip", "ce_stream_ref.hip", "ce_process.hip", "ce_embed.hip", "ce_norm.hip",
+           "ce_api.cpp", "ce_linear.cpp", "ce_ops.cpp"]
+
 
 def _run(cmd):
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -56,18 +59,12 @@ def build(verbose: bool = False, variant: str = "") -> str:
     lib = PHASES_LIB if variant else LIB
     extra = ["-DCE_PHASE_CLOCK"] if variant else []
     os.makedirs(bdir, exist_ok=True)
-    kobj = os.path.join(bdir, "ce_kernels.o")
-    aobj = os.path.join(bdir, "ce_api.o")
-    lobj = os.path.join(bdir, "ce_linear.o")
-    gobj = os.path.join(bdir, "ce_gemm.o")
-    robj = os.path.join(bdir, "ce_stream_ref.o")
-    steps = [
-        [HIPCC, *DEVICE, *COMMON, *extra, "-c", os.path.join(CSRC, "ce_kernels.hip"), "-o", kobj],
-        [HIPCC, *DEVICE, *COMMON, *extra, "-c", os.path.join(CSRC, "ce_gemm.hip"), "-o", gobj],
-        [HIPCC, *DEVICE, *COMMON, *extra, "-c", os.path.join(CSRC, "ce_stream_ref.hip"), "-o", robj],
-        [HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, "ce_api.cpp"), "-o", aobj],
-        [HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, "ce_linear.cpp"), "-o", lobj],
-    ]
+    objs, steps = [], []
+    for src in SOURCES:
+        obj = os.path.join(bdir, os.path.splitext(src)[0] + ".o")
+        device = DEVICE if src.endswith(".hip") else []
+        steps.append([HIPCC, *device, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
+        objs.append(obj)
     for cmd in steps:
         out = _run(cmd)
         if verbose and out.strip():
@@ -75,7 +72,7 @@ def build(verbose: bool = False, variant: str = "") -> str:
     tmp = lib + ".tmp"
     # the chunked linear call's products run on the library's MFMA kernel (ce_gemm.hip) or on hipBLASLt
     # (ROCm's matrix-core GEMM library), per ce_linear.gemm
-    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", kobj, gobj, robj, aobj, lobj, "-L/opt/rocm/lib",
+    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-L/opt/rocm/lib",
           "-lhipblaslt", "-o", tmp])
     os.replace(tmp, lib)
     return lib

@@ -240,6 +240,8 @@ unsigned long long* phase_buffer(size_t bytes) { return bytes <= g_phase_bytes ?
 #else
 unsigned long long* phase_buffer(size_t) { return nullptr; }
 #endif
+ce_status check_logits_desc(const ce_logits* x) { return check_logits(x, false); }
+void profile_next(hipEvent_t* e0, hipEvent_t* e1) { prof_next(e0, e1); }
 void set_last_error(const char* msg) { snprintf(g_err, sizeof g_err, "%s", msg); }
 size_t fused_workspace_bytes(int64_t N, int32_t dtype, int64_t V, bool reduce) {
   return ws_layout(N, fused_auto_chunks(dtype, V), reduce, true).total;

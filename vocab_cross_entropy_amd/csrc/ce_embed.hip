@@ -1,0 +1,488 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   out_n = scale W[id_n]
+//   dW[v] (+)= scale * sum over { n : id_n = v } of dout_n
+//
+// Lookup: one read of the rows named and one write of the output.
+//
+// Gradient: every row of dout is read once and every row of dW that a token
+// names is written once (read once too when it is added to).  To make the sum's
+// order fixed and its writes few, the tokens are sorted by id first, ties by
+// position (a stable sort of N small keys, little beside the N rows of D values):
+//   up to kRankMax tokens whose (id, position) pair fits 32 bits: one launch in
+//     which each token's place is the count of smaller pairs (N^2 compares of LDS
+//     words, N^2 / 16384 cycles of the whole chip);
+//   more: a stable radix sort, 9 bits at most a pass, three launches a pass.
+// The sorted list is then cut into tiles of equally many tokens, so a token that
+// makes up a large share of the batch costs no more than the others.  A
+// workgroup adds up the runs of equal ids in its tile in FP32; a run inside one
+// tile goes straight to dW, a run that crosses tiles leaves one partial sum per
+// tile, and a last launch adds those in tile order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ce_internal.h"
+#include "ce_vec.h"
+
+namespace vce {
+namespace {
+
+constexpr int kT = 256;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // a launch holds below 2^32 work-items
+
+__host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Lanes that share one row: the smallest power of two that covers its groups, at most a workgroup.
+int lanes_log2(int64_t groups) {
+  int l = 0;
+  while (l < 8 && ((int64_t)1 << l) < groups) ++l;
+  return l;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
+  constexpr int EB = VecT<DT>::EB;
+  const int lanes = 1 << lanes_shift;
+  const int lane = (int)threadIdx.x & (lanes - 1);
+  const int64_t per = kT >> lanes_shift;
+  for (int64_t n = (int64_t)blockIdx.x * per + ((int)threadIdx.x >> lanes_shift); n < a.N;
+       n += (int64_t)gridDim.x * per) {
+    const int64_t id = a.ids[n * a.id_stride];
+    const uint64_t v = (uint64_t)id - (uint64_t)a.vocab_start;
+    char* out = a.out + n * a.out_ld * EB;
+    if (v < (uint64_t)a.V) {
+      const char* w = a.w + (int64_t)v * a.w_ld * EB;
+      for (int64_t j = (int64_t)lane * kG; j < a.D; j += (int64_t)lanes * kG) {
+        float f[kG];
+        load_f32<DT>(w, j, a.D, f);
+#pragma unroll
+        for (int e = 0; e < kG; ++e) f[e] *= a.scale;
+        store_group<DT, true>(out, j, a.D, f32_to_raw<DT>(f));
+      }
+    } else {
+      // another shard's id adds nothing here; an id outside the vocabulary is a caller's error
+      const float fill = (uint64_t)id < (uint64_t)a.vocab_total ? 0.f : __builtin_nanf("");
+      float f[kG];
+#pragma unroll
+      for (int e = 0; e < kG; ++e) f[e] = fill;
+      for (int64_t j = (int64_t)lane * kG; j < a.D; j += (int64_t)lanes * kG)
+        store_group<DT, true>(out, j, a.D, f32_to_raw<DT>(f));
+    }
+  }
+}
+
+// ---- sorting -------------------------------------------------------------
+
+// The sort key of token n: its row of this shard, or V for a token without a gradient here (the
+// padding id, another shard's, or no id at all); those come last.
+__device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t n) {
+  const int64_t id = a.ids[n * a.id_stride];
+  const uint64_t v = (uint64_t)id - (uint64_t)a.vocab_start;
+  return v < (uint64_t)a.V && (a.padding_idx < 0 || id != a.padding_idx) ? (uint32_t)v : (uint32_t)a.V;
+}
+
+int bits_of(int64_t v) {  // of the values 0 .. v
+  int b = 1;
+  while (b < 63 && ((int64_t)1 << b) <= v) ++b;
+  return b;
+}
+
+constexpr int64_t kRankMax = 8192;
+constexpr int kRankTokens = 32;  // tokens a workgroup places; 8 threads count for each
+
+// Place of every token among the pairs (key, position): the count of smaller ones.
+__global__ __launch_bounds__(kT) void k_rank(EmbedGradArgs a, int pos_bits, uint32_t* skey, uint32_t* sidx) {
+  __shared__ __align__(16) uint32_t pair[kRankMax];
+  __shared__ uint32_t part[kT / kRankTokens][kRankTokens];
+  constexpr int SL = kT / kRankTokens;
+  const int n = (int)a.N;
+  const int per = ((n + SL * 4 - 1) / (SL * 4)) * 4;  // pairs per slice, whole 16-byte words
+  for (int i = (int)threadIdx.x; i < per * SL; i += kT)
+    pair[i] = i < n ? (token_key(a, i) << pos_bits) | (uint32_t)i : 0xffffffffu;
+  __syncthreads();
+  const int tok = (int)threadIdx.x % kRankTokens, slice = (int)threadIdx.x / kRankTokens;
+  const int me = (int)blockIdx.x * kRankTokens + tok;
+  const uint32_t mine = me < n ? pair[me] : 0u;
+  uint32_t less = 0;
+  const u32x4v* p = reinterpret_cast<const u32x4v*>(pair + slice * per);
+  for (int i = 0; i < per / 4; ++i) {
+    const u32x4v q = p[i];
+    less += (q.x < mine ? 1u : 0u) + (q.y < mine ? 1u : 0u) + (q.z < mine ? 1u : 0u) + (q.w < mine ? 1u : 0u);
+  }
+  part[slice][tok] = less;
+  __syncthreads();
+  if (slice == 0 && me < n) {
+    for (int k = 1; k < SL; ++k) less += part[k][tok];
+    skey[less] = mine >> pos_bits;
+    sidx[less] = mine & ((1u << pos_bits) - 1u);
+  }
+}
+
+constexpr int kSortTile = 2048;
+constexpr int kMaxDigit = 9;
+constexpr int kWaves = kT / 64;
+
+struct SortPass {
+  const uint32_t* key_in;  // NULL: the first pass reads the ids
+  const uint32_t* idx_in;
+  uint32_t* key_out;
+  uint32_t* idx_out;
+  uint32_t* hist;          // [bins][tiles]
+  int64_t tiles;
+  int shift, bits;
+};
+
+__global__ __launch_bounds__(kT) void k_sort_count(EmbedGradArgs a, SortPass s) {
+  __shared__ uint32_t h[1 << kMaxDigit];
+  const int bins = 1 << s.bits;
+  for (int i = (int)threadIdx.x; i < bins; i += kT) h[i] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * kSortTile, hi = min64(lo + kSortTile, a.N);
+  for (int64_t n = lo + (int)threadIdx.x; n < hi; n += kT) {
+    const uint32_t key = s.key_in ? s.key_in[n] : token_key(a, n);
+    atomicAdd(&h[(key >> s.shift) & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < bins; i += kT) s.hist[(int64_t)i * s.tiles + blockIdx.x] = h[i];
+}
+
+// Exclusive sums over n counts, in place, by one workgroup.
+__global__ __launch_bounds__(1024) void k_sort_scan(uint32_t* h, int64_t n) {
+  __shared__ uint32_t wave_total[16];
+  uint32_t base = 0;
+  const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
+  for (int64_t at = 0; at < n; at += 4096) {
+    const int64_t i = at + (int64_t)threadIdx.x * 4;
+    uint32_t v[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = i + k < n ? h[i + k] : 0u;
+      sum += v[k];
+    }
+    uint32_t scan = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(scan, d, 64);
+      if (lane >= d) scan += o;
+    }
+    __syncthreads();
+    if (lane == 63) wave_total[w] = scan;
+    __syncthreads();
+    uint32_t before = base, all = 0;
+    for (int k = 0; k < 16; ++k) {
+      if (k < w) before += wave_total[k];
+      all += wave_total[k];
+    }
+    uint32_t run = before + scan - sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k < n) h[i + k] = run;
+      run += v[k];
+    }
+    base += all;
+  }
+}
+
+// Moves a tile's tokens to their places.  Wave w takes the w-th quarter of the
+// tile in order; a token's place is its bin's start for this tile (from the
+// scan), plus the tokens of that bin in earlier waves, plus those earlier in
+// its own wave: equal keys keep their order.
+__global__ __launch_bounds__(kT) void k_sort_move(EmbedGradArgs a, SortPass s) {
+  __shared__ uint32_t next[kWaves][1 << kMaxDigit];
+  const int bins = 1 << s.bits;
+  for (int i = (int)threadIdx.x; i < kWaves * bins; i += kT) next[i / bins][i % bins] = 0;
+  __syncthreads();
+  constexpr int QUARTER = kSortTile / kWaves, ROUNDS = QUARTER / 64;
+  const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
+  const int64_t lo = (int64_t)blockIdx.x * kSortTile + w * QUARTER;
+  uint32_t key[ROUNDS], idx[ROUNDS];
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    const int64_t n = lo + k * 64 + lane;
+    key[k] = n < a.N ? (s.key_in ? s.key_in[n] : token_key(a, n)) : 0u;
+    idx[k] = n < a.N ? (s.idx_in ? s.idx_in[n] : (uint32_t)n) : 0u;
+    if (n < a.N) atomicAdd(&next[w][(key[k] >> s.shift) & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < bins; i += kT) {
+    uint32_t at = s.hist[(int64_t)i * s.tiles + blockIdx.x];
+    for (int k = 0; k < kWaves; ++k) {
+      const uint32_t c = next[k][i];
+      next[k][i] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  // rounds are kept in step by barriers: a wave reads its bins' next places, then their last lanes move them on
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    const bool live = lo + k * 64 + lane < a.N;
+    const uint32_t bin = (key[k] >> s.shift) & (bins - 1);
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < s.bits; ++b) {
+      const bool bit = (bin >> b) & 1u;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    const uint32_t before = (uint32_t)__popcll(same & (((uint64_t)1 << lane) - 1));
+    const uint32_t first = live ? next[w][bin] : 0u;
+    __syncthreads();
+    if (live) {
+      const uint32_t to = first + before;
+      s.key_out[to] = key[k];
+      s.idx_out[to] = idx[k];
+      if (before + 1 == (uint32_t)__popcll(same)) next[w][bin] = to + 1;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- sums ----------------------------------------------------------------
+
+struct SumArgs {
+  const uint32_t* skey;
+  const uint32_t* sidx;
+  float* parts;            // [2 tiles][D]: a tile's run from the tile before, its run into the next
+  int64_t tiles, tile;     // tokens per tile
+  int64_t col_blocks;      // workgroups across a row
+  int lanes_shift;
+  int64_t fill_blocks;     // workgroups that write the rows no token names (0 when dW is added to)
+};
+constexpr int kFillRows = 32;
+
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t v, int64_t j, const float (&acc)[kG]) {
+  char* row = reinterpret_cast<char*>(a.dw + (int64_t)v * a.dw_ld);
+  float f[kG];
+  if (a.accumulate) {
+    load_f32<CE_F32>(row, j, a.D, f);
+#pragma unroll
+    for (int e = 0; e < kG; ++e) f[e] = __builtin_fmaf(acc[e], a.scale, f[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kG; ++e) f[e] = acc[e] * a.scale;
+  }
+  store_group<CE_F32>(row, j, a.D, f32_to_raw<CE_F32>(f));
+}
+
+// Rows of dW that no token names: a search of the sorted keys for each, zeros where it is not found.
+__device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
+  __shared__ uint32_t named;
+  const int64_t v0 = block * kFillRows;
+  if (threadIdx.x < 64) {
+    const int64_t v = v0 + (int)threadIdx.x;
+    int64_t lo = 0, hi = a.N;  // the first sorted token with a key of at least v
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (s.skey[mid] < (uint32_t)v) lo = mid + 1; else hi = mid;
+    }
+    const bool found = lo < a.N && s.skey[lo] == (uint32_t)v;
+    const uint64_t all = __ballot(found);
+    if (threadIdx.x == 0) named = (uint32_t)all;
+  }
+  __syncthreads();
+  const float zero[kG] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const Raw<CE_F32> z = f32_to_raw<CE_F32>(zero);
+  for (int k = 0; k < kFillRows && v0 + k < a.V; ++k) {
+    if ((named >> k) & 1u) continue;
+    char* row = reinterpret_cast<char*>(a.dw + (v0 + k) * a.dw_ld);
+    for (int64_t j = (int64_t)threadIdx.x * kG; j < a.D; j += (int64_t)kT * kG)
+      store_group<CE_F32, true>(row, j, a.D, z);
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
+  constexpr int EB = VecT<DT>::EB;
+  for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
+    if (b >= sum_blocks) {
+      __syncthreads();
+      fill_rows(a, s, b - sum_blocks);
+      continue;
+    }
+    const int64_t cb = b % s.col_blocks;
+    const int64_t t = (b / s.col_blocks) * (kT >> s.lanes_shift) + ((int)threadIdx.x >> s.lanes_shift);
+    const int64_t j = ((cb << s.lanes_shift) + ((int)threadIdx.x & ((1 << s.lanes_shift) - 1))) * kG;
+    if (t >= s.tiles || j >= a.D) continue;
+    const int64_t i0 = t * s.tile, i1 = min64(i0 + s.tile, a.N);
+    float acc[kG];
+#pragma unroll
+    for (int e = 0; e < kG; ++e) acc[e] = 0.f;
+    bool from_before = i0 > 0 && s.skey[i0 - 1] == s.skey[i0];
+    uint32_t key = s.skey[i0];
+    for (int64_t i = i0; i < i1 && key != (uint32_t)a.V; ++i) {
+      float f[kG];
+      load_f32<DT, true>(a.dout + (int64_t)s.sidx[i] * a.dout_ld * EB, j, a.D, f);
+#pragma unroll
+      for (int e = 0; e < kG; ++e) acc[e] += f[e];
+      const uint32_t nk = i + 1 < a.N ? s.skey[i + 1] : 0xffffffffu;
+      const bool last = i + 1 == i1;
+      if (nk != key || last) {
+        const bool goes_on = nk == key;
+        if (from_before || goes_on)
+          store_group<CE_F32>(reinterpret_cast<char*>(s.parts + (2 * t + (from_before ? 0 : 1)) * a.D), j, a.D,
+                              f32_to_raw<CE_F32>(acc));
+        else
+          write_row(a, key, j, acc);
+#pragma unroll
+        for (int e = 0; e < kG; ++e) acc[e] = 0.f;
+        from_before = false;
+        key = nk;
+      }
+    }
+  }
+}
+
+// The runs that cross tiles: the workgroup of the tile where a run starts adds
+// its partial sums in tile order.  Four waves take a quarter of them each (256
+// columns, four a lane).
+__global__ __launch_bounds__(kT) void k_embed_join(EmbedGradArgs a, SumArgs s) {
+  __shared__ float part[kWaves][256];
+  const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
+  for (int64_t t = blockIdx.x; t < s.tiles - 1; t += gridDim.x) {
+    const int64_t i1 = (t + 1) * s.tile;
+    const uint32_t key = s.skey[i1 - 1];
+    if (key == (uint32_t)a.V || s.skey[i1] != key) continue;        // nothing crosses
+    const int64_t i0 = t * s.tile;
+    if (i0 > 0 && s.skey[i0] == key && s.skey[i0 - 1] == key) continue;  // started in an earlier tile
+    // tiles t + 1 .. last begin with the run's key
+    int64_t lo = t + 1, hi = s.tiles - 1;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (s.skey[mid * s.tile] == key) lo = mid; else hi = mid - 1;
+    }
+    const int64_t n = lo - t + 1;  // partial sums: the start's, then one per later tile
+    const int64_t per = ceil_div(n, kWaves);
+    for (int64_t c = (int64_t)blockIdx.y * 256; c < a.D; c += (int64_t)gridDim.y * 256) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int64_t k = w * per; k < min64((w + 1) * per, n); ++k) {
+        const float* p = s.parts + (k == 0 ? 2 * t + 1 : 2 * (t + k)) * a.D + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t j = e * 64 + lane;
+          if (c + j < a.D) acc[e] += p[j];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[w][e * 64 + lane] = acc[e];
+      __syncthreads();
+      const int64_t j = c + (int)threadIdx.x;
+      if (j < a.D) {
+        float v = part[0][threadIdx.x];
+        for (int k = 1; k < kWaves; ++k) v += part[k][threadIdx.x];
+        float* d = a.dw + (int64_t)key * a.dw_ld + j;
+        *d = a.accumulate ? __builtin_fmaf(v, a.scale, *d) : v * a.scale;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Workspace: sorted keys and positions (twice for the radix sort's passes), its counts, the partial sums.
+struct GradLayout {
+  bool rank;
+  int key_bits, passes, digit;
+  int64_t sort_tiles, tile, tiles;
+  size_t keys[2], idx[2], hist, parts, total;
+};
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+GradLayout grad_layout(int64_t N, int64_t D, int64_t V) {
+  GradLayout g{};
+  g.key_bits = bits_of(V);
+  g.rank = N <= kRankMax && g.key_bits + bits_of(N - 1) < 32;  // the all-ones pair stays free
+  g.passes = g.rank ? 0 : (g.key_bits + kMaxDigit - 1) / kMaxDigit;
+  g.digit = g.rank ? 0 : (g.key_bits + g.passes - 1) / g.passes;
+  g.sort_tiles = ceil_div(N, kSortTile);
+  // tokens per tile: 16, more where that would leave over 4096 tiles (and as many partial sums)
+  g.tile = ceil_div(N, 4096);
+  if (g.tile < 16) g.tile = 16;
+  g.tiles = ceil_div(N, g.tile);
+  size_t off = 0;
+  for (int k = 0; k < (g.rank ? 1 : 2); ++k) {
+    g.keys[k] = off;
+    off = align256(off + (size_t)N * 4);
+    g.idx[k] = off;
+    off = align256(off + (size_t)N * 4);
+  }
+  g.hist = off;
+  if (!g.rank) off = align256(off + ((size_t)g.sort_tiles << g.digit) * 4);
+  g.parts = off;
+  off = align256(off + (size_t)g.tiles * 2 * (size_t)D * 4);
+  g.total = off < 256 ? 256 : off;
+  return g;
+}
+
+}  // namespace
+
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream) {
+  if (a.N == 0) return hipSuccess;
+  const int sh = lanes_log2(ceil_div(a.D, kG));
+  const dim3 grid((uint32_t)min64(ceil_div(a.N, kT >> sh), kMaxBlocks));
+  if (a.dtype == CE_BF16)
+    hipLaunchKernelGGL(k_embed<CE_BF16>, grid, dim3(kT), 0, stream, a, sh);
+  else
+    hipLaunchKernelGGL(k_embed<CE_F32>, grid, dim3(kT), 0, stream, a, sh);
+  return hipGetLastError();
+}
+
+size_t embed_grad_workspace(int64_t N, int64_t D, int64_t V) { return grad_layout(N, D, V).total; }
+
+hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
+  hipError_t e;
+  if (a.N == 0) return a.accumulate ? hipSuccess : launch_fill_f32(a.dw, a.V, a.D, a.dw_ld, stream);
+  const GradLayout g = grad_layout(a.N, a.D, a.V);
+  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(a.ws + g.keys[0]), reinterpret_cast<uint32_t*>(a.ws + g.keys[1])};
+  uint32_t* idx[2] = {reinterpret_cast<uint32_t*>(a.ws + g.idx[0]), reinterpret_cast<uint32_t*>(a.ws + g.idx[1])};
+  int cur = 0;
+  if (g.rank) {
+    hipLaunchKernelGGL(k_rank, dim3((uint32_t)ceil_div(a.N, kRankTokens)), dim3(kT), 0, stream, a,
+                       bits_of(a.N - 1), key[0], idx[0]);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else {
+    for (int p = 0; p < g.passes; ++p) {
+      SortPass s;
+      s.key_in = p ? key[cur] : nullptr;
+      s.idx_in = p ? idx[cur] : nullptr;
+      s.key_out = key[p ? cur ^ 1 : 0];
+      s.idx_out = idx[p ? cur ^ 1 : 0];
+      s.hist = reinterpret_cast<uint32_t*>(a.ws + g.hist);
+      s.tiles = g.sort_tiles;
+      s.shift = p * g.digit;
+      s.bits = g.digit;
+      const dim3 grid((uint32_t)g.sort_tiles);
+      hipLaunchKernelGGL(k_sort_count, grid, dim3(kT), 0, stream, a, s);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(1024), 0, stream, s.hist, g.sort_tiles << g.digit);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      hipLaunchKernelGGL(k_sort_move, grid, dim3(kT), 0, stream, a, s);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      if (p) cur ^= 1;
+    }
+  }
+  SumArgs s;
+  s.skey = key[cur];
+  s.sidx = idx[cur];
+  s.parts = reinterpret_cast<float*>(a.ws + g.parts);
+  s.tiles = g.tiles;
+  s.tile = g.tile;
+  s.lanes_shift = lanes_log2(ceil_div(a.D, kG));
+  s.col_blocks = ceil_div(ceil_div(a.D, kG), (int64_t)1 << s.lanes_shift);
+  s.fill_blocks = a.accumulate ? 0 : ceil_div(a.V, kFillRows);
+  const int64_t sum_blocks = ceil_div(g.tiles, kT >> s.lanes_shift) * s.col_blocks;
+  const dim3 grid((uint32_t)min64(sum_blocks + s.fill_blocks, kMaxBlocks));
+  if (a.dtype == CE_BF16)
+    hipLaunchKernelGGL(k_embed_sum<CE_BF16>, grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else
+    hipLaunchKernelGGL(k_embed_sum<CE_F32>, grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (g.tiles > 1) {
+    const dim3 jgrid((uint32_t)min64(g.tiles - 1, 1 << 20), (uint32_t)min64(ceil_div(a.D, 256), 16));
+    hipLaunchKernelGGL(k_embed_join, jgrid, dim3(kT), 0, stream, a, s);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace vce

@@ -208,6 +208,102 @@ struct GemmBf16 {
 bool gemm_bf16_supported(const GemmBf16& g);
 hipError_t launch_gemm_bf16(const GemmBf16& g, hipStream_t stream);
 
+// Logit processing (ce_process.hip): row r = i0 * d1 + i1 of x to the same row of z.
+struct ProcessArgs {
+  const char* x;
+  char* z;
+  int32_t dtype;
+  int64_t N, d1, V;
+  int64_t s0, s1, zs0, zs1;   // element strides of x and z
+  int64_t vocab_start;
+  const int64_t* hist;        // hist_max tokens per row, or NULL
+  int64_t hs0, hs1, hist_max;
+  const int32_t* hist_len;    // [N] or NULL: hist_max
+  const int32_t* prompt_len;  // [N] or NULL: 0
+  const float* repetition;    // [N] or NULL: 1
+  const float* frequency;     // [N] or NULL: 0
+  const float* presence;      // [N] or NULL: 0
+  const float* temperature;   // [N] or NULL: 1
+  const float* bias;          // V values per row, or NULL
+  int64_t bs0, bs1;
+  const uint32_t* mask;       // ceil(V / 32) words per row, or NULL
+  int64_t ms0, ms1;
+  uint8_t* signs;             // ceil(V / 8) bytes per row, or NULL
+  int64_t signs_ld;
+  // set by process_plan
+  int64_t chunk_cols;         // columns per workgroup item, a multiple of 8
+  int64_t chunks;             // items per row
+};
+void process_plan(ProcessArgs* a);
+hipError_t launch_process(const ProcessArgs& a, bool backward, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
+
+// Embedding (ce_embed.hip).
+struct EmbedArgs {
+  const int64_t* ids;         // N ids, id_stride apart
+  int64_t id_stride, N, D;
+  const char* w;              // [V_local, D] rows w_ld elements apart
+  int64_t w_ld, V, vocab_start, vocab_total;
+  char* out;                  // [N, D] rows out_ld elements apart
+  int64_t out_ld;
+  int32_t dtype;
+  float scale;
+};
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
+
+struct EmbedGradArgs {
+  const int64_t* ids;
+  int64_t id_stride, N, D;
+  const char* dout;           // [N, D] rows dout_ld elements apart
+  int64_t dout_ld;
+  int32_t dtype;
+  int64_t V, vocab_start, padding_idx;  // padding_idx < 0: none
+  float* dw;                  // [V, D] rows dw_ld elements apart
+  int64_t dw_ld;
+  float scale;
+  int32_t accumulate;
+  char* ws;
+};
+constexpr int64_t kEmbedMaxTokens = (int64_t)1 << 26;
+size_t embed_grad_workspace(int64_t N, int64_t D, int64_t V);
+hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream);
+
+// RMS norm (ce_norm.hip).
+constexpr int64_t kNormMaxCols = 32768;
+struct NormArgs {
+  const char* x;
+  const char* residual;       // or NULL
+  const char* weight;         // D values
+  int32_t dtype, wdtype;
+  int64_t N, D, x_ld, r_ld;
+  float eps;
+  char* y;                    // the type's own output, or NULL
+  int64_t y_ld;
+  uint8_t* q;                 // e4m3 output, or NULL
+  int64_t q_ld;
+  float* scales;              // [N, ceil(D / group)]
+  int32_t group;              // columns per scale; 0: the row
+  char* sum;                  // x + residual, or NULL
+  int64_t sum_ld;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormGradArgs {
+  const char* s;              // the forward's sum
+  const char* dy;
+  const char* dsum;           // or NULL
+  const char* weight;
+  int32_t dtype, wdtype;
+  int64_t N, D, s_ld, dy_ld, dsum_ld;
+  float eps;
+  char* dx;                   // or NULL
+  int64_t dx_ld;
+  float* dweight;             // [D] or NULL
+  int32_t accumulate;
+  float* parts;               // workspace
+};
+size_t norm_grad_workspace(int64_t N, int64_t D);
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
+
 // The instrumented build's phase-stamp buffer when it holds `bytes`, else NULL
 // (always NULL in the normal build).
 unsigned long long* phase_buffer(size_t bytes);
@@ -215,6 +311,8 @@ unsigned long long* phase_buffer(size_t bytes);
 // Shared by the entry points (ce_api.cpp): the calling thread's error detail,
 // and the fused call's workspace need for N whole rows of V columns.
 void set_last_error(const char* msg);
+ce_status check_logits_desc(const ce_logits* x);
+void profile_next(hipEvent_t* e0, hipEvent_t* e1);
 size_t fused_workspace_bytes(int64_t N, int32_t dtype, int64_t V, bool reduce);
 // every check of ce_fwd_bwd_fused that depends on the logits' shape and the
 // parameters (none on buffers), and the plan: chunks per row K, body vectors

@@ -1,0 +1,156 @@
+// Device helpers shared by the kernels around the loss (logit processing,
+// embedding, RMS norm): groups of eight columns at any element alignment, and
+// sums over a wave or a workgroup.
+//
+// A row is walked in groups of eight columns that start at multiples of eight
+// whatever the row's address, so that per-column side data (mask bits, count
+// words, scale groups) lines up with the groups.  gfx950 serves 16-byte global
+// accesses at any alignment, so a row that starts off a 16-byte boundary takes
+// the same instructions as an aligned one, with more cache lines per access.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ce.h"
+
+namespace vce {
+
+constexpr int kG = 8;  // columns per group
+
+typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
+// the same 16 bytes at element alignment
+typedef u32x4v u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4v u32x4_a4 __attribute__((aligned(4)));
+
+template <int DT>
+struct VecT;
+template <>
+struct VecT<CE_BF16> {
+  static constexpr int EB = 2;
+  static constexpr int NV = 1;  // 16-byte words per group
+  typedef u32x4_a2 Word;
+};
+template <>
+struct VecT<CE_F32> {
+  static constexpr int EB = 4;
+  static constexpr int NV = 2;
+  typedef u32x4_a4 Word;
+};
+
+// eight columns as loaded
+template <int DT>
+struct Raw {
+  u32x4v w[VecT<DT>::NV];
+};
+
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  f2 in = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(in, b2));
+}
+
+template <int DT>
+__device__ __forceinline__ void raw_to_f32(const Raw<DT>& r, float (&f)[kG]) {
+  if constexpr (DT == CE_BF16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(r.w[0][k] << 16);
+      f[2 * k + 1] = __uint_as_float(r.w[0][k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kG; ++k) f[k] = __uint_as_float(r.w[k / 4][k % 4]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> f32_to_raw(const float (&f)[kG]) {
+  Raw<DT> r;
+  if constexpr (DT == CE_BF16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.w[0][k] = pack2_bf16(f[2 * k], f[2 * k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kG; ++k) r.w[k / 4][k % 4] = __float_as_uint(f[k]);
+  }
+  return r;
+}
+
+// Columns j .. j + 7 of a row of `cols` columns; those past the row's end read
+// as zero and are never touched in memory.  NT sets the non-temporal bit, for
+// data that is touched once.
+template <int DT, bool NT = false>
+__device__ __forceinline__ Raw<DT> load_group(const char* row, int64_t j, int64_t cols) {
+  typedef typename VecT<DT>::Word Word;
+  Raw<DT> r;
+  if (j + kG <= cols) {
+#pragma unroll
+    for (int k = 0; k < VecT<DT>::NV; ++k) {
+      const Word* p = reinterpret_cast<const Word*>(row + j * VecT<DT>::EB) + k;
+      if constexpr (NT)
+        r.w[k] = __builtin_nontemporal_load(p);
+      else
+        r.w[k] = *p;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < VecT<DT>::NV; ++k) r.w[k] = u32x4v{0u, 0u, 0u, 0u};
+    // a loop over the elements that are there, with every index a constant
+    // (registers cannot be indexed)
+#pragma unroll
+    for (int e = 0; e < kG - 1; ++e) {
+      if (j + e < cols) {
+        if constexpr (DT == CE_BF16)
+          r.w[0][e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[j + e] << (16 * (e & 1));
+        else
+          r.w[e / 4][e % 4] = reinterpret_cast<const uint32_t*>(row)[j + e];
+      }
+    }
+  }
+  return r;
+}
+
+template <int DT, bool NT = false>
+__device__ __forceinline__ void store_group(char* row, int64_t j, int64_t cols, const Raw<DT>& r) {
+  typedef typename VecT<DT>::Word Word;
+  if (j + kG <= cols) {
+#pragma unroll
+    for (int k = 0; k < VecT<DT>::NV; ++k) {
+      Word* p = reinterpret_cast<Word*>(row + j * VecT<DT>::EB) + k;
+      if constexpr (NT)
+        __builtin_nontemporal_store(r.w[k], p);
+      else
+        *p = r.w[k];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kG - 1; ++e) {
+      if (j + e < cols) {
+        if constexpr (DT == CE_BF16)
+          reinterpret_cast<uint16_t*>(row)[j + e] = (uint16_t)(r.w[0][e / 2] >> (16 * (e & 1)));
+        else
+          reinterpret_cast<uint32_t*>(row)[j + e] = r.w[e / 4][e % 4];
+      }
+    }
+  }
+}
+
+template <int DT, bool NT = false>
+__device__ __forceinline__ void load_f32(const char* row, int64_t j, int64_t cols, float (&f)[kG]) {
+  raw_to_f32<DT>(load_group<DT, NT>(row, j, cols), f);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+  return v;
+}
+
+}  // namespace vce
