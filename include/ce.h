@@ -441,14 +441,16 @@ typedef struct ce_process {
                              vocabulary indices; any outside this buffer's columns (padding, another shard's)
                              count nowhere */
   int64_t history_s0, history_s1;
-  int64_t history_max;    /* tokens of the longest row (the width of `history`), below 2^31 */
+  int64_t history_max;    /* tokens of the longest row, below 2^31; every row has this many readable (the width of
+                             `history`), whatever its history_len */
   const int32_t* history_len; /* [N] tokens of row r, taken into [0, history_max]; NULL: history_max */
   const int32_t* prompt_len;  /* [N] how many of them, the first ones, are the prompt's; NULL: 0 */
   const float* repetition;    /* [N], > 0; penalties need a history (CE_EINVAL) */
   const float* frequency;     /* [N] */
   const float* presence;      /* [N] */
   const float* temperature;   /* [N], > 0 and at least 2^-126 */
-  const float* bias;      /* row (i0, i1)'s v_local values at i0 * bias_s0 + i1 * bias_s1 (stride 0: shared) */
+  const float* bias;      /* row (i0, i1)'s v_local values at i0 * bias_s0 + i1 * bias_s1 (stride 0: shared), a row
+                             below 4 GiB (CE_ELAYOUT) */
   int64_t bias_s0, bias_s1;
   const uint32_t* mask;   /* row (i0, i1)'s ceil(v_local / 32) words, strides in words (0: shared); bit j % 32 of
                              word j / 32 is 1 where local column j is allowed */
@@ -483,7 +485,7 @@ ce_status ce_logits_process_backward(const ce_logits* dz, const ce_logits* out, 
 typedef struct ce_embedding_desc {
   const int64_t* ids;  /* device, id n at ids[n * id_stride] */
   int64_t id_stride;   /* >= 0 */
-  int64_t N, D;        /* tokens (at most 2^26) and columns */
+  int64_t N, D;        /* tokens (at most 2^26) and columns (an FP32 row below 4 GiB, else CE_ELAYOUT) */
   const void* weight;  /* device [v_local, D], row stride w_ld elements (not read by the gradient) */
   int64_t w_ld;
   int32_t dtype;       /* CE_BF16 or CE_F32, for weight, out and dout */

@@ -60,6 +60,8 @@ PROCESS = [
     ("temperature_misaligned", dict(p=dict(temperature=P + 2)), ELAYOUT),
     ("mask_misaligned", dict(p=dict(mask=P + 1)), ELAYOUT),
     ("bias_misaligned", dict(p=dict(bias=P + 3)), ELAYOUT),
+    ("bias_row_of_4gib", dict(x=dict(d0=1, d1=1, s0=1 << 30, s1=1 << 30, v_local=1 << 30, vocab_total=1 << 30),
+                              p=dict(bias=P, signs_ld=1 << 28)), ELAYOUT),
     ("mask_negative_stride", dict(p=dict(mask_s0=-1)), ELAYOUT),
     ("bias_negative_stride", dict(p=dict(bias=P, bias_s1=-1)), ELAYOUT),
     ("signs_narrow", dict(p=dict(signs_ld=1)), ELAYOUT),
@@ -94,6 +96,7 @@ EMBED = [
     ("no_columns", dict(m=dict(D=0)), EINVAL),
     ("no_rows", dict(m=dict(v_local=0)), EINVAL),
     ("columns_many", dict(m=dict(D=1 << 31)), EINVAL),
+    ("row_of_4gib", dict(m=dict(D=1 << 30, w_ld=1 << 30), out_ld=1 << 30), ELAYOUT),
     ("past_vocabulary", dict(m=dict(vocab_start=1)), ELAYOUT),
     ("null_ids", dict(m=dict(ids=None)), EINVAL),
     ("ids_misaligned", dict(m=dict(ids=P + 4)), ELAYOUT),

@@ -25,14 +25,21 @@ __all__ = [
 ]
 
 
+# These calls are small beside the loss (one decoding step's norm takes 4 us on the device), so the checks below
+# first test the common case in one expression and name what is wrong only when it fails.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(dev: torch.device, fn, *args):
     """Run an entry point on torch's current stream of ``dev``, with ``dev`` the current device (kernels are
     looked up per device)."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)))
+    if dev.index == _current_device():
+        status = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+            status = fn(*args, _stream(dev))
+    if status:
+        _check(status)
 
 
 def _einval(msg: str):
@@ -44,15 +51,18 @@ def _elayout(msg: str):
 
 
 def _rows(dev, what, t, shape, dtype):
-    """``t`` is a [rows, columns] matrix on ``dev`` with contiguous columns; its row stride."""
-    if t is None:
-        _einval(f"{what} is missing")
-    _need(dev, what, t, dtype, contiguous=False)
-    if tuple(t.shape) != tuple(shape):
-        _einval(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    """``t`` is a [rows, columns] matrix on ``dev`` with contiguous columns (``dtype`` None: any); its row stride."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev.index
+            and (dtype is None or t.dtype == dtype)):
+        if t is None:
+            _einval(f"{what} is missing")
+        _need(dev, what, t, dtype, contiguous=False)
+        if tuple(t.shape) != tuple(shape):
+            _einval(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    ld, col = t.stride()
+    if col != 1 and shape[1] > 1:
         _elayout(f"{what} needs contiguous columns")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
 # ---- logit processing ------------------------------------------------------------------------------------
@@ -63,37 +73,46 @@ def _side(dev, what, t, x, width, dtype):
     if t is None:
         return None, 0, 0
     _need(dev, what, t, dtype, contiguous=False)
-    if t.dim() != 3 or t.shape[:2] != x.shape[:2] or t.shape[2] < width:
-        _einval(f"{what} must be ({x.shape[0]}, {x.shape[1]}, {width}), got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    shape = t.shape
+    if len(shape) != 3 or shape[:2] != x.shape[:2] or shape[2] < width:
+        _einval(f"{what} must be ({x.shape[0]}, {x.shape[1]}, {width}), got {tuple(shape)}")
+    s0, s1, col = t.stride()
+    if col != 1 and shape[2] > 1:
         _elayout(f"{what} needs a contiguous last dimension")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), s0, s1
+
+
+def _per_row(dev, what, t, N, dtype):
+    """The address of an [N] array on ``dev``, None without one."""
+    if t is None:
+        return None
+    _need(dev, what, t, dtype, N)
+    return t.data_ptr()
 
 
 def _process_desc(dev, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask,
                   temperature, signs):
-    N, V = x.shape[0] * x.shape[1], x.shape[2]
-    p = _abi.CeProcess()
-    p.history, p.history_s0, p.history_s1 = _side(dev, "history", history, x, 0, torch.int64)
-    p.history_max = 0 if history is None else history.shape[2]
-    for what, t, dtype in (("history_len", history_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
-                           ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
-                           ("presence", presence, torch.float32), ("temperature", temperature, torch.float32)):
-        if t is not None:
-            _need(dev, what, t, dtype, N)
-            setattr(p, what, t.data_ptr())
-    if history is not None and history.numel() == 0:
-        # no row has a token, so nothing is counted; an empty tensor has no address
-        p.history_max = 0
-        p.history = p.history_len = p.prompt_len = p.repetition = p.frequency = p.presence = None
-    p.bias, p.bias_s0, p.bias_s1 = _side(dev, "bias", bias, x, V, torch.float32)
-    p.mask, p.mask_s0, p.mask_s1 = _side(dev, "mask", mask, x, (V + 31) // 32, torch.int32)
+    d0, d1, V = x.shape
+    N = d0 * d1
+    # no row has a token where the tensor is empty (and it has no address): nothing is counted then
+    counted = history is not None and history.numel() > 0
+    hist = _side(dev, "history", history, x, 0, torch.int64)
+    hist_len, prompt = (_per_row(dev, "history_len", history_len, N, torch.int32),
+                        _per_row(dev, "prompt_len", prompt_len, N, torch.int32))
+    penalties = (_per_row(dev, "repetition", repetition, N, torch.float32),
+                 _per_row(dev, "frequency", frequency, N, torch.float32),
+                 _per_row(dev, "presence", presence, N, torch.float32))
+    if history is not None and not counted:
+        hist, hist_len, prompt, penalties = (None, 0, 0), None, None, (None, None, None)
+    signs_ptr, signs_ld = None, 0
     if signs is not None:
         if signs.dim() != 2 or signs.shape[1] < (V + 7) // 8:
             _einval(f"signs must be ({N}, {(V + 7) // 8}), see logits_signs")
-        p.signs_ld = _rows(dev, "signs", signs, (N, signs.shape[1]), torch.uint8)
-        p.signs = signs.data_ptr()
-    return p
+        signs_ptr, signs_ld = signs.data_ptr(), _rows(dev, "signs", signs, (N, signs.shape[1]), torch.uint8)
+    return _abi.CeProcess(*hist, history.shape[2] if counted else 0, hist_len, prompt, *penalties,
+                          _per_row(dev, "temperature", temperature, N, torch.float32),
+                          *_side(dev, "bias", bias, x, V, torch.float32),
+                          *_side(dev, "mask", mask, x, (V + 31) // 32, torch.int32), signs_ptr, signs_ld)
 
 
 def _process(fn, x, out, vocab_start, vocab_total, **steps):
@@ -233,14 +252,11 @@ def processed_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False,
 # ---- embedding -------------------------------------------------------------------------------------------
 
 
-def _embedding_desc(ids, dtype_of, D, v_local, scale, vocab_start, vocab_total):
-    m = _abi.CeEmbeddingDesc()
+def _embedding_desc(ids, weight_ptr, w_ld, of, D, v_local, scale, vocab_start, vocab_total):
     N = ids.shape[0]
-    m.ids, m.id_stride, m.N, m.D = ids.data_ptr() if N else None, ids.stride(0) if N > 1 else 1, N, D
-    m.dtype, m.v_local, m.vocab_start = _dtype_code(dtype_of), v_local, int(vocab_start)
-    m.vocab_total = v_local if vocab_total is None else int(vocab_total)
-    m.scale = float(scale)
-    return m
+    return _abi.CeEmbeddingDesc(ids.data_ptr(), ids.stride(0) if N > 1 else 1, N, D, weight_ptr, w_ld,
+                                _dtype_code(of), 0, v_local, vocab_start,
+                                v_local if vocab_total is None else vocab_total, scale)
 
 
 def _need_ids(dev, ids):
@@ -257,11 +273,13 @@ def ce_embedding(ids, weight, scale=1.0, *, out=None, vocab_start=0, vocab_total
         _einval("weight must be [V, D]")
     _need_ids(dev, ids)
     V, D = weight.shape
-    m = _embedding_desc(ids, weight, D, V, scale, vocab_start, vocab_total)
-    m.weight, m.w_ld = weight.data_ptr(), _rows(dev, "weight", weight, (V, D), None)
+    m = _embedding_desc(ids, weight.data_ptr(), _rows(dev, "weight", weight, weight.shape, None), weight, D, V, scale,
+                        vocab_start, vocab_total)
     if out is None:
-        out = torch.empty((m.N, D), dtype=weight.dtype, device=dev)
-    _call(dev, lib.ce_embedding, ctypes.byref(m), _ptr(out), _rows(dev, "out", out, (m.N, D), weight.dtype))
+        out, out_ld = torch.empty((m.N, D), dtype=weight.dtype, device=dev), D
+    else:
+        out_ld = _rows(dev, "out", out, (m.N, D), weight.dtype)
+    _call(dev, lib.ce_embedding, ctypes.byref(m), out.data_ptr(), out_ld)
     return out
 
 
@@ -286,16 +304,18 @@ def ce_embedding_backward(dout, ids, v_local, scale=1.0, *, padding_idx=None, dw
         _einval(f"{ids.shape[0]} ids for {N} rows of dout")
     if padding_idx is not None and padding_idx < 0:
         _einval("padding_idx must be a vocabulary index")
-    m = _embedding_desc(ids, dout, D, int(v_local), scale, vocab_start, vocab_total)
-    if accumulate and dw is None:
-        _einval("accumulate needs dw")
-    need = ce_embedding_workspace_bytes(N, D, v_local)
-    dw = torch.empty((v_local, D), dtype=torch.float32, device=dev) if dw is None else dw
-    ws = _workspace(need, dev) if ws is None else ws
+    v_local = int(v_local)
+    m = _embedding_desc(ids, None, D, dout, D, v_local, scale, vocab_start, vocab_total)
+    if dw is None:
+        if accumulate:
+            _einval("accumulate needs dw")
+        dw = torch.empty((v_local, D), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = _workspace(ce_embedding_workspace_bytes(N, D, v_local), dev)
     _need(dev, "workspace", ws, torch.uint8)
-    _call(dev, lib.ce_embedding_backward, ctypes.byref(m), _ptr(dout), _rows(dev, "dout", dout, (N, D), None),
-          -1 if padding_idx is None else int(padding_idx), _ptr(dw),
-          _rows(dev, "dw", dw, (v_local, D), torch.float32), int(bool(accumulate)), _ptr(ws), ws.numel())
+    _call(dev, lib.ce_embedding_backward, ctypes.byref(m), dout.data_ptr(), _rows(dev, "dout", dout, dout.shape, None),
+          -1 if padding_idx is None else padding_idx, dw.data_ptr(),
+          _rows(dev, "dw", dw, (v_local, D), torch.float32), 1 if accumulate else 0, ws.data_ptr(), ws.numel())
     return dw
 
 
@@ -338,27 +358,29 @@ def embedding(ids, weight, scale=1.0, *, padding_idx=None, grad_buffer=None, voc
 def _norm_desc(dev, x, weight, residual, eps):
     if x.dim() != 2:
         _einval("x must be [N, D]")
-    N, D = x.shape
+    shape = x.shape
+    N, D = shape
     _need(dev, "weight", weight, None, D)
-    if weight is None or tuple(weight.shape) != (D,):
+    if weight is None or weight.shape != (D,):
         _einval(f"weight must be [{D}]")
-    n = _abi.CeNorm()
-    n.x, n.x_ld, n.N, n.D = x.data_ptr(), _rows(dev, "x", x, (N, D), None), N, D
-    n.weight, n.dtype, n.weight_dtype, n.eps = weight.data_ptr(), _dtype_code(x), _dtype_code(weight), float(eps)
+    res, res_ld = None, 0
     if residual is not None:
-        n.residual, n.residual_ld = residual.data_ptr(), _rows(dev, "residual", residual, (N, D), x.dtype)
-        if N == 0:
-            n.residual = None
-    return n
+        res, res_ld = residual.data_ptr(), _rows(dev, "residual", residual, shape, x.dtype)
+    return _abi.CeNorm(x.data_ptr(), res, weight.data_ptr(), _dtype_code(x), _dtype_code(weight), N, D,
+                       _rows(dev, "x", x, shape, None), res_ld, eps)
 
 
-def _sum_arg(dev, x, residual, sum_out):
-    """The buffer the sum goes to (None without a residual unless one is given) and its arguments."""
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    if sum_out is None:
-        return None, 0
-    return sum_out, _rows(dev, "sum_out", sum_out, x.shape, x.dtype)
+def _like(dev, what, t, x):
+    """``t``, or a new tensor like ``x``: (tensor, address, row stride)."""
+    if t is None:
+        t = torch.empty_like(x)
+        return t, t.data_ptr(), t.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return t, t.data_ptr(), _rows(dev, what, t, x.shape, x.dtype)
+
+
+def _sum_out(dev, x, residual, sum_out):
+    """Where the sum goes: nowhere without a residual unless a buffer is given."""
+    return (None, None, 0) if residual is None and sum_out is None else _like(dev, "sum_out", sum_out, x)
 
 
 def ce_rms_norm(x, weight, residual=None, eps=1e-6, *, out=None, sum_out=None):
@@ -366,10 +388,9 @@ def ce_rms_norm(x, weight, residual=None, eps=1e-6, *, out=None, sum_out=None):
     ``sum_out`` asks for it).  ``out`` and ``sum_out`` may be x or residual themselves."""
     dev = _device_of(x, "x")
     n = _norm_desc(dev, x, weight, residual, eps)
-    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    total, total_ld = _sum_arg(dev, x, residual, sum_out)
-    _call(dev, lib.ce_rms_norm, ctypes.byref(n), _ptr(out), _rows(dev, "out", out, x.shape, x.dtype), _ptr(total),
-          total_ld)
+    out, ptr, ld = _like(dev, "out", out, x)
+    total, total_ptr, total_ld = _sum_out(dev, x, residual, sum_out)
+    _call(dev, lib.ce_rms_norm, ctypes.byref(n), ptr, ld, total_ptr, total_ld)
     return out, total
 
 
@@ -383,9 +404,9 @@ def ce_rms_norm_quant(x, weight, residual=None, eps=1e-6, *, group=0, out=None, 
     out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=dev) if out is None else out
     scales = torch.empty((N, groups), dtype=torch.float32, device=dev) if scales is None else scales
     _need(dev, "scales", scales, torch.float32, N * groups)
-    total, total_ld = _sum_arg(dev, x, residual, sum_out)
-    _call(dev, lib.ce_rms_norm_quant, ctypes.byref(n), _ptr(out),
-          _rows(dev, "out", out, (N, D), torch.float8_e4m3fn), int(group), _ptr(scales), _ptr(total), total_ld)
+    total, total_ptr, total_ld = _sum_out(dev, x, residual, sum_out)
+    _call(dev, lib.ce_rms_norm_quant, ctypes.byref(n), out.data_ptr(),
+          _rows(dev, "out", out, (N, D), torch.float8_e4m3fn), int(group), scales.data_ptr(), total_ptr, total_ld)
     return out, scales, total
 
 
@@ -404,21 +425,24 @@ def ce_rms_norm_backward(dy, s, weight, eps=1e-6, *, dsum=None, dx=None, dweight
     dev = _device_of(s, "s")
     n = _norm_desc(dev, s, weight, None, eps)
     N, D = s.shape
-    dy_ld = _rows(dev, "dy", dy, (N, D), s.dtype)
-    dsum_ld = _rows(dev, "dsum", dsum, (N, D), s.dtype) if dsum is not None and N else 0
-    if accumulate and dweight is None:
-        _einval("accumulate needs dweight")
-    if dx is None and want_dx:
-        dx = torch.empty((N, D), dtype=s.dtype, device=dev)
-    if dweight is None and want_dweight:
-        dweight = torch.empty(D, dtype=torch.float32, device=dev)
-    _need(dev, "dweight", dweight, torch.float32, D)
-    if dweight is not None and ws is None:
-        ws = _workspace(ce_rms_norm_workspace_bytes(N, D), dev)
-    _need(dev, "workspace", ws, torch.uint8)
-    _call(dev, lib.ce_rms_norm_backward, ctypes.byref(n), _ptr(dy), dy_ld, _ptr(dsum) if N else None, dsum_ld,
-          _ptr(dx), _rows(dev, "dx", dx, (N, D), s.dtype) if dx is not None else 0, _ptr(dweight),
-          int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0)
+    dy_ptr, dy_ld = _like(dev, "dy", dy, s)[1:] if dy is not None else _einval("dy is missing")
+    dsum_ptr, dsum_ld = (None, 0) if dsum is None else _like(dev, "dsum", dsum, s)[1:]
+    dx_ptr, dx_ld = None, 0
+    if dx is not None or want_dx:
+        dx, dx_ptr, dx_ld = _like(dev, "dx", dx, s)
+    if dweight is None:
+        if accumulate:
+            _einval("accumulate needs dweight")
+        if want_dweight:
+            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+    ws_bytes = 0
+    if dweight is not None:
+        _need(dev, "dweight", dweight, torch.float32, D)
+        ws = _workspace(ce_rms_norm_workspace_bytes(N, D), dev) if ws is None else ws
+        _need(dev, "workspace", ws, torch.uint8)
+        ws_bytes = ws.numel()
+    _call(dev, lib.ce_rms_norm_backward, ctypes.byref(n), dy_ptr, dy_ld, dsum_ptr, dsum_ld, dx_ptr, dx_ld,
+          _ptr(dweight), 1 if accumulate else 0, _ptr(ws) if ws_bytes else None, ws_bytes)
     return dx, dweight
 
 

@@ -46,6 +46,7 @@ __global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
   const int lanes = 1 << lanes_shift;
   const int lane = (int)threadIdx.x & (lanes - 1);
   const int64_t per = kT >> lanes_shift;
+  const uint32_t D = (uint32_t)a.D;
   for (int64_t n = (int64_t)blockIdx.x * per + ((int)threadIdx.x >> lanes_shift); n < a.N;
        n += (int64_t)gridDim.x * per) {
     const int64_t id = a.ids[n * a.id_stride];
@@ -53,12 +54,12 @@ __global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
     char* out = a.out + n * a.out_ld * EB;
     if (v < (uint64_t)a.V) {
       const char* w = a.w + (int64_t)v * a.w_ld * EB;
-      for (int64_t j = (int64_t)lane * kG; j < a.D; j += (int64_t)lanes * kG) {
+      for (uint32_t j = (uint32_t)lane * kG; j < D; j += (uint32_t)lanes * kG) {
         float f[kG];
-        load_f32<DT>(w, j, a.D, f);
+        load_f32<DT>(w, j, D, f);
 #pragma unroll
         for (int e = 0; e < kG; ++e) f[e] *= a.scale;
-        store_group<DT, true>(out, j, a.D, f32_to_raw<DT>(f));
+        store_group<DT, true>(out, j, D, f32_to_raw<DT>(f));
       }
     } else {
       // another shard's id adds nothing here; an id outside the vocabulary is a caller's error
@@ -66,8 +67,8 @@ __global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
       float f[kG];
 #pragma unroll
       for (int e = 0; e < kG; ++e) f[e] = fill;
-      for (int64_t j = (int64_t)lane * kG; j < a.D; j += (int64_t)lanes * kG)
-        store_group<DT, true>(out, j, a.D, f32_to_raw<DT>(f));
+      for (uint32_t j = (uint32_t)lane * kG; j < D; j += (uint32_t)lanes * kG)
+        store_group<DT, true>(out, j, D, f32_to_raw<DT>(f));
     }
   }
 }
@@ -89,33 +90,63 @@ int bits_of(int64_t v) {  // of the values 0 .. v
 }
 
 constexpr int64_t kRankMax = 8192;
-constexpr int kRankTokens = 32;  // tokens a workgroup places; 8 threads count for each
+constexpr int kRankT = 1024;
+constexpr int kRankTokens = 32;                    // tokens a workgroup places
+constexpr int kRankOwn = 4;                        // of them, tokens a thread counts for
+constexpr int kRankSlices = kRankT / (kRankTokens / kRankOwn);  // of the pairs, one a thread
 
-// Place of every token among the pairs (key, position): the count of smaller ones.
-__global__ __launch_bounds__(kT) void k_rank(EmbedGradArgs a, int pos_bits, uint32_t* skey, uint32_t* sidx) {
+// Place of every token among the pairs (key, position): the count of smaller
+// ones.  A workgroup holds all pairs in LDS; 8 threads share a slice of them,
+// 4 tokens each, so a 16-byte LDS read serves 16 compares.
+__global__ __launch_bounds__(kRankT) void k_rank(EmbedGradArgs a, int pos_bits, uint32_t* skey, uint32_t* sidx) {
   __shared__ __align__(16) uint32_t pair[kRankMax];
-  __shared__ uint32_t part[kT / kRankTokens][kRankTokens];
-  constexpr int SL = kT / kRankTokens;
-  const int n = (int)a.N;
-  const int per = ((n + SL * 4 - 1) / (SL * 4)) * 4;  // pairs per slice, whole 16-byte words
-  for (int i = (int)threadIdx.x; i < per * SL; i += kT)
-    pair[i] = i < n ? (token_key(a, i) << pos_bits) | (uint32_t)i : 0xffffffffu;
-  __syncthreads();
-  const int tok = (int)threadIdx.x % kRankTokens, slice = (int)threadIdx.x / kRankTokens;
-  const int me = (int)blockIdx.x * kRankTokens + tok;
-  const uint32_t mine = me < n ? pair[me] : 0u;
-  uint32_t less = 0;
-  const u32x4v* p = reinterpret_cast<const u32x4v*>(pair + slice * per);
-  for (int i = 0; i < per / 4; ++i) {
-    const u32x4v q = p[i];
-    less += (q.x < mine ? 1u : 0u) + (q.y < mine ? 1u : 0u) + (q.z < mine ? 1u : 0u) + (q.w < mine ? 1u : 0u);
+  __shared__ uint32_t part[kRankSlices / 8][kRankTokens];
+  const uint32_t n = (uint32_t)a.N;
+  const uint32_t per = (n + kRankSlices * 4 - 1) / (kRankSlices * 4) * 4;  // pairs per slice, whole 16-byte words
+  constexpr int LOADS = (int)(kRankMax / kRankT);
+  uint32_t key[LOADS];
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) {
+    const uint32_t i = k * kRankT + threadIdx.x;
+    key[k] = i < n ? (token_key(a, i) << pos_bits) | i : 0xffffffffu;
   }
-  part[slice][tok] = less;
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) pair[k * kRankT + threadIdx.x] = key[k];
   __syncthreads();
-  if (slice == 0 && me < n) {
-    for (int k = 1; k < SL; ++k) less += part[k][tok];
-    skey[less] = mine >> pos_bits;
-    sidx[less] = mine & ((1u << pos_bits) - 1u);
+  constexpr int OWNERS = kRankTokens / kRankOwn;
+  const uint32_t own = threadIdx.x % OWNERS, slice = threadIdx.x / OWNERS;
+  const uint32_t base = blockIdx.x * kRankTokens;
+  uint32_t mine[kRankOwn], less[kRankOwn];
+#pragma unroll
+  for (int k = 0; k < kRankOwn; ++k) {
+    const uint32_t me = base + k * OWNERS + own;
+    mine[k] = me < n ? pair[me] : 0u;
+    less[k] = 0;
+  }
+  const u32x4v* p = reinterpret_cast<const u32x4v*>(pair + slice * per);
+#pragma unroll 4
+  for (uint32_t i = 0; i < per / 4; ++i) {
+    const u32x4v q = p[i];
+#pragma unroll
+    for (int k = 0; k < kRankOwn; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) less[k] += q[e] < mine[k] ? 1u : 0u;
+  }
+  // a wave holds 8 slices: add them across its lanes, then the waves' sums in LDS
+#pragma unroll
+  for (int k = 0; k < kRankOwn; ++k) {
+#pragma unroll
+    for (int m = OWNERS; m < 64; m <<= 1) less[k] += __shfl_xor(less[k], m, 64);
+    if ((threadIdx.x & 63) < OWNERS) part[threadIdx.x >> 6][k * OWNERS + own] = less[k];
+  }
+  __syncthreads();
+  const uint32_t me = base + threadIdx.x;
+  if (threadIdx.x < kRankTokens && me < n) {
+    uint32_t at = 0;
+#pragma unroll
+    for (int k = 0; k < kRankSlices / 8; ++k) at += part[k][threadIdx.x];
+    skey[at] = pair[me] >> pos_bits;
+    sidx[at] = pair[me] & ((1u << pos_bits) - 1u);
   }
 }
 
@@ -437,7 +468,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
   uint32_t* idx[2] = {reinterpret_cast<uint32_t*>(a.ws + g.idx[0]), reinterpret_cast<uint32_t*>(a.ws + g.idx[1])};
   int cur = 0;
   if (g.rank) {
-    hipLaunchKernelGGL(k_rank, dim3((uint32_t)ceil_div(a.N, kRankTokens)), dim3(kT), 0, stream, a,
+    hipLaunchKernelGGL(k_rank, dim3((uint32_t)ceil_div(a.N, kRankTokens)), dim3(kRankT), 0, stream, a,
                        bits_of(a.N - 1), key[0], idx[0]);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {

@@ -13,7 +13,8 @@
 //
 // Bound: each input read once and each output written once.  A row's columns
 // stay in one workgroup's registers between the sum of squares and the output;
-// narrow rows take one wave each.
+// narrow rows take one wave each.  Columns are 32-bit offsets from a uniform row
+// pointer (64-bit ones cost two registers an access and a third of the waves).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,39 +27,34 @@ namespace {
 constexpr float kFp8Max = 448.f;
 constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126, the smallest normal
 
-// The sum (or largest) of v over the T threads of a row; every thread gets it.
-// T = 64: one wave.  Else `red` holds T / 64 floats, and the call synchronises
-// the workgroup twice.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+// Sums of N values over the T threads of a row; every thread gets them.  T = 64:
+// one wave.  Else the waves exchange them in LDS with one barrier: `red` holds
+// two sets, and a row takes the one its predecessor did not (`turn`), whose
+// readers have all passed the predecessor's barrier.
+template <int T, int N>
+struct RowRed {
+  float v[2][N][T / 64];
+};
+template <int T, int N, bool MAX = false>
+__device__ __forceinline__ void row_reduce(float (&v)[N], RowRed<T, N>& red, int turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = MAX ? wave_max(v[i]) : wave_sum(v[i]);
   if constexpr (T > 64) {
     const int w = (int)threadIdx.x >> 6;
-    __syncthreads();  // `red` may still be read from the last call
-    if ((threadIdx.x & 63) == 0) red[w] = v;
-    __syncthreads();
-    v = red[0];
 #pragma unroll
-    for (int k = 1; k < T / 64; ++k) v += red[k];
-  }
-  return v;
-}
-template <int T>
-__device__ __forceinline__ float row_max(float v, float* red) {
-  v = wave_max(v);
-  if constexpr (T > 64) {
-    const int w = (int)threadIdx.x >> 6;
+    for (int i = 0; i < N; ++i)
+      if ((threadIdx.x & 63) == 0) red.v[turn][i][w] = v[i];
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[w] = v;
-    __syncthreads();
-    v = red[0];
 #pragma unroll
-    for (int k = 1; k < T / 64; ++k) v = fmaxf(v, red[k]);
+    for (int i = 0; i < N; ++i) {
+      v[i] = red.v[turn][i][0];
+#pragma unroll
+      for (int k = 1; k < T / 64; ++k) v[i] = MAX ? fmaxf(v[i], red.v[turn][i][k]) : v[i] + red.v[turn][i][k];
+    }
   }
-  return v;
 }
 
-__device__ __forceinline__ void load_weight(const char* w, int32_t wdtype, int64_t j, int64_t D, float (&f)[kG]) {
+__device__ __forceinline__ void load_weight(const char* w, int32_t wdtype, uint32_t j, uint32_t D, float (&f)[kG]) {
   if (wdtype == CE_BF16)
     load_f32<CE_BF16>(w, j, D, f);
   else
@@ -75,7 +71,7 @@ __device__ __forceinline__ uint2 pack_fp8(const float (&f)[kG]) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-__device__ __forceinline__ void store_fp8(uint8_t* row, int64_t j, int64_t D, uint2 v) {
+__device__ __forceinline__ void store_fp8(uint8_t* row, uint32_t j, uint32_t D, uint2 v) {
   typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
   typedef u32x2v u32x2_a1 __attribute__((aligned(1)));
   if (j + kG <= D) {
@@ -88,233 +84,429 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, int64_t j, int64_t D, ui
   }
 }
 
+// Which of its workgroup's rows a thread works on, as a uniform value
+template <int T>
+__device__ __forceinline__ int row_of() {
+  return T < 256 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+}
+
 // A row of at most T x P groups by T threads, P groups each (group p T + t):
 // T = 64: a wave per row, four rows per workgroup; else a workgroup per row.
-template <int DT, int T, int P, bool QUANT>
+// WHOLE: D is a multiple of 8.
+template <int DT, int T, int P, bool QUANT, bool WHOLE>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm(NormArgs a) {
-  __shared__ float red[T / 64];
+  __shared__ RowRed<T, 1> red, red_top;
   constexpr int RPW = T < 256 ? 256 / T : 1;
   const int t = (int)threadIdx.x % T;
+  const uint32_t D = (uint32_t)a.D;
   const int64_t stride = (int64_t)gridDim.x * RPW;
   constexpr int EB = VecT<DT>::EB;
+  int turn = 0;
   // a workgroup's threads share one row where they synchronise (T > 64)
-  for (int64_t r = (int64_t)blockIdx.x * RPW + (int)threadIdx.x / T; r < a.N; r += stride) {
+  for (int64_t r = (int64_t)blockIdx.x * RPW + row_of<T>(); r < a.N; r += stride, turn ^= 1) {
     const char* x = a.x + r * a.x_ld * EB;
-    const char* res = a.residual ? a.residual + r * a.r_ld * EB : nullptr;
-    float v[P][kG];
-    float ss = 0.f;
+    Raw<DT> xr[P], rr[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int64_t j = (int64_t)(p * T + t) * kG;
-      if (j < a.D) {
-        load_f32<DT>(x, j, a.D, v[p]);
-        if (res) {
-          float b[kG];
-          load_f32<DT>(res, j, a.D, b);
+    for (int p = 0; p < P; ++p) xr[p] = fetch_group<DT, WHOLE>(x, (uint32_t)(p * T + t) * kG, D);
+    if (a.residual) {
+      const char* res = a.residual + r * a.r_ld * EB;
 #pragma unroll
-          for (int e = 0; e < kG; ++e) v[p][e] += b[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kG; ++e) v[p][e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < kG; ++e) ss = __builtin_fmaf(v[p][e], v[p][e], ss);
+      for (int p = 0; p < P; ++p) rr[p] = fetch_group<DT, WHOLE>(res, (uint32_t)(p * T + t) * kG, D);
     }
-    ss = row_sum<T>(ss, red);
-    const float rstd = 1.f / sqrtf(ss / (float)a.D + a.eps);
-    float top = 0.f;
+    float v[P][kG];
+    float ss[1] = {0.f};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int64_t j = (int64_t)(p * T + t) * kG;
-      if (j < a.D) {
-        if (a.sum) store_group<DT>(a.sum + r * a.sum_ld * EB, j, a.D, f32_to_raw<DT>(v[p]));
+      raw_to_f32<DT>(xr[p], v[p]);
+      if (a.residual) {
+        float b[kG];
+        raw_to_f32<DT>(rr[p], b);
+#pragma unroll
+        for (int e = 0; e < kG; ++e) v[p][e] += b[e];
+      }
+      const bool in = (uint32_t)(p * T + t) * kG < D;
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        v[p][e] = in ? v[p][e] : 0.f;
+        ss[0] = __builtin_fmaf(v[p][e], v[p][e], ss[0]);
+      }
+    }
+    row_reduce<T, 1>(ss, red, turn);
+    const float rstd = 1.f / sqrtf(ss[0] / (float)D + a.eps);
+    float top[1] = {0.f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t j = (uint32_t)(p * T + t) * kG;
+      if (j < D) {
+        if (a.sum) store_group<DT>(a.sum + r * a.sum_ld * EB, j, D, f32_to_raw<DT>(v[p]));
         float w[kG];
-        load_weight(a.weight, a.wdtype, j, a.D, w);
+        load_weight(a.weight, a.wdtype, j, D, w);
 #pragma unroll
         for (int e = 0; e < kG; ++e) v[p][e] = v[p][e] * rstd * w[e];
-        if constexpr (!QUANT) store_group<DT>(a.y + r * a.y_ld * EB, j, a.D, f32_to_raw<DT>(v[p]));
+        if constexpr (!QUANT) store_group<DT>(a.y + r * a.y_ld * EB, j, D, f32_to_raw<DT>(v[p]));
       }
       if constexpr (QUANT) {
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < kG; ++e) m = fmaxf(m, fabsf(v[p][e]));
         if (a.group) {  // 32, 64 or 128 columns: 4, 8 or 16 neighbouring lanes
-          for (int k = 1; k < a.group / kG; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
+          m = row_max16(m, a.group / kG);
           const float sc = fmaxf(m / kFp8Max, kScaleMin);
           const float inv = 1.f / sc;
-          if (j < a.D) {
+          if (j < D) {
 #pragma unroll
             for (int e = 0; e < kG; ++e) v[p][e] *= inv;
-            store_fp8(a.q + r * a.q_ld, j, a.D, pack_fp8(v[p]));
-            if (j % a.group == 0) a.scales[r * ((a.D + a.group - 1) / a.group) + j / a.group] = sc;
+            store_fp8(a.q + r * a.q_ld, j, D, pack_fp8(v[p]));
+            if (j % a.group == 0) a.scales[r * ((D + a.group - 1) / a.group) + j / a.group] = sc;
           }
         } else {
-          top = fmaxf(top, m);
+          top[0] = fmaxf(top[0], m);
         }
       }
     }
     if constexpr (QUANT) {
       if (!a.group) {
-        top = row_max<T>(top, red);
-        const float sc = fmaxf(top / kFp8Max, kScaleMin);
+        row_reduce<T, 1, true>(top, red_top, turn);
+        const float sc = fmaxf(top[0] / kFp8Max, kScaleMin);
         const float inv = 1.f / sc;
         if (t == 0) a.scales[r] = sc;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const int64_t j = (int64_t)(p * T + t) * kG;
-          if (j < a.D) {
+          const uint32_t j = (uint32_t)(p * T + t) * kG;
+          if (j < D) {
 #pragma unroll
             for (int e = 0; e < kG; ++e) v[p][e] *= inv;
-            store_fp8(a.q + r * a.q_ld, j, a.D, pack_fp8(v[p]));
+            store_fp8(a.q + r * a.q_ld, j, D, pack_fp8(v[p]));
           }
         }
+      }
+    }
+  }
+}
+
+// Rows of more than 2 groups for each of 1024 threads (D > 16384): the row is
+// read again, from L2, for each step that needs the whole of the one before,
+// instead of being held (which spilled).  Outputs are written in the last step
+// only, each after the same thread's last read of its columns.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void wide_sum(const char* x, const char* res, uint32_t j, uint32_t D, float (&v)[kG]) {
+  raw_to_f32<DT>(fetch_group<DT, WHOLE>(x, j, D), v);
+  if (res) {
+    float b[kG];
+    raw_to_f32<DT>(fetch_group<DT, WHOLE>(res, j, D), b);
+#pragma unroll
+    for (int e = 0; e < kG; ++e) v[e] += b[e];
+  }
+}
+template <int DT, bool QUANT, bool WHOLE>
+__global__ __launch_bounds__(1024) void k_norm_wide(NormArgs a) {
+  constexpr int T = 1024, EB = VecT<DT>::EB;
+  __shared__ RowRed<T, 1> red, red_top;
+  const uint32_t D = (uint32_t)a.D;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, turn ^= 1) {
+    const char* x = a.x + r * a.x_ld * EB;
+    const char* res = a.residual ? a.residual + r * a.r_ld * EB : nullptr;
+    float ss[1] = {0.f};
+    for (uint32_t j = threadIdx.x * kG; j < D; j += T * kG) {
+      float v[kG];
+      wide_sum<DT, WHOLE>(x, res, j, D, v);
+#pragma unroll
+      for (int e = 0; e < kG; ++e) ss[0] = __builtin_fmaf(v[e], v[e], ss[0]);
+    }
+    row_reduce<T, 1>(ss, red, turn);
+    const float rstd = 1.f / sqrtf(ss[0] / (float)D + a.eps);
+    float sc = 0.f;
+    if (QUANT && !a.group) {
+      float top[1] = {0.f};
+      for (uint32_t j = threadIdx.x * kG; j < D; j += T * kG) {
+        float v[kG], w[kG];
+        wide_sum<DT, WHOLE>(x, res, j, D, v);
+        load_weight(a.weight, a.wdtype, j, D, w);
+#pragma unroll
+        for (int e = 0; e < kG; ++e) top[0] = fmaxf(top[0], fabsf(v[e] * rstd * w[e]));
+      }
+      row_reduce<T, 1, true>(top, red_top, turn);
+      sc = fmaxf(top[0] / kFp8Max, kScaleMin);
+      if (threadIdx.x == 0) a.scales[r] = sc;
+    }
+    // every lane takes every step: a group's scale is found across lanes
+    for (uint32_t base = 0; base < D; base += T * kG) {
+      const uint32_t j = base + threadIdx.x * kG;
+      float v[kG], w[kG];
+#pragma unroll
+      for (int e = 0; e < kG; ++e) v[e] = w[e] = 0.f;
+      if (j < D) {
+        wide_sum<DT, WHOLE>(x, res, j, D, v);
+        if (a.sum) store_group<DT>(a.sum + r * a.sum_ld * EB, j, D, f32_to_raw<DT>(v));
+        load_weight(a.weight, a.wdtype, j, D, w);
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        v[e] = v[e] * rstd * w[e];
+        m = fmaxf(m, fabsf(v[e]));
+      }
+      if constexpr (QUANT) {
+        if (a.group) sc = fmaxf(row_max16(m, a.group / kG) / kFp8Max, kScaleMin);
+        const float inv = 1.f / sc;
+#pragma unroll
+        for (int e = 0; e < kG; ++e) v[e] *= inv;
+        if (j < D) {
+          store_fp8(a.q + r * a.q_ld, j, D, pack_fp8(v));
+          if (a.group && j % a.group == 0) a.scales[r * ((D + a.group - 1) / a.group) + j / a.group] = sc;
+        }
+      } else {
+        if (j < D) store_group<DT>(a.y + r * a.y_ld * EB, j, D, f32_to_raw<DT>(v));
       }
     }
   }
 }
 
 // The gradient: rows r, r + G, ... of the grid's G row slots, with the slot's
-// share of dw in registers; a second kernel adds the slots' shares.
-template <int DT, int T, int P>
+// share of dw and the weight in registers; a second kernel adds the slots'
+// shares.  PRE: the next row's loads are issued before this row's sums are
+// exchanged, where the registers allow it.
+template <int DT, int P>
+struct GradRow {
+  Raw<DT> s[P], dy[P], dsum[P];
+};
+template <int DT, int T, int P, bool WHOLE>
+__device__ __forceinline__ void fetch_grad_row(const NormGradArgs& a, int64_t r, int t, GradRow<DT, P>& g) {
+  constexpr int EB = VecT<DT>::EB;
+  const uint32_t D = (uint32_t)a.D;
+#pragma unroll
+  for (int p = 0; p < P; ++p) g.s[p] = fetch_group<DT, WHOLE>(a.s + r * a.s_ld * EB, (uint32_t)(p * T + t) * kG, D);
+#pragma unroll
+  for (int p = 0; p < P; ++p) g.dy[p] = fetch_group<DT, WHOLE>(a.dy + r * a.dy_ld * EB, (uint32_t)(p * T + t) * kG, D);
+  if (a.dsum) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      g.dsum[p] = fetch_group<DT, WHOLE>(a.dsum + r * a.dsum_ld * EB, (uint32_t)(p * T + t) * kG, D);
+  }
+}
+
+template <int DT, int T, int P, bool WHOLE>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradArgs a) {
-  __shared__ float red[T / 64];
+  constexpr bool PRE = P * VecT<DT>::EB <= 4 && T < 1024;
+  __shared__ RowRed<T, 2> red;
   constexpr int RPW = T < 256 ? 256 / T : 1;
   const int t = (int)threadIdx.x % T;
-  const int64_t slot = (int64_t)blockIdx.x * RPW + (int)threadIdx.x / T;
+  const uint32_t D = (uint32_t)a.D;
+  const int64_t slot = (int64_t)blockIdx.x * RPW + row_of<T>();
   const int64_t slots = (int64_t)gridDim.x * RPW;
   constexpr int EB = VecT<DT>::EB;
-  float acc[P][kG];
+  float acc[P][kG], w[P][kG];
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < P; ++p) {
+    const uint32_t j = (uint32_t)(p * T + t) * kG;
 #pragma unroll
-    for (int e = 0; e < kG; ++e) acc[p][e] = 0.f;
-  for (int64_t r = slot; r < a.N; r += slots) {
-    const char* sr = a.s + r * a.s_ld * EB;
-    const char* dyr = a.dy + r * a.dy_ld * EB;
-    Raw<DT> s[P], dy[P];
-    float ss = 0.f, dot = 0.f;
+    for (int e = 0; e < kG; ++e) acc[p][e] = w[p][e] = 0.f;
+    if (j < D) load_weight(a.weight, a.wdtype, j, D, w[p]);  // 0 past the row's end
+  }
+  GradRow<DT, P> cur, next;
+  if (PRE && slot < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, slot, t, cur);
+  int turn = 0;
+  for (int64_t r = slot; r < a.N; r += slots, turn ^= 1) {
+    if constexpr (PRE) {
+      if (r + slots < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, r + slots, t, next);
+    } else {
+      fetch_grad_row<DT, T, P, WHOLE>(a, r, t, cur);
+    }
+    float sums[2] = {0.f, 0.f};  // of s^2 and of dy w s
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int64_t j = (int64_t)(p * T + t) * kG;
-      if (j < a.D) {
-        s[p] = load_group<DT>(sr, j, a.D);
-        dy[p] = load_group<DT>(dyr, j, a.D);
-        float f[kG], g[kG], w[kG];
-        raw_to_f32<DT>(s[p], f);
-        raw_to_f32<DT>(dy[p], g);
-        load_weight(a.weight, a.wdtype, j, a.D, w);
+      const bool in = (uint32_t)(p * T + t) * kG < D;
+      float f[kG], g[kG];
+      raw_to_f32<DT>(cur.s[p], f);
+      raw_to_f32<DT>(cur.dy[p], g);
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          ss = __builtin_fmaf(f[e], f[e], ss);
-          dot = __builtin_fmaf(g[e] * w[e], f[e], dot);
-        }
+      for (int e = 0; e < kG; ++e) {
+        const float fe = in ? f[e] : 0.f, ge = in ? g[e] : 0.f;
+        sums[0] = __builtin_fmaf(fe, fe, sums[0]);
+        sums[1] = __builtin_fmaf(ge * w[p][e], fe, sums[1]);
       }
     }
-    ss = row_sum<T>(ss, red);
-    dot = row_sum<T>(dot, red);
-    const float rstd = 1.f / sqrtf(ss / (float)a.D + a.eps);
-    const float k = rstd * rstd * rstd * (dot / (float)a.D);
+    row_reduce<T, 2>(sums, red, turn);
+    const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
+    const float k = rstd * rstd * rstd * (sums[1] / (float)D);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int64_t j = (int64_t)(p * T + t) * kG;
-      if (j < a.D) {
-        float f[kG], g[kG], w[kG], d[kG];
-        raw_to_f32<DT>(s[p], f);
-        raw_to_f32<DT>(dy[p], g);
-        load_weight(a.weight, a.wdtype, j, a.D, w);
-        if (a.dsum)
-          load_f32<DT>(a.dsum + r * a.dsum_ld * EB, j, a.D, d);
-        else
+      const uint32_t j = (uint32_t)(p * T + t) * kG;
+      float f[kG], g[kG], d[kG];
+      raw_to_f32<DT>(cur.s[p], f);
+      raw_to_f32<DT>(cur.dy[p], g);
+      if (a.dsum)
+        raw_to_f32<DT>(cur.dsum[p], d);
+      else
 #pragma unroll
-          for (int e = 0; e < kG; ++e) d[e] = 0.f;
+        for (int e = 0; e < kG; ++e) d[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          acc[p][e] = __builtin_fmaf(g[e], f[e] * rstd, acc[p][e]);
-          d[e] += __builtin_fmaf(g[e] * w[e], rstd, -(f[e] * k));
-        }
-        if (a.dx) store_group<DT>(a.dx + r * a.dx_ld * EB, j, a.D, f32_to_raw<DT>(d));
+      for (int e = 0; e < kG; ++e) {
+        acc[p][e] = __builtin_fmaf(g[e], f[e] * rstd, acc[p][e]);
+        d[e] += __builtin_fmaf(g[e] * w[p][e], rstd, -(f[e] * k));
       }
+      if (a.dx && j < D) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
     }
+    if constexpr (PRE) cur = next;
   }
   if (a.dweight) {
     char* part = reinterpret_cast<char*>(a.parts + slot * a.D);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int64_t j = (int64_t)(p * T + t) * kG;
-      if (j < a.D) store_group<CE_F32>(part, j, a.D, f32_to_raw<CE_F32>(acc[p]));
+      const uint32_t j = (uint32_t)(p * T + t) * kG;
+      if (j < D) store_group<CE_F32>(part, j, D, f32_to_raw<CE_F32>(acc[p]));
     }
   }
 }
 
-// dw[j] (+)= the slots' shares: 64 columns per workgroup, wave k adds slots k, k + 4, ..., in order,
-// and the waves are added in order.
-constexpr int kDwWaves = 16;
-__global__ __launch_bounds__(64 * kDwWaves) void k_norm_dw(const float* parts, int64_t slots, int64_t D, float* dw,
-                                                           int32_t accumulate) {
-  __shared__ float part[kDwWaves][64];
-  const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
-  const int64_t j = (int64_t)blockIdx.x * 64 + lane;
+// The same for D > 16384: the row is read twice, and the slot's share of dw is
+// kept in LDS (4 D bytes), each thread its own columns.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(1024) void k_norm_grad_wide(NormGradArgs a) {
+  constexpr int T = 1024, EB = VecT<DT>::EB;
+  __shared__ RowRed<T, 2> red;
+  extern __shared__ __align__(16) float share[];  // group g's element e at (g / T) 8 T + e T + g % T
+  const uint32_t D = (uint32_t)a.D;
+  const int t = (int)threadIdx.x;
+  for (uint32_t j = t * kG, at = t; j < D; j += T * kG, at += T * kG)
+#pragma unroll
+    for (int e = 0; e < kG; ++e) share[at + e * T] = 0.f;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, turn ^= 1) {
+    const char* s = a.s + r * a.s_ld * EB;
+    const char* dy = a.dy + r * a.dy_ld * EB;
+    float sums[2] = {0.f, 0.f};
+    for (uint32_t j = t * kG; j < D; j += T * kG) {
+      float f[kG], g[kG], w[kG];
+      raw_to_f32<DT>(fetch_group<DT, WHOLE>(s, j, D), f);
+      raw_to_f32<DT>(fetch_group<DT, WHOLE>(dy, j, D), g);
+      load_weight(a.weight, a.wdtype, j, D, w);
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        sums[0] = __builtin_fmaf(f[e], f[e], sums[0]);
+        sums[1] = __builtin_fmaf(g[e] * w[e], f[e], sums[1]);
+      }
+    }
+    row_reduce<T, 2>(sums, red, turn);
+    const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
+    const float k = rstd * rstd * rstd * (sums[1] / (float)D);
+    for (uint32_t j = t * kG, at = t; j < D; j += T * kG, at += T * kG) {
+      float f[kG], g[kG], w[kG], d[kG];
+      raw_to_f32<DT>(fetch_group<DT, WHOLE>(s, j, D), f);
+      raw_to_f32<DT>(fetch_group<DT, WHOLE>(dy, j, D), g);
+      load_weight(a.weight, a.wdtype, j, D, w);
+      if (a.dsum)
+        raw_to_f32<DT>(fetch_group<DT, WHOLE>(a.dsum + r * a.dsum_ld * EB, j, D), d);
+      else
+#pragma unroll
+        for (int e = 0; e < kG; ++e) d[e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        share[at + e * T] = __builtin_fmaf(g[e], f[e] * rstd, share[at + e * T]);
+        d[e] += __builtin_fmaf(g[e] * w[e], rstd, -(f[e] * k));
+      }
+      if (a.dx) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
+    }
+  }
+  if (a.dweight) {
+    char* part = reinterpret_cast<char*>(a.parts + (int64_t)blockIdx.x * a.D);
+    for (uint32_t j = t * kG, at = t; j < D; j += T * kG, at += T * kG) {
+      float f[kG];
+#pragma unroll
+      for (int e = 0; e < kG; ++e) f[e] = share[at + e * T];
+      store_group<CE_F32>(part, j, D, f32_to_raw<CE_F32>(f));
+    }
+  }
+}
+
+// dw[j] (+)= the slots' shares: 32 columns per workgroup, thread row k of 32
+// adds slots k, k + 32, ... in order, and the rows are added in order.
+constexpr int kDwCols = 32, kDwRows = 32;
+__global__ __launch_bounds__(kDwCols * kDwRows) void k_norm_dw(const float* parts, int64_t slots, int64_t D, float* dw,
+                                                               int32_t accumulate) {
+  __shared__ float part[kDwRows][kDwCols];
+  const int c = (int)threadIdx.x % kDwCols, w = (int)threadIdx.x / kDwCols;
+  const int64_t j = (int64_t)blockIdx.x * kDwCols + c;
   float v = 0.f;
-  if (j < D)
-    for (int64_t k = w; k < slots; k += kDwWaves) v += parts[k * D + j];
-  part[w][lane] = v;
+  if (j < D) {
+#pragma unroll 8
+    for (int64_t k = w; k < slots; k += kDwRows) v += parts[k * D + j];
+  }
+  part[w][c] = v;
   __syncthreads();
   if (w == 0 && j < D) {
-    for (int k = 1; k < kDwWaves; ++k) v += part[k][lane];
+#pragma unroll
+    for (int k = 1; k < kDwRows; ++k) v += part[k][c];
     dw[j] = accumulate ? dw[j] + v : v;
   }
 }
 
-// Row slots of the gradient kernel for N rows (one workgroup holds 4 where a
-// wave takes a row).
+// Row slots of the gradient kernel for N rows: about 16 waves a CU, at most
+// one per row (a workgroup holds 4 where a wave takes a row).
 int64_t grad_slots(int64_t N, int64_t D) {
-  const int64_t most = D <= 2048 ? 2048 : 512;
-  int64_t s = N < most ? N : most;
-  if (D <= 2048) s = (s + 3) & ~(int64_t)3;
-  return s;
+  const int64_t g = (D + kG - 1) / kG;
+  if (g <= 128) {
+    const int64_t s = N < 2048 ? N : 2048;
+    return (s + 3) & ~(int64_t)3;
+  }
+  const int64_t most = g <= 256 ? 1024 : g <= 1024 ? 512 : 256;
+  return N < most ? N : most;
 }
 
-template <int DT, bool QUANT>
+template <int DT, bool QUANT, bool WHOLE>
 void norm_shape(const NormArgs& a, hipStream_t stream) {
   constexpr int64_t most = 1 << 22;  // a launch holds below 2^32 work-items
   const int64_t g = (a.D + kG - 1) / kG;
   const int64_t rows = a.N < most ? a.N : most;
   const int64_t rows4 = (a.N + 3) / 4 < most ? (a.N + 3) / 4 : most;
-#define VCE_NORM(T, P, R) hipLaunchKernelGGL((k_norm<DT, T, P, QUANT>), dim3((uint32_t)(R)), dim3(T < 256 ? 256 : T), 0, stream, a)
+#define VCE_NORM(T, P, R) \
+  hipLaunchKernelGGL((k_norm<DT, T, P, QUANT, WHOLE>), dim3((uint32_t)(R)), dim3(T < 256 ? 256 : T), 0, stream, a)
   if (g <= 64) VCE_NORM(64, 1, rows4);
   else if (g <= 128) VCE_NORM(64, 2, rows4);
-  else if (g <= 256) VCE_NORM(64, 4, rows4);
-  else if (g <= 512) VCE_NORM(256, 2, rows);
-  else if (g <= 1024) VCE_NORM(256, 4, rows);
+  else if (g <= 256) VCE_NORM(256, 1, rows);
+  else if (g <= 512) VCE_NORM(512, 1, rows);
+  else if (g <= 1024) VCE_NORM(512, 2, rows);
   else if (g <= 2048) VCE_NORM(1024, 2, rows);
-  else VCE_NORM(1024, 4, rows);
+  else hipLaunchKernelGGL((k_norm_wide<DT, QUANT, WHOLE>), dim3((uint32_t)rows), dim3(1024), 0, stream, a);
 #undef VCE_NORM
 }
 
-template <int DT>
+template <int DT, bool WHOLE>
 void grad_shape(const NormGradArgs& a, hipStream_t stream) {
   const int64_t g = (a.D + kG - 1) / kG;
   const int64_t slots = grad_slots(a.N, a.D);
-#define VCE_GRAD(T, P, R) hipLaunchKernelGGL((k_norm_grad<DT, T, P>), dim3((uint32_t)(R)), dim3(T < 256 ? 256 : T), 0, stream, a)
+#define VCE_GRAD(T, P, R) \
+  hipLaunchKernelGGL((k_norm_grad<DT, T, P, WHOLE>), dim3((uint32_t)(R)), dim3(T < 256 ? 256 : T), 0, stream, a)
   if (g <= 64) VCE_GRAD(64, 1, slots / 4);
   else if (g <= 128) VCE_GRAD(64, 2, slots / 4);
-  else if (g <= 256) VCE_GRAD(64, 4, slots / 4);
-  else if (g <= 512) VCE_GRAD(256, 2, slots);
-  else if (g <= 1024) VCE_GRAD(256, 4, slots);
+  else if (g <= 256) VCE_GRAD(256, 1, slots);
+  else if (g <= 512) VCE_GRAD(512, 1, slots);
+  else if (g <= 1024) VCE_GRAD(512, 2, slots);
   else if (g <= 2048) VCE_GRAD(1024, 2, slots);
-  else VCE_GRAD(1024, 4, slots);
+  else
+    hipLaunchKernelGGL((k_norm_grad_wide<DT, WHOLE>), dim3((uint32_t)slots), dim3(1024),
+                       (size_t)((g + 1023) / 1024 * 1024 * kG) * 4, stream, a);
 #undef VCE_GRAD
+}
+
+template <int DT>
+void norm_dt(const NormArgs& a, hipStream_t stream) {
+  if (a.D % kG == 0)
+    a.q ? norm_shape<DT, true, true>(a, stream) : norm_shape<DT, false, true>(a, stream);
+  else
+    a.q ? norm_shape<DT, true, false>(a, stream) : norm_shape<DT, false, false>(a, stream);
+}
+template <int DT>
+void grad_dt(const NormGradArgs& a, hipStream_t stream) {
+  a.D % kG == 0 ? grad_shape<DT, true>(a, stream) : grad_shape<DT, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   if (a.N == 0) return hipSuccess;
-  if (a.dtype == CE_BF16)
-    a.q ? norm_shape<CE_BF16, true>(a, stream) : norm_shape<CE_BF16, false>(a, stream);
-  else
-    a.q ? norm_shape<CE_F32, true>(a, stream) : norm_shape<CE_F32, false>(a, stream);
+  a.dtype == CE_BF16 ? norm_dt<CE_BF16>(a, stream) : norm_dt<CE_F32>(a, stream);
   return hipGetLastError();
 }
 
@@ -323,11 +515,11 @@ size_t norm_grad_workspace(int64_t N, int64_t D) { return (size_t)grad_slots(N, 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.N > 0) {
-    a.dtype == CE_BF16 ? grad_shape<CE_BF16>(a, stream) : grad_shape<CE_F32>(a, stream);
+    a.dtype == CE_BF16 ? grad_dt<CE_BF16>(a, stream) : grad_dt<CE_F32>(a, stream);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.dweight) {
-    hipLaunchKernelGGL(k_norm_dw, dim3((uint32_t)((a.D + 63) / 64)), dim3(64 * kDwWaves), 0, stream, a.parts,
+    hipLaunchKernelGGL(k_norm_dw, dim3((uint32_t)((a.D + kDwCols - 1) / kDwCols)), dim3(kDwCols * kDwRows), 0, stream, a.parts,
                        a.N > 0 ? grad_slots(a.N, a.D) : (int64_t)0, a.D, a.dweight, a.accumulate);
     e = hipGetLastError();
   }

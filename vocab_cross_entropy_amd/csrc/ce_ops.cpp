@@ -31,6 +31,7 @@ bool known(int32_t dtype) { return dtype == CE_F32 || dtype == CE_BF16; }
 bool off(const void* p, int32_t dtype) { return (uintptr_t)p % (uintptr_t)elem_bytes(dtype) != 0; }
 
 constexpr int64_t kMax31 = 0x7fffffffLL;
+constexpr int64_t kMaxCols32 = 0xffffffffLL / 4;  // FP32 columns of a row below 4 GiB: kernels use 32-bit byte offsets
 
 // a matrix of `rows` rows of D contiguous elements, ld apart
 ce_status check_rows(const char* name, const void* p, int32_t dtype, int64_t rows, int64_t D, int64_t ld) {
@@ -66,6 +67,8 @@ ce_status check_process(const ce_logits* x, const ce_logits* out, const ce_proce
     if ((uintptr_t)q % 4u) return ofail(CE_ELAYOUT, "a per-row parameter, bias or mask is not 4-byte aligned");
   if (!p->history && (p->repetition || p->frequency || p->presence))
     return ofail(CE_EINVAL, "penalties need a history");
+  if (p->bias && x->v_local > kMaxCols32)
+    return ofail(CE_ELAYOUT, "bias rows of %lld columns exceed 4 GiB", (long long)x->v_local);
   if (p->bias && (p->bias_s0 < 0 || p->bias_s1 < 0)) return ofail(CE_ELAYOUT, "negative bias strides are not supported");
   if (p->mask && (p->mask_s0 < 0 || p->mask_s1 < 0)) return ofail(CE_ELAYOUT, "negative mask strides are not supported");
   if (p->signs && p->signs_ld < (x->v_local + 7) / 8)
@@ -129,6 +132,7 @@ ce_status check_embedding(const ce_embedding_desc* m, bool table) {
     return ofail(CE_EINVAL, "%lld tokens outside [0, 2^26]", (long long)m->N);
   if (m->D < 1 || m->D > kMax31 || m->v_local < 1 || m->v_local > kMax31)
     return ofail(CE_EINVAL, "need 1 <= D, v_local < 2^31 (got %lld, %lld)", (long long)m->D, (long long)m->v_local);
+  if (m->D > kMaxCols32) return ofail(CE_ELAYOUT, "rows of %lld FP32 columns exceed 4 GiB", (long long)m->D);
   if (m->vocab_start < 0 || m->vocab_total < 1 || m->vocab_start > m->vocab_total - m->v_local)
     return ofail(CE_ELAYOUT, "shard [%lld, %lld) does not fit a vocabulary of %lld", (long long)m->vocab_start,
                  (long long)(m->vocab_start + m->v_local), (long long)m->vocab_total);

@@ -12,12 +12,12 @@
 //
 // Bound: one read and one write of the logits.  What the penalties need from
 // the history is a count per column.  A workgroup owns a chunk of one row's
-// columns and keeps the chunk's counts in LDS: it reads the row's history
-// (from L2: every chunk of the row reads it), adds the tokens that fall into
-// its chunk with integer LDS atomics (whose order cannot change the result),
-// and then streams its columns once.  Counts take 16 bits with the prompt
-// flag in the top one while the history holds at most 32767 tokens, and 32 bits
-// beyond.
+// columns: it issues the loads of its first history tokens and of all its
+// columns, keeps the chunk's counts in LDS (integer atomics, whose order cannot
+// change the result) while the columns arrive, and then processes and writes
+// them.  Every chunk of a row reads the row's history, from L2.  Counts take
+// 16 bits with the prompt flag in the top one while the history holds at most
+// 32767 tokens, and 32 bits beyond.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,68 +27,87 @@
 namespace vce {
 namespace {
 
-constexpr int kProcT = 256;
-constexpr int kProcSpan = kProcT * kG;  // columns one step of a workgroup covers
-
-constexpr int64_t kProcMaxGrid = 1 << 23;
+constexpr int64_t kProcMaxGrid = 1 << 22;
 
 enum { kHistNone = 0, kHist16 = 1, kHist32 = 2 };
+constexpr int kHistAhead = 4;  // tokens per thread loaded ahead of the columns
 
 template <int HIST>
-struct CountT {
-  typedef uint16_t Word;
-};
-template <>
-struct CountT<kHist32> {
-  typedef uint32_t Word;
-};
+__device__ __forceinline__ void count_token(uint32_t* tab, uint64_t id, uint64_t first, uint32_t cols, bool prompt) {
+  // a token of another chunk or vocabulary shard, or no token at all (negative), wraps to or past the end
+  const uint64_t j = id - first;
+  if (j >= cols) return;
+  if constexpr (HIST == kHist16) {
+    const int sh = 16 * ((int)j & 1);
+    if (prompt)
+      atomicOr(&tab[j >> 1], 0x8000u << sh);
+    else
+      atomicAdd(&tab[j >> 1], 1u << sh);
+  } else {
+    if (prompt)
+      atomicOr(&tab[j], 0x80000000u);
+    else
+      atomicAdd(&tab[j], 1u);
+  }
+}
 
-template <int DT, int HIST, bool BWD>
+// The counts of eight columns as the chunk's table holds them: the prompt flag
+// in bit 31 of each, occurrences below.  False when all are 0.
+template <int HIST>
+__device__ __forceinline__ bool read_counts(const char* tab, uint32_t col, uint32_t (&c)[kG]) {
+  if constexpr (HIST == kHist16) {
+    const u32x4v w = reinterpret_cast<const u32x4v*>(tab)[col >> 3];
+    if ((w.x | w.y | w.z | w.w) == 0u) return false;
+#pragma unroll
+    for (int e = 0; e < kG; ++e) {
+      const uint32_t h16 = (w[e / 2] >> (16 * (e & 1))) & 0xffffu;
+      c[e] = (h16 & 0x7fffu) | ((h16 & 0x8000u) << 16);
+    }
+    return true;
+  } else {
+    const u32x4v w0 = reinterpret_cast<const u32x4v*>(tab)[col >> 2];
+    const u32x4v w1 = reinterpret_cast<const u32x4v*>(tab)[(col >> 2) + 1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = w0[e];
+      c[e + 4] = w1[e];
+    }
+    return (w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0u;
+  }
+}
+
+// One chunk: U groups of eight columns for each of T threads.
+template <int DT, int HIST, bool BWD, int T, int U>
 __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, uint32_t chunk, char* smem) {
-  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
-  const int64_t lo = (int64_t)chunk * a.chunk_cols;
-  const int64_t hi = lo + a.chunk_cols < a.V ? lo + a.chunk_cols : a.V;
   constexpr int EB = VecT<DT>::EB;
+  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const uint32_t V = (uint32_t)a.V;
+  const uint32_t lo = chunk * (uint32_t)a.chunk_cols;
+  const uint32_t hi = V - lo < (uint32_t)a.chunk_cols ? V : lo + (uint32_t)a.chunk_cols;
+  const uint32_t tid = threadIdx.x;
   const char* x = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   char* z = a.z + (i0 * a.zs0 + i1 * a.zs1) * EB;
-  const int tid = (int)threadIdx.x;
 
+  const int64_t* h = nullptr;
+  uint64_t id[kHistAhead];
   if constexpr (HIST != kHistNone) {
-    constexpr int per16 = HIST == kHist16 ? 8 : 4;
-    const int words = (int)((hi - lo + per16 - 1) / per16);
-    // whole groups are read below: clear the last group's end too
-    const int clear = HIST == kHist32 ? (words + 1) & ~1 : words;
-    for (int i = tid; i < clear; i += kProcT) reinterpret_cast<u32x4v*>(smem)[i] = u32x4v{0u, 0u, 0u, 0u};
-    __syncthreads();
-    const int64_t* h = a.hist + i0 * a.hs0 + i1 * a.hs1;
-    int64_t n = a.hist_max;
-    if (a.hist_len) {
-      n = a.hist_len[r];
-      n = n < 0 ? 0 : n > a.hist_max ? a.hist_max : n;
+    // loads return in order: the tokens', waited for first, go out first
+    h = a.hist + i0 * a.hs0 + i1 * a.hs1;
+#pragma unroll
+    for (int k = 0; k < kHistAhead; ++k) {
+      const uint32_t i = tid + k * T;
+      id[k] = i < (uint32_t)a.hist_max ? (uint64_t)h[i] : ~(uint64_t)0;
     }
-    const int64_t np = a.prompt_len ? a.prompt_len[r] : 0;
-    const uint64_t first = (uint64_t)(a.vocab_start + lo);
-    uint32_t* tab = reinterpret_cast<uint32_t*>(smem);
-    for (int64_t i = tid; i < n; i += kProcT) {
-      // a token of another chunk or vocabulary shard, or no token at all (negative), wraps to or past the end
-      const uint64_t j = (uint64_t)h[i] - first;
-      if (j >= (uint64_t)(hi - lo)) continue;
-      if constexpr (HIST == kHist16) {
-        const int sh = 16 * ((int)j & 1);
-        if (i < np)
-          atomicOr(&tab[j >> 1], 0x8000u << sh);
-        else
-          atomicAdd(&tab[j >> 1], 1u << sh);
-      } else {
-        if (i < np)
-          atomicOr(&tab[j], 0x80000000u);
-        else
-          atomicAdd(&tab[j], 1u);
-      }
-    }
-    __syncthreads();
   }
-
+  Raw<DT> raw[U];
+  const uint32_t whole = V & ~7u;  // columns in whole groups
+  if (whole) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {  // lanes past them read some whole group, so that no load stands behind a branch
+      const uint32_t j = lo + (u * T + tid) * kG;
+      raw[u] = fetch_group<DT, true, true>(x, j, whole);
+    }
+  }
   const float theta = a.repetition ? a.repetition[r] : 1.f;
   const float fr = a.frequency ? a.frequency[r] : 0.f;
   const float pr = a.presence ? a.presence[r] : 0.f;
@@ -97,10 +116,47 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
   const float* bias = a.bias ? a.bias + i0 * a.bs0 + i1 * a.bs1 : nullptr;
   uint8_t* signs = a.signs ? a.signs + r * a.signs_ld : nullptr;
 
-  for (int64_t j = lo + (int64_t)tid * kG; j < hi; j += kProcSpan) {
+  if constexpr (HIST != kHistNone) {
+    uint32_t n = (uint32_t)a.hist_max;
+    if (a.hist_len) {
+      const int32_t len = a.hist_len[r];
+      n = len < 0 ? 0u : min((uint32_t)len, n);
+    }
+    const int32_t plen = a.prompt_len ? a.prompt_len[r] : 0;
+    const uint32_t np = plen < 0 ? 0u : (uint32_t)plen;
+    constexpr int bytes = T * U * kG * (HIST == kHist16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < bytes / 16 / T; ++i) reinterpret_cast<u32x4v*>(smem)[i * T + tid] = u32x4v{0u, 0u, 0u, 0u};
+    __syncthreads();
+    uint32_t* tab = reinterpret_cast<uint32_t*>(smem);
+    const uint64_t first = (uint64_t)a.vocab_start + lo;
+#pragma unroll
+    for (int k = 0; k < kHistAhead; ++k) {
+      const uint32_t i = tid + k * T;
+      if (i < n) count_token<HIST>(tab, id[k], first, hi - lo, i < np);
+    }
+    for (uint32_t base = kHistAhead * T; base < n; base += kHistAhead * T) {
+#pragma unroll
+      for (int k = 0; k < kHistAhead; ++k) {
+        const uint32_t i = base + tid + k * T;
+        id[k] = i < n ? (uint64_t)h[i] : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kHistAhead; ++k) {
+        const uint32_t i = base + tid + k * T;
+        if (i < n) count_token<HIST>(tab, id[k], first, hi - lo, i < np);
+      }
+    }
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t j = lo + (u * T + tid) * kG;
+    if (j >= hi) continue;
+    if (j >= whole) raw[u] = load_group<DT>(x, j, V);
     float v[kG];
-    const Raw<DT> raw = load_group<DT, true>(x, j, a.V);
-    raw_to_f32<DT>(raw, v);
+    raw_to_f32<DT>(raw[u], v);
     if constexpr (!BWD) {
       if (signs) {
         uint32_t up = 0;
@@ -111,26 +167,7 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
     }
     if constexpr (HIST != kHistNone) {
       uint32_t c[kG];
-      bool any;
-      if constexpr (HIST == kHist16) {
-        const u32x4v w = reinterpret_cast<const u32x4v*>(smem)[(j - lo) >> 3];
-        any = (w.x | w.y | w.z | w.w) != 0u;
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          const uint32_t h16 = (w[e / 2] >> (16 * (e & 1))) & 0xffffu;
-          c[e] = (h16 & 0x7fffu) | ((h16 & 0x8000u) << 16);
-        }
-      } else {
-        const u32x4v w0 = reinterpret_cast<const u32x4v*>(smem)[(j - lo) >> 2];
-        const u32x4v w1 = reinterpret_cast<const u32x4v*>(smem)[((j - lo) >> 2) + 1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[e] = w0[e];
-          c[e + 4] = w1[e];
-        }
-        any = (w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0u;
-      }
-      if (any) {
+      if (read_counts<HIST>(smem, j - lo, c)) {
         uint32_t up = 0;
         if constexpr (BWD) up = signs ? signs[j >> 3] : 0u;
 #pragma unroll
@@ -149,7 +186,7 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
     if constexpr (!BWD) {
       if (bias) {
         float b[kG];
-        load_f32<CE_F32>(reinterpret_cast<const char*>(bias), j, a.V, b);
+        load_f32<CE_F32>(reinterpret_cast<const char*>(bias), j, V, b);
 #pragma unroll
         for (int e = 0; e < kG; ++e) v[e] += b[e];
       }
@@ -162,44 +199,56 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
 #pragma unroll
       for (int e = 0; e < kG; ++e) v[e] = (m >> e) & 1u ? v[e] : off;
     }
-    store_group<DT, true>(z, j, a.V, f32_to_raw<DT>(v));
+    store_group<DT, true>(z, j, V, f32_to_raw<DT>(v));
   }
 }
 
-template <int DT, int HIST, bool BWD>
-__global__ __launch_bounds__(kProcT) void k_process(ProcessArgs a) {
-  extern __shared__ __align__(16) char smem[];
+template <int DT, int HIST, bool BWD, int T, int U>
+__global__ __launch_bounds__(T) void k_process(ProcessArgs a) {
+  __shared__ __align__(16) char smem[HIST == kHistNone ? 16 : T * U * kG * (HIST == kHist16 ? 2 : 4)];
   const int64_t items = a.N * a.chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t r = it / a.chunks;
     if constexpr (HIST != kHistNone) __syncthreads();  // the last item's counts have been read
-    process_item<DT, HIST, BWD>(a, r, (uint32_t)(it - r * a.chunks), smem);
+    process_item<DT, HIST, BWD, T, U>(a, r, (uint32_t)(it - r * a.chunks), smem);
   }
 }
 
+// Chunk shapes (threads, groups per thread)
+struct ProcShape {
+  int t, u;
+};
+#ifndef PROC_BIG
+#define PROC_BIG 512, 4
+#endif
+constexpr ProcShape kProcBig = {PROC_BIG};
+constexpr ProcShape kProcSmall = {256, 1};
+
+template <int DT, int HIST, bool BWD>
+hipError_t launch_shape(const ProcessArgs& a, dim3 grid, hipStream_t stream) {
+  if (a.threads == kProcBig.t)
+    hipLaunchKernelGGL((k_process<DT, HIST, BWD, kProcBig.t, kProcBig.u>), grid, dim3(kProcBig.t), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_process<DT, HIST, BWD, kProcSmall.t, kProcSmall.u>), grid, dim3(kProcSmall.t), 0, stream, a);
+  return hipGetLastError();
+}
 template <int DT, bool BWD>
 hipError_t launch_dt(const ProcessArgs& a, int hist, dim3 grid, hipStream_t stream) {
-  const size_t col = (size_t)((a.chunk_cols + 7) & ~(int64_t)7);
-  switch (hist) {
-    case kHistNone:
-      hipLaunchKernelGGL((k_process<DT, kHistNone, BWD>), grid, dim3(kProcT), 0, stream, a);
-      break;
-    case kHist16:
-      hipLaunchKernelGGL((k_process<DT, kHist16, BWD>), grid, dim3(kProcT), col * 2, stream, a);
-      break;
-    default:
-      hipLaunchKernelGGL((k_process<DT, kHist32, BWD>), grid, dim3(kProcT), col * 4, stream, a);
-      break;
-  }
-  return hipGetLastError();
+  return hist == kHistNone ? launch_shape<DT, kHistNone, BWD>(a, grid, stream)
+         : hist == kHist16 ? launch_shape<DT, kHist16, BWD>(a, grid, stream)
+                           : launch_shape<DT, kHist32, BWD>(a, grid, stream);
 }
 
 }  // namespace
 
 void process_plan(ProcessArgs* a) {
-  const int64_t cols = 8192;
-  a->chunk_cols = cols;
-  a->chunks = (a->V + cols - 1) / cols;
+  // large chunks read the history fewer times; small ones fill the chip with few rows
+  const int64_t big = (int64_t)kProcBig.t * kProcBig.u * kG, small = (int64_t)kProcSmall.t * kProcSmall.u * kG;
+  const bool few = a->N * ((a->V + big - 1) / big) < 512;
+  const int64_t most = few ? small : big;
+  a->threads = few ? kProcSmall.t : kProcBig.t;
+  a->chunks = (a->V + most - 1) / most;
+  a->chunk_cols = ((a->V + a->chunks - 1) / a->chunks + kG - 1) / kG * kG;  // even shares of whole groups
 }
 
 hipError_t launch_process(const ProcessArgs& a, bool backward, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1) {

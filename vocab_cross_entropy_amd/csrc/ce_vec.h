@@ -80,9 +80,10 @@ __device__ __forceinline__ Raw<DT> f32_to_raw(const float (&f)[kG]) {
 
 // Columns j .. j + 7 of a row of `cols` columns; those past the row's end read
 // as zero and are never touched in memory.  NT sets the non-temporal bit, for
-// data that is touched once.
+// data that is touched once.  Columns are uint32_t (a row is below 4 GiB): with a
+// uniform row pointer an access is then one scalar base and one offset register.
 template <int DT, bool NT = false>
-__device__ __forceinline__ Raw<DT> load_group(const char* row, int64_t j, int64_t cols) {
+__device__ __forceinline__ Raw<DT> load_group(const char* row, uint32_t j, uint32_t cols) {
   typedef typename VecT<DT>::Word Word;
   Raw<DT> r;
   if (j + kG <= cols) {
@@ -112,8 +113,30 @@ __device__ __forceinline__ Raw<DT> load_group(const char* row, int64_t j, int64_
   return r;
 }
 
+// The same for a row of whole groups (cols a multiple of 8): lanes past its
+// end read the first group, so that no load stands behind a branch; what they
+// hold is the caller's to drop.
+template <int DT, bool WHOLE, bool NT = false>
+__device__ __forceinline__ Raw<DT> fetch_group(const char* row, uint32_t j, uint32_t cols) {
+  if constexpr (WHOLE) {
+    typedef typename VecT<DT>::Word Word;
+    Raw<DT> r;
+    const Word* p = reinterpret_cast<const Word*>(row + (j < cols ? j : 0) * VecT<DT>::EB);
+#pragma unroll
+    for (int k = 0; k < VecT<DT>::NV; ++k) {
+      if constexpr (NT)
+        r.w[k] = __builtin_nontemporal_load(p + k);
+      else
+        r.w[k] = p[k];
+    }
+    return r;
+  } else {
+    return load_group<DT, NT>(row, j, cols);
+  }
+}
+
 template <int DT, bool NT = false>
-__device__ __forceinline__ void store_group(char* row, int64_t j, int64_t cols, const Raw<DT>& r) {
+__device__ __forceinline__ void store_group(char* row, uint32_t j, uint32_t cols, const Raw<DT>& r) {
   typedef typename VecT<DT>::Word Word;
   if (j + kG <= cols) {
 #pragma unroll
@@ -138,19 +161,46 @@ __device__ __forceinline__ void store_group(char* row, int64_t j, int64_t cols, 
 }
 
 template <int DT, bool NT = false>
-__device__ __forceinline__ void load_f32(const char* row, int64_t j, int64_t cols, float (&f)[kG]) {
+__device__ __forceinline__ void load_f32(const char* row, uint32_t j, uint32_t cols, float (&f)[kG]) {
   raw_to_f32<DT>(load_group<DT, NT>(row, j, cols), f);
 }
 
+// Sums and maxima across lanes by DPP (a lane reads a neighbour's register in
+// the add itself; a shuffle goes through LDS, about 60 cycles a step).  The
+// steps' order is fixed.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float v) {  // lanes without a source, and rows outside ROWS, read 0
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, true));
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E;        // quad_perm [1, 0, 3, 2] and [2, 3, 0, 1]
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // of 8 and of 16 lanes
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143;    // the last lane of a row of 16, of the lower half, to the next
+
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  v += dpp<kSwap1>(v);
+  v += dpp<kSwap2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  v += dpp<kBcast15, 0xa>(v);
+  v += dpp<kBcast31, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// the largest of values >= 0 over 4, 8 or 16 neighbouring lanes (in each of them), and over the wave
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, dpp<kSwap1>(v));
+  return fmaxf(v, dpp<kSwap2>(v));
+}
+__device__ __forceinline__ float row_max16(float v, int lanes) {
+  v = quad_max(v);
+  if (lanes > 4) v = fmaxf(v, dpp<kHalfMirror>(v));
+  if (lanes > 8) v = fmaxf(v, dpp<kMirror>(v));
   return v;
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  return v;
+  v = row_max16(v, 16);
+  v = fmaxf(v, dpp<kBcast15, 0xa>(v));
+  v = fmaxf(v, dpp<kBcast31, 0xc>(v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 }  // namespace vce
