@@ -497,7 +497,8 @@ typedef struct ce_embedding_desc {
 /* out: device [N, D] in the weight's dtype, row stride out_ld, one rounding of scale W. */
 ce_status ce_embedding(const ce_embedding_desc* m, void* out, int64_t out_ld, hipStream_t stream);
 
-/* Workspace bytes of ce_embedding_backward; 0 if the sizes are refused. */
+/* Workspace bytes of ce_embedding_backward (enough for fewer tokens of the same table too); 0 if the sizes
+ * are refused. */
 size_t ce_embedding_workspace_bytes(int64_t N, int64_t D, int64_t v_local);
 
 /*
@@ -550,7 +551,7 @@ ce_status ce_rms_norm(const ce_norm* n, void* y, int64_t y_ld, void* sum, int64_
 ce_status ce_rms_norm_quant(const ce_norm* n, void* q, int64_t q_ld, int32_t group, float* scales, void* sum,
                             int64_t sum_ld, hipStream_t stream);
 
-/* Workspace bytes of ce_rms_norm_backward; 0 if the sizes are refused. */
+/* Workspace bytes of ce_rms_norm_backward (enough for fewer rows too); 0 if the sizes are refused. */
 size_t ce_rms_norm_workspace_bytes(int64_t N, int64_t D);
 
 /*

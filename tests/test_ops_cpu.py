@@ -198,6 +198,12 @@ def test_norm_refuses(form, change, status):
 def test_workspace_sizes():
     assert vce.ce_embedding_workspace_bytes(0, 1, 1) >= 256 and vce.ce_rms_norm_workspace_bytes(0, 1) >= 256
     assert vce.ce_embedding_workspace_bytes(1 << 26, 1, (1 << 31) - 1) > 0
+    # a workspace serves every smaller batch
+    counts = sorted({max(0, (1 << k) + d) for k in range(18) for d in (-1, 0, 1, 7)} | {515, 1500, 3000, 65540})
+    for D in (5, 600, 4096, 9000, 20000):
+        for size in (lambda n: vce.ce_rms_norm_workspace_bytes(n, D), lambda n: vce.ce_embedding_workspace_bytes(n, D, 999)):
+            sizes = [size(n) for n in counts]
+            assert sizes == sorted(sizes)
     for call in (lambda: vce.ce_embedding_workspace_bytes(-1, 1, 1), lambda: vce.ce_embedding_workspace_bytes(1, 0, 1),
                  lambda: vce.ce_embedding_workspace_bytes((1 << 26) + 1, 1, 1),
                  lambda: vce.ce_rms_norm_workspace_bytes(1, 32769), lambda: vce.ce_rms_norm_workspace_bytes(-1, 8)):

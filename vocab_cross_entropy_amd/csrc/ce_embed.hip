@@ -12,12 +12,14 @@
 //   up to kRankMax tokens whose (id, position) pair fits 32 bits: one launch in
 //     which each token's place is the count of smaller pairs (N^2 compares of LDS
 //     words, N^2 / 16384 cycles of the whole chip);
-//   more: a stable radix sort, 9 bits at most a pass, three launches a pass.
+//   more: a stable radix sort, 9 bits at most a pass, in one launch a pass up to
+//     kOneMax tokens (every workgroup counts all keys) and three beyond.
 // The sorted list is then cut into tiles of equally many tokens, so a token that
 // makes up a large share of the batch costs no more than the others.  A
-// workgroup adds up the runs of equal ids in its tile in FP32; a run inside one
-// tile goes straight to dW, a run that crosses tiles leaves one partial sum per
-// tile, and a last launch adds those in tile order.
+// workgroup adds up the runs of equal ids in its tile in FP32 and writes them to
+// dW.  A run of at most a tile's length that crosses a boundary belongs whole to
+// the tile where it starts; a longer one leaves one partial sum per tile, and a
+// last launch adds those in tile order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -102,7 +104,7 @@ __global__ __launch_bounds__(kRankT) void k_rank(EmbedGradArgs a, int pos_bits, 
   __shared__ __align__(16) uint32_t pair[kRankMax];
   __shared__ uint32_t part[kRankSlices / 8][kRankTokens];
   const uint32_t n = (uint32_t)a.N;
-  const uint32_t per = (n + kRankSlices * 4 - 1) / (kRankSlices * 4) * 4;  // pairs per slice, whole 16-byte words
+  const uint32_t steps = (n + kRankSlices * 4 - 1) / (kRankSlices * 4);  // 16-byte words per slice
   constexpr int LOADS = (int)(kRankMax / kRankT);
   uint32_t key[LOADS];
 #pragma unroll
@@ -123,10 +125,10 @@ __global__ __launch_bounds__(kRankT) void k_rank(EmbedGradArgs a, int pos_bits, 
     mine[k] = me < n ? pair[me] : 0u;
     less[k] = 0;
   }
-  const u32x4v* p = reinterpret_cast<const u32x4v*>(pair + slice * per);
+  const u32x4v* p = reinterpret_cast<const u32x4v*>(pair) + slice;
 #pragma unroll 4
-  for (uint32_t i = 0; i < per / 4; ++i) {
-    const u32x4v q = p[i];
+  for (uint32_t i = 0; i < steps; ++i) {
+    const u32x4v q = p[i * kRankSlices];  // a wave's 8 slices read 128 bytes side by side
 #pragma unroll
     for (int k = 0; k < kRankOwn; ++k)
 #pragma unroll
@@ -269,31 +271,139 @@ __global__ __launch_bounds__(kT) void k_sort_move(EmbedGradArgs a, SortPass s) {
   }
 }
 
+// Adds one to h[bin] for every live lane of a wave; the lanes that agree with
+// the first one go as one addition (a batch may hold one token many times).
+__device__ __forceinline__ void count_bin(uint32_t* h, uint32_t bin, bool live) {
+  const uint64_t all = __ballot(live);
+  if (all == 0) return;
+  const int first = __builtin_ctzll(all);
+  const uint32_t lead = (uint32_t)__builtin_amdgcn_readlane((int)bin, first);
+  const uint64_t same = __ballot(live && bin == lead);
+  if (live && ((int)(threadIdx.x & 63) == first || bin != lead))
+    atomicAdd(&h[bin], bin == lead ? (uint32_t)__popcll(same) : 1u);
+}
+
+// A pass over up to kOneMax tokens in one launch: every workgroup counts all
+// keys itself, those before its tile apart, so none waits for another.  Its tile
+// is one token per thread.
+constexpr int kOneT = 1024;
+constexpr int64_t kOneMax = 65536;
+__global__ __launch_bounds__(kOneT) void k_sort_one(EmbedGradArgs a, SortPass s) {
+  constexpr int BINS = 1 << kMaxDigit, W = kOneT / 64;
+  __shared__ uint32_t before[BINS], rest[BINS], next[W][BINS], wave_total[BINS / 64];
+  const uint32_t n = (uint32_t)a.N, mask = (1u << s.bits) - 1u;
+  const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
+  if (threadIdx.x < BINS) before[threadIdx.x] = rest[threadIdx.x] = 0;
+  for (int i = (int)threadIdx.x; i < W * BINS; i += kOneT) next[0][i] = 0;
+  __syncthreads();
+  uint32_t mine = 0;
+  const uint32_t tiles = (n + kOneT - 1) / kOneT;
+  for (uint32_t t0 = 0; t0 < tiles; t0 += 8) {
+    uint32_t key[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t i = (t0 + k) * kOneT + threadIdx.x;
+      key[k] = i < n ? (s.key_in ? s.key_in[i] : token_key(a, i)) : 0u;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t t = t0 + k;
+      if (t == blockIdx.x) mine = key[k];
+      if (t < tiles) count_bin(t < blockIdx.x ? before : rest, (key[k] >> s.shift) & mask, t * kOneT + threadIdx.x < n);
+    }
+  }
+  // this tile: lanes of a wave with the same bin, in order
+  const uint32_t at = blockIdx.x * kOneT + threadIdx.x;
+  const bool live = at < n;
+  const uint32_t bin = (mine >> s.shift) & mask;
+  uint64_t same = __ballot(live);
+  for (int b = 0; b < s.bits; ++b) {
+    const bool bit = (bin >> b) & 1u;
+    const uint64_t set = __ballot(bit);
+    same &= bit ? set : ~set;
+  }
+  const uint32_t rank = (uint32_t)__popcll(same & (((uint64_t)1 << lane) - 1));
+  if (live && rank == 0) next[w][bin] = (uint32_t)__popcll(same);
+  __syncthreads();
+  // places: bins before this one, this bin in the tiles before, this bin in the waves before
+  uint32_t scan = 0, all = 0;
+  if (threadIdx.x < BINS) {
+    all = before[threadIdx.x] + rest[threadIdx.x];
+    scan = all;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(scan, d, 64);
+      if (lane >= d) scan += o;
+    }
+    if (lane == 63) wave_total[w] = scan;
+  }
+  __syncthreads();
+  if (threadIdx.x < BINS) {
+    uint32_t place = scan - all + before[threadIdx.x];
+    for (int k = 0; k < w; ++k) place += wave_total[k];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const uint32_t c = next[k][threadIdx.x];
+      next[k][threadIdx.x] = place;
+      place += c;
+    }
+  }
+  __syncthreads();
+  if (live) {
+    const uint32_t to = next[w][bin] + rank;
+    s.key_out[to] = mine;
+    s.idx_out[to] = s.idx_in ? s.idx_in[at] : at;
+  }
+}
+
 // ---- sums ----------------------------------------------------------------
+
+constexpr int64_t kTileTokens = 16, kMaxTiles = 4096;
 
 struct SumArgs {
   const uint32_t* skey;
   const uint32_t* sidx;
-  float* parts;            // [2 tiles][D]: a tile's run from the tile before, its run into the next
+  float* parts;            // [2 tiles][D]: a tile's share of a long run from the tile before, of one into the next
+  uint32_t* starts;        // [tiles] 1 where a long run starts, else 0
   int64_t tiles, tile;     // tokens per tile
-  int64_t col_blocks;      // workgroups across a row
+  int64_t col_blocks;      // units across a row: a unit is a tile's tokens over 8 << lanes_shift columns
   int lanes_shift;
   int64_t fill_blocks;     // workgroups that write the rows no token names (0 when dW is added to)
 };
 constexpr int kFillRows = 32;
 
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t v, int64_t j, const float (&acc)[kG]) {
-  char* row = reinterpret_cast<char*>(a.dw + (int64_t)v * a.dw_ld);
-  float f[kG];
-  if (a.accumulate) {
-    load_f32<CE_F32>(row, j, a.D, f);
-#pragma unroll
-    for (int e = 0; e < kG; ++e) f[e] = __builtin_fmaf(acc[e], a.scale, f[e]);
+// Tokens with key `key` that follow one another from position `at` on (UP) or
+// from at - 1 down, at most `limit` of them.  UNI: by the lanes of a wave, 64 at a
+// time; else by a search of each thread's own.
+template <bool UNI, bool UP>
+__device__ __forceinline__ uint32_t run_from(const SumArgs& s, uint32_t N, uint32_t at, uint32_t key, uint32_t limit) {
+  const uint32_t there = UP ? N - at : at, most = there < limit ? there : limit;
+  if constexpr (UNI) {
+    const uint32_t lane = threadIdx.x & 63;
+    for (uint32_t base = 0; base < most; base += 64) {
+      const uint32_t d = base + lane;
+      const bool in = d < most && s.skey[UP ? at + d : at - 1 - d] == key;
+      const uint64_t all = __ballot(in);
+      if (all != ~(uint64_t)0) return base + (uint32_t)__builtin_ctzll(~all);
+    }
+    return most;
   } else {
-#pragma unroll
-    for (int e = 0; e < kG; ++e) f[e] = acc[e] * a.scale;
+    uint32_t lo = 0, hi = most;  // sorted: the matches come first
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) >> 1;
+      if (s.skey[UP ? at + mid : at - 1 - mid] == key) lo = mid + 1; else hi = mid;
+    }
+    return lo;
   }
-  store_group<CE_F32>(row, j, a.D, f32_to_raw<CE_F32>(f));
+}
+// Whether the run across boundary `b` (0 < b < N, both sides of one key) is longer than a tile; *ahead: its tokens
+// from b on, where it is not.
+template <bool UNI>
+__device__ __forceinline__ bool long_run(const SumArgs& s, uint32_t N, uint32_t b, uint32_t key, uint32_t* ahead) {
+  const uint32_t tile = (uint32_t)s.tile;
+  const uint32_t back = run_from<UNI, false>(s, N, b, key, tile);
+  *ahead = run_from<UNI, true>(s, N, b, key, tile);
+  return back + *ahead > tile;
 }
 
 // Rows of dW that no token names: a search of the sorted keys for each, zeros where it is not found.
@@ -302,106 +412,177 @@ __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs&
   const int64_t v0 = block * kFillRows;
   if (threadIdx.x < 64) {
     const int64_t v = v0 + (int)threadIdx.x;
-    int64_t lo = 0, hi = a.N;  // the first sorted token with a key of at least v
+    uint32_t lo = 0, hi = (uint32_t)a.N;  // the first sorted token with a key of at least v
     while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
+      const uint32_t mid = (lo + hi) >> 1;
       if (s.skey[mid] < (uint32_t)v) lo = mid + 1; else hi = mid;
     }
-    const bool found = lo < a.N && s.skey[lo] == (uint32_t)v;
+    const bool found = lo < (uint32_t)a.N && s.skey[lo] == (uint32_t)v;
     const uint64_t all = __ballot(found);
     if (threadIdx.x == 0) named = (uint32_t)all;
   }
   __syncthreads();
-  const float zero[kG] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const Raw<CE_F32> z = f32_to_raw<CE_F32>(zero);
+  const uint32_t D = (uint32_t)a.D;
+  const u32x4v zero = {0u, 0u, 0u, 0u};
   for (int k = 0; k < kFillRows && v0 + k < a.V; ++k) {
     if ((named >> k) & 1u) continue;
-    char* row = reinterpret_cast<char*>(a.dw + (v0 + k) * a.dw_ld);
-    for (int64_t j = (int64_t)threadIdx.x * kG; j < a.D; j += (int64_t)kT * kG)
-      store_group<CE_F32, true>(row, j, a.D, z);
+    // 16-byte stores from the row's first 16-byte boundary on, single columns before and after
+    float* row = a.dw + (v0 + k) * a.dw_ld;
+    uint32_t head = (uint32_t)((16 - ((uintptr_t)row & 15)) & 15) / 4;
+    head = head < D ? head : D;
+    const uint32_t body = (D - head) / 4;
+    if (threadIdx.x < head) row[threadIdx.x] = 0.f;
+    for (uint32_t j = threadIdx.x; j < body; j += kT)
+      __builtin_nontemporal_store(zero, reinterpret_cast<u32x4v*>(row + head) + j);
+    const uint32_t tail = head + body * 4 + threadIdx.x;
+    if (threadIdx.x < 4 && tail < D) row[tail] = 0.f;
   }
 }
 
-template <int DT>
+// A tile's tokens in batches: the batch's rows of dout, and the rows of dW
+// that its run ends add to, are all loaded before the first is used.  UNI: a
+// wave holds one unit (rows of more than 256 columns), so that tokens, keys and row
+// addresses are scalars.
+// NT: dout is read with the non-temporal bit, where each 16-byte load of a wave
+// covers whole cache lines (BF16 rows on 16-byte boundaries); where lines are
+// shared by two loads it has them fetched twice (20011 x 1037 FP32: 99 against
+// 88 us; 8192 x 4096 BF16: 75 against 84).
+template <int DT, bool UNI, bool NT>
 __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
   constexpr int EB = VecT<DT>::EB;
+  constexpr int B = 4;  // (8 took the registers of a third of the waves: 75 against 71 us)
+  const uint32_t D = (uint32_t)a.D, whole = D & ~7u, N = (uint32_t)a.N, none = (uint32_t)a.V;
   for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
     if (b >= sum_blocks) {
       __syncthreads();
       fill_rows(a, s, b - sum_blocks);
       continue;
     }
-    const int64_t cb = b % s.col_blocks;
-    const int64_t t = (b / s.col_blocks) * (kT >> s.lanes_shift) + ((int)threadIdx.x >> s.lanes_shift);
-    const int64_t j = ((cb << s.lanes_shift) + ((int)threadIdx.x & ((1 << s.lanes_shift) - 1))) * kG;
-    if (t >= s.tiles || j >= a.D) continue;
-    const int64_t i0 = t * s.tile, i1 = min64(i0 + s.tile, a.N);
+    int sub = (int)threadIdx.x >> s.lanes_shift;
+    if constexpr (UNI) sub = __builtin_amdgcn_readfirstlane(sub);
+    const int64_t unit = b * (kT >> s.lanes_shift) + sub;
+    const int64_t t = unit / s.col_blocks, cb = unit - t * s.col_blocks;
+    const uint32_t j = (uint32_t)(((cb << s.lanes_shift) + ((int)threadIdx.x & ((1 << s.lanes_shift) - 1))) * kG);
+    if (t >= s.tiles) continue;
+    uint32_t i0 = (uint32_t)(t * s.tile), i1 = (uint32_t)min64((int64_t)i0 + s.tile, a.N);
+    bool from_before = false, goes_on = false;  // shares of long runs
+    const uint32_t first = s.skey[i0], last = s.skey[i1 - 1];
+    const bool crosses_in = i0 > 0 && s.skey[i0 > 0 ? i0 - 1 : 0] == first && first != none;
+    const bool crosses_out = i1 < N && s.skey[i1 < N ? i1 : 0] == last && last != none;
+    if (crosses_in) {
+      uint32_t ahead;
+      from_before = long_run<UNI>(s, N, i0, first, &ahead);
+      if (!from_before) i0 += ahead;
+    }
+    if (crosses_out) {
+      uint32_t ahead;
+      goes_on = long_run<UNI>(s, N, i1, last, &ahead);
+      if (!goes_on) i1 += ahead;
+    }
+    if (j >= D) continue;  // (only here: the lanes look for a run's end together)
+    if (j == 0) s.starts[t] = goes_on && !(from_before && first == last);
     float acc[kG];
 #pragma unroll
     for (int e = 0; e < kG; ++e) acc[e] = 0.f;
-    bool from_before = i0 > 0 && s.skey[i0 - 1] == s.skey[i0];
-    uint32_t key = s.skey[i0];
-    for (int64_t i = i0; i < i1 && key != (uint32_t)a.V; ++i) {
-      float f[kG];
-      load_f32<DT, true>(a.dout + (int64_t)s.sidx[i] * a.dout_ld * EB, j, a.D, f);
+    for (uint32_t i = i0; i < i1; i += B) {
+      uint32_t key[B + 1], idx[B];
 #pragma unroll
-      for (int e = 0; e < kG; ++e) acc[e] += f[e];
-      const uint32_t nk = i + 1 < a.N ? s.skey[i + 1] : 0xffffffffu;
-      const bool last = i + 1 == i1;
-      if (nk != key || last) {
-        const bool goes_on = nk == key;
-        if (from_before || goes_on)
-          store_group<CE_F32>(reinterpret_cast<char*>(s.parts + (2 * t + (from_before ? 0 : 1)) * a.D), j, a.D,
-                              f32_to_raw<CE_F32>(acc));
-        else
-          write_row(a, key, j, acc);
+      for (int k = 0; k < B; ++k) {
+        const uint32_t at = i + k < N ? i + k : N - 1;
+        key[k] = s.skey[at];
+        idx[k] = s.sidx[at];
+      }
+      key[B] = i + B < N ? s.skey[i + B] : 0xffffffffu;
+      if (key[0] == none) break;  // sorted: nothing with a gradient follows
+      Raw<DT> row[B];
+      Raw<CE_F32> old[B];
 #pragma unroll
-        for (int e = 0; e < kG; ++e) acc[e] = 0.f;
-        from_before = false;
-        key = nk;
+      for (int k = 0; k < B; ++k) {
+        const char* p = a.dout + (int64_t)idx[k] * a.dout_ld * EB;
+        row[k] = whole ? fetch_whole<DT, NT>(p, j, whole) : load_group<DT>(p, j, D);
+      }
+      if (a.accumulate) {
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+          if (i + k < i1 && key[k] != none && (i + k + 1 >= N || key[k + 1] != key[k])) {  // a run ends here
+            const char* w = reinterpret_cast<const char*>(a.dw + (int64_t)key[k] * a.dw_ld);
+            old[k] = load_group<CE_F32>(w, j, D);
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (i + k < i1 && key[k] != none) {
+          float f[kG];
+          if (whole) fix_tail<DT>(row[k], a.dout + (int64_t)idx[k] * a.dout_ld * EB, j, whole, D);
+          raw_to_f32<DT>(row[k], f);
+#pragma unroll
+          for (int e = 0; e < kG; ++e) acc[e] += f[e];
+          const bool ends = i + k + 1 >= N || key[k + 1] != key[k];
+          if (ends || i + k + 1 == i1) {
+            if (from_before || !ends) {
+              store_group<CE_F32>(reinterpret_cast<char*>(s.parts + (2 * t + (from_before ? 0 : 1)) * a.D), j, D,
+                                  f32_to_raw<CE_F32>(acc));
+            } else {
+              float o[kG];
+              raw_to_f32<CE_F32>(old[k], o);
+#pragma unroll
+              for (int e = 0; e < kG; ++e)
+                acc[e] = a.accumulate ? __builtin_fmaf(acc[e], a.scale, o[e]) : acc[e] * a.scale;
+              store_group<CE_F32>(reinterpret_cast<char*>(a.dw + (int64_t)key[k] * a.dw_ld), j, D,
+                                  f32_to_raw<CE_F32>(acc));
+            }
+#pragma unroll
+            for (int e = 0; e < kG; ++e) acc[e] = 0.f;
+            from_before = false;
+          }
+        }
       }
     }
   }
 }
 
-// The runs that cross tiles: the workgroup of the tile where a run starts adds
-// its partial sums in tile order.  Four waves take a quarter of them each (256
-// columns, four a lane).
-__global__ __launch_bounds__(kT) void k_embed_join(EmbedGradArgs a, SumArgs s) {
-  __shared__ float part[kWaves][256];
+// The long runs: workgroup x takes those that start in tiles x, x + 64, ... (one
+// lane a tile finds them) and adds their partial sums in tile order, an eighth
+// of them per wave (256 columns, four a lane).
+constexpr int kJoinWaves = 8, kJoinBlocks = 64;
+constexpr int kJoinT = 64 * kJoinWaves;
+__global__ __launch_bounds__(kJoinT) void k_embed_join(EmbedGradArgs a, SumArgs s) {
+  static_assert(kMaxTiles <= (int64_t)kJoinBlocks * 64, "one lane a tile");
+  __shared__ float part[kJoinWaves][256];
   const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < s.tiles - 1; t += gridDim.x) {
-    const int64_t i1 = (t + 1) * s.tile;
-    const uint32_t key = s.skey[i1 - 1];
-    if (key == (uint32_t)a.V || s.skey[i1] != key) continue;        // nothing crosses
-    const int64_t i0 = t * s.tile;
-    if (i0 > 0 && s.skey[i0] == key && s.skey[i0 - 1] == key) continue;  // started in an earlier tile
-    // tiles t + 1 .. last begin with the run's key
-    int64_t lo = t + 1, hi = s.tiles - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (s.skey[mid * s.tile] == key) lo = mid; else hi = mid - 1;
+  const uint32_t D = (uint32_t)a.D;
+  const int64_t look = blockIdx.x + (int64_t)lane * kJoinBlocks;
+  uint64_t found = __ballot(look < s.tiles && s.starts[look < s.tiles ? look : 0] != 0u);
+  while (found) {
+    const int64_t t = blockIdx.x + (int64_t)__builtin_ctzll(found) * kJoinBlocks;
+    found &= found - 1;
+    const uint32_t key = s.skey[(t + 1) * s.tile];
+    // tiles t + 1 .. t + n - 1 begin with the run's key: one lane a tile
+    int64_t n = 1;
+    for (int64_t u = t + 1;; u += 64) {
+      const bool in = u + lane < s.tiles && s.skey[(u + lane) * s.tile] == key;
+      const uint64_t all = __ballot(in);
+      n += all == ~(uint64_t)0 ? 64 : __builtin_ctzll(~all);
+      if (all != ~(uint64_t)0) break;
     }
-    const int64_t n = lo - t + 1;  // partial sums: the start's, then one per later tile
-    const int64_t per = ceil_div(n, kWaves);
-    for (int64_t c = (int64_t)blockIdx.y * 256; c < a.D; c += (int64_t)gridDim.y * 256) {
+    const int64_t per = ceil_div(n, kJoinWaves);
+    const int64_t k0 = w * per, k1 = min64(k0 + per, n);
+    for (uint32_t c = blockIdx.y * 256; c < D; c += gridDim.y * 256) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t k = w * per; k < min64((w + 1) * per, n); ++k) {
+#pragma unroll 4
+      for (int64_t k = k0; k < k1; ++k) {
         const float* p = s.parts + (k == 0 ? 2 * t + 1 : 2 * (t + k)) * a.D + c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t j = e * 64 + lane;
-          if (c + j < a.D) acc[e] += p[j];
-        }
+        for (int e = 0; e < 4; ++e) acc[e] += p[c + e * 64 + lane < D ? e * 64 + lane : 0];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) part[w][e * 64 + lane] = acc[e];
       __syncthreads();
-      const int64_t j = c + (int)threadIdx.x;
-      if (j < a.D) {
+      if (threadIdx.x < 256 && c + threadIdx.x < D) {
         float v = part[0][threadIdx.x];
-        for (int k = 1; k < kWaves; ++k) v += part[k][threadIdx.x];
-        float* d = a.dw + (int64_t)key * a.dw_ld + j;
+#pragma unroll
+        for (int k = 1; k < kJoinWaves; ++k) v += part[k][threadIdx.x];
+        float* d = a.dw + (int64_t)key * a.dw_ld + c + threadIdx.x;
         *d = a.accumulate ? __builtin_fmaf(v, a.scale, *d) : v * a.scale;
       }
       __syncthreads();
@@ -409,12 +590,23 @@ __global__ __launch_bounds__(kT) void k_embed_join(EmbedGradArgs a, SumArgs s) {
   }
 }
 
+template <int DT>
+void launch_sum(const EmbedGradArgs& a, const SumArgs& s, int64_t sum_blocks, dim3 grid, hipStream_t stream) {
+  const bool nt = DT == CE_BF16 && (uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0 && a.D % kG == 0;
+  if (s.lanes_shift >= 6 && nt)
+    hipLaunchKernelGGL((k_embed_sum<DT, true, DT == CE_BF16>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else if (s.lanes_shift >= 6)
+    hipLaunchKernelGGL((k_embed_sum<DT, true, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else
+    hipLaunchKernelGGL((k_embed_sum<DT, false, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+}
+
 // Workspace: sorted keys and positions (twice for the radix sort's passes), its counts, the partial sums.
 struct GradLayout {
   bool rank;
   int key_bits, passes, digit;
   int64_t sort_tiles, tile, tiles;
-  size_t keys[2], idx[2], hist, parts, total;
+  size_t keys[2], idx[2], hist, starts, parts, total;
 };
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -426,9 +618,9 @@ GradLayout grad_layout(int64_t N, int64_t D, int64_t V) {
   g.passes = g.rank ? 0 : (g.key_bits + kMaxDigit - 1) / kMaxDigit;
   g.digit = g.rank ? 0 : (g.key_bits + g.passes - 1) / g.passes;
   g.sort_tiles = ceil_div(N, kSortTile);
-  // tokens per tile: 16, more where that would leave over 4096 tiles (and as many partial sums)
-  g.tile = ceil_div(N, 4096);
-  if (g.tile < 16) g.tile = 16;
+  // tokens per tile: 16, more where that would leave over kMaxTiles tiles (and twice as many partial sums)
+  g.tile = ceil_div(N, kMaxTiles);
+  if (g.tile < kTileTokens) g.tile = kTileTokens;
   g.tiles = ceil_div(N, g.tile);
   size_t off = 0;
   for (int k = 0; k < (g.rank ? 1 : 2); ++k) {
@@ -439,8 +631,11 @@ GradLayout grad_layout(int64_t N, int64_t D, int64_t V) {
   }
   g.hist = off;
   if (!g.rank) off = align256(off + ((size_t)g.sort_tiles << g.digit) * 4);
+  g.starts = off;
+  off = align256(off + (size_t)min64(ceil_div(N, kTileTokens), kMaxTiles) * 4);
   g.parts = off;
-  off = align256(off + (size_t)g.tiles * 2 * (size_t)D * 4);
+  // (room for the tiles of any smaller N too: a workspace serves batches up to its own)
+  off = align256(off + (size_t)min64(ceil_div(N, kTileTokens), kMaxTiles) * 2 * (size_t)D * 4);
   g.total = off < 256 ? 256 : off;
   return g;
 }
@@ -482,6 +677,12 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
       s.tiles = g.sort_tiles;
       s.shift = p * g.digit;
       s.bits = g.digit;
+      if (p) cur ^= 1;
+      if (a.N <= kOneMax) {
+        hipLaunchKernelGGL(k_sort_one, dim3((uint32_t)ceil_div(a.N, kOneT)), dim3(kOneT), 0, stream, a, s);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        continue;
+      }
       const dim3 grid((uint32_t)g.sort_tiles);
       hipLaunchKernelGGL(k_sort_count, grid, dim3(kT), 0, stream, a, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -489,28 +690,29 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
       if ((e = hipGetLastError()) != hipSuccess) return e;
       hipLaunchKernelGGL(k_sort_move, grid, dim3(kT), 0, stream, a, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      if (p) cur ^= 1;
     }
   }
   SumArgs s;
   s.skey = key[cur];
   s.sidx = idx[cur];
   s.parts = reinterpret_cast<float*>(a.ws + g.parts);
+  s.starts = reinterpret_cast<uint32_t*>(a.ws + g.starts);
   s.tiles = g.tiles;
   s.tile = g.tile;
   s.lanes_shift = lanes_log2(ceil_div(a.D, kG));
+  if (s.lanes_shift > 6) s.lanes_shift = 6;  // at most a wave: a row's last unit wastes the fewest lanes
   s.col_blocks = ceil_div(ceil_div(a.D, kG), (int64_t)1 << s.lanes_shift);
   s.fill_blocks = a.accumulate ? 0 : ceil_div(a.V, kFillRows);
-  const int64_t sum_blocks = ceil_div(g.tiles, kT >> s.lanes_shift) * s.col_blocks;
+  const int64_t sum_blocks = ceil_div(g.tiles * s.col_blocks, kT >> s.lanes_shift);
   const dim3 grid((uint32_t)min64(sum_blocks + s.fill_blocks, kMaxBlocks));
   if (a.dtype == CE_BF16)
-    hipLaunchKernelGGL(k_embed_sum<CE_BF16>, grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    launch_sum<CE_BF16>(a, s, sum_blocks, grid, stream);
   else
-    hipLaunchKernelGGL(k_embed_sum<CE_F32>, grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    launch_sum<CE_F32>(a, s, sum_blocks, grid, stream);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (g.tiles > 1) {
-    const dim3 jgrid((uint32_t)min64(g.tiles - 1, 1 << 20), (uint32_t)min64(ceil_div(a.D, 256), 16));
-    hipLaunchKernelGGL(k_embed_join, jgrid, dim3(kT), 0, stream, a, s);
+    const dim3 jgrid((uint32_t)min64(g.tiles - 1, kJoinBlocks), (uint32_t)min64(ceil_div(a.D, 256), 16));
+    hipLaunchKernelGGL(k_embed_join, jgrid, dim3(kJoinT), 0, stream, a, s);
     e = hipGetLastError();
   }
   return e;

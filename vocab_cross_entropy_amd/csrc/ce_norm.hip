@@ -40,7 +40,7 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], RowRed<T, N>& red, int
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = MAX ? wave_max(v[i]) : wave_sum(v[i]);
   if constexpr (T > 64) {
-    const int w = (int)threadIdx.x >> 6;
+    const int w = (int)(threadIdx.x % T) >> 6;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if ((threadIdx.x & 63) == 0) red.v[turn][i][w] = v[i];
@@ -263,9 +263,12 @@ __global__ __launch_bounds__(1024) void k_norm_wide(NormArgs a) {
   }
 }
 
-// The gradient: rows r, r + G, ... of the grid's G row slots, with the slot's
-// share of dw and the weight in registers; a second kernel adds the slots'
-// shares.  PRE: the next row's loads are issued before this row's sums are
+// The gradient.  A workgroup of 1024 threads takes R = 1024 / T rows at a time,
+// T threads each, and keeps its share of dw in registers over all its rows; the
+// share is added over the R rows in LDS at the end, and a second kernel adds the
+// workgroups' shares.  At most one workgroup a CU: each share more is D floats
+// written, flushed and read again (1023 x 4096 BF16: 17.6 us with a share per
+// row).  PRE: the next rows' loads are issued before this row's sums are
 // exchanged, where the registers allow it.
 template <int DT, int P>
 struct GradRow {
@@ -286,17 +289,23 @@ __device__ __forceinline__ void fetch_grad_row(const NormGradArgs& a, int64_t r,
   }
 }
 
+constexpr int kGradT = 1024;
+
 template <int DT, int T, int P, bool WHOLE>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradArgs a) {
-  constexpr bool PRE = P * VecT<DT>::EB <= 4 && T < 1024;
-  __shared__ RowRed<T, 2> red;
-  constexpr int RPW = T < 256 ? 256 / T : 1;
-  const int t = (int)threadIdx.x % T;
-  const uint32_t D = (uint32_t)a.D;
-  const int64_t slot = (int64_t)blockIdx.x * RPW + row_of<T>();
-  const int64_t slots = (int64_t)gridDim.x * RPW;
+__global__ __launch_bounds__(kGradT) void k_norm_grad(NormGradArgs a) {
+  constexpr int R = kGradT / T;
+  constexpr bool PRE = P == 1;
   constexpr int EB = VecT<DT>::EB;
+  __shared__ RowRed<T, 2> red[R];
+  __shared__ __align__(16) float share[R > 1 ? R : 1][R > 1 ? T * P * kG : 4];
+  const int t = (int)threadIdx.x % T;
+  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / T);
+  const uint32_t D = (uint32_t)a.D;
+  const int64_t step = (int64_t)gridDim.x * R;
   float acc[P][kG], w[P][kG];
+  GradRow<DT, P> cur, next;
+  int64_t r = (int64_t)blockIdx.x * R + sub;
+  if (PRE && r < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, r, t, cur);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const uint32_t j = (uint32_t)(p * T + t) * kG;
@@ -304,63 +313,82 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradArgs a)
     for (int e = 0; e < kG; ++e) acc[p][e] = w[p][e] = 0.f;
     if (j < D) load_weight(a.weight, a.wdtype, j, D, w[p]);  // 0 past the row's end
   }
-  GradRow<DT, P> cur, next;
-  if (PRE && slot < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, slot, t, cur);
   int turn = 0;
-  for (int64_t r = slot; r < a.N; r += slots, turn ^= 1) {
+  // the workgroup's rows go together (its threads synchronise); those past the last row only keep step
+  for (; r - sub < a.N; r += step, turn ^= 1) {
+    const bool live = r < a.N;
     if constexpr (PRE) {
-      if (r + slots < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, r + slots, t, next);
+      if (r + step < a.N) fetch_grad_row<DT, T, P, WHOLE>(a, r + step, t, next);
     } else {
-      fetch_grad_row<DT, T, P, WHOLE>(a, r, t, cur);
+      if (live) fetch_grad_row<DT, T, P, WHOLE>(a, r, t, cur);
     }
     float sums[2] = {0.f, 0.f};  // of s^2 and of dy w s
+    if (live) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const bool in = (uint32_t)(p * T + t) * kG < D;
-      float f[kG], g[kG];
-      raw_to_f32<DT>(cur.s[p], f);
-      raw_to_f32<DT>(cur.dy[p], g);
+      for (int p = 0; p < P; ++p) {
+        const bool in = (uint32_t)(p * T + t) * kG < D;
+        float f[kG], g[kG];
+        raw_to_f32<DT>(cur.s[p], f);
+        raw_to_f32<DT>(cur.dy[p], g);
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const float fe = in ? f[e] : 0.f, ge = in ? g[e] : 0.f;
-        sums[0] = __builtin_fmaf(fe, fe, sums[0]);
-        sums[1] = __builtin_fmaf(ge * w[p][e], fe, sums[1]);
+        for (int e = 0; e < kG; ++e) {
+          const float fe = in ? f[e] : 0.f, ge = in ? g[e] : 0.f;
+          sums[0] = __builtin_fmaf(fe, fe, sums[0]);
+          sums[1] = __builtin_fmaf(ge * w[p][e], fe, sums[1]);
+        }
       }
     }
-    row_reduce<T, 2>(sums, red, turn);
-    const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
-    const float k = rstd * rstd * rstd * (sums[1] / (float)D);
+    row_reduce<T, 2>(sums, red[sub], turn);
+    if (live) {
+      const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
+      const float k = rstd * rstd * rstd * (sums[1] / (float)D);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const uint32_t j = (uint32_t)(p * T + t) * kG;
-      float f[kG], g[kG], d[kG];
-      raw_to_f32<DT>(cur.s[p], f);
-      raw_to_f32<DT>(cur.dy[p], g);
-      if (a.dsum)
-        raw_to_f32<DT>(cur.dsum[p], d);
-      else
+      for (int p = 0; p < P; ++p) {
+        const uint32_t j = (uint32_t)(p * T + t) * kG;
+        float f[kG], g[kG], d[kG];
+        raw_to_f32<DT>(cur.s[p], f);
+        raw_to_f32<DT>(cur.dy[p], g);
+        if (a.dsum)
+          raw_to_f32<DT>(cur.dsum[p], d);
+        else
 #pragma unroll
-        for (int e = 0; e < kG; ++e) d[e] = 0.f;
+          for (int e = 0; e < kG; ++e) d[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        acc[p][e] = __builtin_fmaf(g[e], f[e] * rstd, acc[p][e]);
-        d[e] += __builtin_fmaf(g[e] * w[p][e], rstd, -(f[e] * k));
+        for (int e = 0; e < kG; ++e) {
+          acc[p][e] = __builtin_fmaf(g[e], f[e] * rstd, acc[p][e]);
+          d[e] += __builtin_fmaf(g[e] * w[p][e], rstd, -(f[e] * k));
+        }
+        if (a.dx && j < D) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
       }
-      if (a.dx && j < D) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
     }
     if constexpr (PRE) cur = next;
   }
-  if (a.dweight) {
-    char* part = reinterpret_cast<char*>(a.parts + slot * a.D);
+  if (!a.dweight) return;
+  float* part = a.parts + (int64_t)blockIdx.x * a.D;
+  if constexpr (R > 1) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<float4*>(&share[sub][(p * T + t) * kG + 4 * k]) =
+            make_float4(acc[p][4 * k], acc[p][4 * k + 1], acc[p][4 * k + 2], acc[p][4 * k + 3]);
+    __syncthreads();
+    for (uint32_t j = threadIdx.x; j < D; j += kGradT) {
+      float v = share[0][j];
+#pragma unroll
+      for (int k = 1; k < R; ++k) v += share[k][j];
+      part[j] = v;
+    }
+  } else {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t j = (uint32_t)(p * T + t) * kG;
-      if (j < D) store_group<CE_F32>(part, j, D, f32_to_raw<CE_F32>(acc[p]));
+      if (j < D) store_group<CE_F32>(reinterpret_cast<char*>(part), j, D, f32_to_raw<CE_F32>(acc[p]));
     }
   }
 }
 
-// The same for D > 16384: the row is read twice, and the slot's share of dw is
+// The same for D > 16384: the row is read twice, and the workgroup's share of dw is
 // kept in LDS (4 D bytes), each thread its own columns.
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(1024) void k_norm_grad_wide(NormGradArgs a) {
@@ -420,10 +448,10 @@ __global__ __launch_bounds__(1024) void k_norm_grad_wide(NormGradArgs a) {
   }
 }
 
-// dw[j] (+)= the slots' shares: 32 columns per workgroup, thread row k of 32
-// adds slots k, k + 32, ... in order, and the rows are added in order.
+// dw[j] (+)= the workgroups' shares: 32 columns per workgroup, thread row k of 32
+// adds shares k, k + 32, ... in order, and the rows are added in order.
 constexpr int kDwCols = 32, kDwRows = 32;
-__global__ __launch_bounds__(kDwCols * kDwRows) void k_norm_dw(const float* parts, int64_t slots, int64_t D, float* dw,
+__global__ __launch_bounds__(kDwCols * kDwRows) void k_norm_dw(const float* parts, int64_t n, int64_t D, float* dw,
                                                                int32_t accumulate) {
   __shared__ float part[kDwRows][kDwCols];
   const int c = (int)threadIdx.x % kDwCols, w = (int)threadIdx.x / kDwCols;
@@ -431,7 +459,7 @@ __global__ __launch_bounds__(kDwCols * kDwRows) void k_norm_dw(const float* part
   float v = 0.f;
   if (j < D) {
 #pragma unroll 8
-    for (int64_t k = w; k < slots; k += kDwRows) v += parts[k * D + j];
+    for (int64_t k = w; k < n; k += kDwRows) v += parts[k * D + j];
   }
   part[w][c] = v;
   __syncthreads();
@@ -442,16 +470,16 @@ __global__ __launch_bounds__(kDwCols * kDwRows) void k_norm_dw(const float* part
   }
 }
 
-// Row slots of the gradient kernel for N rows: about 16 waves a CU, at most
-// one per row (a workgroup holds 4 where a wave takes a row).
-int64_t grad_slots(int64_t N, int64_t D) {
+// Threads that share a row in the gradient kernel (a row of at most 2 groups
+// for each), and its workgroups: as many as the rows fill, at most one a CU.
+int grad_threads(int64_t D) {
   const int64_t g = (D + kG - 1) / kG;
-  if (g <= 128) {
-    const int64_t s = N < 2048 ? N : 2048;
-    return (s + 3) & ~(int64_t)3;
-  }
-  const int64_t most = g <= 256 ? 1024 : g <= 1024 ? 512 : 256;
-  return N < most ? N : most;
+  return g <= 128 ? 64 : g <= 256 ? 256 : g <= 512 ? 512 : 1024;
+}
+constexpr int64_t kGradBlocks = 256;
+int64_t grad_blocks(int64_t N, int64_t D) {
+  const int64_t rows = kGradT / grad_threads(D), b = (N + rows - 1) / rows;
+  return b < kGradBlocks ? b : kGradBlocks;
 }
 
 template <int DT, bool QUANT, bool WHOLE>
@@ -475,17 +503,16 @@ void norm_shape(const NormArgs& a, hipStream_t stream) {
 template <int DT, bool WHOLE>
 void grad_shape(const NormGradArgs& a, hipStream_t stream) {
   const int64_t g = (a.D + kG - 1) / kG;
-  const int64_t slots = grad_slots(a.N, a.D);
-#define VCE_GRAD(T, P, R) \
-  hipLaunchKernelGGL((k_norm_grad<DT, T, P, WHOLE>), dim3((uint32_t)(R)), dim3(T < 256 ? 256 : T), 0, stream, a)
-  if (g <= 64) VCE_GRAD(64, 1, slots / 4);
-  else if (g <= 128) VCE_GRAD(64, 2, slots / 4);
-  else if (g <= 256) VCE_GRAD(256, 1, slots);
-  else if (g <= 512) VCE_GRAD(512, 1, slots);
-  else if (g <= 1024) VCE_GRAD(512, 2, slots);
-  else if (g <= 2048) VCE_GRAD(1024, 2, slots);
+  const dim3 grid((uint32_t)grad_blocks(a.N, a.D));
+#define VCE_GRAD(T, P) hipLaunchKernelGGL((k_norm_grad<DT, T, P, WHOLE>), grid, dim3(kGradT), 0, stream, a)
+  if (g <= 64) VCE_GRAD(64, 1);
+  else if (g <= 128) VCE_GRAD(64, 2);
+  else if (g <= 256) VCE_GRAD(256, 1);
+  else if (g <= 512) VCE_GRAD(512, 1);
+  else if (g <= 1024) VCE_GRAD(1024, 1);
+  else if (g <= 2048) VCE_GRAD(1024, 2);
   else
-    hipLaunchKernelGGL((k_norm_grad_wide<DT, WHOLE>), dim3((uint32_t)slots), dim3(1024),
+    hipLaunchKernelGGL((k_norm_grad_wide<DT, WHOLE>), grid, dim3(1024),
                        (size_t)((g + 1023) / 1024 * 1024 * kG) * 4, stream, a);
 #undef VCE_GRAD
 }
@@ -510,7 +537,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-size_t norm_grad_workspace(int64_t N, int64_t D) { return (size_t)grad_slots(N, D) * (size_t)D * 4u; }
+size_t norm_grad_workspace(int64_t N, int64_t D) { return (size_t)grad_blocks(N, D) * (size_t)D * 4u; }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
   hipError_t e = hipSuccess;
@@ -520,7 +547,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
   }
   if (a.dweight) {
     hipLaunchKernelGGL(k_norm_dw, dim3((uint32_t)((a.D + kDwCols - 1) / kDwCols)), dim3(kDwCols * kDwRows), 0, stream, a.parts,
-                       a.N > 0 ? grad_slots(a.N, a.D) : (int64_t)0, a.D, a.dweight, a.accumulate);
+                       a.N > 0 ? grad_blocks(a.N, a.D) : (int64_t)0, a.D, a.dweight, a.accumulate);
     e = hipGetLastError();
   }
   return e;

@@ -12,10 +12,9 @@
 //
 // Bound: one read and one write of the logits.  What the penalties need from
 // the history is a count per column.  A workgroup owns a chunk of one row's
-// columns: it issues the loads of its first history tokens and of all its
-// columns, keeps the chunk's counts in LDS (integer atomics, whose order cannot
-// change the result) while the columns arrive, and then processes and writes
-// them.  Every chunk of a row reads the row's history, from L2.  Counts take
+// columns: it issues the loads of all its columns, counts the row's tokens that
+// fall into the chunk in LDS (integer atomics, whose order cannot change the
+// result) while the columns arrive, and then processes and writes them.  Every chunk of a row reads the row's history, from L2.  Counts take
 // 16 bits with the prompt flag in the top one while the history holds at most
 // 32767 tokens, and 32 bits beyond.
 #include <hip/hip_runtime.h>
@@ -30,7 +29,7 @@ namespace {
 constexpr int64_t kProcMaxGrid = 1 << 22;
 
 enum { kHistNone = 0, kHist16 = 1, kHist32 = 2 };
-constexpr int kHistAhead = 4;  // tokens per thread loaded ahead of the columns
+constexpr int kHistStep = 4;  // tokens per thread in flight
 
 template <int HIST>
 __device__ __forceinline__ void count_token(uint32_t* tab, uint64_t id, uint64_t first, uint32_t cols, bool prompt) {
@@ -51,29 +50,35 @@ __device__ __forceinline__ void count_token(uint32_t* tab, uint64_t id, uint64_t
   }
 }
 
-// The counts of eight columns as the chunk's table holds them: the prompt flag
-// in bit 31 of each, occurrences below.  False when all are 0.
+// Which of eight columns have a count, as bits: column 2 k in bit k, column
+// 2 k + 1 in bit 16 + k.
 template <int HIST>
-__device__ __forceinline__ bool read_counts(const char* tab, uint32_t col, uint32_t (&c)[kG]) {
+__device__ __forceinline__ uint32_t seen_columns(const char* tab, uint32_t col) {
+  uint32_t seen = 0;
   if constexpr (HIST == kHist16) {
     const u32x4v w = reinterpret_cast<const u32x4v*>(tab)[col >> 3];
-    if ((w.x | w.y | w.z | w.w) == 0u) return false;
+    if ((w.x | w.y | w.z | w.w) == 0u) return 0u;
 #pragma unroll
-    for (int e = 0; e < kG; ++e) {
-      const uint32_t h16 = (w[e / 2] >> (16 * (e & 1))) & 0xffffu;
-      c[e] = (h16 & 0x7fffu) | ((h16 & 0x8000u) << 16);
-    }
-    return true;
+    for (int k = 0; k < 4; ++k)  // the top bit of each half that is not 0
+      seen |= ((((w[k] & 0x7fff7fffu) + 0x7fff7fffu) | w[k]) & 0x80008000u) >> (15 - k);
   } else {
     const u32x4v w0 = reinterpret_cast<const u32x4v*>(tab)[col >> 2];
     const u32x4v w1 = reinterpret_cast<const u32x4v*>(tab)[(col >> 2) + 1];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[e] = w0[e];
-      c[e + 4] = w1[e];
+    for (int k = 0; k < 2; ++k) {
+      seen |= (w0[2 * k] ? 1u : 0u) << k | (w0[2 * k + 1] ? 1u : 0u) << (16 + k);
+      seen |= (w1[2 * k] ? 1u : 0u) << (2 + k) | (w1[2 * k + 1] ? 1u : 0u) << (18 + k);
     }
-    return (w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0u;
   }
+  return seen;
+}
+// A column's occurrences in the output (the count without the prompt flag)
+template <int HIST>
+__device__ __forceinline__ uint32_t occurrences(const char* tab, uint32_t col) {
+  if constexpr (HIST == kHist16)
+    return reinterpret_cast<const uint16_t*>(tab)[col] & 0x7fffu;
+  else
+    return reinterpret_cast<const uint32_t*>(tab)[col] & 0x7fffffffu;
 }
 
 // One chunk: U groups of eight columns for each of T threads.
@@ -88,25 +93,11 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
   const char* x = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   char* z = a.z + (i0 * a.zs0 + i1 * a.zs1) * EB;
 
-  const int64_t* h = nullptr;
-  uint64_t id[kHistAhead];
-  if constexpr (HIST != kHistNone) {
-    // loads return in order: the tokens', waited for first, go out first
-    h = a.hist + i0 * a.hs0 + i1 * a.hs1;
-#pragma unroll
-    for (int k = 0; k < kHistAhead; ++k) {
-      const uint32_t i = tid + k * T;
-      id[k] = i < (uint32_t)a.hist_max ? (uint64_t)h[i] : ~(uint64_t)0;
-    }
-  }
   Raw<DT> raw[U];
   const uint32_t whole = V & ~7u;  // columns in whole groups
   if (whole) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {  // lanes past them read some whole group, so that no load stands behind a branch
-      const uint32_t j = lo + (u * T + tid) * kG;
-      raw[u] = fetch_group<DT, true, true>(x, j, whole);
-    }
+    for (int u = 0; u < U; ++u) raw[u] = fetch_whole<DT>(x, lo + (u * T + tid) * kG, whole);
   }
   const float theta = a.repetition ? a.repetition[r] : 1.f;
   const float fr = a.frequency ? a.frequency[r] : 0.f;
@@ -117,6 +108,7 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
   uint8_t* signs = a.signs ? a.signs + r * a.signs_ld : nullptr;
 
   if constexpr (HIST != kHistNone) {
+    const int64_t* h = a.hist + i0 * a.hs0 + i1 * a.hs1;
     uint32_t n = (uint32_t)a.hist_max;
     if (a.hist_len) {
       const int32_t len = a.hist_len[r];
@@ -127,22 +119,18 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
     constexpr int bytes = T * U * kG * (HIST == kHist16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < bytes / 16 / T; ++i) reinterpret_cast<u32x4v*>(smem)[i * T + tid] = u32x4v{0u, 0u, 0u, 0u};
-    __syncthreads();
     uint32_t* tab = reinterpret_cast<uint32_t*>(smem);
     const uint64_t first = (uint64_t)a.vocab_start + lo;
+    for (uint32_t base = 0; base < n; base += kHistStep * T) {
+      uint64_t id[kHistStep];
 #pragma unroll
-    for (int k = 0; k < kHistAhead; ++k) {
-      const uint32_t i = tid + k * T;
-      if (i < n) count_token<HIST>(tab, id[k], first, hi - lo, i < np);
-    }
-    for (uint32_t base = kHistAhead * T; base < n; base += kHistAhead * T) {
-#pragma unroll
-      for (int k = 0; k < kHistAhead; ++k) {
+      for (int k = 0; k < kHistStep; ++k) {
         const uint32_t i = base + tid + k * T;
         id[k] = i < n ? (uint64_t)h[i] : 0u;
       }
+      if (base == 0) __syncthreads();  // the table is clear
 #pragma unroll
-      for (int k = 0; k < kHistAhead; ++k) {
+      for (int k = 0; k < kHistStep; ++k) {
         const uint32_t i = base + tid + k * T;
         if (i < n) count_token<HIST>(tab, id[k], first, hi - lo, i < np);
       }
@@ -154,7 +142,7 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
   for (int u = 0; u < U; ++u) {
     const uint32_t j = lo + (u * T + tid) * kG;
     if (j >= hi) continue;
-    if (j >= whole) raw[u] = load_group<DT>(x, j, V);
+    fix_tail<DT>(raw[u], x, j, whole, V);
     float v[kG];
     raw_to_f32<DT>(raw[u], v);
     if constexpr (!BWD) {
@@ -166,21 +154,26 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
       }
     }
     if constexpr (HIST != kHistNone) {
-      uint32_t c[kG];
-      if (read_counts<HIST>(smem, j - lo, c)) {
-        uint32_t up = 0;
-        if constexpr (BWD) up = signs ? signs[j >> 3] : 0u;
+      // one seen column of each lane at a time: nearly every wave has a lane with one and few lanes have two, so
+      // the penalty's arithmetic for all eight columns cost more than the pass' memory traffic
+      uint32_t seen = seen_columns<HIST>(smem, j - lo);
+      uint32_t up = 0;
+      if constexpr (BWD) up = seen && signs ? signs[j >> 3] : 0u;
+      while (seen) {
+        const uint32_t bit = (uint32_t)__builtin_ctz(seen);
+        seen &= seen - 1;
+        const uint32_t e = (bit & 15u) * 2 + (bit >> 4);
+        float t = v[0];
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          if (c[e] != 0u) {
-            const bool pos = BWD ? (up >> e) & 1u : v[e] > 0.f;
-            v[e] = pos ? v[e] / theta : v[e] * theta;
-            if constexpr (!BWD) {
-              const uint32_t n = c[e] & 0x7fffffffu;
-              v[e] = __builtin_fmaf(-fr, (float)n, v[e]) - (n ? pr : 0.f);
-            }
-          }
+        for (uint32_t k = 1; k < kG; ++k) t = e == k ? v[k] : t;
+        const bool pos = BWD ? (up >> e) & 1u : t > 0.f;
+        t = pos ? t / theta : t * theta;
+        if constexpr (!BWD) {
+          const uint32_t n = occurrences<HIST>(smem, j - lo + e);
+          t = __builtin_fmaf(-fr, (float)n, t) - (n ? pr : 0.f);
         }
+#pragma unroll
+        for (uint32_t k = 0; k < kG; ++k) v[k] = e == k ? t : v[k];
       }
     }
     if constexpr (!BWD) {

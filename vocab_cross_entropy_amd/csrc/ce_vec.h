@@ -113,26 +113,36 @@ __device__ __forceinline__ Raw<DT> load_group(const char* row, uint32_t j, uint3
   return r;
 }
 
-// The same for a row of whole groups (cols a multiple of 8): lanes past its
-// end read the first group, so that no load stands behind a branch; what they
-// hold is the caller's to drop.
-template <int DT, bool WHOLE, bool NT = false>
-__device__ __forceinline__ Raw<DT> fetch_group(const char* row, uint32_t j, uint32_t cols) {
-  if constexpr (WHOLE) {
-    typedef typename VecT<DT>::Word Word;
-    Raw<DT> r;
-    const Word* p = reinterpret_cast<const Word*>(row + (j < cols ? j : 0) * VecT<DT>::EB);
+// The same in two steps, for many loads in flight: fetch_whole reads a group of
+// the first `whole` columns (cols rounded down to groups; at least one group),
+// lanes past them some other one, so that no load stands behind a branch;
+// fix_tail then reads the row's partial group where a lane has it.  Lanes past
+// the row hold other columns, theirs to drop.
+template <int DT, bool NT = false>
+__device__ __forceinline__ Raw<DT> fetch_whole(const char* row, uint32_t j, uint32_t whole) {
+  typedef typename VecT<DT>::Word Word;
+  Raw<DT> r;
+  const Word* p = reinterpret_cast<const Word*>(row + (j < whole ? j : 0) * VecT<DT>::EB);
 #pragma unroll
-    for (int k = 0; k < VecT<DT>::NV; ++k) {
-      if constexpr (NT)
-        r.w[k] = __builtin_nontemporal_load(p + k);
-      else
-        r.w[k] = p[k];
-    }
-    return r;
-  } else {
-    return load_group<DT, NT>(row, j, cols);
+  for (int k = 0; k < VecT<DT>::NV; ++k) {
+    if constexpr (NT)
+      r.w[k] = __builtin_nontemporal_load(p + k);
+    else
+      r.w[k] = p[k];
   }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void fix_tail(Raw<DT>& r, const char* row, uint32_t j, uint32_t whole, uint32_t cols) {
+  if (j >= whole && j < cols) r = load_group<DT>(row, j, cols);
+}
+// fetch_whole for a kernel instance whose rows have no partial group (WHOLE), load_group otherwise
+template <int DT, bool WHOLE>
+__device__ __forceinline__ Raw<DT> fetch_group(const char* row, uint32_t j, uint32_t cols) {
+  if constexpr (WHOLE)
+    return fetch_whole<DT>(row, j, cols);
+  else
+    return load_group<DT>(row, j, cols);
 }
 
 template <int DT, bool NT = false>
