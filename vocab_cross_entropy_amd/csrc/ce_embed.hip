@@ -79,10 +79,13 @@ __global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
 
 // The sort key of token n: its row of this shard, or V for a token without a gradient here (the
 // padding id, another shard's, or no id at all); those come last.
-__device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t n) {
-  const int64_t id = a.ids[n * a.id_stride];
+__device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t id) {
   const uint64_t v = (uint64_t)id - (uint64_t)a.vocab_start;
   return v < (uint64_t)a.V && (a.padding_idx < 0 || id != a.padding_idx) ? (uint32_t)v : (uint32_t)a.V;
+}
+
+__device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t n) {
+  return key_of(a, a.ids[n * a.id_stride]);
 }
 
 int bits_of(int64_t v) {  // of the values 0 .. v
@@ -106,14 +109,17 @@ __global__ __launch_bounds__(kRankT) void k_rank(EmbedGradArgs a, int pos_bits, 
   const uint32_t n = (uint32_t)a.N;
   const uint32_t steps = (n + kRankSlices * 4 - 1) / (kRankSlices * 4);  // 16-byte words per slice
   constexpr int LOADS = (int)(kRankMax / kRankT);
-  uint32_t key[LOADS];
+  int64_t id[LOADS];
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) {  // without a branch, so that all are in flight
+    const uint32_t i = k * kRankT + threadIdx.x;
+    id[k] = a.ids[(int64_t)(i < n ? i : n - 1) * a.id_stride];
+  }
 #pragma unroll
   for (int k = 0; k < LOADS; ++k) {
     const uint32_t i = k * kRankT + threadIdx.x;
-    key[k] = i < n ? (token_key(a, i) << pos_bits) | i : 0xffffffffu;
+    pair[i] = i < n ? (key_of(a, id[k]) << pos_bits) | i : 0xffffffffu;
   }
-#pragma unroll
-  for (int k = 0; k < LOADS; ++k) pair[k * kRankT + threadIdx.x] = key[k];
   __syncthreads();
   constexpr int OWNERS = kRankTokens / kRankOwn;
   const uint32_t own = threadIdx.x % OWNERS, slice = threadIdx.x / OWNERS;
@@ -271,18 +277,6 @@ __global__ __launch_bounds__(kT) void k_sort_move(EmbedGradArgs a, SortPass s) {
   }
 }
 
-// Adds one to h[bin] for every live lane of a wave; the lanes that agree with
-// the first one go as one addition (a batch may hold one token many times).
-__device__ __forceinline__ void count_bin(uint32_t* h, uint32_t bin, bool live) {
-  const uint64_t all = __ballot(live);
-  if (all == 0) return;
-  const int first = __builtin_ctzll(all);
-  const uint32_t lead = (uint32_t)__builtin_amdgcn_readlane((int)bin, first);
-  const uint64_t same = __ballot(live && bin == lead);
-  if (live && ((int)(threadIdx.x & 63) == first || bin != lead))
-    atomicAdd(&h[bin], bin == lead ? (uint32_t)__popcll(same) : 1u);
-}
-
 // A pass over up to kOneMax tokens in one launch: every workgroup counts all
 // keys itself, those before its tile apart, so none waits for another.  Its tile
 // is one token per thread.
@@ -290,26 +284,40 @@ constexpr int kOneT = 1024;
 constexpr int64_t kOneMax = 65536;
 __global__ __launch_bounds__(kOneT) void k_sort_one(EmbedGradArgs a, SortPass s) {
   constexpr int BINS = 1 << kMaxDigit, W = kOneT / 64;
-  __shared__ uint32_t before[BINS], rest[BINS], next[W][BINS], wave_total[BINS / 64];
+  // counts before this tile and from it on, in 8 copies side by side: lanes of one bin do not all meet in one word
+  constexpr int C = 8;
+  __shared__ uint32_t before[BINS * C], rest[BINS * C], next[W][BINS], wave_total[BINS / 64];
   const uint32_t n = (uint32_t)a.N, mask = (1u << s.bits) - 1u;
   const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
-  if (threadIdx.x < BINS) before[threadIdx.x] = rest[threadIdx.x] = 0;
+  for (int i = (int)threadIdx.x; i < BINS * C; i += kOneT) before[i] = rest[i] = 0;
   for (int i = (int)threadIdx.x; i < W * BINS; i += kOneT) next[0][i] = 0;
   __syncthreads();
   uint32_t mine = 0;
   const uint32_t tiles = (n + kOneT - 1) / kOneT;
   for (uint32_t t0 = 0; t0 < tiles; t0 += 8) {
     uint32_t key[8];
+    if (s.key_in) {
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-      const uint32_t i = (t0 + k) * kOneT + threadIdx.x;
-      key[k] = i < n ? (s.key_in ? s.key_in[i] : token_key(a, i)) : 0u;
+      for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t i = (t0 + k) * kOneT + threadIdx.x;
+        key[k] = s.key_in[i < n ? i : n - 1];
+      }
+    } else {
+      int64_t id[8];
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t i = (t0 + k) * kOneT + threadIdx.x;
+        id[k] = a.ids[(int64_t)(i < n ? i : n - 1) * a.id_stride];
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) key[k] = key_of(a, id[k]);
     }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
       const uint32_t t = t0 + k;
       if (t == blockIdx.x) mine = key[k];
-      if (t < tiles) count_bin(t < blockIdx.x ? before : rest, (key[k] >> s.shift) & mask, t * kOneT + threadIdx.x < n);
+      if (t * kOneT + threadIdx.x < n)
+        atomicAdd(&(t < blockIdx.x ? before : rest)[((key[k] >> s.shift) & mask) * C + (lane & (C - 1))], 1u);
     }
   }
   // this tile: lanes of a wave with the same bin, in order
@@ -326,9 +334,14 @@ __global__ __launch_bounds__(kOneT) void k_sort_one(EmbedGradArgs a, SortPass s)
   if (live && rank == 0) next[w][bin] = (uint32_t)__popcll(same);
   __syncthreads();
   // places: bins before this one, this bin in the tiles before, this bin in the waves before
-  uint32_t scan = 0, all = 0;
+  uint32_t scan = 0, all = 0, prior = 0;
   if (threadIdx.x < BINS) {
-    all = before[threadIdx.x] + rest[threadIdx.x];
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      prior += before[threadIdx.x * C + k];
+      all += rest[threadIdx.x * C + k];
+    }
+    all += prior;
     scan = all;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -339,7 +352,7 @@ __global__ __launch_bounds__(kOneT) void k_sort_one(EmbedGradArgs a, SortPass s)
   }
   __syncthreads();
   if (threadIdx.x < BINS) {
-    uint32_t place = scan - all + before[threadIdx.x];
+    uint32_t place = scan - all + prior;
     for (int k = 0; k < w; ++k) place += wave_total[k];
 #pragma unroll
     for (int k = 0; k < W; ++k) {
@@ -528,7 +541,7 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
 #pragma unroll
               for (int e = 0; e < kG; ++e)
                 acc[e] = a.accumulate ? __builtin_fmaf(acc[e], a.scale, o[e]) : acc[e] * a.scale;
-              store_group<CE_F32>(reinterpret_cast<char*>(a.dw + (int64_t)key[k] * a.dw_ld), j, D,
+              store_group<CE_F32, true>(reinterpret_cast<char*>(a.dw + (int64_t)key[k] * a.dw_ld), j, D,
                                   f32_to_raw<CE_F32>(acc));
             }
 #pragma unroll

@@ -233,7 +233,7 @@ struct ProcessArgs {
   // set by process_plan
   int64_t chunk_cols;         // columns per workgroup item, a multiple of 8
   int64_t chunks;             // items per row
-  int32_t threads;            // workgroup size
+  int32_t shape;              // the chunk shape
 };
 void process_plan(ProcessArgs* a);
 hipError_t launch_process(const ProcessArgs& a, bool backward, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
