@@ -452,19 +452,18 @@ __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs&
   }
 }
 
-// A tile's tokens in batches: the batch's rows of dout, and the rows of dW
-// that its run ends add to, are all loaded before the first is used.  UNI: a
-// wave holds one unit (rows of more than 256 columns), so that tokens, keys and row
-// addresses are scalars.
-// NT: dout is read with the non-temporal bit, where each 16-byte load of a wave
-// covers whole cache lines (BF16 rows on 16-byte boundaries); where lines are
-// shared by two loads it has them fetched twice (20011 x 1037 FP32: 99 against
-// 88 us; 8192 x 4096 BF16: 75 against 84).
+// A unit's tokens in batches: the batch's rows of dout, and the rows of dW
+// that its run ends add to, are all loaded before the first is used.  A lane
+// takes two quads of columns, half a unit apart.  UNI: a wave holds one unit (rows
+// of more than 256 columns), so that tokens, keys and row addresses are scalars.
+// NT: dout is read with the non-temporal bit, where a wave's loads cover whole
+// cache lines (rows on 16-byte boundaries); where lines are shared by two loads it
+// has them fetched twice.
 template <int DT, bool UNI, bool NT>
 __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
   constexpr int EB = VecT<DT>::EB;
   constexpr int B = 4;  // (8 took the registers of a third of the waves: 75 against 71 us)
-  const uint32_t D = (uint32_t)a.D, whole = D & ~7u, N = (uint32_t)a.N, none = (uint32_t)a.V;
+  const uint32_t D = (uint32_t)a.D, whole = D & ~3u, N = (uint32_t)a.N, none = (uint32_t)a.V;
   for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
     if (b >= sum_blocks) {
       __syncthreads();
@@ -475,7 +474,10 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
     if constexpr (UNI) sub = __builtin_amdgcn_readfirstlane(sub);
     const int64_t unit = b * (kT >> s.lanes_shift) + sub;
     const int64_t t = unit / s.col_blocks, cb = unit - t * s.col_blocks;
-    const uint32_t j = (uint32_t)(((cb << s.lanes_shift) + ((int)threadIdx.x & ((1 << s.lanes_shift) - 1))) * kG);
+    const uint32_t lanes = 1u << s.lanes_shift;
+    uint32_t j[2];
+    j[0] = (uint32_t)cb * lanes * kG + (threadIdx.x & (lanes - 1)) * 4;
+    j[1] = j[0] + lanes * 4;
     if (t >= s.tiles) continue;
     uint32_t i0 = (uint32_t)(t * s.tile), i1 = (uint32_t)min64((int64_t)i0 + s.tile, a.N);
     bool from_before = false, goes_on = false;  // shares of long runs
@@ -492,11 +494,13 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
       goes_on = long_run<UNI>(s, N, i1, last, &ahead);
       if (!goes_on) i1 += ahead;
     }
-    if (j >= D) continue;  // (only here: the lanes look for a run's end together)
-    if (j == 0) s.starts[t] = goes_on && !(from_before && first == last);
-    float acc[kG];
+    if (j[0] >= D) continue;  // (only here: the lanes look for a run's end together)
+    if (j[0] == 0) s.starts[t] = goes_on && !(from_before && first == last);
+    float acc[2][4];
 #pragma unroll
-    for (int e = 0; e < kG; ++e) acc[e] = 0.f;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
     for (uint32_t i = i0; i < i1; i += B) {
       uint32_t key[B + 1], idx[B];
 #pragma unroll
@@ -507,47 +511,56 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
       }
       key[B] = i + B < N ? s.skey[i + B] : 0xffffffffu;
       if (key[0] == none) break;  // sorted: nothing with a gradient follows
-      Raw<DT> row[B];
-      Raw<CE_F32> old[B];
+      u32x4v row[B][2], old[B][2];
+      if (whole) {
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const char* p = a.dout + (int64_t)idx[k] * a.dout_ld * EB;
-        row[k] = whole ? fetch_whole<DT, NT>(p, j, whole) : load_group<DT>(p, j, D);
+        for (int k = 0; k < B; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            row[k][h] = fetch_quad<DT, NT>(a.dout + (int64_t)idx[k] * a.dout_ld * EB, j[h] < whole ? j[h] : 0);
       }
-      if (a.accumulate) {
+      if (a.accumulate && whole) {
 #pragma unroll
         for (int k = 0; k < B; ++k)
           if (i + k < i1 && key[k] != none && (i + k + 1 >= N || key[k + 1] != key[k])) {  // a run ends here
-            const char* w = reinterpret_cast<const char*>(a.dw + (int64_t)key[k] * a.dw_ld);
-            old[k] = load_group<CE_F32>(w, j, D);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              old[k][h] = fetch_quad<CE_F32>(reinterpret_cast<const char*>(a.dw + (int64_t)key[k] * a.dw_ld),
+                                             j[h] < whole ? j[h] : 0);
           }
       }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         if (i + k < i1 && key[k] != none) {
-          float f[kG];
-          if (whole) fix_tail<DT>(row[k], a.dout + (int64_t)idx[k] * a.dout_ld * EB, j, whole, D);
-          raw_to_f32<DT>(row[k], f);
-#pragma unroll
-          for (int e = 0; e < kG; ++e) acc[e] += f[e];
           const bool ends = i + k + 1 >= N || key[k + 1] != key[k];
-          if (ends || i + k + 1 == i1) {
-            if (from_before || !ends) {
-              store_group<CE_F32>(reinterpret_cast<char*>(s.parts + (2 * t + (from_before ? 0 : 1)) * a.D), j, D,
-                                  f32_to_raw<CE_F32>(acc));
-            } else {
-              float o[kG];
-              raw_to_f32<CE_F32>(old[k], o);
+          float* const dw = a.dw + (int64_t)key[k] * a.dw_ld;
+          float* const part = s.parts + (2 * t + (from_before ? 0 : 1)) * a.D;
 #pragma unroll
-              for (int e = 0; e < kG; ++e)
-                acc[e] = a.accumulate ? __builtin_fmaf(acc[e], a.scale, o[e]) : acc[e] * a.scale;
-              store_group<CE_F32, true>(reinterpret_cast<char*>(a.dw + (int64_t)key[k] * a.dw_ld), j, D,
-                                  f32_to_raw<CE_F32>(acc));
+          for (int h = 0; h < 2; ++h) {
+            if (j[h] >= whole && j[h] < D) {
+              row[k][h] = partial_quad<DT>(a.dout + (int64_t)idx[k] * a.dout_ld * EB, j[h], D);
+              if (a.accumulate && ends) old[k][h] = partial_quad<CE_F32>(reinterpret_cast<const char*>(dw), j[h], D);
             }
+            float f[4];
+            quad_to_f32<DT>(row[k][h], f);
 #pragma unroll
-            for (int e = 0; e < kG; ++e) acc[e] = 0.f;
-            from_before = false;
+            for (int e = 0; e < 4; ++e) acc[h][e] += f[e];
+            if (ends || i + k + 1 == i1) {
+              if (from_before || !ends) {
+                if (j[h] < D) store_quad(part, j[h], D, acc[h]);
+              } else {
+                float o[4];
+                quad_to_f32<CE_F32>(old[k][h], o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  o[e] = a.accumulate ? __builtin_fmaf(acc[h][e], a.scale, o[e]) : acc[h][e] * a.scale;
+                if (j[h] < D) store_quad<true>(dw, j[h], D, o);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
+            }
           }
+          if (ends || i + k + 1 == i1) from_before = false;
         }
       }
     }
@@ -605,9 +618,9 @@ __global__ __launch_bounds__(kJoinT) void k_embed_join(EmbedGradArgs a, SumArgs 
 
 template <int DT>
 void launch_sum(const EmbedGradArgs& a, const SumArgs& s, int64_t sum_blocks, dim3 grid, hipStream_t stream) {
-  const bool nt = DT == CE_BF16 && (uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0 && a.D % kG == 0;
+  const bool nt = (uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0;
   if (s.lanes_shift >= 6 && nt)
-    hipLaunchKernelGGL((k_embed_sum<DT, true, DT == CE_BF16>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    hipLaunchKernelGGL((k_embed_sum<DT, true, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else if (s.lanes_shift >= 6)
     hipLaunchKernelGGL((k_embed_sum<DT, true, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else

@@ -44,6 +44,59 @@ struct Raw {
   u32x4v w[VecT<DT>::NV];
 };
 
+// Four columns at element alignment, as FP32.  A wave whose lanes take four FP32
+// columns each covers 1 KiB without holes, where groups of eight leave every other
+// 16 bytes to a second access of the same lines.
+template <int DT>
+__device__ __forceinline__ void quad_to_f32(const u32x4v& w, float (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    f[k] = __uint_as_float(DT == CE_F32 ? w[k] : k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+}
+template <int DT, bool NT = false>
+__device__ __forceinline__ u32x4v fetch_quad(const char* row, uint32_t j) {
+  if constexpr (DT == CE_F32) {
+    const u32x4_a4* p = reinterpret_cast<const u32x4_a4*>(row + j * 4);
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+  } else {
+    typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
+    typedef u32x2v u32x2_a2 __attribute__((aligned(2)));
+    const u32x2_a2* p = reinterpret_cast<const u32x2_a2*>(row + j * 2);
+    u32x2v v;
+    if constexpr (NT) v = __builtin_nontemporal_load(p);
+    else v = *p;
+    return u32x4v{v.x, v.y, 0u, 0u};
+  }
+}
+// the columns of a row's last quad that are there, zeros for the others
+template <int DT>
+__device__ __forceinline__ u32x4v partial_quad(const char* row, uint32_t j, uint32_t cols) {
+  u32x4v r = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if (j + e < cols) {
+      if constexpr (DT == CE_F32)
+        r[e] = reinterpret_cast<const uint32_t*>(row)[j + e];
+      else
+        r[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[j + e] << (16 * (e & 1));
+    }
+  return r;
+}
+template <bool NT = false>
+__device__ __forceinline__ void store_quad(float* row, uint32_t j, uint32_t cols, const float (&f)[4]) {
+  if (j + 4 <= cols) {
+    const u32x4v w = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    u32x4_a4* p = reinterpret_cast<u32x4_a4*>(row + j);
+    if constexpr (NT) __builtin_nontemporal_store(w, p);
+    else *p = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (j + e < cols) row[j + e] = f[e];
+  }
+}
+
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
