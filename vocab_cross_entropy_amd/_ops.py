@@ -8,14 +8,12 @@ and run on torch's current stream of the tensors' device; ``process_logits``,
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from . import (CeArgumentError, _check, _device_of, _dtype_code, _need, _ptr, _stream, _workspace,
-               ce_fwd_bwd_fused, ce_scale_grad_inplace, lib, linear_cross_entropy, logits_desc, reduction_code)
+from . import (CeArgumentError, _check, _device_of, _need, _raw_stream, _workspace, ce_fwd_bwd_fused,
+               ce_scale_grad_inplace, lib, linear_cross_entropy, reduction_code)
 
 __all__ = [
     "ce_logits_process", "ce_logits_process_backward", "logits_signs", "process_logits", "processed_cross_entropy",
@@ -25,19 +23,32 @@ __all__ = [
 ]
 
 
-# These calls are small beside the loss (one decoding step's norm takes 4 us on the device), so the checks below
-# first test the common case in one expression and name what is wrong only when it fails.
+# These calls are small beside the loss (one decoding step's norm takes 3 us on the device), so the checks below
+# first test the common case in one expression, with devices as their index, and name what is wrong only when it
+# fails.
+_Tensor = torch.Tensor
+_code = {torch.float32: _abi.CE_F32, torch.bfloat16: _abi.CE_BF16}.get
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-def _call(dev: torch.device, fn, *args):
-    """Run an entry point on torch's current stream of ``dev``, with ``dev`` the current device (kernels are
+def _index(x, what) -> int:
+    """The index of the GPU that ``x`` is on."""
+    if isinstance(x, _Tensor) and x.is_cuda:
+        return x.get_device()
+    _device_of(x, what)  # raises
+
+
+def _call(dev: int, fn, *args):
+    """Run an entry point on torch's current stream of GPU ``dev``, with ``dev`` the current device (kernels are
     looked up per device)."""
-    if dev.index == _current_device():
-        status = fn(*args, _stream(dev))
+    if dev == _current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
+            status = fn(*args, _raw_stream(dev))
     if status:
         _check(status)
 
@@ -50,13 +61,24 @@ def _elayout(msg: str):
     raise CeArgumentError(_abi.CE_ELAYOUT, msg)
 
 
+def _flat(dev, what, t, dtype, n):
+    """The address of a contiguous array of at least ``n`` elements on GPU ``dev`` (None without one)."""
+    if t is None:
+        return None
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype and t.numel() >= n
+            and t.is_contiguous()):
+        _need(torch.device("cuda", dev), what, t, dtype, n)  # raises
+    return t.data_ptr()
+
+
 def _rows(dev, what, t, shape, dtype):
-    """``t`` is a [rows, columns] matrix on ``dev`` with contiguous columns (``dtype`` None: any); its row stride."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev.index
-            and (dtype is None or t.dtype == dtype)):
+    """``t`` is a [rows, columns] matrix on GPU ``dev`` with contiguous columns (``dtype`` None: any): its row
+    stride."""
+    if not (isinstance(t, _Tensor) and t.shape == shape and t.get_device() == dev
+            and (dtype is None or t.dtype is dtype)):
         if t is None:
             _einval(f"{what} is missing")
-        _need(dev, what, t, dtype, contiguous=False)
+        _need(torch.device("cuda", dev), what, t, dtype, contiguous=False)
         if tuple(t.shape) != tuple(shape):
             _einval(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
     ld, col = t.stride()
@@ -68,65 +90,64 @@ def _rows(dev, what, t, shape, dtype):
 # ---- logit processing ------------------------------------------------------------------------------------
 
 
-def _side(dev, what, t, x, width, dtype):
+def _side(dev, what, t, d0, d1, width, dtype):
     """A (d0, d1, >= width) companion of the logits, any row strides: (pointer, s0, s1)."""
     if t is None:
         return None, 0, 0
-    _need(dev, what, t, dtype, contiguous=False)
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype):
+        _need(torch.device("cuda", dev), what, t, dtype, contiguous=False)  # raises
     shape = t.shape
-    if len(shape) != 3 or shape[:2] != x.shape[:2] or shape[2] < width:
-        _einval(f"{what} must be ({x.shape[0]}, {x.shape[1]}, {width}), got {tuple(shape)}")
+    if len(shape) != 3 or shape[0] != d0 or shape[1] != d1 or shape[2] < width:
+        _einval(f"{what} must be ({d0}, {d1}, {width}), got {tuple(shape)}")
     s0, s1, col = t.stride()
     if col != 1 and shape[2] > 1:
         _elayout(f"{what} needs a contiguous last dimension")
     return t.data_ptr(), s0, s1
 
 
-def _per_row(dev, what, t, N, dtype):
-    """The address of an [N] array on ``dev``, None without one."""
-    if t is None:
-        return None
-    _need(dev, what, t, dtype, N)
-    return t.data_ptr()
+def _logits(x, what, vocab_start, vocab_total):
+    """logits_desc, and the dimensions."""
+    if len(x.shape) != 3:
+        _einval(f"{what} must be a 3-d (d0, d1, V) tensor")
+    d0, d1, v = x.shape
+    s0, s1, col = x.stride()
+    if col != 1 and v > 1:
+        _elayout(f"{what} columns must be contiguous (stride 1)")
+    return _abi.CeLogits(x.data_ptr(), _code(x.dtype, -1), 0, d0, d1, s0, s1, v, vocab_start,
+                         v if vocab_total is None else vocab_total), d0, d1, v
 
 
-def _process_desc(dev, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask,
-                  temperature, signs):
-    d0, d1, V = x.shape
-    N = d0 * d1
-    # no row has a token where the tensor is empty (and it has no address): nothing is counted then
-    counted = history is not None and history.numel() > 0
-    hist = _side(dev, "history", history, x, 0, torch.int64)
-    hist_len, prompt = (_per_row(dev, "history_len", history_len, N, torch.int32),
-                        _per_row(dev, "prompt_len", prompt_len, N, torch.int32))
-    penalties = (_per_row(dev, "repetition", repetition, N, torch.float32),
-                 _per_row(dev, "frequency", frequency, N, torch.float32),
-                 _per_row(dev, "presence", presence, N, torch.float32))
-    if history is not None and not counted:
-        hist, hist_len, prompt, penalties = (None, 0, 0), None, None, (None, None, None)
+def _process(fn, x, out, vocab_start, vocab_total, history, history_len, prompt_len, repetition, presence, frequency,
+             bias, mask, temperature, signs):
+    dev = _index(x, "logits")
+    xd, d0, d1, V = _logits(x, "logits", vocab_start, vocab_total)
+    zd, N = xd, d0 * d1
+    if out is not None and out is not x:
+        if not (isinstance(out, _Tensor) and out.get_device() == dev and out.dtype is x.dtype):
+            _need(torch.device("cuda", dev), "out", out, x.dtype, contiguous=False)  # raises
+        if out.shape != x.shape:
+            _einval(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
+        zd = _logits(out, "out", vocab_start, vocab_total)[0]
+    f32, i32 = torch.float32, torch.int32
+    hist, h0, h1 = _side(dev, "history", history, d0, d1, 0, torch.int64)
+    hist_max = 0 if history is None else history.shape[2]
+    hist_len, prompt = _flat(dev, "history_len", history_len, i32, N), _flat(dev, "prompt_len", prompt_len, i32, N)
+    rep, freq, pres = (_flat(dev, "repetition", repetition, f32, N), _flat(dev, "frequency", frequency, f32, N),
+                       _flat(dev, "presence", presence, f32, N))
+    if history is not None and not hist:
+        # an empty tensor (it has no address): no row has a token, and nothing is counted
+        hist = hist_len = prompt = rep = freq = pres = None
+        hist_max = 0
     signs_ptr, signs_ld = None, 0
     if signs is not None:
         if signs.dim() != 2 or signs.shape[1] < (V + 7) // 8:
             _einval(f"signs must be ({N}, {(V + 7) // 8}), see logits_signs")
         signs_ptr, signs_ld = signs.data_ptr(), _rows(dev, "signs", signs, (N, signs.shape[1]), torch.uint8)
-    return _abi.CeProcess(*hist, history.shape[2] if counted else 0, hist_len, prompt, *penalties,
-                          _per_row(dev, "temperature", temperature, N, torch.float32),
-                          *_side(dev, "bias", bias, x, V, torch.float32),
-                          *_side(dev, "mask", mask, x, (V + 31) // 32, torch.int32), signs_ptr, signs_ld)
-
-
-def _process(fn, x, out, vocab_start, vocab_total, **steps):
-    dev = _device_of(x)
-    out = x if out is None else out
-    xd = logits_desc(x, vocab_start, vocab_total)
-    if out is not x:
-        _need(dev, "out", out, x.dtype, contiguous=False)
-        if out.shape != x.shape:
-            _einval(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
-    zd = xd if out is x else logits_desc(out, vocab_start, vocab_total)
-    p = _process_desc(dev, x, **steps)
-    _call(dev, fn, ctypes.byref(xd), ctypes.byref(zd), ctypes.byref(p))
-    return out
+    p = _abi.CeProcess(hist, h0, h1, hist_max, hist_len, prompt, rep, freq, pres,
+                       _flat(dev, "temperature", temperature, f32, N), *_side(dev, "bias", bias, d0, d1, V, f32),
+                       *_side(dev, "mask", mask, d0, d1, (V + 31) // 32, i32), signs_ptr, signs_ld)
+    _call(dev, fn, xd, zd, p)
+    return x if out is None else out
 
 
 def logits_signs(x: torch.Tensor) -> torch.Tensor:
@@ -144,18 +165,16 @@ def ce_logits_process(x, *, out=None, history=None, history_len=None, prompt_len
     ``bias`` (d0, d1, V) FP32 and ``mask`` (d0, d1, ceil(V / 32)) int32 words of allowed columns, both any row
     strides.  ``signs`` (see logits_signs) is written for the gradient.  Each is optional.  Returns the
     processed logits."""
-    return _process(lib.ce_logits_process, x, out, vocab_start, vocab_total, history=history,
-                    history_len=history_len, prompt_len=prompt_len, repetition=repetition, presence=presence,
-                    frequency=frequency, bias=bias, mask=mask, temperature=temperature, signs=signs)
+    return _process(lib.ce_logits_process, x, out, vocab_start, vocab_total, history, history_len, prompt_len,
+                    repetition, presence, frequency, bias, mask, temperature, signs)
 
 
 def ce_logits_process_backward(dz, *, out=None, signs=None, history=None, history_len=None, prompt_len=None,
                                repetition=None, mask=None, temperature=None, vocab_start=0, vocab_total=None):
     """The gradient of ce_logits_process with respect to the logits, in place over ``dz`` or into ``out``.
     ``signs`` are the forward's, needed with ``repetition``."""
-    return _process(lib.ce_logits_process_backward, dz, out, vocab_start, vocab_total, history=history,
-                    history_len=history_len, prompt_len=prompt_len, repetition=repetition, presence=None,
-                    frequency=None, bias=None, mask=mask, temperature=temperature, signs=signs)
+    return _process(lib.ce_logits_process_backward, dz, out, vocab_start, vocab_total, history, history_len,
+                    prompt_len, repetition, None, None, None, mask, temperature, signs)
 
 
 def _constants(**steps):
@@ -255,12 +274,13 @@ def processed_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False,
 def _embedding_desc(ids, weight_ptr, w_ld, of, D, v_local, scale, vocab_start, vocab_total):
     N = ids.shape[0]
     return _abi.CeEmbeddingDesc(ids.data_ptr(), ids.stride(0) if N > 1 else 1, N, D, weight_ptr, w_ld,
-                                _dtype_code(of), 0, v_local, vocab_start,
+                                _code(of.dtype, -1), 0, v_local, vocab_start,
                                 v_local if vocab_total is None else vocab_total, scale)
 
 
 def _need_ids(dev, ids):
-    _need(dev, "ids", ids, torch.int64, contiguous=False)
+    if not (isinstance(ids, _Tensor) and ids.get_device() == dev and ids.dtype is torch.int64):
+        _need(torch.device("cuda", dev), "ids", ids, torch.int64, contiguous=False)  # raises
     if ids is None or ids.dim() != 1:
         _einval("ids must be a 1-d int64 tensor")
 
@@ -268,7 +288,7 @@ def _need_ids(dev, ids):
 def ce_embedding(ids, weight, scale=1.0, *, out=None, vocab_start=0, vocab_total=None):
     """``scale * weight[ids]`` for [N] int64 ``ids`` and a [V, D] table, or the rows from ``vocab_start`` on of a
     vocabulary of ``vocab_total`` (other shards' ids give zeros).  Returns [N, D]."""
-    dev = _device_of(weight, "weight")
+    dev = _index(weight, "weight")
     if weight.dim() != 2:
         _einval("weight must be [V, D]")
     _need_ids(dev, ids)
@@ -276,10 +296,10 @@ def ce_embedding(ids, weight, scale=1.0, *, out=None, vocab_start=0, vocab_total
     m = _embedding_desc(ids, weight.data_ptr(), _rows(dev, "weight", weight, weight.shape, None), weight, D, V, scale,
                         vocab_start, vocab_total)
     if out is None:
-        out, out_ld = torch.empty((m.N, D), dtype=weight.dtype, device=dev), D
+        out, out_ld = weight.new_empty((m.N, D)), D
     else:
         out_ld = _rows(dev, "out", out, (m.N, D), weight.dtype)
-    _call(dev, lib.ce_embedding, ctypes.byref(m), out.data_ptr(), out_ld)
+    _call(dev, lib.ce_embedding, m, out.data_ptr(), out_ld)
     return out
 
 
@@ -295,7 +315,7 @@ def ce_embedding_backward(dout, ids, v_local, scale=1.0, *, padding_idx=None, dw
     """The table's FP32 [v_local, D] gradient from ``dout`` [N, D], written to ``dw`` or added to it
     (``accumulate``; a tied head's ce_linear_cross_entropy gradient).  Tokens equal to ``padding_idx`` add
     nothing.  Returns dw."""
-    dev = _device_of(dout, "dout")
+    dev = _index(dout, "dout")
     if dout.dim() != 2:
         _einval("dout must be [N, D]")
     _need_ids(dev, ids)
@@ -309,13 +329,13 @@ def ce_embedding_backward(dout, ids, v_local, scale=1.0, *, padding_idx=None, dw
     if dw is None:
         if accumulate:
             _einval("accumulate needs dw")
-        dw = torch.empty((v_local, D), dtype=torch.float32, device=dev)
+        dw = torch.empty((v_local, D), dtype=torch.float32, device=dout.device)
     if ws is None:
-        ws = _workspace(ce_embedding_workspace_bytes(N, D, v_local), dev)
-    _need(dev, "workspace", ws, torch.uint8)
-    _call(dev, lib.ce_embedding_backward, ctypes.byref(m), dout.data_ptr(), _rows(dev, "dout", dout, dout.shape, None),
+        ws = _workspace(ce_embedding_workspace_bytes(N, D, v_local), dout.device)
+    ws_ptr = _flat(dev, "workspace", ws, torch.uint8, 0)
+    _call(dev, lib.ce_embedding_backward, m, dout.data_ptr(), _rows(dev, "dout", dout, dout.shape, None),
           -1 if padding_idx is None else padding_idx, dw.data_ptr(),
-          _rows(dev, "dw", dw, (v_local, D), torch.float32), 1 if accumulate else 0, ws.data_ptr(), ws.numel())
+          _rows(dev, "dw", dw, (v_local, D), torch.float32), 1 if accumulate else 0, ws_ptr, ws.numel())
     return dw
 
 
@@ -348,7 +368,7 @@ def embedding(ids, weight, scale=1.0, *, padding_idx=None, grad_buffer=None, voc
     backward adds the gradient to it instead and ``weight.grad`` stays as it is: with a tied head, the buffer that
     ce_linear_cross_entropy adds its dw to."""
     if grad_buffer is not None:
-        _rows(_device_of(weight, "weight"), "grad_buffer", grad_buffer, weight.shape, torch.float32)
+        _rows(_index(weight, "weight"), "grad_buffer", grad_buffer, weight.shape, torch.float32)
     return Embedding.apply(weight, ids, scale, padding_idx, grad_buffer, vocab_start, vocab_total)
 
 
@@ -360,13 +380,14 @@ def _norm_desc(dev, x, weight, residual, eps):
         _einval("x must be [N, D]")
     shape = x.shape
     N, D = shape
-    _need(dev, "weight", weight, None, D)
-    if weight is None or weight.shape != (D,):
-        _einval(f"weight must be [{D}]")
+    if not (isinstance(weight, _Tensor) and weight.get_device() == dev and weight.shape == (D,)
+            and weight.is_contiguous()):
+        _need(torch.device("cuda", dev), "weight", weight, None, D)
+        _einval(f"weight must be a contiguous [{D}] tensor")
     res, res_ld = None, 0
     if residual is not None:
         res, res_ld = residual.data_ptr(), _rows(dev, "residual", residual, shape, x.dtype)
-    return _abi.CeNorm(x.data_ptr(), res, weight.data_ptr(), _dtype_code(x), _dtype_code(weight), N, D,
+    return _abi.CeNorm(x.data_ptr(), res, weight.data_ptr(), _code(x.dtype, -1), _code(weight.dtype, -1), N, D,
                        _rows(dev, "x", x, shape, None), res_ld, eps)
 
 
@@ -386,27 +407,26 @@ def _sum_out(dev, x, residual, sum_out):
 def ce_rms_norm(x, weight, residual=None, eps=1e-6, *, out=None, sum_out=None):
     """RMS norm of ``x + residual`` ([N, D]); returns (y, sum), the sum None without a residual (unless
     ``sum_out`` asks for it).  ``out`` and ``sum_out`` may be x or residual themselves."""
-    dev = _device_of(x, "x")
+    dev = _index(x, "x")
     n = _norm_desc(dev, x, weight, residual, eps)
     out, ptr, ld = _like(dev, "out", out, x)
     total, total_ptr, total_ld = _sum_out(dev, x, residual, sum_out)
-    _call(dev, lib.ce_rms_norm, ctypes.byref(n), ptr, ld, total_ptr, total_ld)
+    _call(dev, lib.ce_rms_norm, n, ptr, ld, total_ptr, total_ld)
     return out, total
 
 
 def ce_rms_norm_quant(x, weight, residual=None, eps=1e-6, *, group=0, out=None, scales=None, sum_out=None):
     """ce_rms_norm with its output in e4m3 (torch.float8_e4m3fn) and FP32 scales, one for each ``group`` columns
     (32, 64 or 128; 0: one for the row).  Returns (q, scales [N, groups], sum or None)."""
-    dev = _device_of(x, "x")
+    dev = _index(x, "x")
     n = _norm_desc(dev, x, weight, residual, eps)
     N, D = x.shape
     groups = -(-D // group) if group > 0 else 1
-    out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=dev) if out is None else out
-    scales = torch.empty((N, groups), dtype=torch.float32, device=dev) if scales is None else scales
-    _need(dev, "scales", scales, torch.float32, N * groups)
+    out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=x.device) if out is None else out
+    scales = torch.empty((N, groups), dtype=torch.float32, device=x.device) if scales is None else scales
     total, total_ptr, total_ld = _sum_out(dev, x, residual, sum_out)
-    _call(dev, lib.ce_rms_norm_quant, ctypes.byref(n), out.data_ptr(),
-          _rows(dev, "out", out, (N, D), torch.float8_e4m3fn), int(group), scales.data_ptr(), total_ptr, total_ld)
+    _call(dev, lib.ce_rms_norm_quant, n, out.data_ptr(), _rows(dev, "out", out, (N, D), torch.float8_e4m3fn),
+          int(group), _flat(dev, "scales", scales, torch.float32, N * groups), total_ptr, total_ld)
     return out, scales, total
 
 
@@ -422,7 +442,7 @@ def ce_rms_norm_backward(dy, s, weight, eps=1e-6, *, dsum=None, dx=None, dweight
     """The gradient from the forward's sum ``s`` ([N, D]): (dx, the gradient of x and of the residual, in s's
     dtype; dweight, FP32 [D]).  ``dsum`` is the gradient that reaches the sum by the residual stream; ``dx`` may
     be dy or dsum itself; ``accumulate`` adds to ``dweight``."""
-    dev = _device_of(s, "s")
+    dev = _index(s, "s")
     n = _norm_desc(dev, s, weight, None, eps)
     N, D = s.shape
     dy_ptr, dy_ld = _like(dev, "dy", dy, s)[1:] if dy is not None else _einval("dy is missing")
@@ -434,15 +454,15 @@ def ce_rms_norm_backward(dy, s, weight, eps=1e-6, *, dsum=None, dx=None, dweight
         if accumulate:
             _einval("accumulate needs dweight")
         if want_dweight:
-            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+            dweight = torch.empty(D, dtype=torch.float32, device=s.device)
+    dweight_ptr = ws_ptr = None
     ws_bytes = 0
     if dweight is not None:
-        _need(dev, "dweight", dweight, torch.float32, D)
-        ws = _workspace(ce_rms_norm_workspace_bytes(N, D), dev) if ws is None else ws
-        _need(dev, "workspace", ws, torch.uint8)
-        ws_bytes = ws.numel()
-    _call(dev, lib.ce_rms_norm_backward, ctypes.byref(n), dy_ptr, dy_ld, dsum_ptr, dsum_ld, dx_ptr, dx_ld,
-          _ptr(dweight), 1 if accumulate else 0, _ptr(ws) if ws_bytes else None, ws_bytes)
+        dweight_ptr = _flat(dev, "dweight", dweight, torch.float32, D)
+        ws = _workspace(ce_rms_norm_workspace_bytes(N, D), s.device) if ws is None else ws
+        ws_ptr, ws_bytes = _flat(dev, "workspace", ws, torch.uint8, 0), ws.numel()
+    _call(dev, lib.ce_rms_norm_backward, n, dy_ptr, dy_ld, dsum_ptr, dsum_ld, dx_ptr, dx_ld, dweight_ptr,
+          1 if accumulate else 0, ws_ptr, ws_bytes)
     return dx, dweight
 
 
