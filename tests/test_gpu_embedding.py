@@ -22,6 +22,10 @@ def _ids(N, V, seed, kind):
         return torch.randint(0, V, (N,), generator=g)
     if kind == "pairs":  # runs of two
         return torch.arange(N) // 2 % V
+    if kind == "runs":  # ids that occur 1, 2, ... 50 times, in any order
+        count = torch.arange(1, 51).repeat(V // 50 + 1)[:V]
+        ids = torch.repeat_interleave(torch.arange(V), count)[:N]
+        return ids[torch.randperm(N, generator=g)]
     return (torch.rand(N, generator=g, dtype=torch.float64) ** 4 * V).long().clamp(max=V - 1)  # long tail
 
 
@@ -69,7 +73,8 @@ def test_lookup_strides_shards_and_bad_ids():
 GRAD = [(1, 1, 1, "tail"), (1, 60, 40, "tail"), (2, 3, 8, "same"), (15, 4, 9, "tail"), (16, 4, 64, "pairs"),
         (17, 40, 5, "same"), (33, 5, 130, "tail"), (400, 30, 2051, "tail"), (700, 3000, 33, "uniform"),
         (2049, 500, 24, "same"), (5000, 700, 12, "tail"), (8192, 50, 7, "pairs"), (8193, 50, 7, "tail"),
-        (12345, 70000, 5, "uniform"), (20000, 300, 3, "same"), (66000, 1100, 2, "tail")]
+        (600, 3, 520, "same"), (3001, 2, 300, "pairs"), (4000, 400, 270, "runs"), (4000, 400, 8, "runs"),
+        (9000, 600, 1030, "runs"), (5000, 1 << 20, 1, "uniform"), (12345, 70000, 5, "uniform"), (20000, 300, 3, "same"), (66000, 1100, 2, "tail")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
@@ -115,6 +120,47 @@ def test_gradient_strides_shards_and_bad_ids():
         ref, size, m = ref_embed_grad(f64(dout), ids.numpy(), hi - lo, 0.5, vocab_start=lo)
         assert_within(f64(buf)[:, 2:2 + D], ref, 1.01 * U * (m + 2) * size + TINY, "shard")
         assert (f64(buf)[:, :2] == 5).all() and (f64(buf)[:, -2:] == 5).all()
+
+
+def test_every_token_is_padding():
+    ids = torch.full((70,), 3).cuda()
+    dout = torch.ones((70, 20), device="cuda")
+    dw = vce.ce_embedding_backward(dout, ids, 5, padding_idx=3, dw=torch.full((5, 20), float("nan"), device="cuda"))
+    assert not dw.any()
+    kept = torch.full((5, 20), 2.0, device="cuda")
+    vce.ce_embedding_backward(dout, ids, 5, padding_idx=3, dw=kept, accumulate=True)
+    assert (kept == 2).all()
+
+
+def test_one_workspace_for_smaller_batches():
+    """A workspace sized for the largest batch serves every smaller one, whichever sort that takes."""
+    V, D = 300, 10
+    ws = torch.empty(vce.ce_embedding_workspace_bytes(70000, D, V), dtype=torch.uint8, device="cuda")
+    for N in (70000, 66000, 65536, 8193, 8192, 100, 1):
+        ids, dout = _ids(N, V, N, "tail"), torch.randn((N, D), generator=_gen(N))
+        say(f"[embed grad] workspace {N}")
+        dw = vce.ce_embedding_backward(dout.cuda(), ids.cuda(), V, dw=torch.empty((V, D), device="cuda"), ws=ws)
+        ref, size, m = ref_embed_grad(f64(dout), ids.numpy(), V, 1.0)
+        assert_within(f64(dw), ref, 1.01 * U * (m + 2) * size + TINY, str(N))
+
+
+def test_refusals():
+    w, ids, dout = torch.ones((6, 5), device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda"), \
+        torch.ones((4, 5), device="cuda")
+    for call in (lambda: vce.ce_embedding(ids.int(), w), lambda: vce.ce_embedding(ids.cpu(), w),
+                 lambda: vce.ce_embedding(ids.view(2, 2), w), lambda: vce.ce_embedding(ids, w.half()),
+                 lambda: vce.ce_embedding(ids, w.t()), lambda: vce.ce_embedding(ids, w, out=dout[:3]),
+                 lambda: vce.ce_embedding(ids, w, out=dout.bfloat16()), lambda: vce.ce_embedding(ids, w, vocab_start=1),
+                 lambda: vce.ce_embedding_backward(dout, ids[:3], 6),
+                 lambda: vce.ce_embedding_backward(dout, ids, 6, dw=w.bfloat16()),
+                 lambda: vce.ce_embedding_backward(dout, ids, 6, dw=w[:5]),
+                 lambda: vce.ce_embedding_backward(dout, ids, 6, accumulate=True),
+                 lambda: vce.ce_embedding_backward(dout, ids, 6, padding_idx=-1),
+                 lambda: vce.ce_embedding_backward(dout, ids, 6, ws=torch.empty(8, dtype=torch.uint8, device="cuda")),
+                 lambda: vce.ce_embedding_backward(dout[:, :1].expand(4, 5), ids, 6),
+                 lambda: vce.embedding(ids, w, grad_buffer=w[:5])):
+        with pytest.raises(vce.CeArgumentError):
+            call()
 
 
 def test_no_tokens():

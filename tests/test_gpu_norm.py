@@ -156,6 +156,27 @@ def test_backward(N, D, dtype):
         assert torch.equal((g, d)[which], dx)
 
 
+def test_refusals():
+    x, w = torch.ones((4, 8), device="cuda"), torch.ones(8, device="cuda")
+    for call in (lambda: vce.ce_rms_norm(x.half(), w), lambda: vce.ce_rms_norm(x, w.half()),
+                 lambda: vce.ce_rms_norm(x, w[:7]), lambda: vce.ce_rms_norm(x, w.cpu()), lambda: vce.ce_rms_norm(x, None),
+                 lambda: vce.ce_rms_norm(x[0], w), lambda: vce.ce_rms_norm(x.t(), w[:4]),
+                 lambda: vce.ce_rms_norm(x[:, :1].expand(4, 8), w), lambda: vce.ce_rms_norm(x[:1].expand(4, 8), w),
+                 lambda: vce.ce_rms_norm(x, w, x[:3]), lambda: vce.ce_rms_norm(x, w, x.bfloat16()),
+                 lambda: vce.ce_rms_norm(x, w, out=x.bfloat16()), lambda: vce.ce_rms_norm(x, w, eps=-1.0),
+                 lambda: vce.ce_rms_norm_quant(x, w, group=48), lambda: vce.ce_rms_norm_quant(x, w, out=x),
+                 lambda: vce.ce_rms_norm_quant(x, w, scales=w[:3]),
+                 lambda: vce.ce_rms_norm_backward(None, x, w), lambda: vce.ce_rms_norm_backward(x[:3], x, w),
+                 lambda: vce.ce_rms_norm_backward(x, x, w, dsum=x.bfloat16()),
+                 lambda: vce.ce_rms_norm_backward(x, x, w, dweight=w[:5]),
+                 lambda: vce.ce_rms_norm_backward(x, x, w, accumulate=True),
+                 lambda: vce.ce_rms_norm_backward(x, x, w, ws=torch.empty(1, dtype=torch.uint8, device="cuda")),
+                 lambda: vce.ce_rms_norm(torch.ones((1, 32769), device="cuda"), torch.ones(32769, device="cuda")),
+                 lambda: vce.rms_norm(x, w, x[:3])):
+        with pytest.raises(vce.CeArgumentError):
+            call()
+
+
 def test_no_rows():
     w = torch.ones(12, device="cuda")
     e = torch.empty((0, 12), device="cuda")

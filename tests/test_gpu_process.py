@@ -342,6 +342,51 @@ def test_graph_replays_and_streams():
             torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(60, 10, 500, 7), (2, 600, 20001, 40), (41, 200, 70, 4), (3, 1000, 24000, 9)], ids=str)
+def test_many_rows(shape, dtype):
+    """Enough rows for the larger chunks; both directions, checked on the first, the last and some other rows."""
+    d0, d1, V, L = shape
+    N = d0 * d1
+    say(f"[process] many rows {shape} {dtype}")
+    s = _inputs(d0, d1, V, dtype, L, seed=N)
+    s["mask"] = _mask(d0, d1, V, seed=N)
+    d = _dev(s)
+    signs = vce.logits_signs(d["x"])
+    z = f64(_call(d, out=torch.empty_like(d["x"]), signs=signs).view(N, V)[:])
+    keep = {k: d[k] for k in ("history", "history_len", "prompt_len", "repetition", "mask", "temperature")}
+    dx = f64(vce.ce_logits_process_backward(d["x"], out=torch.empty_like(d["x"]), signs=signs, **keep).view(N, V))
+    pick = np.unique(np.concatenate([[0, 1, 2, N - 2, N - 1], np.random.RandomState(1).randint(0, N, 40)]))
+    sub = {k: v.reshape(N, 1, -1)[pick] if k in ("x", "history", "mask") else v[pick] for k, v in s.items()}
+    ref, budget, seen, allowed = _reference(sub)
+    _check(torch.from_numpy(z[pick]), ref, budget, dtype, "z")
+    x = f64(sub["x"]).reshape(len(pick), V)
+    ref = ref_process_grad(x, x > 0, seen, f64(sub["repetition"]), f64(sub["temperature"]), allowed)
+    assert_within(dx[pick], ref, (3.03 * U + half_step(dtype)) * np.abs(ref) + 1e-37, "dx")
+
+
+def test_refusals():
+    s = _dev(_inputs(2, 3, 70, torch.float32, 10, seed=1))
+    s["mask"] = _mask(2, 3, 70, seed=1).cuda()
+    x = s["x"]
+    for change in (dict(x=x[0]), dict(x=x.half()), dict(x=x.transpose(1, 2)), dict(x=x[:1].expand(2, 3, 70)),
+                   dict(history=s["history"].int()), dict(history=s["history"][0]), dict(history=s["history"][:1]),
+                   dict(history=s["history"].transpose(1, 2)), dict(history_len=s["history_len"].long()),
+                   dict(history_len=s["history_len"][:5]), dict(prompt_len=s["prompt_len"].cpu()),
+                   dict(history=None), dict(repetition=s["repetition"].double()), dict(temperature=s["temperature"][:5]),
+                   dict(mask=s["mask"][..., :2]), dict(mask=s["mask"].long()), dict(mask=s["mask"][:1]),
+                   dict(bias=x[..., :69]), dict(bias=x.bfloat16()), dict(bias=x[0]), dict(out=x[..., :69]),
+                   dict(out=x.bfloat16()), dict(signs=torch.empty((6, 8), dtype=torch.uint8, device="cuda")),
+                   dict(signs=torch.empty((5, 9), dtype=torch.uint8, device="cuda")), dict(vocab_start=1)):
+        kw = dict(s, **change)
+        with pytest.raises(vce.CeArgumentError):
+            vce.ce_logits_process(kw.pop("x"), **kw)
+    keep = {k: s[k] for k in ("history", "history_len", "prompt_len", "repetition", "mask", "temperature")}
+    with pytest.raises(vce.CeArgumentError):
+        vce.ce_logits_process_backward(x, **keep)  # no signs
+    assert torch.equal(x, _dev(_inputs(2, 3, 70, torch.float32, 10, seed=1))["x"]), "a refused call must touch nothing"
+
+
 def test_no_rows_and_empty_history():
     x = torch.empty((0, 3, 17), device="cuda")
     assert vce.ce_logits_process(x, temperature=torch.empty(0, device="cuda")).numel() == 0

@@ -6,9 +6,11 @@
 // Lookup: one read of the rows named and one write of the output.
 //
 // Gradient: every row of dout is read once and every row of dW that a token
-// names is written once (read once too when it is added to).  To make the sum's
-// order fixed and its writes few, the tokens are sorted by id first, ties by
-// position (a stable sort of N small keys, little beside the N rows of D values):
+// names is written once (read once too when it is added to).  Few tokens take one
+// launch: each token's workgroups look through all ids and, if its own has not
+// come before, add up the rows of that id.  With more tokens, to make the sum's order fixed and its writes few, they are sorted by id
+// first, ties by position (a stable sort of N small keys, little beside the N rows
+// of D values):
 //   up to kRankMax tokens whose (id, position) pair fits 32 bits: one launch in
 //     which each token's place is the count of smaller pairs (N^2 compares of LDS
 //     words, N^2 / 16384 cycles of the whole chip);
@@ -383,7 +385,7 @@ struct SumArgs {
   int lanes_shift;
   int64_t fill_blocks;     // workgroups that write the rows no token names (0 when dW is added to)
 };
-constexpr int kFillRows = 32;
+constexpr int kFillRows = 8;  // (32: 72 against 68 us on 20011 x 1037 FP32 tokens, 32000 rows)
 
 // Tokens with key `key` that follow one another from position `at` on (UP) or
 // from at - 1 down, at most `limit` of them.  UNI: by the lanes of a wave, 64 at a
@@ -419,6 +421,33 @@ __device__ __forceinline__ bool long_run(const SumArgs& s, uint32_t N, uint32_t 
   return back + *ahead > tile;
 }
 
+// Zeros in the rows v0 .. v0 + kFillRows - 1 of dW whose bit in `named` is not set:
+// 16-byte stores from a row's first 16-byte boundary on, single columns before and
+// after.  Rows that share cache lines are written with the non-temporal bit (20011 x
+// 1037 FP32 tokens: 68 against 85 us), whole lines without (32000 x 4096: 94 against
+// 98 us).
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t v0, uint32_t named) {
+  const uint32_t D = (uint32_t)a.D;
+  const u32x4v zero = {0u, 0u, 0u, 0u};
+  const bool lines = (((uintptr_t)a.dw | (uintptr_t)(a.dw_ld * 4)) & 127) == 0;
+  for (int k = 0; k < kFillRows && v0 + k < a.V; ++k) {
+    if ((named >> k) & 1u) continue;
+    float* row = a.dw + (v0 + k) * a.dw_ld;
+    uint32_t head = (uint32_t)((16 - ((uintptr_t)row & 15)) & 15) / 4;
+    head = head < D ? head : D;
+    const uint32_t body = (D - head) / 4;
+    if (threadIdx.x < head) row[threadIdx.x] = 0.f;
+    u32x4v* const p = reinterpret_cast<u32x4v*>(row + head);
+    if (lines) {
+      for (uint32_t j = threadIdx.x; j < body; j += kT) p[j] = zero;
+    } else {
+      for (uint32_t j = threadIdx.x; j < body; j += kT) __builtin_nontemporal_store(zero, p + j);
+    }
+    const uint32_t tail = head + body * 4 + threadIdx.x;
+    if (threadIdx.x < 4 && tail < D) row[tail] = 0.f;
+  }
+}
+
 // Rows of dW that no token names: a search of the sorted keys for each, zeros where it is not found.
 __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
   __shared__ uint32_t named;
@@ -435,21 +464,154 @@ __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs&
     if (threadIdx.x == 0) named = (uint32_t)all;
   }
   __syncthreads();
-  const uint32_t D = (uint32_t)a.D;
-  const u32x4v zero = {0u, 0u, 0u, 0u};
-  for (int k = 0; k < kFillRows && v0 + k < a.V; ++k) {
-    if ((named >> k) & 1u) continue;
-    // 16-byte stores from the row's first 16-byte boundary on, single columns before and after
-    float* row = a.dw + (v0 + k) * a.dw_ld;
-    uint32_t head = (uint32_t)((16 - ((uintptr_t)row & 15)) & 15) / 4;
-    head = head < D ? head : D;
-    const uint32_t body = (D - head) / 4;
-    if (threadIdx.x < head) row[threadIdx.x] = 0.f;
-    for (uint32_t j = threadIdx.x; j < body; j += kT)
-      __builtin_nontemporal_store(zero, reinterpret_cast<u32x4v*>(row + head) + j);
-    const uint32_t tail = head + body * 4 + threadIdx.x;
-    if (threadIdx.x < 4 && tail < D) row[tail] = 0.f;
+  zero_rows(a, v0, named);
+}
+
+// Few tokens, no sort: block (n, c) is token n's, for the 512 columns from 512 c
+// on.  Every thread compares the keys of M tokens with token n's; the block of an
+// id's first token adds up the rows of all of them, a quarter of the batch's
+// positions per wave, and the waves' sums in order.
+constexpr int64_t kDirectMax = 1024, kDirectBlocks = 4096;
+template <int DT, int M>
+__global__ __launch_bounds__(kT) void k_embed_direct(EmbedGradArgs a, int64_t col_blocks, int64_t sum_blocks,
+                                                     int64_t blocks) {
+  constexpr int EB = VecT<DT>::EB;
+  constexpr int B = 4;
+  // word w M + k, bit l: whether token (w M + k) 64 + l has the block's key, so wave w has a quarter in order
+  __shared__ uint64_t match[kWaves * M];
+  __shared__ float part[kWaves][512];
+  __shared__ uint32_t mine, named;
+  const uint32_t D = (uint32_t)a.D, whole = D & ~3u, N = (uint32_t)a.N, none = (uint32_t)a.V, t = threadIdx.x;
+  const uint32_t lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)(t >> 6));
+  int64_t id[M];
+#pragma unroll
+  for (int k = 0; k < M; ++k) {
+    const uint32_t m = (uint32_t)(w * M + k) * 64 + lane;
+    id[k] = a.ids[(int64_t)(m < N ? m : N - 1) * a.id_stride];
   }
+  uint32_t key[M];
+#pragma unroll
+  for (int k = 0; k < M; ++k) key[k] = (uint32_t)(w * M + k) * 64 + lane < N ? key_of(a, id[k]) : none;
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    __syncthreads();  // what the last block left in LDS has been read
+    if (b >= sum_blocks) {
+      const uint32_t v0 = (uint32_t)(b - sum_blocks) * kFillRows;
+      if (t == 0) named = 0;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < M; ++k)
+        if (key[k] != none && key[k] - v0 < (uint32_t)kFillRows) atomicOr(&named, 1u << (key[k] - v0));
+      __syncthreads();
+      zero_rows(a, v0, named);
+      continue;
+    }
+    const uint32_t n = (uint32_t)(b / col_blocks);
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+      if ((uint32_t)(w * M + k) * 64 + lane == n) mine = key[k];
+    __syncthreads();
+    const uint32_t own = mine;
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      const uint64_t same = __ballot(key[k] == own);
+      if (lane == 0) match[w * M + k] = same;
+    }
+    __syncthreads();
+    bool first = own != none;
+#pragma unroll
+    for (int k = 0; k < kWaves * M; ++k) {
+      const uint32_t at = (uint32_t)k * 64;
+      const uint64_t before = n >= at + 64 ? ~(uint64_t)0 : n > at ? ((uint64_t)1 << (n - at)) - 1 : 0;
+      first = first && (match[k] & before) == 0;
+    }
+    if (!first) continue;  // (the same for the whole workgroup)
+    const uint32_t c = (uint32_t)(b - n * col_blocks) * 512;
+    uint32_t j[2];
+    j[0] = c + lane * 4;
+    j[1] = j[0] + 256;
+    float* const dw = a.dw + (int64_t)own * a.dw_ld;
+    float old[2] = {0.f, 0.f};  // of columns c + t and c + 256 + t, which this thread writes
+    if (a.accumulate) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (c + h * 256 + t < D) old[h] = dw[c + h * 256 + t];
+    }
+    float acc[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
+    for (int k = 0; k < M; ++k) {
+      const uint64_t found = match[w * M + k];
+      // (scalars: the same for all lanes)
+      uint64_t bits = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(found >> 32)) << 32 |
+                      (uint32_t)__builtin_amdgcn_readfirstlane((int)found);
+      while (bits) {
+        const int count = min(B, (int)__popcll(bits));
+        uint32_t at[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {  // past the last one, the last one again
+          at[i] = (uint32_t)((w * M + k) * 64 + __builtin_ctzll(bits));
+          if (i + 1 < count) bits &= bits - 1;
+        }
+        bits &= bits - 1;
+        u32x4v row[B][2];
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              row[i][h] = fetch_quad<DT>(a.dout + (int64_t)at[i] * a.dout_ld * EB, j[h] < whole ? j[h] : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          if (i < count) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j[h] >= whole && j[h] < D)
+                row[i][h] = partial_quad<DT>(a.dout + (int64_t)at[i] * a.dout_ld * EB, j[h], D);
+              float f[4];
+              quad_to_f32<DT>(row[i][h], f);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[h][e] += f[e];
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float4*>(&part[w][h * 256 + lane * 4]) = make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t q = h * 256 + t;
+      if (c + q < D) {
+        float v = part[0][q];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) v += part[k][q];
+        dw[c + q] = a.accumulate ? __builtin_fmaf(v, a.scale, old[h]) : v * a.scale;
+      }
+    }
+  }
+}
+
+// Whether the direct kernel takes a call.  Its blocks cost 1.5 us a few thousand, where the sort's launches cost 12
+// (300 x 4096: 12.6 against 21.6 us; 1000 x 1037: 14.7 and 25.7; 1000 x 4096, 8000 blocks: 31.6 and 24.8), and an id
+// that takes up the batch has one block per 512 columns (1000 tokens of one id: 42 us, sorted 20; 2000: 80).
+bool direct(int64_t N, int64_t D) { return N <= kDirectMax && N * ceil_div(D, 512) <= kDirectBlocks; }
+
+template <int DT>
+hipError_t launch_direct(const EmbedGradArgs& a, hipStream_t stream) {
+  const int64_t col_blocks = ceil_div(a.D, 512), sum_blocks = a.N * col_blocks;
+  const int64_t blocks = sum_blocks + (a.accumulate ? 0 : ceil_div(a.V, kFillRows));
+  const dim3 grid((uint32_t)min64(blocks, kMaxBlocks));
+  if (a.N <= kT)
+    hipLaunchKernelGGL((k_embed_direct<DT, 1>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks);
+  else
+    hipLaunchKernelGGL((k_embed_direct<DT, 4>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks);
+  return hipGetLastError();
 }
 
 // A unit's tokens in batches: the batch's rows of dout, and the rows of dW
@@ -679,11 +841,14 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-size_t embed_grad_workspace(int64_t N, int64_t D, int64_t V) { return grad_layout(N, D, V).total; }
+size_t embed_grad_workspace(int64_t N, int64_t D, int64_t V) {
+  return direct(N, D) ? 256 : grad_layout(N, D, V).total;
+}
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
   hipError_t e;
   if (a.N == 0) return a.accumulate ? hipSuccess : launch_fill_f32(a.dw, a.V, a.D, a.dw_ld, stream);
+  if (direct(a.N, a.D)) return a.dtype == CE_BF16 ? launch_direct<CE_BF16>(a, stream) : launch_direct<CE_F32>(a, stream);
   const GradLayout g = grad_layout(a.N, a.D, a.V);
   uint32_t* key[2] = {reinterpret_cast<uint32_t*>(a.ws + g.keys[0]), reinterpret_cast<uint32_t*>(a.ws + g.keys[1])};
   uint32_t* idx[2] = {reinterpret_cast<uint32_t*>(a.ws + g.idx[0]), reinterpret_cast<uint32_t*>(a.ws + g.idx[1])};

@@ -486,7 +486,7 @@ int64_t grad_blocks(int64_t N, int64_t D) {
 
 template <int DT, bool QUANT, bool WHOLE, bool NT>
 void norm_shape(const NormArgs& a, hipStream_t stream) {
-  constexpr int64_t most = 1 << 22;  // a launch holds below 2^32 work-items
+  constexpr int64_t most = 1 << 21;  // a launch holds below 2^32 work-items
   const int64_t g = (a.D + kG - 1) / kG;
   const int64_t rows = a.N < most ? a.N : most;
   const int64_t rows4 = (a.N + 3) / 4 < most ? (a.N + 3) / 4 : most;
