@@ -99,13 +99,23 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
 #pragma unroll
     for (int u = 0; u < U; ++u) raw[u] = fetch_whole<DT>(x, lo + (u * T + tid) * kG, whole);
   }
+  const uint8_t* mask = a.mask ? reinterpret_cast<const uint8_t*>(a.mask + i0 * a.ms0 + i1 * a.ms1) : nullptr;
+  uint8_t* signs = a.signs ? a.signs + r * a.signs_ld : nullptr;
+  // BF16: the groups' mask bits and signs, a byte each, go out with the columns (4096 x 32000: 107 against 125 us, the
+  // gradient 106 against 141; FP32, with twice the bytes a column, lost: 228 against 211)
+  constexpr bool AHEAD = DT == CE_BF16;
+  uint32_t allowed[U], up[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t j = lo + (u * T + tid) * kG, at = (j < hi ? j : lo) >> 3;
+    allowed[u] = AHEAD && mask ? mask[at] : 0u;
+    up[u] = AHEAD && BWD && HIST != kHistNone && signs ? signs[at] : 0u;
+  }
   const float theta = a.repetition ? a.repetition[r] : 1.f;
   const float fr = a.frequency ? a.frequency[r] : 0.f;
   const float pr = a.presence ? a.presence[r] : 0.f;
   const float rt = a.temperature ? 1.f / a.temperature[r] : 1.f;
-  const uint8_t* mask = a.mask ? reinterpret_cast<const uint8_t*>(a.mask + i0 * a.ms0 + i1 * a.ms1) : nullptr;
   const float* bias = a.bias ? a.bias + i0 * a.bs0 + i1 * a.bs1 : nullptr;
-  uint8_t* signs = a.signs ? a.signs + r * a.signs_ld : nullptr;
 
   if constexpr (HIST != kHistNone) {
     const int64_t* h = a.hist + i0 * a.hs0 + i1 * a.hs1;
@@ -116,9 +126,9 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
     }
     const int32_t plen = a.prompt_len ? a.prompt_len[r] : 0;
     const uint32_t np = plen < 0 ? 0u : (uint32_t)plen;
-    constexpr int bytes = T * U * kG * (HIST == kHist16 ? 2 : 4);
-#pragma unroll
-    for (int i = 0; i < bytes / 16 / T; ++i) reinterpret_cast<u32x4v*>(smem)[i * T + tid] = u32x4v{0u, 0u, 0u, 0u};
+    // the chunk's counts, in whole groups
+    const uint32_t words = (hi - lo + kG - 1) / kG * (HIST == kHist16 ? 1 : 2);
+    for (uint32_t i = tid; i < words; i += T) reinterpret_cast<u32x4v*>(smem)[i] = u32x4v{0u, 0u, 0u, 0u};
     uint32_t* tab = reinterpret_cast<uint32_t*>(smem);
     const uint64_t first = (uint64_t)a.vocab_start + lo;
     for (uint32_t base = 0; base < n; base += kHistStep * T) {
@@ -147,18 +157,17 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
     raw_to_f32<DT>(raw[u], v);
     if constexpr (!BWD) {
       if (signs) {
-        uint32_t up = 0;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int e = 0; e < kG; ++e) up |= (v[e] > 0.f ? 1u : 0u) << e;  // columns past the end hold 0
-        signs[j >> 3] = (uint8_t)up;
+        for (int e = 0; e < kG; ++e) bits |= (v[e] > 0.f ? 1u : 0u) << e;  // columns past the end hold 0
+        signs[j >> 3] = (uint8_t)bits;
       }
     }
     if constexpr (HIST != kHistNone) {
       // one seen column of each lane at a time: nearly every wave has a lane with one and few lanes have two, so
       // the penalty's arithmetic for all eight columns cost more than the pass' memory traffic
       uint32_t seen = seen_columns<HIST>(smem, j - lo);
-      uint32_t up = 0;
-      if constexpr (BWD) up = seen && signs ? signs[j >> 3] : 0u;
+      if constexpr (BWD && !AHEAD) up[u] = seen && signs ? signs[j >> 3] : 0u;
       while (seen) {
         const uint32_t bit = (uint32_t)__builtin_ctz(seen);
         seen &= seen - 1;
@@ -166,7 +175,7 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
         float t = v[0];
 #pragma unroll
         for (uint32_t k = 1; k < kG; ++k) t = e == k ? v[k] : t;
-        const bool pos = BWD ? (up >> e) & 1u : t > 0.f;
+        const bool pos = BWD ? (up[u] >> e) & 1u : t > 0.f;
         t = pos ? t / theta : t * theta;
         if constexpr (!BWD) {
           const uint32_t n = occurrences<HIST>(smem, j - lo + e);
@@ -187,10 +196,10 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
 #pragma unroll
     for (int e = 0; e < kG; ++e) v[e] *= rt;
     if (mask) {
-      const uint32_t m = mask[j >> 3];
+      if constexpr (!AHEAD) allowed[u] = mask[j >> 3];
       const float off = BWD ? 0.f : -__builtin_inff();
 #pragma unroll
-      for (int e = 0; e < kG; ++e) v[e] = (m >> e) & 1u ? v[e] : off;
+      for (int e = 0; e < kG; ++e) v[e] = (allowed[u] >> e) & 1u ? v[e] : off;
     }
     store_group<DT, true>(z, j, V, f32_to_raw<DT>(v));
   }
@@ -236,12 +245,17 @@ hipError_t launch_dt(const ProcessArgs& a, int hist, dim3 grid, hipStream_t stre
 void process_plan(ProcessArgs* a) {
   // Many rows: 8192-column chunks by 256 threads, the fastest stream (8192 x 128000 BF16: 741 us, 818 by 512 threads
   // on 16384 columns).  Some: 512 threads, which count a long history in half the steps (64 x 128000 FP32 with up to
-  // 4096 tokens: 17.1 against 18.4 us).  Few: 2048-column chunks, for workgroups enough.
+  // 4096 tokens: 17.1 against 18.4 us).  Few, or of few columns: 2048-column chunks, for workgroups enough and few
+  // idle threads (5600 x 500 BF16: 19 us, 36 by 512 threads).
   const auto items = [a](ProcShape s) {
     const int64_t cols = (int64_t)s.t * s.u * kG;
     return a->N * ((a->V + cols - 1) / cols);
   };
-  a->shape = items(kProcMany) >= 8192 ? 0 : items(kProcSome) >= 512 ? 1 : 2;
+  const bool one_chunk = a->V <= kProcMany.t * kProcMany.u * kG;  // a row of it
+  a->shape = a->V <= kProcFew.t * kProcFew.u * kG                 ? 2
+             : items(kProcMany) >= (one_chunk ? 512 : 8192)       ? 0
+             : items(kProcSome) >= 512                            ? 1
+                                                                  : 2;
   const ProcShape s = a->shape == 0 ? kProcMany : a->shape == 1 ? kProcSome : kProcFew;
   const int64_t most = (int64_t)s.t * s.u * kG;
   a->chunks = (a->V + most - 1) / most;
