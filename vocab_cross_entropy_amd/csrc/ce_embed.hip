@@ -506,7 +506,7 @@ __global__ __launch_bounds__(kT) void k_embed_direct(EmbedGradArgs a, int64_t co
       zero_rows(a, v0, named);
       continue;
     }
-    const uint32_t n = (uint32_t)(b / col_blocks);
+    const uint32_t n = (uint32_t)b / (uint32_t)col_blocks;  // (sum_blocks is at most kDirectBlocks)
 #pragma unroll
     for (int k = 0; k < M; ++k)
       if ((uint32_t)(w * M + k) * 64 + lane == n) mine = key[k];
@@ -634,11 +634,13 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
     }
     int sub = (int)threadIdx.x >> s.lanes_shift;
     if constexpr (UNI) sub = __builtin_amdgcn_readfirstlane(sub);
-    const int64_t unit = b * (kT >> s.lanes_shift) + sub;
-    const int64_t t = unit / s.col_blocks, cb = unit - t * s.col_blocks;
+    // (32 bits: a unit has 4 KiB of partial sums in the workspace)
+    const uint32_t unit = (uint32_t)b * (uint32_t)(kT >> s.lanes_shift) + (uint32_t)sub;
+    const uint32_t cb = unit % (uint32_t)s.col_blocks;
+    const int64_t t = unit / (uint32_t)s.col_blocks;
     const uint32_t lanes = 1u << s.lanes_shift;
     uint32_t j[2];
-    j[0] = (uint32_t)cb * lanes * kG + (threadIdx.x & (lanes - 1)) * 4;
+    j[0] = cb * lanes * kG + (threadIdx.x & (lanes - 1)) * 4;
     j[1] = j[0] + lanes * 4;
     if (t >= s.tiles) continue;
     uint32_t i0 = (uint32_t)(t * s.tile), i1 = (uint32_t)min64((int64_t)i0 + s.tile, a.N);

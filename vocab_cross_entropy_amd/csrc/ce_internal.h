@@ -282,7 +282,8 @@ struct NormArgs {
   uint8_t* q;                 // e4m3 output, or NULL
   int64_t q_ld;
   float* scales;              // [N, ceil(D / group)]
-  int32_t group;              // columns per scale; 0: the row
+  int32_t group, group_shift; // columns per scale, a power of two, and its logarithm; 0: the row
+  int64_t groups;             // scales per row
   char* sum;                  // x + residual, or NULL
   int64_t sum_ld;
 };

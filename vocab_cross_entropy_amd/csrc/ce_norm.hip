@@ -159,7 +159,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < kG; ++e) v[p][e] *= inv;
             store_fp8(a.q + r * a.q_ld, j, D, pack_fp8(v[p]));
-            if (j % a.group == 0) a.scales[r * ((D + a.group - 1) / a.group) + j / a.group] = sc;
+            if ((j & (a.group - 1)) == 0) a.scales[r * a.groups + (j >> a.group_shift)] = sc;
           }
         } else {
           top[0] = fmaxf(top[0], m);
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(1024) void k_norm_wide(NormArgs a) {
         for (int e = 0; e < kG; ++e) v[e] *= inv;
         if (j < D) {
           store_fp8(a.q + r * a.q_ld, j, D, pack_fp8(v));
-          if (a.group && j % a.group == 0) a.scales[r * ((D + a.group - 1) / a.group) + j / a.group] = sc;
+          if (a.group && (j & (a.group - 1)) == 0) a.scales[r * a.groups + (j >> a.group_shift)] = sc;
         }
       } else {
         if (j < D) store_group<DT>(a.y + r * a.y_ld * EB, j, D, f32_to_raw<DT>(v));

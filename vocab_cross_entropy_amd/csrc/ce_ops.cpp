@@ -118,6 +118,7 @@ ce_status process(const ce_logits* x, const ce_logits* out, const ce_process* p,
   a.signs_ld = p->signs_ld;
   if (a.N == 0) return CE_OK;
   vce::process_plan(&a);
+  if (a.chunks > 0xffffffffLL / a.N) return ofail(CE_EINVAL, "more than 2^32-1 chunks of columns");
   hipEvent_t e0, e1;
   vce::profile_next(&e0, &e1);
   return launched(vce::launch_process(a, backward, stream, e0, e1), backward ? "process backward" : "process");
@@ -179,6 +180,8 @@ ce_status norm(const ce_norm* n, void* y, int64_t y_ld, void* q, int64_t q_ld, i
   a.q_ld = q_ld;
   a.scales = scales;
   a.group = group;
+  a.group_shift = group == 32 ? 5 : group == 64 ? 6 : 7;
+  a.groups = group ? (n->D + group - 1) / group : 1;
   a.sum = static_cast<char*>(sum);
   a.sum_ld = sum_ld;
   return launched(vce::launch_norm(a, stream), "norm launch");

@@ -81,11 +81,26 @@ __device__ __forceinline__ uint32_t occurrences(const char* tab, uint32_t col) {
     return reinterpret_cast<const uint32_t*>(tab)[col] & 0x7fffffffu;
 }
 
+// FP32: a lane's eight columns are two 16-byte words, and lanes reading their own
+// would leave holes that a second access of the same lines fills.  So a wave reads
+// (and writes) its 512 columns as two runs of 256, four columns a lane, and
+// neighbouring lanes swap halves: the even one ends up with eight columns of the
+// first run, the odd one of the second.  It is its own inverse.
+__device__ __forceinline__ void swap_halves(u32x4v (&w)[2]) {
+  const bool odd = threadIdx.x & 1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int got = __builtin_amdgcn_update_dpp(0, (int)(odd ? w[0][e] : w[1][e]), kSwap1, 0xf, 0xf, true);
+    w[0][e] = odd ? (uint32_t)got : w[0][e];
+    w[1][e] = odd ? w[1][e] : (uint32_t)got;
+  }
+}
+
 // One chunk: U groups of eight columns for each of T threads.
 template <int DT, int HIST, bool BWD, int T, int U>
-__device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, uint32_t chunk, char* smem) {
+__device__ __forceinline__ void process_item(const ProcessArgs& a, uint32_t r, uint32_t chunk, char* smem) {
   constexpr int EB = VecT<DT>::EB;
-  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const int64_t i0 = r / (uint32_t)a.d1, i1 = r % (uint32_t)a.d1;
   const uint32_t V = (uint32_t)a.V;
   const uint32_t lo = chunk * (uint32_t)a.chunk_cols;
   const uint32_t hi = V - lo < (uint32_t)a.chunk_cols ? V : lo + (uint32_t)a.chunk_cols;
@@ -93,23 +108,38 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
   const char* x = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   char* z = a.z + (i0 * a.zs0 + i1 * a.zs1) * EB;
 
+  // this thread's group in step u, and where its wave's 512 columns start
+  const uint32_t lane = tid & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
+  const auto start = [=](int u) { return lo + u * T * kG + wave * 512; };
+  const auto column = [=](int u) {
+    return DT == CE_F32 ? start(u) + (lane & 1) * 256 + (lane >> 1) * kG : lo + (u * T + tid) * kG;
+  };
+  // FP32: whether the wave reads runs and swaps (all of its columns are there)
+  const auto runs = [=](int u) { return DT == CE_F32 && start(u) + 512 <= hi; };
   Raw<DT> raw[U];
   const uint32_t whole = V & ~7u;  // columns in whole groups
   if (whole) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = fetch_whole<DT>(x, lo + (u * T + tid) * kG, whole);
+    for (int u = 0; u < U; ++u) {
+      if constexpr (DT == CE_F32) {
+        const uint32_t j = column(u) < whole ? column(u) : 0;
+        raw[u].w[0] = fetch_quad<CE_F32>(x, runs(u) ? start(u) + lane * 4 : j);
+        raw[u].w[1] = fetch_quad<CE_F32>(x, runs(u) ? start(u) + 256 + lane * 4 : j + 4);
+      } else {
+        raw[u] = fetch_whole<DT>(x, column(u), whole);
+      }
+    }
   }
   const uint8_t* mask = a.mask ? reinterpret_cast<const uint8_t*>(a.mask + i0 * a.ms0 + i1 * a.ms1) : nullptr;
-  uint8_t* signs = a.signs ? a.signs + r * a.signs_ld : nullptr;
-  // BF16: the groups' mask bits and signs, a byte each, go out with the columns (4096 x 32000: 107 against 125 us, the
-  // gradient 106 against 141; FP32, with twice the bytes a column, lost: 228 against 211)
-  constexpr bool AHEAD = DT == CE_BF16;
+  uint8_t* signs = a.signs ? a.signs + (int64_t)r * a.signs_ld : nullptr;
+  // the groups' mask bits and signs, a byte each, go out with the columns (4096 x 32000 BF16: 107 against 125 us, the
+  // gradient 106 against 141; FP32 195 against 200 and 197 against 211)
   uint32_t allowed[U], up[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t j = lo + (u * T + tid) * kG, at = (j < hi ? j : lo) >> 3;
-    allowed[u] = AHEAD && mask ? mask[at] : 0u;
-    up[u] = AHEAD && BWD && HIST != kHistNone && signs ? signs[at] : 0u;
+    const uint32_t j = column(u), at = (j < hi ? j : lo) >> 3;
+    allowed[u] = mask ? mask[at] : 0u;
+    up[u] = BWD && HIST != kHistNone && signs ? signs[at] : 0u;
   }
   const float theta = a.repetition ? a.repetition[r] : 1.f;
   const float fr = a.frequency ? a.frequency[r] : 0.f;
@@ -150,7 +180,10 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t j = lo + (u * T + tid) * kG;
+    const uint32_t j = column(u);
+    if constexpr (DT == CE_F32) {
+      if (runs(u)) swap_halves(raw[u].w);
+    }
     if (j >= hi) continue;
     fix_tail<DT>(raw[u], x, j, whole, V);
     float v[kG];
@@ -164,10 +197,8 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
       }
     }
     if constexpr (HIST != kHistNone) {
-      // one seen column of each lane at a time: nearly every wave has a lane with one and few lanes have two, so
-      // the penalty's arithmetic for all eight columns cost more than the pass' memory traffic
+      // one seen column of each lane at a time: many waves have a lane with one, few lanes have two
       uint32_t seen = seen_columns<HIST>(smem, j - lo);
-      if constexpr (BWD && !AHEAD) up[u] = seen && signs ? signs[j >> 3] : 0u;
       while (seen) {
         const uint32_t bit = (uint32_t)__builtin_ctz(seen);
         seen &= seen - 1;
@@ -196,25 +227,36 @@ __device__ __forceinline__ void process_item(const ProcessArgs& a, int64_t r, ui
 #pragma unroll
     for (int e = 0; e < kG; ++e) v[e] *= rt;
     if (mask) {
-      if constexpr (!AHEAD) allowed[u] = mask[j >> 3];
       const float off = BWD ? 0.f : -__builtin_inff();
 #pragma unroll
       for (int e = 0; e < kG; ++e) v[e] = (allowed[u] >> e) & 1u ? v[e] : off;
     }
-    store_group<DT, true>(z, j, V, f32_to_raw<DT>(v));
+    Raw<DT> out = f32_to_raw<DT>(v);
+    if constexpr (DT == CE_F32) {
+      if (runs(u)) {
+        swap_halves(out.w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          __builtin_nontemporal_store(out.w[h], reinterpret_cast<u32x4_a4*>(z + (start(u) + h * 256 + lane * 4) * 4));
+        continue;
+      }
+    }
+    store_group<DT, true>(z, j, V, out);
   }
 }
 
 template <int DT, int HIST, bool BWD, int T, int U>
 __global__ __launch_bounds__(T) void k_process(ProcessArgs a) {
   __shared__ __align__(16) char smem[HIST == kHistNone ? 16 : T * U * kG * (HIST == kHist16 ? 2 : 4)];
-  const int64_t items = a.N * a.chunks;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t r = it / a.chunks;
+  // (32-bit divisions: 64-bit ones delay the first load by hundreds of cycles)
+  const uint32_t chunks = (uint32_t)a.chunks, items = (uint32_t)a.N * chunks;
+  for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const uint32_t r = it / chunks;
     if constexpr (HIST != kHistNone) __syncthreads();  // the last item's counts have been read
     // a row's chunks in an order that shifts from row to row: workgroups go to the 8 XCDs in turn, and with 8 chunks a
     // row one XCD would get the chunk of the frequent tokens of every row (8192 x 128000 BF16: 858 us)
-    process_item<DT, HIST, BWD, T, U>(a, r, (uint32_t)((it + r) % a.chunks), smem);
+    process_item<DT, HIST, BWD, T, U>(a, r, (it + r % chunks) % chunks, smem);
+    if (items - it <= gridDim.x) break;
   }
 }
 
