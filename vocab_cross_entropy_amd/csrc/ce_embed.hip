@@ -8,9 +8,9 @@
 // Gradient: every row of dout is read once and every row of dW that a token
 // names is written once (read once too when it is added to).  Few tokens take one
 // launch: each token's workgroups look through all ids and, if its own has not
-// come before, add up the rows of that id.  With more tokens, to make the sum's order fixed and its writes few, they are sorted by id
-// first, ties by position (a stable sort of N small keys, little beside the N rows
-// of D values):
+// come before, add up the rows of that id.  With more tokens, to make the sum's
+// order fixed and its writes few, they are sorted by id first, ties by position (a
+// stable sort of N small keys, little beside the N rows of D values):
 //   up to kRankMax tokens whose (id, position) pair fits 32 bits: one launch in
 //     which each token's place is the count of smaller pairs (N^2 compares of LDS
 //     words, N^2 / 16384 cycles of the whole chip);
@@ -180,10 +180,15 @@ __global__ __launch_bounds__(kT) void k_sort_count(EmbedGradArgs a, SortPass s) 
   for (int i = (int)threadIdx.x; i < bins; i += kT) h[i] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * kSortTile, hi = min64(lo + kSortTile, a.N);
-  for (int64_t n = lo + (int)threadIdx.x; n < hi; n += kT) {
-    const uint32_t key = s.key_in ? s.key_in[n] : token_key(a, n);
-    atomicAdd(&h[(key >> s.shift) & (bins - 1)], 1u);
+  uint32_t key[kSortTile / kT];
+#pragma unroll
+  for (int k = 0; k < kSortTile / kT; ++k) {
+    const int64_t n = min64(lo + k * kT + (int)threadIdx.x, hi - 1);
+    key[k] = s.key_in ? s.key_in[n] : token_key(a, n);
   }
+#pragma unroll
+  for (int k = 0; k < kSortTile / kT; ++k)
+    if (lo + k * kT + (int)threadIdx.x < hi) atomicAdd(&h[(key[k] >> s.shift) & (bins - 1)], 1u);
   __syncthreads();
   for (int i = (int)threadIdx.x; i < bins; i += kT) s.hist[(int64_t)i * s.tiles + blockIdx.x] = h[i];
 }
@@ -240,11 +245,13 @@ __global__ __launch_bounds__(kT) void k_sort_move(EmbedGradArgs a, SortPass s) {
   uint32_t key[ROUNDS], idx[ROUNDS];
 #pragma unroll
   for (int k = 0; k < ROUNDS; ++k) {
-    const int64_t n = lo + k * 64 + lane;
-    key[k] = n < a.N ? (s.key_in ? s.key_in[n] : token_key(a, n)) : 0u;
-    idx[k] = n < a.N ? (s.idx_in ? s.idx_in[n] : (uint32_t)n) : 0u;
-    if (n < a.N) atomicAdd(&next[w][(key[k] >> s.shift) & (bins - 1)], 1u);
+    const int64_t n = min64(lo + k * 64 + lane, a.N - 1);
+    key[k] = s.key_in ? s.key_in[n] : token_key(a, n);
+    idx[k] = s.idx_in ? s.idx_in[n] : (uint32_t)n;
   }
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k)
+    if (lo + k * 64 + lane < a.N) atomicAdd(&next[w][(key[k] >> s.shift) & (bins - 1)], 1u);
   __syncthreads();
   for (int i = (int)threadIdx.x; i < bins; i += kT) {
     uint32_t at = s.hist[(int64_t)i * s.tiles + blockIdx.x];
