@@ -441,8 +441,8 @@ typedef struct ce_process {
                              vocabulary indices; any outside this buffer's columns (padding, another shard's)
                              count nowhere */
   int64_t history_s0, history_s1;
-  int64_t history_max;    /* tokens of the longest row, below 2^31; every row has this many readable (the width of
-                             `history`), whatever its history_len */
+  int64_t history_max;    /* tokens of the longest row (the width of `history`), below 2^31; a row's tokens past its
+                             history_len are not read */
   const int32_t* history_len; /* [N] tokens of row r, taken into [0, history_max]; NULL: history_max */
   const int32_t* prompt_len;  /* [N] how many of them, the first ones, are the prompt's; NULL: 0 */
   const float* repetition;    /* [N], > 0; penalties need a history (CE_EINVAL) */
@@ -523,7 +523,7 @@ ce_status ce_embedding_backward(const ce_embedding_desc* m, const void* dout, in
  *   s = x + residual,  y = s (mean_j s_j^2 + eps)^(-1/2) weight
  * in FP32, y and the written s rounded once each (y is formed from s before
  * its rounding).  Squares are FP32: a row whose mean square exceeds FP32 comes
- * out 0, and a row holding a NaN comes out NaN.  Rows of at most 32768 columns
+ * out 0 (NaN where it is infinite), and a row holding a NaN comes out NaN.  Rows of at most 32768 columns
  * (CE_ELAYOUT).
  */
 typedef struct ce_norm {

@@ -220,6 +220,24 @@ def test_autograd_forms():
                 assert_within(f64(a.grad), g, 200 * U * (np.abs(g) + np.abs(g).max()), f"{use} {name}")
 
 
+def test_expanded_inputs():
+    """A residual (and an input) broadcast over the rows: the same values, and their gradients summed."""
+    x, r, w = _rand((5, 40), torch.float32, 1), _rand((40,), torch.float32, 2), _rand((40,), torch.float32, 3)
+    c = _rand((5, 40), torch.float32, 4).cuda()
+    for swap in (False, True):
+        grads = []
+        for dense in (False, True):
+            xd, rd = x.cuda().requires_grad_(), r.cuda().requires_grad_()
+            re = rd.expand(5, 40).contiguous() if dense else rd.expand(5, 40)
+            y, s = vce.rms_norm(re, w.cuda(), xd) if swap else vce.rms_norm(xd, w.cuda(), re)
+            ((y + s) * c).sum().backward()
+            grads.append((y.detach(), xd.grad, rd.grad))
+        for a, b in zip(*grads):
+            assert torch.equal(a, b)
+    one = vce.rms_norm(r.cuda().expand(3, 40), w.cuda())
+    assert torch.equal(one[0], one[2])
+
+
 def test_gradient_against_differences():
     N, D = 4, 96
     s, w, c = _rand((N, D), torch.float32, 1), _rand((D,), torch.float32, 2), _rand((N, D), torch.float32, 3)

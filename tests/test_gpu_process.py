@@ -1,10 +1,13 @@
 """Logit processing and its gradient against the 64-bit definition."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import vocab_cross_entropy_amd as vce
 from gpu_util import say
+from vocab_cross_entropy_amd import _abi
 from ops_util import (U, allowed_columns, assert_within, f64, half_step, history_counts, ref_process,
                       ref_process_grad)
 
@@ -270,6 +273,39 @@ def test_process_logits_leaves_its_input_and_takes_any_gradient():
     assert torch.equal(first, x.grad)
     z = vce.process_logits(x.transpose(0, 1), temperature=steps["temperature"])
     assert z.shape == (3, 2, 300)
+    wide = vce.process_logits(x[:1].expand(2, 3, 300), temperature=steps["temperature"])
+    assert torch.equal(wide[1], vce.process_logits(x[:1], temperature=steps["temperature"][3:])[0])
+
+
+def test_processed_cross_entropy_refuses_before_it_writes():
+    s = _dev(_inputs(2, 3, 70, torch.float32, 10, seed=1))
+    x, before = s.pop("x"), None
+    before = x.clone()
+    good = torch.zeros((2, 3), dtype=torch.int64, device="cuda")
+    for target, kw in ((good[:1], {}), (good.int(), {}), (good.cpu(), {}), (None, {}), (good, dict(label_smoothing=2.0)),
+                       (good, dict(smoothing="some")), (good, dict(reduce_loss="avg"))):
+        with pytest.raises(vce.CeArgumentError):
+            vce.processed_cross_entropy(x, target, **kw, **s)
+    assert torch.equal(x, before)
+
+
+def test_tokens_past_the_length_are_not_read():
+    """Rows of a history laid end to end: the last row's tokens end with the buffer, its width is another row's."""
+    V = 100
+    flat = torch.randint(0, V, (13,), generator=_gen(1)).cuda()  # (torch refuses the view: the C descriptor allows it)
+    x = torch.randn((1, 2, V), generator=_gen(2)).cuda()
+    want = x.clone()
+    n = torch.tensor([10, 3], dtype=torch.int32).cuda()
+    pen = torch.full((2,), 0.5, device="cuda")
+    xd = vce.logits_desc(x)
+    p = _abi.CeProcess(flat.data_ptr(), 0, 10, 10, n.data_ptr(), None, None, pen.data_ptr(), None, None, None, 0, 0,
+                       None, 0, 0, None, 0)
+    say("[process] rows end to end")
+    assert vce.lib.ce_logits_process(ctypes.byref(xd), ctypes.byref(xd), ctypes.byref(p),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    for r, tokens in ((0, flat[:10]), (1, flat[10:])):
+        want[0, r] -= 0.5 * torch.bincount(tokens, minlength=V)
+    assert torch.allclose(x, want, rtol=0, atol=1e-6)
 
 
 @pytest.mark.parametrize("reduce", ["none", "mean", "sum"])

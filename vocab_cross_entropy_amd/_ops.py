@@ -12,8 +12,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from . import (CeArgumentError, _check, _device_of, _need, _raw_stream, _workspace, ce_fwd_bwd_fused,
-               ce_scale_grad_inplace, lib, linear_cross_entropy, reduction_code)
+from . import (CeArgumentError, _check, _device_of, _need, _need_targets, _raw_stream, _workspace,
+               ce_fwd_bwd_fused, ce_scale_grad_inplace, ce_workspace_bytes, lib, linear_cross_entropy, reduction_code)
 
 __all__ = [
     "ce_logits_process", "ce_logits_process_backward", "logits_signs", "process_logits", "processed_cross_entropy",
@@ -183,10 +183,10 @@ def _constants(**steps):
             _einval(f"{name} is a constant of the processing and gets no gradient (it requires one)")
 
 
-def _grad_rows(g: torch.Tensor) -> torch.Tensor:
-    """An incoming gradient the kernels can read: contiguous columns, rows of their own."""
-    ok = g.stride(-1) == 1 and all(n <= 1 or s >= g.shape[-1] for n, s in zip(g.shape[:-1], g.stride()[:-1]))
-    return g if ok and g.shape[-1] > 0 else g.contiguous()
+def _own_rows(t: torch.Tensor) -> torch.Tensor:
+    """``t`` as the kernels can read it: contiguous columns, rows of their own (an expanded tensor is copied)."""
+    ok = t.stride(-1) == 1 and all(n <= 1 or s >= t.shape[-1] for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    return t if ok and t.shape[-1] > 0 else t.contiguous()
 
 
 class ProcessLogits(torch.autograd.Function):
@@ -196,7 +196,8 @@ class ProcessLogits(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask, temperature):
         signs = logits_signs(x) if repetition is not None and ctx.needs_input_grad[0] else None
-        z = ce_logits_process(x.detach(), out=torch.empty_like(x), history=history, history_len=history_len,
+        x = _own_rows(x.detach())
+        z = ce_logits_process(x, out=torch.empty_like(x), history=history, history_len=history_len,
                               prompt_len=prompt_len, repetition=repetition, presence=presence, frequency=frequency,
                               bias=bias, mask=mask, temperature=temperature, signs=signs)
         ctx.save_for_backward(signs, history, history_len, prompt_len, repetition, mask, temperature)
@@ -208,7 +209,7 @@ class ProcessLogits(torch.autograd.Function):
         signs, history, history_len, prompt_len, repetition, mask, temperature = ctx.saved_tensors
         if repetition is None:
             history = history_len = prompt_len = None
-        dz = _grad_rows(dz)
+        dz = _own_rows(dz)
         dx = ce_logits_process_backward(dz, out=torch.empty_like(dz), signs=signs, history=history,
                                         history_len=history_len, prompt_len=prompt_len, repetition=repetition,
                                         mask=mask, temperature=temperature)
@@ -233,11 +234,17 @@ class ProcessedCrossEntropy(torch.autograd.Function):
     def forward(ctx, inp, target, label_smoothing, reduce_loss, ignore_idx, smoothing, history, history_len,
                 prompt_len, repetition, presence, frequency, bias, mask, temperature):
         buf = inp.detach()
+        # the loss's own checks come first: a refused call leaves the logits as they are
+        if buf.dim() != 3:
+            _einval("logits must be a 3-d (d0, d1, V) tensor")
+        _need_targets(torch.device("cuda", _index(buf, "logits")), target, buf.shape[0], buf.shape[1])
+        ws = _workspace(ce_workspace_bytes(buf, label_smoothing, reduce_loss, ignore_idx, smoothing=smoothing),
+                        buf.device)
         signs = logits_signs(buf) if repetition is not None else None
         ce_logits_process(buf, history=history, history_len=history_len, prompt_len=prompt_len,
                           repetition=repetition, presence=presence, frequency=frequency, bias=bias, mask=mask,
                           temperature=temperature, signs=signs)
-        loss, _ = ce_fwd_bwd_fused(buf, target, label_smoothing, reduce_loss, ignore_idx, smoothing=smoothing)
+        loss, _ = ce_fwd_bwd_fused(buf, target, label_smoothing, reduce_loss, ignore_idx, smoothing=smoothing, ws=ws)
         if repetition is None:
             history = history_len = prompt_len = None
         if repetition is not None or mask is not None or temperature is not None:
@@ -366,7 +373,7 @@ def embedding(ids, weight, scale=1.0, *, padding_idx=None, grad_buffer=None, voc
     """``scale * weight[ids]`` for int64 ``ids`` of any shape; reaches autograd through Embedding (the FP32
     gradient, which autograd casts to the weight's dtype).  With ``grad_buffer``, an FP32 [V, D] tensor, the
     backward adds the gradient to it instead and ``weight.grad`` stays as it is: with a tied head, the buffer that
-    ce_linear_cross_entropy adds its dw to."""
+    ce_linear_cross_entropy adds its dw to.  (A weight that requires no gradient has none in either.)"""
     if grad_buffer is not None:
         _rows(_index(weight, "weight"), "grad_buffer", grad_buffer, weight.shape, torch.float32)
     return Embedding.apply(weight, ids, scale, padding_idx, grad_buffer, vocab_start, vocab_total)
@@ -473,8 +480,8 @@ class RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         D = x.shape[-1]
-        flat = x.reshape(-1, D)
-        y, total = ce_rms_norm(flat, weight, None if residual is None else residual.reshape(-1, D), eps)
+        flat = _own_rows(x.reshape(-1, D))
+        y, total = ce_rms_norm(flat, weight, None if residual is None else _own_rows(residual.reshape(-1, D)), eps)
         ctx.eps = eps
         ctx.set_materialize_grads(False)
         if residual is None:
@@ -493,9 +500,9 @@ class RmsNorm(torch.autograd.Function):
         D = s.shape[-1]
 
         def flat(t):
-            return None if t is None else _grad_rows(t.reshape(-1, D))
+            return None if t is None else _own_rows(t.reshape(-1, D))
 
-        dx, dweight = ce_rms_norm_backward(flat(dy), s.reshape(-1, D), weight, ctx.eps, dsum=flat(dsum),
+        dx, dweight = ce_rms_norm_backward(flat(dy), flat(s), weight, ctx.eps, dsum=flat(dsum),
                                            want_dx=ctx.needs_input_grad[0] or ctx.needs_input_grad[2],
                                            want_dweight=ctx.needs_input_grad[1])
         dx = None if dx is None else dx.view(s.shape)

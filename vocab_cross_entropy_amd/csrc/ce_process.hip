@@ -14,9 +14,11 @@
 // the history is a count per column.  A workgroup owns a chunk of one row's
 // columns: it issues the loads of all its columns, counts the row's tokens that
 // fall into the chunk in LDS (integer atomics, whose order cannot change the
-// result) while the columns arrive, and then processes and writes them.  Every chunk of a row reads the row's history, from L2.  Counts take
-// 16 bits with the prompt flag in the top one while the history holds at most
-// 32767 tokens, and 32 bits beyond.
+// result) while the columns arrive, and then processes and writes them.  Every
+// chunk of a row reads the row's history, from L2.  Counts take 16 bits with the
+// prompt flag in the top one while the history holds at most 32767 tokens, and 32
+// bits beyond.  8192 x 128000 BF16 with the prefixes of 2048 tokens: 733 us, 5.7
+// TB/s of the 6.0 that a copy reaches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
