@@ -105,6 +105,18 @@ def test_gradient(N, V, D, kind, dtype):
         assert torch.equal(acc.cpu()[untouched], base[untouched])
 
 
+# rows of several units and of partial quads, with runs shorter and longer than a unit's tokens, in both forms of the sum
+MORE = [(1500, 700, 515, "tail"), (2000, 64, 1030, "pairs"), (1100, 3, 1027, "uniform"), (2500, 2500, 257, "uniform"),
+        (1025, 40, 128, "tail"), (3000, 150, 129, "runs"), (7200, 40, 1027, "tail"), (29000, 1200, 257, "runs"),
+        (7400, 2, 1001, "pairs"), (66000, 900, 131, "tail"), (70000, 3, 6, "uniform"), (65537, 65537, 4, "runs")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,V,D,kind", MORE, ids=lambda v: str(v))
+def test_gradient_units(N, V, D, kind, dtype):
+    test_gradient(N, V, D, kind, dtype)
+
+
 def test_gradient_strides_shards_and_bad_ids():
     N, V, D = 500, 64, 30
     ids = torch.randint(-20, V + 20, (N,), generator=_gen(5))

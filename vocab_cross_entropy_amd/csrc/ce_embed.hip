@@ -388,8 +388,9 @@ struct SumArgs {
   float* parts;            // [2 tiles][D]: a tile's share of a long run from the tile before, of one into the next
   uint32_t* starts;        // [tiles] 1 where a long run starts, else 0
   int64_t tiles, tile;     // tokens per tile
-  int64_t col_blocks;      // units across a row: a unit is a tile's tokens over 8 << lanes_shift columns
-  int lanes_shift;
+  int64_t col_blocks;      // k_embed_sum's units across a row: a unit is a tile's tokens over 512 columns
+  bool narrow;
+  int lanes_shift;         // k_embed_narrow: lanes of a row
   int64_t fill_blocks;     // workgroups that write the rows no token names (0 when dW is added to)
 };
 constexpr int kFillRows = 8;  // (32: 72 against 68 us on 20011 x 1037 FP32 tokens, 32000 rows)
@@ -426,6 +427,59 @@ __device__ __forceinline__ bool long_run(const SumArgs& s, uint32_t N, uint32_t 
   const uint32_t back = run_from<UNI, false>(s, N, b, key, tile);
   *ahead = run_from<UNI, true>(s, N, b, key, tile);
   return back + *ahead > tile;
+}
+
+// Where a tile's work begins and ends: [i0, i1) without the share of a run from the tile before that is short (it is
+// that tile's) and with the whole of a short one that it starts; and whether its first and last runs are shares of long
+// ones.  Tiles of 16 tokens, with 16 before and after: one load of a wave (5000 x 256 BF16 tokens: 25 against 27 us).
+struct TileRuns {
+  uint32_t i0, i1;
+  bool from_before, goes_on, one_run;
+};
+__device__ __forceinline__ TileRuns tile_runs(const SumArgs& s, uint32_t N, uint32_t none, int64_t t) {
+  TileRuns r;
+  r.i0 = (uint32_t)(t * s.tile);
+  r.i1 = (uint32_t)min64((int64_t)r.i0 + s.tile, N);
+  r.from_before = r.goes_on = false;
+  constexpr uint32_t kTT = (uint32_t)kTileTokens;
+  static_assert(kTT == 16, "windows of three tiles in a wave's lanes, in 16-bit fields");
+  if (s.tile == kTileTokens) {
+    const uint32_t len = r.i1 - r.i0;
+    const int64_t at = (int64_t)r.i0 - kTT + (threadIdx.x & 63);
+    const bool in = (threadIdx.x & 63) < 3 * kTT && at >= 0 && at < (int64_t)N;
+    const uint32_t key = s.skey[in ? at : (int64_t)r.i0];
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)key, kTT);
+    const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)key, (int)(kTT - 1 + len));
+    const uint64_t eq_first = __ballot(in && key == first), eq_last = __ballot(in && key == last);
+    const uint32_t back_in = (uint32_t)__popcll(eq_first & 0xffff);
+    const uint32_t ahead_in = (uint32_t)__popcll((eq_first >> kTT) & 0xffff);
+    const uint32_t back_out = (uint32_t)__popcll((eq_last >> len) & 0xffff);
+    const uint32_t ahead_out = (uint32_t)__popcll((eq_last >> (kTT + len)) & 0xffff);
+    if (back_in && first != none) {
+      r.from_before = back_in + ahead_in > kTT;
+      if (!r.from_before) r.i0 += ahead_in;
+    }
+    if (ahead_out && last != none) {
+      r.goes_on = back_out + ahead_out > kTT;
+      if (!r.goes_on) r.i1 += ahead_out;
+    }
+    r.one_run = first == last;
+    return r;
+  }
+  const uint32_t first = s.skey[r.i0], last = s.skey[r.i1 - 1];
+  const bool crosses_in = r.i0 > 0 && s.skey[r.i0 > 0 ? r.i0 - 1 : 0] == first && first != none;
+  const bool crosses_out = r.i1 < N && s.skey[r.i1 < N ? r.i1 : 0] == last && last != none;
+  uint32_t ahead;
+  if (crosses_in) {
+    r.from_before = long_run<true>(s, N, r.i0, first, &ahead);
+    if (!r.from_before) r.i0 += ahead;
+  }
+  if (crosses_out) {
+    r.goes_on = long_run<true>(s, N, r.i1, last, &ahead);
+    if (!r.goes_on) r.i1 += ahead;
+  }
+  r.one_run = first == last;
+  return r;
 }
 
 // Zeros in the rows v0 .. v0 + kFillRows - 1 of dW whose bit in `named` is not set:
@@ -621,14 +675,39 @@ hipError_t launch_direct(const EmbedGradArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The four columns from j on, in two steps so that a load waits for nothing: a row's last, partial quad (and any past
+// it) is loaded as the row's last four columns, and its columns are moved to the front when they are used (what is
+// behind them is never stored).  SHORT: rows of fewer than four columns.
+template <int DT, bool NT, bool SHORT>
+__device__ __forceinline__ u32x4v load_quad(const char* row, uint32_t j, uint32_t whole, uint32_t D) {
+  if constexpr (SHORT) return partial_quad<DT>(row, j, D);
+  else return fetch_quad<DT, NT>(row, j < whole ? j : D - 4);
+}
+template <int DT, bool SHORT>
+__device__ __forceinline__ u32x4v tail_quad(u32x4v w, uint32_t j, uint32_t whole, uint32_t D) {
+  if constexpr (!SHORT) {
+    const uint32_t n = j < whole ? 0u : D - whole;  // columns of a partial quad
+    if constexpr (DT == CE_F32) {
+      w.x = n == 1 ? w.w : n == 2 ? w.z : n == 3 ? w.y : w.x;
+      w.y = n == 2 ? w.w : n == 3 ? w.z : w.y;
+      w.z = n == 3 ? w.w : w.z;
+    } else {
+      const uint64_t v = ((uint64_t)w.y << 32 | w.x) >> (16 * ((4 - n) & 3));
+      w.x = (uint32_t)v;
+      w.y = (uint32_t)(v >> 32);
+    }
+  }
+  return w;
+}
+
 // A unit's tokens in batches: the batch's rows of dout, and the rows of dW
 // that its run ends add to, are all loaded before the first is used.  A lane
-// takes two quads of columns, half a unit apart.  UNI: a wave holds one unit (rows
-// of more than 256 columns), so that tokens, keys and row addresses are scalars.
+// takes two quads of columns, half a unit apart.  A wave holds one unit, so that
+// tokens, keys and row addresses are scalars (rows of more than kNarrow columns).
 // NT: dout is read with the non-temporal bit, where a wave's loads cover whole
 // cache lines (rows on 16-byte boundaries); where lines are shared by two loads it
 // has them fetched twice.
-template <int DT, bool UNI, bool NT>
+template <int DT, bool NT>
 __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
   constexpr int EB = VecT<DT>::EB;
   constexpr int B = 4;  // (8 took the registers of a third of the waves: 75 against 71 us)
@@ -639,66 +718,58 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
       fill_rows(a, s, b - sum_blocks);
       continue;
     }
-    int sub = (int)threadIdx.x >> s.lanes_shift;
-    if constexpr (UNI) sub = __builtin_amdgcn_readfirstlane(sub);
     // (32 bits: a unit has 4 KiB of partial sums in the workspace)
-    const uint32_t unit = (uint32_t)b * (uint32_t)(kT >> s.lanes_shift) + (uint32_t)sub;
+    const uint32_t unit = (uint32_t)b * kWaves + (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const uint32_t cb = unit % (uint32_t)s.col_blocks;
     const int64_t t = unit / (uint32_t)s.col_blocks;
-    const uint32_t lanes = 1u << s.lanes_shift;
     uint32_t j[2];
-    j[0] = cb * lanes * kG + (threadIdx.x & (lanes - 1)) * 4;
-    j[1] = j[0] + lanes * 4;
+    j[0] = cb * 512 + (threadIdx.x & 63) * 4;
+    j[1] = j[0] + 256;
     if (t >= s.tiles) continue;
-    uint32_t i0 = (uint32_t)(t * s.tile), i1 = (uint32_t)min64((int64_t)i0 + s.tile, a.N);
-    bool from_before = false, goes_on = false;  // shares of long runs
-    const uint32_t first = s.skey[i0], last = s.skey[i1 - 1];
-    const bool crosses_in = i0 > 0 && s.skey[i0 > 0 ? i0 - 1 : 0] == first && first != none;
-    const bool crosses_out = i1 < N && s.skey[i1 < N ? i1 : 0] == last && last != none;
-    if (crosses_in) {
-      uint32_t ahead;
-      from_before = long_run<UNI>(s, N, i0, first, &ahead);
-      if (!from_before) i0 += ahead;
-    }
-    if (crosses_out) {
-      uint32_t ahead;
-      goes_on = long_run<UNI>(s, N, i1, last, &ahead);
-      if (!goes_on) i1 += ahead;
-    }
+    const TileRuns run = tile_runs(s, N, none, t);
+    const uint32_t i0 = run.i0, i1 = run.i1;
+    bool from_before = run.from_before;
     if (j[0] >= D) continue;  // (only here: the lanes look for a run's end together)
-    if (j[0] == 0) s.starts[t] = goes_on && !(from_before && first == last);
+    if (j[0] == 0) s.starts[t] = run.goes_on && !(from_before && run.one_run);
     float acc[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
+    // a batch's keys and positions are loaded before the rows of the one before are used
+    uint32_t key[B + 1], idx[B], next_key[B], next_idx[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const uint32_t at = i0 + k < N ? i0 + k : N - 1;
+      next_key[k] = s.skey[at];
+      next_idx[k] = s.sidx[at];
+    }
     for (uint32_t i = i0; i < i1; i += B) {
-      uint32_t key[B + 1], idx[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
-        const uint32_t at = i + k < N ? i + k : N - 1;
-        key[k] = s.skey[at];
-        idx[k] = s.sidx[at];
+        key[k] = next_key[k];
+        idx[k] = next_idx[k];
+        const uint32_t at = i + B + k < N ? i + B + k : N - 1;
+        next_key[k] = s.skey[at];
+        next_idx[k] = s.sidx[at];
       }
-      key[B] = i + B < N ? s.skey[i + B] : 0xffffffffu;
+      key[B] = i + B < N ? next_key[0] : 0xffffffffu;
       if (key[0] == none) break;  // sorted: nothing with a gradient follows
       u32x4v row[B][2], old[B][2];
-      if (whole) {
 #pragma unroll
-        for (int k = 0; k < B; ++k)
+      for (int k = 0; k < B; ++k)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            row[k][h] = fetch_quad<DT, NT>(a.dout + (int64_t)idx[k] * a.dout_ld * EB, j[h] < whole ? j[h] : 0);
-      }
-      if (a.accumulate && whole) {
+        for (int h = 0; h < 2; ++h)
+          row[k][h] = load_quad<DT, NT, false>(a.dout + (int64_t)idx[k] * a.dout_ld * EB, j[h], whole, D);
+      if (a.accumulate) {
 #pragma unroll
-        for (int k = 0; k < B; ++k)
+        for (int k = 0; k < B; ++k) {
           if (i + k < i1 && key[k] != none && (i + k + 1 >= N || key[k + 1] != key[k])) {  // a run ends here
+            const char* dw = reinterpret_cast<const char*>(a.dw + (int64_t)key[k] * a.dw_ld);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              old[k][h] = fetch_quad<CE_F32>(reinterpret_cast<const char*>(a.dw + (int64_t)key[k] * a.dw_ld),
-                                             j[h] < whole ? j[h] : 0);
+            for (int h = 0; h < 2; ++h) old[k][h] = load_quad<CE_F32, false, false>(dw, j[h], whole, D);
           }
+        }
       }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
@@ -708,12 +779,8 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
           float* const part = s.parts + (2 * t + (from_before ? 0 : 1)) * a.D;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (j[h] >= whole && j[h] < D) {
-              row[k][h] = partial_quad<DT>(a.dout + (int64_t)idx[k] * a.dout_ld * EB, j[h], D);
-              if (a.accumulate && ends) old[k][h] = partial_quad<CE_F32>(reinterpret_cast<const char*>(dw), j[h], D);
-            }
             float f[4];
-            quad_to_f32<DT>(row[k][h], f);
+            quad_to_f32<DT>(tail_quad<DT, false>(row[k][h], j[h], whole, D), f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[h][e] += f[e];
             if (ends || i + k + 1 == i1) {
@@ -721,7 +788,7 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
                 if (j[h] < D) store_quad(part, j[h], D, acc[h]);
               } else {
                 float o[4];
-                quad_to_f32<CE_F32>(old[k][h], o);
+                quad_to_f32<CE_F32>(tail_quad<CE_F32, false>(old[k][h], j[h], whole, D), o);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   o[e] = a.accumulate ? __builtin_fmaf(acc[h][e], a.scale, o[e]) : acc[h][e] * a.scale;
@@ -735,6 +802,86 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
         }
       }
     }
+  }
+}
+
+// Rows of at most kNarrow columns: a unit is a sorted token over all columns, a quad a
+// lane, and works where a run starts (a short run, or a long one up to its tile's
+// end) or where a tile begins inside a long one.  One token's chain of loads is what
+// few tokens take, and short code: with a tile a unit and its tokens unrolled, most
+// of the time went to fetching instructions (1500 x 16 BF16 tokens: 21 us for this
+// launch alone).
+constexpr int64_t kNarrow = 128, kFewElems = 7 << 20;
+template <int DT, bool SHORT>
+__global__ __launch_bounds__(kT) void k_embed_narrow(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
+  constexpr int EB = VecT<DT>::EB;
+  constexpr int B = 4;
+  const uint32_t D = (uint32_t)a.D, whole = D & ~3u, N = (uint32_t)a.N, none = (uint32_t)a.V, T = (uint32_t)s.tile;
+  for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
+    if (b >= sum_blocks) {
+      __syncthreads();
+      fill_rows(a, s, b - sum_blocks);
+      continue;
+    }
+    const uint32_t unit = (uint32_t)b * (uint32_t)(kT >> s.lanes_shift) + (threadIdx.x >> s.lanes_shift);
+    const uint32_t i = unit / (uint32_t)s.col_blocks, cb = unit - i * (uint32_t)s.col_blocks;
+    const uint32_t j = cb * 256 + (threadIdx.x & ((1u << s.lanes_shift) - 1)) * 4;
+    if (i >= N) continue;
+    const uint32_t t = i / T, edge = t * T, end = N - edge < T ? N : edge + T;
+    const uint32_t key = s.skey[i], before = s.skey[i ? i - 1 : 0], last = s.skey[end - 1];
+    const uint32_t far = s.skey[N - i > T ? i + T : N - 1];
+    const bool starts = i == 0 || before != key, inside = !starts && i == edge;
+    bool is_long = starts && N - i > T && far == key;
+    if (inside) {
+      uint32_t ahead;
+      is_long = long_run<false>(s, N, i, key, &ahead);
+    }
+    // the first place of the tile's last run tells the join whether a long one starts
+    if (j == 0 && (starts || inside) && key == last) s.starts[t] = key != none && starts && is_long;
+    if (key == none || !(starts || (inside && is_long)) || j >= D) continue;
+    const uint32_t stop = is_long ? end : N - i < T ? N : i + T;
+    float* const to = is_long ? s.parts + (2 * (int64_t)t + (starts ? 1 : 0)) * a.D : a.dw + (int64_t)key * a.dw_ld;
+    const bool add = a.accumulate && !is_long;
+    u32x4v old = {0u, 0u, 0u, 0u};
+    if (a.accumulate) old = load_quad<CE_F32, false, SHORT>(reinterpret_cast<const char*>(to), j, whole, D);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t next_key[B], next_idx[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const uint32_t at = i + k < N ? i + k : N - 1;
+      next_key[k] = s.skey[at];
+      next_idx[k] = s.sidx[at];
+    }
+    for (uint32_t n = i;;) {
+      bool in[B];
+      u32x4v row[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        in[k] = n + k < stop && next_key[k] == key;
+        const int64_t idx = in[k] ? next_idx[k] : next_idx[0];  // past the run, its first row of this step again
+        row[k] = load_quad<DT, false, SHORT>(a.dout + idx * a.dout_ld * EB, j, whole, D);
+      }
+      n += B;
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const uint32_t at = n + k < N ? n + k : N - 1;
+        next_key[k] = s.skey[at];
+        next_idx[k] = s.sidx[at];
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        float f[4];
+        quad_to_f32<DT>(tail_quad<DT, SHORT>(row[k], j, whole, D), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = in[k] ? acc[e] + f[e] : acc[e];
+      }
+      if (n >= stop || next_key[0] != key) break;
+    }
+    float o[4];
+    quad_to_f32<CE_F32>(tail_quad<CE_F32, SHORT>(old, j, whole, D), o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = is_long ? acc[e] : add ? __builtin_fmaf(acc[e], a.scale, o[e]) : acc[e] * a.scale;
+    store_quad(to, j, D, o);
   }
 }
 
@@ -789,13 +936,14 @@ __global__ __launch_bounds__(kJoinT) void k_embed_join(EmbedGradArgs a, SumArgs 
 
 template <int DT>
 void launch_sum(const EmbedGradArgs& a, const SumArgs& s, int64_t sum_blocks, dim3 grid, hipStream_t stream) {
-  const bool nt = (uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0;
-  if (s.lanes_shift >= 6 && nt)
-    hipLaunchKernelGGL((k_embed_sum<DT, true, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
-  else if (s.lanes_shift >= 6)
-    hipLaunchKernelGGL((k_embed_sum<DT, true, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  if (a.D < 4)
+    hipLaunchKernelGGL((k_embed_narrow<DT, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else if (s.narrow)
+    hipLaunchKernelGGL((k_embed_narrow<DT, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else if ((uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0)
+    hipLaunchKernelGGL((k_embed_sum<DT, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else
-    hipLaunchKernelGGL((k_embed_sum<DT, false, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    hipLaunchKernelGGL((k_embed_sum<DT, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
 }
 
 // Workspace: sorted keys and positions (twice for the radix sort's passes), its counts, the partial sums.
@@ -899,11 +1047,13 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
   s.starts = reinterpret_cast<uint32_t*>(a.ws + g.starts);
   s.tiles = g.tiles;
   s.tile = g.tile;
-  s.lanes_shift = lanes_log2(ceil_div(a.D, kG));
-  if (s.lanes_shift > 6) s.lanes_shift = 6;  // at most a wave: a row's last unit wastes the fewest lanes
-  s.col_blocks = ceil_div(ceil_div(a.D, kG), (int64_t)1 << s.lanes_shift);
+  const bool narrow = a.D <= kNarrow || a.N * a.D <= kFewElems;
+  s.narrow = narrow;
+  s.lanes_shift = narrow ? (int)min64(lanes_log2(ceil_div(a.D, 4)), 6) : 0;
+  s.col_blocks = ceil_div(a.D, narrow ? 256 : 512);
   s.fill_blocks = a.accumulate ? 0 : ceil_div(a.V, kFillRows);
-  const int64_t sum_blocks = ceil_div(g.tiles * s.col_blocks, kT >> s.lanes_shift);
+  const int64_t sum_blocks =
+      narrow ? ceil_div(a.N * s.col_blocks, kT >> s.lanes_shift) : ceil_div(g.tiles * s.col_blocks, kWaves);
   const dim3 grid((uint32_t)min64(sum_blocks + s.fill_blocks, kMaxBlocks));
   if (a.dtype == CE_BF16)
     launch_sum<CE_BF16>(a, s, sum_blocks, grid, stream);
