@@ -117,6 +117,24 @@ def test_gradient_units(N, V, D, kind, dtype):
     test_gradient(N, V, D, kind, dtype)
 
 
+@pytest.mark.parametrize("N", [1, 200, 900, 1500, 9000, 66000])
+@pytest.mark.parametrize("V,D", [(1, 1), (9000, 1), (3001, 3), (700, 7), (333, 64), (211, 515), (41, 1037)])
+def test_rows_that_no_token_names(N, V, D):
+    """Zeros in every row no token names, whichever way they are written, and nothing before or behind dW."""
+    ids = torch.randint(0, V, (N,), generator=_gen(N)) // 3 * 3
+    dout = torch.ones((N, D), device="cuda", dtype=torch.bfloat16)
+    count = torch.bincount(ids, minlength=V).float()[:, None].expand(V, D)
+    say(f"[embed grad] fill {N} {V} {D}")
+    for ld in (D, D + 1):  # rows end to end, and with a gap
+        for first in (4, 5):  # on a 16-byte boundary, and off it
+            buf = torch.full((first + V * ld + 4,), -3.0, device="cuda")
+            dw = torch.as_strided(buf, (V, D), (ld, 1), first)
+            vce.ce_embedding_backward(dout, ids.cuda(), V, 1.0, dw=dw)
+            assert torch.equal(dw.cpu(), count)
+            dw.fill_(-3.0)
+            assert (buf == -3.0).all()
+
+
 def test_gradient_strides_shards_and_bad_ids():
     N, V, D = 500, 64, 30
     ids = torch.randint(-20, V + 20, (N,), generator=_gen(5))

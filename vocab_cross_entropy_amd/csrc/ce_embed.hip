@@ -392,6 +392,7 @@ struct SumArgs {
   bool narrow;
   int lanes_shift;         // k_embed_narrow: lanes of a row
   int64_t fill_blocks;     // workgroups that write the rows no token names (0 when dW is added to)
+  bool flat;               // they take dW as one array (fill_flat)
 };
 constexpr int kFillRows = 8;  // (32: 72 against 68 us on 20011 x 1037 FP32 tokens, 32000 rows)
 
@@ -509,6 +510,99 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t v0, ui
   }
 }
 
+// The same where dW's rows lie end to end from a 16-byte boundary on: a workgroup takes E values, whatever rows they
+// belong to, a quad a thread and step.  For rows of few columns (8 rows a workgroup against 8192 values a workgroup:
+// 3000 tokens in 120000 x 64 columns 56 and 20 us, 30000 in 120000 x 300 104 and 69, but 20011 in 32000 x 1037 76 and
+// 84), and for any with at most 256 tokens, then 4096 values (3 in 64703 x 4096: 186 and 164 us).
+constexpr int kFlatFew = 4096, kFlat = 8192;
+constexpr int64_t kFlatCols = 512;
+template <int E>
+struct FillShare {
+  uint32_t named[E / 32 + 2];  // a bit per row that the share touches
+  uint32_t any;
+};
+bool end_to_end(const EmbedGradArgs& a) { return (a.dw_ld == a.D || a.V == 1) && (uintptr_t)a.dw % 16 == 0; }
+// the rows of a share: the first one, and how many
+template <int E>
+__device__ __forceinline__ uint32_t fill_first(const EmbedGradArgs& a, int64_t block, uint32_t* count) {
+  const int64_t e0 = block * E, end = min64(e0 + E, a.V * a.D) - 1;
+  const uint32_t r0 = (uint32_t)(e0 / a.D);
+  *count = (uint32_t)(end / a.D) - r0 + 1;
+  return r0;
+}
+template <int E>
+__device__ __forceinline__ void fill_clear(FillShare<E>& f, uint32_t rows) {
+  for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kT) f.named[i] = 0;
+  if (threadIdx.x == 0) f.any = 0;
+}
+template <int E>
+__device__ __forceinline__ void fill_name(FillShare<E>& f, uint32_t row) {
+  atomicOr(&f.named[row >> 5], 1u << (row & 31));
+  f.any = 1;
+}
+template <int E>
+__device__ __forceinline__ void zero_share(const EmbedGradArgs& a, int64_t block, uint32_t r0, const FillShare<E>& f) {
+  const int64_t e0 = block * E;
+  const uint32_t count = (uint32_t)min64(E, a.V * a.D - e0), D = (uint32_t)a.D;
+  float* const p = a.dw + e0;
+  const u32x4v zero = {0u, 0u, 0u, 0u};
+  const bool any = f.any;
+  const auto unnamed = [&](uint32_t row) { return ((f.named[row >> 5] >> (row & 31)) & 1u) == 0; };
+  uint32_t col = (uint32_t)(e0 - (int64_t)r0 * a.D) + threadIdx.x * 4, row = col / D;
+  col -= row * D;
+  const uint32_t step_row = 4 * kT / D, step_col = 4 * kT - step_row * D;
+#pragma unroll 4
+  for (uint32_t at = threadIdx.x * 4; at < count; at += 4 * kT) {
+    if (at + 4 <= count && (!any || (col + 4 <= D && unnamed(row)))) {
+      *reinterpret_cast<u32x4v*>(p + at) = zero;
+    } else {
+      uint32_t r = row, c = col;
+      for (uint32_t e = 0; e < 4 && at + e < count; ++e) {
+        if (!any || unnamed(r)) p[at + e] = 0.f;
+        if (++c == D) {
+          c = 0;
+          ++r;
+        }
+      }
+    }
+    row += step_row;
+    col += step_col;
+    if (col >= D) {
+      col -= D;
+      ++row;
+    }
+  }
+}
+
+// The first sorted token with a key of at least v, by a wave: 64 places a step.
+__device__ __forceinline__ uint32_t lower_bound(const SumArgs& s, uint32_t N, uint32_t v) {
+  uint32_t lo = 0, n = N;  // it is one of lo .. lo + n
+  while (n > 0) {
+    const uint32_t step = (n + 63) / 64, at = lo + ((threadIdx.x & 63) + 1) * step - 1;  // the last of each part
+    const uint64_t less = __ballot(at < lo + n && s.skey[at < N ? at : N - 1] < v);
+    const uint32_t parts = (uint32_t)__popcll(less);  // parts that lie wholly before it
+    const uint32_t skip = parts * step < n ? parts * step : n;
+    lo += skip;
+    n = n - skip < step - 1 ? n - skip : step - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ void fill_flat(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
+  __shared__ FillShare<kFlat> f;
+  __shared__ uint32_t range[2];
+  uint32_t rows;
+  const uint32_t r0 = fill_first<kFlat>(a, block, &rows), N = (uint32_t)a.N;
+  fill_clear(f, rows);
+  if (threadIdx.x < 128) {
+    const uint32_t at = lower_bound(s, N, threadIdx.x < 64 ? r0 : r0 + rows);
+    if ((threadIdx.x & 63) == 0) range[threadIdx.x >> 6] = at;
+  }
+  __syncthreads();
+  for (uint32_t n = range[0] + threadIdx.x; n < range[1]; n += kT) fill_name(f, s.skey[n] - r0);
+  __syncthreads();
+  zero_share(a, block, r0, f);
+}
+
 // Rows of dW that no token names: a search of the sorted keys for each, zeros where it is not found.
 __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
   __shared__ uint32_t named;
@@ -535,7 +629,7 @@ __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, const SumArgs&
 constexpr int64_t kDirectMax = 1024, kDirectBlocks = 4096;
 template <int DT, int M>
 __global__ __launch_bounds__(kT) void k_embed_direct(EmbedGradArgs a, int64_t col_blocks, int64_t sum_blocks,
-                                                     int64_t blocks) {
+                                                     int64_t blocks, bool flat) {
   constexpr int EB = VecT<DT>::EB;
   constexpr int B = 4;
   // word w M + k, bit l: whether token (w M + k) 64 + l has the block's key, so wave w has a quarter in order
@@ -556,6 +650,20 @@ __global__ __launch_bounds__(kT) void k_embed_direct(EmbedGradArgs a, int64_t co
   for (int k = 0; k < M; ++k) key[k] = (uint32_t)(w * M + k) * 64 + lane < N ? key_of(a, id[k]) : none;
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     __syncthreads();  // what the last block left in LDS has been read
+    if (b >= sum_blocks && flat) {
+      constexpr int E = M == 1 ? kFlatFew : kFlat;
+      __shared__ FillShare<E> f;
+      uint32_t rows;
+      const uint32_t r0 = fill_first<E>(a, b - sum_blocks, &rows);
+      fill_clear(f, rows);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < M; ++k)
+        if (key[k] != none && key[k] - r0 < rows) fill_name(f, key[k] - r0);
+      __syncthreads();
+      zero_share(a, b - sum_blocks, r0, f);
+      continue;
+    }
     if (b >= sum_blocks) {
       const uint32_t v0 = (uint32_t)(b - sum_blocks) * kFillRows;
       if (t == 0) named = 0;
@@ -666,12 +774,14 @@ bool direct(int64_t N, int64_t D) { return N <= kDirectMax && N * ceil_div(D, 51
 template <int DT>
 hipError_t launch_direct(const EmbedGradArgs& a, hipStream_t stream) {
   const int64_t col_blocks = ceil_div(a.D, 512), sum_blocks = a.N * col_blocks;
-  const int64_t blocks = sum_blocks + (a.accumulate ? 0 : ceil_div(a.V, kFillRows));
+  const bool few = a.N <= kT, flat = end_to_end(a) && (few || a.D <= kFlatCols);
+  const int64_t fill = flat ? ceil_div(a.V * a.D, few ? kFlatFew : kFlat) : ceil_div(a.V, kFillRows);
+  const int64_t blocks = sum_blocks + (a.accumulate ? 0 : fill);
   const dim3 grid((uint32_t)min64(blocks, kMaxBlocks));
-  if (a.N <= kT)
-    hipLaunchKernelGGL((k_embed_direct<DT, 1>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks);
+  if (few)
+    hipLaunchKernelGGL((k_embed_direct<DT, 1>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks, flat);
   else
-    hipLaunchKernelGGL((k_embed_direct<DT, 4>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks);
+    hipLaunchKernelGGL((k_embed_direct<DT, 4>), grid, dim3(kT), 0, stream, a, col_blocks, sum_blocks, blocks, flat);
   return hipGetLastError();
 }
 
@@ -707,7 +817,7 @@ __device__ __forceinline__ u32x4v tail_quad(u32x4v w, uint32_t j, uint32_t whole
 // NT: dout is read with the non-temporal bit, where a wave's loads cover whole
 // cache lines (rows on 16-byte boundaries); where lines are shared by two loads it
 // has them fetched twice.
-template <int DT, bool NT>
+template <int DT, bool NT, bool FLAT>
 __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, int64_t sum_blocks) {
   constexpr int EB = VecT<DT>::EB;
   constexpr int B = 4;  // (8 took the registers of a third of the waves: 75 against 71 us)
@@ -715,7 +825,10 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
   for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
     if (b >= sum_blocks) {
       __syncthreads();
-      fill_rows(a, s, b - sum_blocks);
+      if constexpr (FLAT)
+        fill_flat(a, s, b - sum_blocks);
+      else
+        fill_rows(a, s, b - sum_blocks);
       continue;
     }
     // (32 bits: a unit has 4 KiB of partial sums in the workspace)
@@ -736,24 +849,15 @@ __global__ __launch_bounds__(kT) void k_embed_sum(EmbedGradArgs a, SumArgs s, in
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
-    // a batch's keys and positions are loaded before the rows of the one before are used
-    uint32_t key[B + 1], idx[B], next_key[B], next_idx[B];
-#pragma unroll
-    for (int k = 0; k < B; ++k) {
-      const uint32_t at = i0 + k < N ? i0 + k : N - 1;
-      next_key[k] = s.skey[at];
-      next_idx[k] = s.sidx[at];
-    }
     for (uint32_t i = i0; i < i1; i += B) {
+      uint32_t key[B + 1], idx[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
-        key[k] = next_key[k];
-        idx[k] = next_idx[k];
-        const uint32_t at = i + B + k < N ? i + B + k : N - 1;
-        next_key[k] = s.skey[at];
-        next_idx[k] = s.sidx[at];
+        const uint32_t at = i + k < N ? i + k : N - 1;
+        key[k] = s.skey[at];
+        idx[k] = s.sidx[at];
       }
-      key[B] = i + B < N ? next_key[0] : 0xffffffffu;
+      key[B] = i + B < N ? s.skey[i + B] : 0xffffffffu;
       if (key[0] == none) break;  // sorted: nothing with a gradient follows
       u32x4v row[B][2], old[B][2];
 #pragma unroll
@@ -820,7 +924,10 @@ __global__ __launch_bounds__(kT) void k_embed_narrow(EmbedGradArgs a, SumArgs s,
   for (int64_t b = blockIdx.x; b < sum_blocks + s.fill_blocks; b += gridDim.x) {
     if (b >= sum_blocks) {
       __syncthreads();
-      fill_rows(a, s, b - sum_blocks);
+      if (s.flat)
+        fill_flat(a, s, b - sum_blocks);
+      else
+        fill_rows(a, s, b - sum_blocks);
       continue;
     }
     const uint32_t unit = (uint32_t)b * (uint32_t)(kT >> s.lanes_shift) + (threadIdx.x >> s.lanes_shift);
@@ -940,10 +1047,12 @@ void launch_sum(const EmbedGradArgs& a, const SumArgs& s, int64_t sum_blocks, di
     hipLaunchKernelGGL((k_embed_narrow<DT, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else if (s.narrow)
     hipLaunchKernelGGL((k_embed_narrow<DT, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+  else if (s.flat)  // (not in the others: its registers cost 8192 x 4096 BF16, added to, 60 instead of 57 us)
+    hipLaunchKernelGGL((k_embed_sum<DT, false, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else if ((uintptr_t)a.dout % 16 == 0 && a.dout_ld % kG == 0)
-    hipLaunchKernelGGL((k_embed_sum<DT, true>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    hipLaunchKernelGGL((k_embed_sum<DT, true, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
   else
-    hipLaunchKernelGGL((k_embed_sum<DT, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
+    hipLaunchKernelGGL((k_embed_sum<DT, false, false>), grid, dim3(kT), 0, stream, a, s, sum_blocks);
 }
 
 // Workspace: sorted keys and positions (twice for the radix sort's passes), its counts, the partial sums.
@@ -1051,7 +1160,8 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream) {
   s.narrow = narrow;
   s.lanes_shift = narrow ? (int)min64(lanes_log2(ceil_div(a.D, 4)), 6) : 0;
   s.col_blocks = ceil_div(a.D, narrow ? 256 : 512);
-  s.fill_blocks = a.accumulate ? 0 : ceil_div(a.V, kFillRows);
+  s.flat = !a.accumulate && end_to_end(a) && a.D <= kFlatCols;
+  s.fill_blocks = a.accumulate ? 0 : s.flat ? ceil_div(a.V * a.D, kFlat) : ceil_div(a.V, kFillRows);
   const int64_t sum_blocks =
       narrow ? ceil_div(a.N * s.col_blocks, kT >> s.lanes_shift) : ceil_div(g.tiles * s.col_blocks, kWaves);
   const dim3 grid((uint32_t)min64(sum_blocks + s.fill_blocks, kMaxBlocks));
