@@ -58,6 +58,30 @@ __global__ __launch_bounds__(kT) void k_embed(EmbedArgs a, int lanes_shift) {
     char* out = a.out + n * a.out_ld * EB;
     if (v < (uint64_t)a.V) {
       const char* w = a.w + (int64_t)v * a.w_ld * EB;
+      if constexpr (DT == CE_F32) {
+        // quads, side by side across the lanes: with eight columns a lane every store leaves half of each line to the
+        // next one (12385 x 4096: 65 against 47 us)
+        const uint32_t whole = D & ~3u, step = (uint32_t)lanes * 4;
+        for (uint32_t at = (uint32_t)lane * 4; at < D; at += 2 * step) {
+          u32x4v q[2];
+          const uint32_t j[2] = {at, at + step};
+          if (whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) q[h] = fetch_quad<DT>(w, j[h] < whole ? j[h] : 0);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j[h] >= D) continue;
+            if (j[h] >= whole) q[h] = partial_quad<DT>(w, j[h], D);
+            float f[4];
+            quad_to_f32<DT>(q[h], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] *= a.scale;
+            store_quad<true>(reinterpret_cast<float*>(out), j[h], D, f);
+          }
+        }
+        continue;
+      }
       for (uint32_t j = (uint32_t)lane * kG; j < D; j += (uint32_t)lanes * kG) {
         float f[kG];
         load_f32<DT>(w, j, D, f);
