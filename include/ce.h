@@ -556,8 +556,9 @@ size_t ce_rms_norm_workspace_bytes(int64_t N, int64_t D);
 
 /*
  * The gradient, from the forward's written sum s as n->x (n->residual NULL):
- *   dx = rstd (dy weight) - s rstd^3 mean_j(dy weight s) + dsum     (also the residual's gradient)
- *   dweight (+)= sum over rows of dy s rstd
+ *   n = s rstd,  rstd = (mean_j s_j^2 + eps)^(-1/2)
+ *   dx = rstd (dy weight - n mean_j(dy weight n)) + dsum     (also the residual's gradient)
+ *   dweight (+)= sum over rows of dy n
  *   dsum     device [N, D], the gradient that reaches s by the residual stream, or NULL
  *   dx       device [N, D] in x's dtype, or NULL; may be dy's or dsum's buffer (same row stride)
  *   dweight  device FP32 [D], or NULL; accumulate = 1 adds to it

@@ -328,3 +328,21 @@ def test_training_step_of_a_tied_model():
     g = f64(leaves[0].grad)
     assert w.grad is None
     assert_within(f64(buf), g, tol * (np.abs(g) + np.abs(g).max()), "one buffer")
+
+
+# rows whose 1 / rms is far from 1: its cube passes FP32's range where the inputs and the gradient do not
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,D", [(5, 24), (3, 777), (3, 4096), (2, 8200), (2, 16392)])
+@pytest.mark.parametrize("rms,eps", [(1e-14, 0.0), (1e-14, 1e-30), (1e13, 1e-6), (1e14, 1e-6), (1e17, 1e-6)])
+def test_backward_of_tiny_and_huge_rows(rms, eps, N, D, dtype):
+    """dy correlated with s, so that the mean's term is as large as the other; a row of zeros where eps allows one."""
+    s = _rand((N, D), torch.float32, D, rms)
+    dy = (_rand((N, D), torch.float32, D + 1) + s / rms).to(dtype)
+    if rms < 1 and eps:
+        s[1] = 0
+    s, w = s.to(dtype), _rand((D,), torch.float32, 3)
+    say(f"[norm grad] rms {rms} eps {eps} {N} {D} {dtype}")
+    dx, dw = vce.ce_rms_norm_backward(dy.cuda(), s.cuda(), w.cuda(), eps)
+    rx, rw, bx, bw = ref_norm_grad(f64(dy), f64(s), f64(w), np.float64(np.float32(eps)), None)
+    assert_within(f64(dx), rx, bx + half_step(dtype) * 1.01 * np.abs(rx), "dx")
+    assert_within(f64(dw), rw, bw, "dweight")

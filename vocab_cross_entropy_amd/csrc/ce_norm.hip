@@ -1,11 +1,12 @@
 // RMS norm with the residual's addition, its 8-bit form and its gradient.
 //
 //   s = x + residual,  y = s rstd w,  rstd = (mean s^2 + eps)^(-1/2)
-//   ds = rstd (dy w) - s rstd^3 mean(dy w s) + dsum,   dw = sum over rows of dy s rstd
+//   n = s rstd,  ds = rstd (dy w - n mean(dy w n)) + dsum,  dw = sum over rows of dy n
 // The sum s is held in FP32; y comes from it unrounded, and its rounding to the
 // input's type is the residual stream that is written.  The gradient takes
-// that written s as its input.  Squares, means and dw are FP32 sums in a
-// fixed order.
+// that written s as its input, and forms n first: the cube of rstd leaves FP32 for
+// rows of an rms above 1e13 or, at eps 0, below 1e-13.  Squares, means and dw are
+// FP32 sums in a fixed order.
 //
 // 8-bit form: per group of columns, scale = max(max |y| / 448, 2^-126), and the
 // e4m3 value of y / scale (448 is e4m3's largest; the floor keeps 1 / scale
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(kGradT) void k_norm_grad(NormGradArgs a) {
     row_reduce<T, 2>(sums, red[sub], turn);
     if (live) {
       const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
-      const float k = rstd * rstd * rstd * (sums[1] / (float)D);
+      const float c = sums[1] / (float)D * rstd;  // mean(dy w n)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const uint32_t j = (uint32_t)(p * T + t) * kG;
@@ -357,8 +358,9 @@ __global__ __launch_bounds__(kGradT) void k_norm_grad(NormGradArgs a) {
           for (int e = 0; e < kG; ++e) d[e] = 0.f;
 #pragma unroll
         for (int e = 0; e < kG; ++e) {
-          acc[p][e] = __builtin_fmaf(g[e], f[e] * rstd, acc[p][e]);
-          d[e] += __builtin_fmaf(g[e] * w[p][e], rstd, -(f[e] * k));
+          const float n = f[e] * rstd;
+          acc[p][e] = __builtin_fmaf(g[e], n, acc[p][e]);
+          d[e] = __builtin_fmaf(__builtin_fmaf(-n, c, g[e] * w[p][e]), rstd, d[e]);
         }
         if (a.dx && j < D) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
       }
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad_wide(NormGradArgs a) {
     }
     row_reduce<T, 2>(sums, red, turn);
     const float rstd = 1.f / sqrtf(sums[0] / (float)D + a.eps);
-    const float k = rstd * rstd * rstd * (sums[1] / (float)D);
+    const float c = sums[1] / (float)D * rstd;
     for (uint32_t j = t * kG, at = t; j < D; j += T * kG, at += T * kG) {
       float f[kG], g[kG], w[kG], d[kG];
       raw_to_f32<DT>(fetch_group<DT, WHOLE>(s, j, D), f);
@@ -433,8 +435,9 @@ __global__ __launch_bounds__(1024) void k_norm_grad_wide(NormGradArgs a) {
         for (int e = 0; e < kG; ++e) d[e] = 0.f;
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
-        share[at + e * T] = __builtin_fmaf(g[e], f[e] * rstd, share[at + e * T]);
-        d[e] += __builtin_fmaf(g[e] * w[e], rstd, -(f[e] * k));
+        const float n = f[e] * rstd;
+        share[at + e * T] = __builtin_fmaf(g[e], n, share[at + e * T]);
+        d[e] = __builtin_fmaf(__builtin_fmaf(-n, c, g[e] * w[e]), rstd, d[e]);
       }
       if (a.dx) store_group<DT>(a.dx + r * a.dx_ld * EB, j, D, f32_to_raw<DT>(d));
     }
