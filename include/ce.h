@@ -543,7 +543,7 @@ ce_status ce_rms_norm(const ce_norm* n, void* y, int64_t y_ld, void* sum, int64_
 /*
  * The same with the output in 8 bits, for each group of `group` columns (0: the
  * row; else 32, 64 or 128, the last of a row possibly short):
- *   scale = max(max |y| / 448, 2^-126),  q = e4m3(y / scale)   (OCP e4m3, round to nearest even)
+ *   scale = max(max |y| / 448, 2^-126),  q = e4m3(y / scale)   (in FP32; OCP e4m3, round to nearest even)
  *   q       device bytes [N, D], row stride q_ld
  *   scales  device FP32 [N, ceil(D / group)] ([N, 1] for group 0), contiguous
  * A NaN in a row makes all its q NaN, with scale 2^-126.

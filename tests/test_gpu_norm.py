@@ -346,3 +346,60 @@ def test_backward_of_tiny_and_huge_rows(rms, eps, N, D, dtype):
     rx, rw, bx, bw = ref_norm_grad(f64(dy), f64(s), f64(w), np.float64(np.float32(eps)), None)
     assert_within(f64(dx), rx, bx + half_step(dtype) * 1.01 * np.abs(rx), "dx")
     assert_within(f64(dw), rw, bw, "dweight")
+
+
+def _border_weights(cols, lead, seed):
+    """``cols`` values whose quotients by the scale of their largest, ``lead``, lie within two FP32 steps of a border
+    between e4m3 values; the first is ``lead``."""
+    grid = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float().double()  # 0 .. 448
+    scale = np.float32(lead) / np.float32(448)
+    g = _gen(seed)
+    at = ((grid[1:] + grid[:-1]) / 2)[torch.randint(0, 126, (cols,), generator=g)]
+    w = (at * float(scale)).float()
+    w = (w.view(torch.int32) + torch.randint(-2, 3, (cols,), generator=g, dtype=torch.int32)).view(torch.float32)
+    w = w * (torch.randint(0, 2, (cols,), generator=g) * 2 - 1)
+    w[0] = lead
+    return w
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [640, 4096, 8192, 16512])
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_quantised_at_the_borders(group, D, dtype):
+    """Rows of +-1 at eps 0 have 1 / rms = 1 exactly, so y is the weight: q is the value nearest to the FP32 quotient
+    y / scale, bit for bit, also where that lies next to a border between two of the type's values."""
+    N, G = 3, group or D
+    leads = torch.rand(D // G, generator=_gen(D)).add_(0.5).mul_(100.0).tolist()
+    w = torch.cat([_border_weights(G, lead, D + k) for k, lead in enumerate(leads)])
+    x = (torch.randint(0, 2, (N, D), generator=_gen(group + 1)) * 2 - 1).to(dtype)
+    y = x.float() * w
+    scale = y.view(N, -1, G).abs().amax(2) / 448
+    want = (y.view(N, -1, G) / scale.unsqueeze(2)).view(N, D).to(torch.float8_e4m3fn)
+    say(f"[norm e4m3] borders {group} {D} {dtype}")
+    q, scales, _ = vce.ce_rms_norm_quant(x.cuda(), w.cuda(), eps=0.0, group=group)
+    assert torch.equal(scales.cpu(), scale)
+    assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("D", [640, 16512])
+@pytest.mark.parametrize("group", [0, 128])
+def test_quantised_extremes(group, D):
+    """The quotient at the ends of the range: an infinite y (its scale is infinite, the others' quotients 0 with their
+    signs), y near FP32's largest, zeros of both signs, and y below the smallest scale."""
+    G = group or D
+    w = torch.ones(D)
+    x = torch.ones((4, D))
+    x[:, 3::7] = -1
+    for name, lead, fill in (("infinite", float("inf"), 2.0), ("largest", 3.3e38, 1.1e38), ("zero", 0.0, 0.0),
+                             ("tiny", 2.0 ** -126, 2.0 ** -130)):
+        w[:G] = fill
+        w[5] = lead
+        y = x * w
+        scale = (y.view(4, -1, G).abs().amax(2) / 448).clamp(min=2.0 ** -126)
+        want = (y.view(4, -1, G) / scale.unsqueeze(2)).view(4, D).to(torch.float8_e4m3fn)
+        say(f"[norm e4m3] {name} {group} {D}")
+        q, scales, _ = vce.ce_rms_norm_quant(x.cuda(), w.cuda(), eps=0.0, group=group)
+        assert torch.equal(scales.cpu(), scale), name
+        got, nan = q.cpu().view(torch.uint8), torch.isnan(want.float())
+        assert torch.equal(torch.isnan(q.cpu().float()), nan) and bool(nan.any()) == (name == "infinite")
+        assert torch.equal(got[~nan], want.view(torch.uint8)[~nan]), name
