@@ -461,7 +461,9 @@ typedef struct ce_process {
 } ce_process;
 
 /* z into `out`, which has x's dtype and shape and its own strides; out->data ==
- * x->data with the same strides works in place, any other overlap does not.
+ * x->data with the same strides works in place, any other overlap is refused
+ * (CE_ELAYOUT; rows of equal strides may lie side by side or in turn, rows of
+ * other strides may share no range of addresses).
  * One kernel launch; sums of counts are whole numbers, so repeats are equal
  * bit for bit. */
 ce_status ce_logits_process(const ce_logits* x, const ce_logits* out, const ce_process* p, hipStream_t stream);
@@ -536,8 +538,10 @@ typedef struct ce_norm {
   float eps;            /* finite, >= 0 */
 } ce_norm;
 
-/* y: device [N, D], row stride y_ld; sum: s, device [N, D], row stride sum_ld, or NULL.  Either may be the
- * same buffer as x or residual (same row stride), for an update in place; not one another. */
+/* y: device [N, D], row stride y_ld; sum: s, device [N, D], row stride sum_ld, or NULL.  Each may be x's or
+ * residual's own rows (same address and row stride), for an update in place; any other overlap with them, or of
+ * y and sum with one another, is refused (CE_ELAYOUT; rows of equal strides may lie side by side or in turn, rows
+ * of other strides may share no range of addresses). */
 ce_status ce_rms_norm(const ce_norm* n, void* y, int64_t y_ld, void* sum, int64_t sum_ld, hipStream_t stream);
 
 /*
@@ -546,7 +550,8 @@ ce_status ce_rms_norm(const ce_norm* n, void* y, int64_t y_ld, void* sum, int64_
  *   scale = max(max |y| / 448, 2^-126),  q = e4m3(y / scale)   (in FP32; OCP e4m3, round to nearest even)
  *   q       device bytes [N, D], row stride q_ld
  *   scales  device FP32 [N, ceil(D / group)] ([N, 1] for group 0), contiguous
- * A NaN in a row makes all its q NaN, with scale 2^-126.
+ * A NaN in a row makes all its q NaN, with scale 2^-126.  sum as above; q may overlap none of x, residual and
+ * sum (CE_ELAYOUT).
  */
 ce_status ce_rms_norm_quant(const ce_norm* n, void* q, int64_t q_ld, int32_t group, float* scales, void* sum,
                             int64_t sum_ld, hipStream_t stream);
@@ -560,7 +565,8 @@ size_t ce_rms_norm_workspace_bytes(int64_t N, int64_t D);
  *   dx = rstd (dy weight - n mean_j(dy weight n)) + dsum     (also the residual's gradient)
  *   dweight (+)= sum over rows of dy n
  *   dsum     device [N, D], the gradient that reaches s by the residual stream, or NULL
- *   dx       device [N, D] in x's dtype, or NULL; may be dy's or dsum's buffer (same row stride)
+ *   dx       device [N, D] in x's dtype, or NULL; may be dy's, dsum's or x's own rows (same address and row
+ *            stride); any other overlap with them is refused, as above
  *   dweight  device FP32 [D], or NULL; accumulate = 1 adds to it
  *   ws       ce_rms_norm_workspace_bytes bytes, 256-byte aligned (needed with dweight), no preparation
  */

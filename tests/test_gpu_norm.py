@@ -403,3 +403,36 @@ def test_quantised_extremes(group, D):
         got, nan = q.cpu().view(torch.uint8), torch.isnan(want.float())
         assert torch.equal(torch.isnan(q.cpu().float()), nan) and bool(nan.any()) == (name == "infinite")
         assert torch.equal(got[~nan], want.view(torch.uint8)[~nan]), name
+
+
+@pytest.mark.parametrize("N,D", [(5, 96), (4, 2000), (2, 16392)])
+def test_buffers_shared_without_overlap(N, D):
+    """Inputs and outputs side by side or in turn in one buffer, and the gradient over the sum's own rows: the same
+    bits as in buffers of their own.  Rows that meet are refused and left as they are."""
+    for dtype in DTYPES:
+        x, r, w = _rand((N, D), dtype, 1).cuda(), _rand((N, D), dtype, 2).cuda(), _rand((D,), dtype, 3).cuda()
+        y, s = vce.ce_rms_norm(x, w, r)
+        dx, dw = vce.ce_rms_norm_backward(r, s, w, dsum=x)
+        say(f"[norm] shared buffers {N} {D} {dtype}")
+        for side in (True, False):
+            b = torch.empty((N, 4, D) if side else (4 * N, D), dtype=dtype, device="cuda")
+            xs, rs, ys, ss = (b[:, k] for k in range(4)) if side else (b[k::4] for k in range(4))
+            xs.copy_(x), rs.copy_(r)
+            vce.ce_rms_norm(xs, w, rs, out=ys, sum_out=ss)
+            assert torch.equal(ys, y) and torch.equal(ss, s) and torch.equal(xs, x) and torch.equal(rs, r)
+            got, gw = vce.ce_rms_norm_backward(rs, ss, w, dsum=xs, dx=ss)
+            assert got is ss and torch.equal(ss, dx) and torch.equal(gw, dw) and torch.equal(xs, x)
+        b = torch.zeros(2 * N * D + D, dtype=dtype, device="cuda")
+        a = b[:N * D].view(N, D)
+        a.copy_(x)
+        wide = b[:2 * N * D].view(N, 2 * D)[:, :D]
+        before = b.clone()
+        for call in (lambda: vce.ce_rms_norm(a, w, out=wide), lambda: vce.ce_rms_norm(a, w, out=b[D:D + N * D].view(N, D)),
+                     lambda: vce.ce_rms_norm(a, w, r, out=y, sum_out=y), lambda: vce.ce_rms_norm(a, w, r, sum_out=wide),
+                     lambda: vce.ce_rms_norm(r, w, a, out=b[1:1 + N * D].view(N, D)),
+                     lambda: vce.ce_rms_norm_quant(a, w, out=b.view(torch.float8_e4m3fn)[:N * D].view(N, D)),
+                     lambda: vce.ce_rms_norm_backward(a, x, w, dx=wide), lambda: vce.ce_rms_norm_backward(x, a, w, dx=wide),
+                     lambda: vce.ce_rms_norm_backward(x, x, w, dsum=a, dx=b[D:D + N * D].view(N, D))):
+            with pytest.raises(vce.CeArgumentError, match="overlaps"):
+                call()
+        assert torch.equal(b, before)

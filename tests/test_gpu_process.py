@@ -432,3 +432,29 @@ def test_no_rows_and_empty_history():
     say("[process] empty history")
     z = _call(d, out=torch.empty_like(d["x"]))
     assert_within(f64(z), f64(s["x"]) / f64(s["temperature"]).reshape(1, 2, 1), 4 * U * np.abs(f64(z)), "no history")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_output_beside_the_input(dtype):
+    """Input and output rows side by side or in turn in one buffer; rows that meet are refused."""
+    d0, d1, V, L = 3, 4, 301, 20
+    s = _dev(_inputs(d0, d1, V, dtype, L, seed=61))
+    x = s.pop("x")
+    want = vce.ce_logits_process(x, out=torch.empty_like(x), **s)
+    say(f"[process] shared buffer {dtype}")
+    for cut in (lambda b, k: b.view(d0, d1, 2, V)[:, :, k], lambda b, k: b.view(d0, 2, d1, V)[:, k],
+                lambda b, k: b.view(2, d1, d0, V)[k].transpose(0, 1), lambda b, k: b.view(d1, 2, d0, V)[:, k].transpose(0, 1)):
+        b = torch.empty(2 * d0 * d1 * V, dtype=dtype, device="cuda")
+        xs, out = cut(b, 0), cut(b, 1)
+        xs.copy_(x)
+        vce.ce_logits_process(xs, out=out, **s)
+        assert torch.equal(out, want) and torch.equal(xs, x)
+    b = torch.zeros(2 * d0 * d1 * V, dtype=dtype, device="cuda")
+    xs = b[:d0 * d1 * V].view(d0, d1, V)
+    xs.copy_(x)
+    before = b.clone()
+    for out in (b[V:V + d0 * d1 * V].view(d0, d1, V), b[8:8 + d0 * d1 * V].view(d0, d1, V),
+                xs.view(d1, d0, V).transpose(0, 1), b.view(d0, 2 * d1, V)[:, :d1]):
+        with pytest.raises(vce.CeArgumentError, match="overlaps"):
+            vce.ce_logits_process(xs, out=out, **s)
+    assert torch.equal(b, before)

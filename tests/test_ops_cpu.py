@@ -238,3 +238,53 @@ def test_constants_of_the_processing_get_no_gradient():
 def test_rms_norm_refuses_another_shape():
     with pytest.raises(vce.CeArgumentError):
         vce.rms_norm(torch.zeros((4, 8)), torch.zeros(8), torch.zeros(8))
+
+
+# x's rows stand at P, two of 128 bytes; Q and R are clear of them and of one another
+Q, R = P + 4096, P + 8192
+OVERLAP = [
+    ("y_over_x_other_stride", "y", dict(y=P, y_ld=72)),
+    ("y_half_a_row_on", "y", dict(y=P + 64)),
+    ("y_a_row_on", "y", dict(y=P + 128)),
+    ("y_a_row_back", "y", dict(m=dict(x=P + 128), y=P)),
+    ("y_among_x", "y", dict(m=dict(x_ld=256), y=P + 64, y_ld=64)),
+    ("y_over_residual_other_stride", "y", dict(m=dict(residual=Q, residual_ld=64), y=Q, y_ld=128)),
+    ("y_into_residual", "y", dict(m=dict(residual=Q, residual_ld=100), y=Q + 126, y_ld=100)),
+    ("sum_is_y", "y", dict(y=Q, total=Q, total_ld=64)),
+    ("sum_and_y_in_place", "y", dict(y=P, total=P, total_ld=64)),
+    ("sum_over_x_other_stride", "y", dict(y=Q, total=P, total_ld=66)),
+    ("sum_into_residual", "y", dict(m=dict(residual=Q, residual_ld=64), y=R, total=Q + 2, total_ld=64)),
+    ("q_over_x", "q", dict(y=P, y_ld=128)),
+    ("q_over_residual", "q", dict(m=dict(residual=Q, residual_ld=64), y=Q + 100)),
+    ("q_over_sum", "q", dict(y=Q + 130, y_ld=128, total=Q, total_ld=64)),
+    ("q_sum_over_x_other_stride", "q", dict(y=Q, total=P, total_ld=70)),
+    ("dx_over_dy_other_stride", "grad", dict(m=dict(x=Q), y=P, y_ld=64, dx=P, dx_ld=80)),
+    ("dx_a_row_on_dy", "grad", dict(m=dict(x=Q), y=P, dx=P + 128)),
+    ("dx_into_dsum", "grad", dict(m=dict(x=Q), y=Q, dsum=P, dsum_ld=64, dx=P + 8)),
+    ("dx_over_x_other_stride", "grad", dict(m=dict(x=Q), y=P, dx=Q, dx_ld=65)),
+]
+
+
+@pytest.mark.parametrize("form,change", [c[1:] for c in OVERLAP], ids=[c[0] for c in OVERLAP])
+def test_norm_refuses_overlaps(form, change):
+    assert norm(form=form, ws=P + (1 << 15), ws_bytes=1 << 14, dweight=None, **change) == ELAYOUT, lib.ce_last_error()
+    assert b"overlaps" in lib.ce_last_error()
+
+
+# x's rows: (2, 3) of 32 bytes, 32 apart
+PROCESS_OVERLAP = [
+    ("half_a_row_on", dict(out=dict(data=P + 16))),
+    ("a_row_on", dict(out=dict(data=P + 32))),
+    ("a_row_back", dict(x=dict(data=P + 32), out=dict(data=P))),
+    ("five_rows_on", dict(out=dict(data=P + 160))),
+    ("other_stride_inside", dict(out=dict(data=P + 160, s0=96))),
+    ("one_column_into_the_gap_of_rows", dict(x=dict(s0=120, s1=40), out=dict(data=P + 50))),
+    ("turned", dict(out=dict(s0=16, s1=32))),
+]
+
+
+@pytest.mark.parametrize("change", [c[1] for c in PROCESS_OVERLAP], ids=[c[0] for c in PROCESS_OVERLAP])
+@pytest.mark.parametrize("backward", [False, True])
+def test_process_refuses_overlaps(change, backward):
+    assert process(backward=backward, **change) == ELAYOUT, lib.ce_last_error()
+    assert b"overlaps" in lib.ce_last_error()

@@ -413,7 +413,7 @@ def _sum_out(dev, x, residual, sum_out):
 
 def ce_rms_norm(x, weight, residual=None, eps=1e-6, *, out=None, sum_out=None):
     """RMS norm of ``x + residual`` ([N, D]); returns (y, sum), the sum None without a residual (unless
-    ``sum_out`` asks for it).  ``out`` and ``sum_out`` may be x or residual themselves."""
+    ``sum_out`` asks for it).  ``out`` and ``sum_out`` may be x or residual themselves, not one another."""
     dev = _index(x, "x")
     n = _norm_desc(dev, x, weight, residual, eps)
     out, ptr, ld = _like(dev, "out", out, x)
@@ -448,7 +448,7 @@ def ce_rms_norm_backward(dy, s, weight, eps=1e-6, *, dsum=None, dx=None, dweight
                          want_dx=True, want_dweight=True):
     """The gradient from the forward's sum ``s`` ([N, D]): (dx, the gradient of x and of the residual, in s's
     dtype; dweight, FP32 [D]).  ``dsum`` is the gradient that reaches the sum by the residual stream; ``dx`` may
-    be dy or dsum itself; ``accumulate`` adds to ``dweight``."""
+    be dy, dsum or s itself; ``accumulate`` adds to ``dweight``."""
     dev = _index(s, "s")
     n = _norm_desc(dev, s, weight, None, eps)
     N, D = s.shape

@@ -41,6 +41,47 @@ ce_status check_rows(const char* name, const void* p, int32_t dtype, int64_t row
   return CE_OK;
 }
 
+// n0 x n1 rows of `width` bytes, s0 and s1 bytes apart, none of which meets another
+struct RowSet {
+  typedef __int128 wide;  // (strides are the caller's numbers)
+  wide p, n0, n1, s0, s1, width;
+};
+RowSet row_set(const void* p, int64_t n0, int64_t n1, int64_t s0, int64_t s1, int64_t columns, int bytes) {
+  typedef RowSet::wide wide;
+  return {(wide)(uintptr_t)p, n0, n1, n0 > 1 ? (wide)s0 * bytes : 0, n1 > 1 ? (wide)s1 * bytes : 0, (wide)columns * bytes};
+}
+
+// Whether two sets of equally many rows meet anywhere, other than by being the same rows where that is allowed.
+// Exact where their strides are equal (columns side by side, rows in turn); sets of other strides may not share a
+// range of addresses.
+bool rows_meet(const RowSet& a, const RowSet& b, bool in_place) {
+  typedef RowSet::wide wide;
+  if (a.n0 == 0 || a.n1 == 0) return false;
+  const bool alike = a.s0 == b.s0 && a.s1 == b.s1;
+  if (a.p == b.p && alike && a.width == b.width) return !in_place;
+  const auto end = [](const RowSet& r) { return r.p + (r.n0 - 1) * r.s0 + (r.n1 - 1) * r.s1 + r.width; };
+  if (end(a) <= b.p || end(b) <= a.p) return false;
+  if (!alike) return true;
+  // b's row lies i outer and j inner steps from a's: only the steps next to where the two are nearest can meet
+  const bool outer0 = a.s0 >= a.s1;
+  const wide so = outer0 ? a.s0 : a.s1, no = outer0 ? a.n0 : a.n1, si = outer0 ? a.s1 : a.s0, ni = outer0 ? a.n1 : a.n0;
+  const wide off = b.p - a.p, io = so ? -off / so : 0;
+  for (wide i = io - 1; i <= io + 1; ++i) {
+    if (i <= -no || i >= no) continue;
+    const wide rest = off + i * so, ji = si ? -rest / si : 0;
+    for (wide j = ji - 1; j <= ji + 1; ++j) {
+      if (j <= -ni || j >= ni) continue;
+      const wide d = rest + j * si;
+      if (d < a.width && -d < b.width) return true;
+    }
+  }
+  return false;
+}
+
+ce_status overlap(const char* out, const char* other) {
+  return ofail(CE_ELAYOUT, "%s overlaps %s (in place: the same address and strides, where that is allowed)", out, other);
+}
+
 // ---- logit processing
 ce_status check_process(const ce_logits* x, const ce_logits* out, const ce_process* p, bool backward) {
   ce_status st;
@@ -50,9 +91,10 @@ ce_status check_process(const ce_logits* x, const ce_logits* out, const ce_proce
   if (x->d0 != out->d0 || x->d1 != out->d1 || x->v_local != out->v_local || x->vocab_start != out->vocab_start ||
       x->vocab_total != out->vocab_total)
     return ofail(CE_ELAYOUT, "input and output differ in shape");
-  if (x->data == out->data &&
-      ((x->d0 > 1 && x->s0 != out->s0) || (x->d1 > 1 && x->s1 != out->s1)))
-    return ofail(CE_ELAYOUT, "in place, input and output need the same strides");
+  const int eb = elem_bytes(x->dtype);
+  if (rows_meet(row_set(x->data, x->d0, x->d1, x->s0, x->s1, x->v_local, eb),
+                row_set(out->data, out->d0, out->d1, out->s0, out->s1, out->v_local, eb), true))
+    return overlap("the output", "the input");
   if (p->history) {
     if ((uintptr_t)p->history % 8u || p->history_s0 < 0 || p->history_s1 < 0)
       return ofail(CE_ELAYOUT, "history misaligned or negative stride");
@@ -163,6 +205,18 @@ ce_status norm(const ce_norm* n, void* y, int64_t y_ld, void* q, int64_t q_ld, i
   ce_status st;
   if (n->residual && (st = check_rows("residual", n->residual, n->dtype, n->N, n->D, n->residual_ld))) return st;
   if (sum && (st = check_rows("sum", sum, n->dtype, n->N, n->D, sum_ld))) return st;
+  const int eb = elem_bytes(n->dtype);
+  const auto rows = [n](const void* p, int64_t ld, int bytes) { return row_set(p, n->N, 1, ld, 0, n->D, bytes); };
+  const RowSet xs = rows(n->x, n->x_ld, eb), rs = rows(n->residual, n->residual_ld, eb), ss = rows(sum, sum_ld, eb);
+  const RowSet ys = q ? rows(q, q_ld, 1) : rows(y, y_ld, eb);
+  const char* const name = q ? "q" : "y";
+  if (rows_meet(ys, xs, !q)) return overlap(name, "x");
+  if (n->residual && rows_meet(ys, rs, !q)) return overlap(name, "residual");
+  if (sum) {
+    if (rows_meet(ys, ss, false)) return overlap(name, "sum");
+    if (rows_meet(ss, xs, true)) return overlap("sum", "x");
+    if (n->residual && rows_meet(ss, rs, true)) return overlap("sum", "residual");
+  }
   vce::NormArgs a{};
   a.x = static_cast<const char*>(n->x);
   a.residual = static_cast<const char*>(n->residual);
@@ -303,6 +357,14 @@ ce_status ce_rms_norm_backward(const ce_norm* n, const void* dy, int64_t dy_ld, 
     if (need > 0 && (!ws || ws_bytes < need))
       return ofail(CE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
     if ((uintptr_t)ws % 256u) return ofail(CE_EWORKSPACE, "workspace must be 256-byte aligned");
+  }
+  if (dx) {
+    const int eb = elem_bytes(n->dtype);
+    const auto rows = [n, eb](const void* p, int64_t ld) { return row_set(p, n->N, 1, ld, 0, n->D, eb); };
+    const RowSet ds = rows(dx, dx_ld);
+    if (rows_meet(ds, rows(n->x, n->x_ld), true)) return overlap("dx", "x");
+    if (rows_meet(ds, rows(dy, dy_ld), true)) return overlap("dx", "dy");
+    if (dsum && rows_meet(ds, rows(dsum, dsum_ld), true)) return overlap("dx", "dsum");
   }
   vce::NormGradArgs a{};
   a.s = static_cast<const char*>(n->x);
