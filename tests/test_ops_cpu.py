@@ -288,3 +288,9 @@ PROCESS_OVERLAP = [
 def test_process_refuses_overlaps(change, backward):
     assert process(backward=backward, **change) == ELAYOUT, lib.ce_last_error()
     assert b"overlaps" in lib.ce_last_error()
+
+
+def test_embedding_refuses_its_padding_at_the_call():
+    ids, w = torch.zeros(4, dtype=torch.int64), torch.zeros((16, 8), requires_grad=True)
+    with pytest.raises(vce.CeArgumentError, match="padding_idx"):
+        vce.embedding(ids, w, padding_idx=-1)

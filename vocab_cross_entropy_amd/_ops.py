@@ -292,6 +292,11 @@ def _need_ids(dev, ids):
         _einval("ids must be a 1-d int64 tensor")
 
 
+def _need_padding(padding_idx):
+    if padding_idx is not None and padding_idx < 0:
+        _einval("padding_idx must be a vocabulary index")
+
+
 def ce_embedding(ids, weight, scale=1.0, *, out=None, vocab_start=0, vocab_total=None):
     """``scale * weight[ids]`` for [N] int64 ``ids`` and a [V, D] table, or the rows from ``vocab_start`` on of a
     vocabulary of ``vocab_total`` (other shards' ids give zeros).  Returns [N, D]."""
@@ -329,8 +334,7 @@ def ce_embedding_backward(dout, ids, v_local, scale=1.0, *, padding_idx=None, dw
     N, D = dout.shape
     if ids.shape[0] != N:
         _einval(f"{ids.shape[0]} ids for {N} rows of dout")
-    if padding_idx is not None and padding_idx < 0:
-        _einval("padding_idx must be a vocabulary index")
+    _need_padding(padding_idx)
     v_local = int(v_local)
     m = _embedding_desc(ids, None, D, dout, D, v_local, scale, vocab_start, vocab_total)
     if dw is None:
@@ -374,6 +378,7 @@ def embedding(ids, weight, scale=1.0, *, padding_idx=None, grad_buffer=None, voc
     gradient, which autograd casts to the weight's dtype).  With ``grad_buffer``, an FP32 [V, D] tensor, the
     backward adds the gradient to it instead and ``weight.grad`` stays as it is: with a tied head, the buffer that
     ce_linear_cross_entropy adds its dw to.  (A weight that requires no gradient has none in either.)"""
+    _need_padding(padding_idx)  # here: the forward has no use for it, and the backward is too late
     if grad_buffer is not None:
         _rows(_index(weight, "weight"), "grad_buffer", grad_buffer, weight.shape, torch.float32)
     return Embedding.apply(weight, ids, scale, padding_idx, grad_buffer, vocab_start, vocab_total)
