@@ -294,3 +294,17 @@ def test_embedding_refuses_its_padding_at_the_call():
     ids, w = torch.zeros(4, dtype=torch.int64), torch.zeros((16, 8), requires_grad=True)
     with pytest.raises(vce.CeArgumentError, match="padding_idx"):
         vce.embedding(ids, w, padding_idx=-1)
+
+
+def test_processing_refuses_by_its_own_error():
+    """Logits of other dimensions, and numbers in place of per-row tensors, in both autograd forms."""
+    x, rows = torch.zeros((2, 3, 16), requires_grad=True), torch.ones(6)
+    t = torch.zeros((2, 3), dtype=torch.int64)
+    for logits in (x[0], x[0, 0], x[None]):
+        for call in (lambda **kw: vce.process_logits(logits, **kw), lambda **kw: vce.processed_cross_entropy(logits, t, **kw)):
+            with pytest.raises(vce.CeArgumentError, match="3-d"):
+                call(repetition=rows)
+    for name in ("repetition", "frequency", "presence", "temperature", "bias"):
+        for call in (lambda **kw: vce.process_logits(x, **kw), lambda **kw: vce.processed_cross_entropy(x, t, **kw)):
+            with pytest.raises(vce.CeArgumentError):
+                call(**{name: 0.7})

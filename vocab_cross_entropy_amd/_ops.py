@@ -179,7 +179,7 @@ def ce_logits_process_backward(dz, *, out=None, signs=None, history=None, histor
 
 def _constants(**steps):
     for name, t in steps.items():
-        if t is not None and t.requires_grad:
+        if isinstance(t, _Tensor) and t.requires_grad:
             _einval(f"{name} is a constant of the processing and gets no gradient (it requires one)")
 
 
@@ -195,6 +195,8 @@ class ProcessLogits(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, history, history_len, prompt_len, repetition, presence, frequency, bias, mask, temperature):
+        if x.dim() != 3:
+            _einval("logits must be a 3-d (d0, d1, V) tensor")
         signs = logits_signs(x) if repetition is not None and ctx.needs_input_grad[0] else None
         x = _own_rows(x.detach())
         z = ce_logits_process(x, out=torch.empty_like(x), history=history, history_len=history_len,
