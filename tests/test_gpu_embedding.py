@@ -278,3 +278,53 @@ def test_graph_replays_and_streams(N):
             res.append(vce.ce_embedding_backward(dout, ids, V, 2.0))
     torch.cuda.synchronize()
     assert all(torch.equal(r, ref[1]) for r in res)
+
+
+# wide rows with a length of whole 16-byte words in batches that the sum by tiles takes; more than 64 tokens to a tile
+LARGE = [(2100, 700, 4096, "tail"), (15000, 600, 520, "runs"), (300000, 5000, 136, "tail"), (300000, 12000, 136, "runs")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,V,D,kind", LARGE, ids=lambda v: str(v))
+def test_gradient_of_large_batches(N, V, D, kind, dtype):
+    ids = _ids(N, V, N + V, kind)
+    assert ids.shape == (N,)
+    dout = torch.randn((N, D), generator=_gen(D)).to(dtype)
+    ref = torch.zeros((V, D), dtype=torch.float64).index_add_(0, ids, dout.double()).mul_(0.75).numpy()
+    size = torch.zeros((V, D), dtype=torch.float64).index_add_(0, ids, dout.double().abs_()).mul_(0.75).numpy()
+    m = torch.bincount(ids, minlength=V).numpy()[:, None]
+    tol = 1.01 * U * (m + 2) * size + TINY
+    say(f"[embed grad] large {N} {V} {D} {kind} {dtype}")
+    dd, idd = dout.cuda(), ids.cuda()
+    dw = vce.ce_embedding_backward(dd, idd, V, 0.75, dw=torch.full((V, D), float("nan"), device="cuda"))
+    assert_within(f64(dw), ref, tol, "overwritten")
+    base = torch.randn((V, D), generator=_gen(7))
+    acc = vce.ce_embedding_backward(dd, idd, V, 0.75, dw=base.cuda(), accumulate=True)
+    assert_within(f64(acc), ref + f64(base), tol + U * np.abs(ref + f64(base)) * 1.01, "added")
+    again = vce.ce_embedding_backward(dd, idd, V, 0.75, dw=base.cuda(), accumulate=True)
+    assert torch.equal(again.view(torch.int32), acc.view(torch.int32))
+
+
+def test_more_tokens_than_one_launch_holds():
+    """2^23 workgroups in a launch, a wide row each: some take a second one."""
+    N, V, D = (1 << 23) + 300, 50, 1032
+    w = torch.randn((V, D), generator=_gen(1)).bfloat16().cuda()
+    ids = torch.randint(0, V, (N,), generator=_gen(2)).cuda()
+    say(f"[embed] {N} tokens")
+    out = vce.ce_embedding(ids, w)
+    for a, b in ((0, 300), ((1 << 23) - 300, 1 << 23), (1 << 23, N)):
+        assert torch.equal(out[a:b], w[ids[a:b]])
+
+
+@pytest.mark.parametrize("N", [3, 1500])
+def test_more_unnamed_rows_than_one_launch_holds(N):
+    """Zeros in 2^26 rows and more, eight to a workgroup, with a gap between rows that is left alone."""
+    V, D = (1 << 26) + 4003, 3
+    ids = torch.randint(0, V, (N,), generator=_gen(N))
+    ids[0], ids[1] = V - 1, 1 << 26
+    dout = torch.ones((N, D), device="cuda")
+    say(f"[embed grad] fill of {V} rows")
+    buf = torch.full((V, D + 1), -3.0, device="cuda")
+    vce.ce_embedding_backward(dout, ids.cuda(), V, dw=buf[:, :D])
+    want = torch.bincount(ids, minlength=V).float().cuda()
+    assert all(torch.equal(buf[:, k], want) for k in range(D)) and bool((buf[:, D] == -3).all())

@@ -436,3 +436,58 @@ def test_buffers_shared_without_overlap(N, D):
             with pytest.raises(vce.CeArgumentError, match="overlaps"):
                 call()
         assert torch.equal(b, before)
+
+
+# several rows for each workgroup and a ragged last round: prefetched rows, alternating exchange buffers, dw over rows
+ROUNDS = [(4099, 24), (4200, 1000), (1030, 2048), (515, 4096), (515, 2731), (300, 8200), (259, 16384), (258, 16392)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,D", ROUNDS)
+def test_backward_of_several_rounds(N, D, dtype):
+    test_backward(N, D, dtype)
+    # and over the sum's own rows
+    s, dy, w = _rand((N, D), dtype, D).cuda(), _rand((N, D), dtype, D + 1).cuda(), _rand((D,), dtype, 3).cuda()
+    dx, dw = vce.ce_rms_norm_backward(dy, s, w)
+    over, dw2 = vce.ce_rms_norm_backward(dy, s, w, dx=s)
+    assert over is s and torch.equal(over, dx) and torch.equal(dw2, dw)
+
+
+def _rows_of_a_batch(x, r, w, parts, group):
+    """The forward calls over a whole batch and over parts of its rows: a row's outputs do not depend on the others."""
+    y, s = vce.ce_rms_norm(x, w, r)
+    q, sc, s2 = vce.ce_rms_norm_quant(x, w, r, group=group)
+    assert torch.equal(s, s2)
+    for a, b in parts:
+        yp, sp = vce.ce_rms_norm(x[a:b], w, r[a:b])
+        qp, scp, _ = vce.ce_rms_norm_quant(x[a:b], w, r[a:b], group=group)
+        assert torch.equal(y[a:b], yp) and torch.equal(s[a:b], sp), (a, b)
+        assert torch.equal(q[a:b].view(torch.uint8), qp.view(torch.uint8)) and torch.equal(sc[a:b], scp), (a, b)
+    return y, s, q
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,D,group", [(4100, 4096, 128), (1030, 16384, 0), (40000, 448, 32), (8200, 2048, 64)])
+def test_outputs_larger_than_the_caches(N, D, group, dtype):
+    """More than 32 MiB in an output, which the kernels write past the caches."""
+    g = torch.Generator("cuda").manual_seed(N)
+    x, r = (torch.randn((N, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    w = _rand((D,), torch.float32, 3).cuda()
+    say(f"[norm] large {N} {D} {dtype} {group}")
+    step = (8 << 20) // D
+    y, s, _ = _rows_of_a_batch(x, r, w, [(a, min(a + step, N)) for a in range(0, N, step)], group)
+    pick = torch.tensor([0, 1, N // 2, N - 2, N - 1])
+    ref, total, _ = ref_norm(f64(x[pick]), f64(r[pick]), f64(w), np.float64(np.float32(1e-6)))
+    assert_within(f64(y[pick]), ref, _y_tol(ref, dtype), "y")
+    assert_within(f64(s[pick]), total, (half_step(dtype) * 1.01 + U) * np.abs(total) + TINY, "sum")
+
+
+@pytest.mark.parametrize("N,D,group", [((1 << 23) + 4003, 8, 0), ((1 << 23) + 4003, 40, 32), ((1 << 21) + 503, 1032, 0)])
+def test_more_rows_than_one_launch_holds(N, D, group):
+    """Workgroups that take a second row (2^21 of them in a launch, four narrow rows each)."""
+    g = torch.Generator("cuda").manual_seed(D)
+    x, r = (torch.randn((N, D), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = _rand((D,), torch.float32, 3).cuda()
+    say(f"[norm] {N} rows of {D}")
+    last = (1 << 21) * (4 if D <= 1024 else 1)
+    _rows_of_a_batch(x, r, w, [(0, 4100), (last - 300, last), (last, N)], group)

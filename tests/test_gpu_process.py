@@ -458,3 +458,67 @@ def test_output_beside_the_input(dtype):
         with pytest.raises(vce.CeArgumentError, match="overlaps"):
             vce.ce_logits_process(xs, out=out, **s)
     assert torch.equal(b, before)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2, 300, 5000, 32768), (2, 130, 20000, 32768), (3, 7, 1500, 32768)], ids=str)
+def test_many_rows_with_long_histories(shape, dtype):
+    """32-bit counts in every chunk shape, both directions."""
+    test_many_rows(shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("L", [5, 32768])
+def test_more_rows_than_one_launch_holds(L, dtype):
+    """2^22 workgroups in a launch: some take a second row, whose counts use the same LDS."""
+    N, V = (1 << 22) + 1001, 13
+    g = torch.Generator("cuda").manual_seed(L)
+    x = torch.randn((1, N, V), generator=g, device="cuda", dtype=dtype)
+    uniform = lambda: torch.rand(N, generator=g, device="cuda") + 0.5  # noqa: E731
+    h = torch.randint(-1, V + 1, (1, 1, L), generator=g, device="cuda")
+    rows = dict(history_len=torch.randint(0, 6, (N,), generator=g, device="cuda", dtype=torch.int32),
+                prompt_len=torch.randint(0, 4, (N,), generator=g, device="cuda", dtype=torch.int32),
+                repetition=uniform(), frequency=uniform(), presence=uniform(), temperature=uniform())
+    mask = torch.randint(0, 1 << 13, (1, N, 1), generator=g, device="cuda", dtype=torch.int32)
+    back = ("history_len", "prompt_len", "repetition", "temperature")
+
+    def run(a, b):
+        xs, sub = x[:, a:b], {k: v[a:b] for k, v in rows.items()}
+        signs = vce.logits_signs(xs).fill_(255)
+        steps = dict(history=h.expand(1, b - a, L), mask=mask[:, a:b])
+        z = vce.ce_logits_process(xs, out=torch.empty_like(xs), signs=signs, **steps, **sub)
+        dx = vce.ce_logits_process_backward(xs, out=torch.empty_like(xs), signs=signs, **steps,
+                                            **{k: sub[k] for k in back})
+        return z, dx, signs
+
+    say(f"[process] {N} rows, {L} {dtype}")
+    z, dx, signs = run(0, N)
+    for a, b in ((0, 4100), ((1 << 22) - 300, 1 << 22), (1 << 22, N)):
+        for whole, part in zip((z[:, a:b], dx[:, a:b], signs[a:b]), run(a, b)):
+            assert torch.equal(whole, part), (a, b)
+    pick = torch.tensor([0, 1, (1 << 22) - 1, 1 << 22, N - 1])
+    sub = {k: v.cpu()[pick] for k, v in rows.items()} | dict(
+        x=x.cpu()[0, pick].view(5, 1, V), history=h.cpu().expand(5, 1, L), mask=mask.cpu()[0, pick].view(5, 1, 1))
+    ref, budget, _, _ = _reference(sub)
+    _check(z[0].cpu()[pick], ref, budget, dtype, "z")
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, (1 << 30) - 1), (torch.bfloat16, (1 << 31) - 1)], ids=["f32", "bf16"])
+def test_a_row_of_nearly_4_gib(dtype, V):
+    """The widest rows: byte offsets up to 2^32, in both directions, with tokens at both ends."""
+    x = torch.empty((1, 1, V), dtype=dtype, device="cuda").fill_(3.0)
+    h = torch.tensor([0, 7, V // 2, V - 9, V - 2, V - 1, V - 1], device="cuda").view(1, 1, -1)
+    two, half = torch.full((1,), 2.0, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    signs = vce.logits_signs(x)
+    say(f"[process] a row of {V} {dtype}")
+    vce.ce_logits_process(x, history=h, repetition=two, presence=half, temperature=half, signs=signs)
+    want = {0: 2.0, 7: 2.0, V // 2: 2.0, V - 9: 2.0, V - 2: 2.0, V - 1: 2.0}  # (3 / 2 - 1 / 2) / (1 / 2)
+    assert all(float(x[0, 0, j]) == z for j, z in want.items())
+    flat, step = x.view(-1), 1 << 28
+    others = [int((flat[a:a + step] != 6.0).sum()) for a in range(0, V, step)]
+    assert sum(others) == len(want), others
+    x.fill_(3.0)
+    vce.ce_logits_process_backward(x, history=h, repetition=two, temperature=half, signs=signs)
+    assert all(float(x[0, 0, j]) == 3.0 for j in want)  # 3 / 2 / (1 / 2)
+    others = [int((flat[a:a + step] != 6.0).sum()) for a in range(0, V, step)]
+    assert sum(others) == len(want), others
