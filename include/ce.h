@@ -524,9 +524,9 @@ ce_status ce_embedding_backward(const ce_embedding_desc* m, const void* dout, in
  * RMS norm with the residual's addition:
  *   s = x + residual,  y = s (mean_j s_j^2 + eps)^(-1/2) weight
  * in FP32, y and the written s rounded once each (y is formed from s before
- * its rounding).  Squares are FP32: a row whose mean square exceeds FP32 comes
- * out 0 (NaN where it is infinite), and a row holding a NaN comes out NaN.  Rows of at most 32768 columns
- * (CE_ELAYOUT).
+ * its rounding).  The sum of squares is FP32: a row whose sum exceeds FP32 (an rms
+ * of 2.9e17 at 4096 columns) comes out 0, NaN where it is infinite, and at eps 0 one of an rms below 1e-19 loses
+ * digits; a row holding a NaN comes out NaN.  Rows of at most 32768 columns (CE_ELAYOUT).
  */
 typedef struct ce_norm {
   const void* x;        /* device [N, D], row stride x_ld */
@@ -560,7 +560,8 @@ ce_status ce_rms_norm_quant(const ce_norm* n, void* q, int64_t q_ld, int32_t gro
 size_t ce_rms_norm_workspace_bytes(int64_t N, int64_t D);
 
 /*
- * The gradient, from the forward's written sum s as n->x (n->residual NULL):
+ * The gradient, from the forward's written sum s as n->x (n->residual NULL), in FP32 over the forward's range of s
+ * (a row whose sum of squares exceeds FP32 gets rstd 0: dx = dsum):
  *   n = s rstd,  rstd = (mean_j s_j^2 + eps)^(-1/2)
  *   dx = rstd (dy weight - n mean_j(dy weight n)) + dsum     (also the residual's gradient)
  *   dweight (+)= sum over rows of dy n

@@ -220,7 +220,8 @@ class ProcessLogits(torch.autograd.Function):
 
 def process_logits(logits, *, history=None, history_len=None, prompt_len=None, repetition=None, presence=None,
                    frequency=None, bias=None, mask=None, temperature=None):
-    """Processed logits (a new tensor, in the logits' dtype) with the options of ce_logits_process; the
+    """Processed logits (a new tensor, in the logits' dtype) with the options of ce_logits_process, for whole rows of
+    the vocabulary (a shard's: ce_logits_process and its backward, with ``vocab_start`` and ``vocab_total``); the
     gradient reaches ``logits``, everything else is a constant."""
     _constants(repetition=repetition, presence=presence, frequency=frequency, bias=bias, temperature=temperature)
     return ProcessLogits.apply(logits, history, history_len, prompt_len, repetition, presence, frequency, bias, mask,
@@ -269,8 +270,8 @@ def processed_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False,
                             history=None, history_len=None, prompt_len=None, repetition=None, presence=None,
                             frequency=None, bias=None, mask=None, temperature=None):
     """Cross-entropy (the negative log-probability) under the distribution that sampling drew from:
-    parallel_cross_entropy of the processed logits, with both options' arguments.  As there, the gradient is
-    staged in place in ``inp``."""
+    parallel_cross_entropy of the processed logits, whole rows of the vocabulary, with its options (reduction,
+    smoothing, ignored index) and those of process_logits.  As there, the gradient is staged in place in ``inp``."""
     _constants(repetition=repetition, presence=presence, frequency=frequency, bias=bias, temperature=temperature)
     return ProcessedCrossEntropy.apply(inp, target, label_smoothing, reduce_loss, ignore_idx, smoothing, history,
                                        history_len, prompt_len, repetition, presence, frequency, bias, mask,

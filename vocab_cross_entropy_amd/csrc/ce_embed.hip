@@ -13,7 +13,8 @@
 // stable sort of N small keys, little beside the N rows of D values):
 //   up to kRankMax tokens whose (id, position) pair fits 32 bits: one launch in
 //     which each token's place is the count of smaller pairs (N^2 compares of LDS
-//     words, N^2 / 16384 cycles of the whole chip);
+//     words, N^2 / 16384 cycles of the whole chip; 8192 tokens added to 128000 x 1024:
+//     35.0 us, 39.0 by the radix sort, but 16384 tokens 58.5 against 51.5);
 //   more: a stable radix sort, 9 bits at most a pass, in one launch a pass up to
 //     kOneMax tokens (every workgroup counts all keys) and three beyond.
 // The sorted list is then cut into tiles of equally many tokens, so a token that
@@ -509,9 +510,9 @@ __device__ __forceinline__ TileRuns tile_runs(const SumArgs& s, uint32_t N, uint
 
 // Zeros in the rows v0 .. v0 + kFillRows - 1 of dW whose bit in `named` is not set:
 // 16-byte stores from a row's first 16-byte boundary on, single columns before and
-// after.  Rows that share cache lines are written with the non-temporal bit (20011 x
-// 1037 FP32 tokens: 68 against 85 us), whole lines without (32000 x 4096: 94 against
-// 98 us).
+// after.  Rows that share cache lines are written with the non-temporal bit (20011
+// tokens of 1037 FP32 columns, 32000 rows: 65 against 82 us), whole lines without (2000
+// tokens of 4096 columns, 32000 rows: 115 against 117 us).
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t v0, uint32_t named) {
   const uint32_t D = (uint32_t)a.D;
   const u32x4v zero = {0u, 0u, 0u, 0u};
@@ -535,9 +536,11 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t v0, ui
 }
 
 // The same where dW's rows lie end to end from a 16-byte boundary on: a workgroup takes E values, whatever rows they
-// belong to, a quad a thread and step.  For rows of few columns (8 rows a workgroup against 8192 values a workgroup:
-// 3000 tokens in 120000 x 64 columns 56 and 20 us, 30000 in 120000 x 300 104 and 69, but 20011 in 32000 x 1037 76 and
-// 84), and for any with at most 256 tokens, then 4096 values (3 in 64703 x 4096: 186 and 164 us).
+// belong to, a quad a thread and step.  For rows of few columns (8 rows a workgroup against 8192 values a workgroup,
+// two tables in turn: 3000 tokens in 120000 x 64 columns 63 and 20 us, 30000 in 120000 x 300 93 and 69, in 120000 x 520
+// 106 and 98.5, but 20011 in 32000 x 1037 65 and 85, 8192 in 32000 x 4096 131 and 134), and for any with at most 256
+// tokens, then 4096 values (3 in 64703 x 4096: 187 and 163 us, 255 in 32000 x 4096 102 and 91; 257 107 and, by 8192
+// values, 109).
 constexpr int kFlatFew = 4096, kFlat = 8192;
 constexpr int64_t kFlatCols = 512;
 template <int E>

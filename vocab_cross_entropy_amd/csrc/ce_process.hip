@@ -17,7 +17,7 @@
 // result) while the columns arrive, and then processes and writes them.  Every
 // chunk of a row reads the row's history, from L2.  Counts take 16 bits with the
 // prompt flag in the top one while the history holds at most 32767 tokens, and 32
-// bits beyond.  8192 x 128000 BF16 with the prefixes of 2048 tokens: 733 us, 5.7
+// bits beyond.  8192 x 128000 BF16 with the prefixes of 2048 tokens: 738 us, 5.7
 // TB/s of the 6.0 that a copy reaches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -288,9 +288,12 @@ hipError_t launch_dt(const ProcessArgs& a, int hist, dim3 grid, hipStream_t stre
 
 void process_plan(ProcessArgs* a) {
   // Many rows: 8192-column chunks by 256 threads, the fastest stream (8192 x 128000 BF16: 741 us, 818 by 512 threads
-  // on 16384 columns).  Some: 512 threads, which count a long history in half the steps (64 x 128000 FP32 with up to
-  // 4096 tokens: 17.1 against 18.4 us).  Few, or of few columns: 2048-column chunks, for workgroups enough and few
-  // idle threads (5600 x 500 BF16: 19 us, 36 by 512 threads).
+  // on 16384 columns; around the limit of 8192 items either is ahead by up to a tenth).  Some: 512 threads, which count a
+  // long history in half the steps and read it less often (64 x 128000 FP32 with up to 4096 tokens: 16.2 us, 20.0 in
+  // 2048-column chunks).  The limit of 512 items is on the high side: with a history, 256 items and more are faster by
+  // 512 threads too (63 x 128000 FP32: 19.7 against 16.1 us), without one they are not (126 x 50257 FP32: 10.3 against
+  // 11.1).  Few, or of few columns: 2048-column chunks, for workgroups enough and few idle threads (5600 x 500 BF16: 19
+  // us, 36 by 512 threads).
   const auto items = [a](ProcShape s) {
     const int64_t cols = (int64_t)s.t * s.u * kG;
     return a->N * ((a->V + cols - 1) / cols);
