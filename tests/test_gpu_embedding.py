@@ -328,3 +328,20 @@ def test_more_unnamed_rows_than_one_launch_holds(N):
     vce.ce_embedding_backward(dout, ids.cuda(), V, dw=buf[:, :D])
     want = torch.bincount(ids, minlength=V).float().cuda()
     assert all(torch.equal(buf[:, k], want) for k in range(D)) and bool((buf[:, D] == -3).all())
+
+
+@pytest.mark.parametrize("D", [3, 40, 130])
+def test_the_most_tokens(D):
+    """2^26 tokens, a twentieth of them one id: whole numbers, so that the sums are exact in any order."""
+    N, V = 1 << 26, 70001
+    g = torch.Generator("cuda").manual_seed(D)
+    ids = torch.randint(0, V, (N,), generator=g, device="cuda")
+    ids[torch.randint(0, N, (N // 20,), generator=g, device="cuda")] = 12345
+    ids[::1009] = 777  # the padding
+    value = ((torch.arange(V, device="cuda")[:, None] * 7 + torch.arange(D, device="cuda")) % 5).float()
+    dout = value.bfloat16()[ids]
+    say(f"[embed grad] {N} tokens x {D}")
+    dw = vce.ce_embedding_backward(dout, ids, V, 2.0, padding_idx=777)
+    count = torch.bincount(ids, minlength=V)
+    count[777] = 0
+    assert torch.equal(dw, value * count.float()[:, None] * 2)
