@@ -79,8 +79,9 @@ extern "C" {
  * 6: ce_linear.gemm (was reserved): the chunked head's GEMM engine; the head's
  *    logits stride in the workspace rounded up to a multiple of 8
  * 7: ce_stream_reference
- * 8: ce_logits_process(_backward), ce_embedding(_backward), ce_rms_norm, _quant and _backward */
-#define CE_ABI_VERSION 8
+ * 8: ce_logits_process(_backward), ce_embedding(_backward), ce_rms_norm, _quant and _backward
+ * 9: ce_token_logprobs(_backward), ce_distill_fwd_bwd */
+#define CE_ABI_VERSION 9
 
 typedef enum ce_status {
   CE_OK = 0,
@@ -575,6 +576,107 @@ ce_status ce_rms_norm_backward(const ce_norm* n, const void* dy, int64_t dy_ld, 
                                void* dx, int64_t dx_ld, float* dweight, int32_t accumulate, void* ws, size_t ws_bytes,
                                hipStream_t stream);
 
+/*
+ * Token log-probabilities: of given tokens, with the entropy and the K
+ * likeliest alternatives, from one read of whole rows of logits, which are left
+ * as they are.  With m = max_j x_j, D = sum_j exp(x_j - m) in FP32 (its largest
+ * term counted apart, so that values near 0 keep their digits):
+ *   logp_t = (x_t - m) - log D,   entropy = -sum_j p_j log p_j,   lse = m + log D
+ * The alternatives are the K columns of the largest logits, largest first, equal
+ * ones by the lower column.  A masked column (-inf) has probability 0, its log -inf.
+ * A row that holds a NaN or +inf, or nothing but -inf, has no distribution: its
+ * logp, top_logp and entropy are NaN; its alternatives are its largest logits all
+ * the same, NaN last.
+ */
+typedef struct ce_logprobs {
+  const int64_t* ids;     /* device, row (i0, i1)'s M tokens at i0 * ids_s0 + i1 * ids_s1, contiguous; NULL with M = 0 */
+  int64_t ids_s0, ids_s1; /* >= 0 (0: shared) */
+  int32_t M;              /* given tokens of a row, 0 to 128 */
+  int32_t K;              /* alternatives of a row, 0 to 128 and at most the number of columns */
+  int64_t ignore_idx;     /* tokens equal to this get logp 0 and no gradient; others outside the vocabulary violate the
+                             precondition: nothing is read out of bounds, the token's logp is NaN and so is the row's
+                             gradient */
+} ce_logprobs;
+
+/* Workspace bytes of ce_token_logprobs with K alternatives for logits like `x` (256: none is used); 0 if the
+ * arguments are refused.  A prepared workspace (ce_workspace_init) of any call will do that is large enough. */
+size_t ce_token_logprobs_workspace_bytes(const ce_logits* x, int32_t K);
+
+/*
+ * One kernel launch (of up to 2^22 workgroups); every output is device memory and may be NULL where it is not asked
+ * for (logp with M = 0, top_ids and top_logp with K = 0):
+ *   logp     FP32 [N, M]          entropy  FP32 [N]          lse  FP32 [N]
+ *   top_ids  int64 [N, K]         top_logp FP32 [N, K]
+ *   stats    FP32 [N][4], 16-byte aligned: what the gradient takes: m, log D, 1 - exp(-log D) (what the likeliest
+ *            column leaves to the others), and the entropy (0 where `entropy` is not asked for)
+ *   ws       as for ce_fwd_bwd_fused: ce_token_logprobs_workspace_bytes bytes, prepared by ce_workspace_init; NULL
+ *            where that is 256.  Not prepared: results NaN, top_ids -1, and ce_workspace_check tells
+ * Rows of at most 1,048,576 BF16 or 524,288 FP32 columns (CE_ELAYOUT).
+ * Results do not depend on scheduling: repeats are equal bit for bit.
+ */
+ce_status ce_token_logprobs(const ce_logits* x, const ce_logprobs* q, float* logp, float* entropy, float* lse,
+                            int64_t* top_ids, float* top_logp, float* stats, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/*
+ * The gradient with respect to the logits, from the logits and the forward's stats:
+ *   dx_v = sum_i g_i [v = t_i] - p_v (sum_i g_i + dentropy (log p_v + entropy))
+ * over the given tokens (dlogp [N, M]) and the alternatives (dtop [N, K] for the forward's top_ids [N, K]; both
+ * NULL with K = 0); a column that is named twice gets both.  dentropy [N] or NULL.  `out` has x's dtype and shape
+ * and its own strides; the same data and strides work in place, any other overlap is refused (CE_ELAYOUT).
+ */
+ce_status ce_token_logprobs_backward(const ce_logits* x, const ce_logits* out, const ce_logprobs* q,
+                                     const float* stats, const float* dlogp, const float* dentropy,
+                                     const int64_t* top_ids, const float* dtop, hipStream_t stream);
+
+/*
+ * Distillation from a teacher's top logits: for row x, its K entries (column
+ * c_k, value t_k) and the temperature T, with q = softmax(x / T),
+ *   CE_TEACHER_LOGITS    p = softmax over the entries of t / T; nothing is left: r = 0
+ *   CE_TEACHER_LOGPROBS  p_k = exp(t_k): t are the teacher's log-probabilities at the temperature T;
+ *                        r = max(0, 1 - sum_k p_k), one more class of all the columns that no entry names
+ *   loss = T^2 (sum_k p_k (log p_k - log q_ck) + r (log r - log q_o)),   q_o = the unnamed columns' share of q
+ *   dx_v = s T (q_v (sum_k p_k + r) - sum of p_k with c_k = v - [v unnamed] q_v r / q_o)
+ * with s the upstream gradient, over the number of counted rows for the mean, as in the losses above.  Terms of
+ * p_k = 0 or r = 0 are left out (0 log 0 = 0); r is 0 where every unnamed column is masked (-inf), or there is none.
+ * A masked column that the teacher names with p_k > 0 makes the loss +inf and its gradient -s T p_k.
+ * A row of no entries counts for nothing: loss 0, gradient 0, not one of the rows of the mean.  A row naming a
+ * column outside the vocabulary violates the precondition: nothing is read or written out of bounds, its loss and
+ * gradient are NaN, as they are for a row that holds a NaN or +inf, or nothing but -inf.
+ * The sum over the unnamed columns is FP32, all else of a row 64-bit; each output is rounded once.
+ */
+enum { CE_TEACHER_LOGITS = 0, CE_TEACHER_LOGPROBS = 1 };
+
+typedef struct ce_distill {
+  const int64_t* ids;        /* device, row (i0, i1)'s K columns at i0 * ids_s0 + i1 * ids_s1, contiguous */
+  int64_t ids_s0, ids_s1;    /* >= 0 */
+  const void* values;        /* device, row (i0, i1)'s K values at i0 * values_s0 + i1 * values_s1, contiguous */
+  int64_t values_s0, values_s1;
+  int32_t values_dtype;      /* CE_F32 or CE_BF16 */
+  int32_t kind;              /* CE_TEACHER_LOGITS or CE_TEACHER_LOGPROBS */
+  int32_t K;                 /* 1 to 128 */
+  float temperature;         /* 2^-32 to 2^32 */
+  const int32_t* len;        /* [N] entries of row r, the first ones, taken into [0, K]; NULL: K */
+} ce_distill;
+
+/* Workspace bytes of ce_distill_fwd_bwd for logits like `x` with any reduction; 0 if the arguments are refused. */
+size_t ce_distill_workspace_bytes(const ce_logits* x);
+
+/*
+ * Loss and gradient, one read of the logits.
+ *   out       the gradient, in x's dtype and shape with its own strides: x's own data and strides (in place), or
+ *             no overlap with it (CE_ELAYOUT); NULL: the loss alone
+ *   reduce_loss, grad_out, loss  as for ce_fwd_bwd_fused
+ *   n_valid   [1] device int32 or NULL: the number of rows with an entry
+ *   ws        ce_distill_workspace_bytes bytes, prepared by ce_workspace_init; not prepared: results NaN, and
+ *             ce_workspace_check tells
+ * Rows of at most 2,097,152 BF16 or 1,048,576 FP32 columns (CE_ELAYOUT).  One launch, and one before it that counts
+ * the rows where n_valid is asked for or the mean has lengths.  Repeats are equal bit for bit.
+ */
+ce_status ce_distill_fwd_bwd(const ce_logits* x, const ce_logits* out, const ce_distill* d, int32_t reduce_loss,
+                             const float* grad_out, float* loss, int32_t* n_valid, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
 /* Waits for `stream` and reports whether any call that used `ws` since it was
  * prepared or last checked gave up waiting in a split-row exchange or count
  * (CE_EDEADLOCK; its results were NaN) or found the workspace unprepared
@@ -601,8 +703,8 @@ ce_status ce_stream_reference(const void* src, void* dst, int64_t bytes, hipStre
  * Kernel timing for benchmarks.  After ce_profile_start(capacity), each of
  * the next `capacity` calls of ce_forward(_ex), ce_backward_inplace(_ex),
  * ce_fwd_bwd_fused(_noalloc), ce_shards_fwd_bwd_fused, ce_shard_partial_stats,
- * ce_scale_grad_inplace, ce_logits_process(_backward) or ce_stream_reference
- * that launch work records a pair
+ * ce_scale_grad_inplace, ce_logits_process(_backward), ce_token_logprobs(_backward),
+ * ce_distill_fwd_bwd or ce_stream_reference that launch work records a pair
  * of HIP events on its stream around its main (bandwidth-dominant) kernel.
  * ce_profile_stop(ms, cap, count) waits for those events, writes up to `cap`
  * durations in milliseconds to host array `ms`, the number recorded to

@@ -19,7 +19,8 @@ CE_F32, CE_BF16 = 0, 1
 CE_REDUCE_NONE, CE_REDUCE_MEAN, CE_REDUCE_SUM = 0, 1, 2
 CE_SMOOTH_ALL, CE_SMOOTH_OTHERS = 0, 1
 CE_GEMM_AUTO, CE_GEMM_NATIVE, CE_GEMM_LIBRARY = 0, 1, 2
-CE_ABI_VERSION = 8
+CE_TEACHER_LOGITS, CE_TEACHER_LOGPROBS = 0, 1
+CE_ABI_VERSION = 9
 
 
 class CeLogits(ctypes.Structure):
@@ -86,6 +87,15 @@ class CeNorm(ctypes.Structure):
     _fields_ = _fields("x:p residual:p weight:p dtype:i weight_dtype:i N:q D:q x_ld:q residual_ld:q eps:f")
 
 
+class CeLogprobs(ctypes.Structure):
+    _fields_ = _fields("ids:p ids_s0:q ids_s1:q M:i K:i ignore_idx:q")
+
+
+class CeDistill(ctypes.Structure):
+    _fields_ = _fields("ids:p ids_s0:q ids_s1:q values:p values_s0:q values_s1:q values_dtype:i kind:i K:i "
+                       "temperature:f len:p")
+
+
 # Every symbol include/ce.h declares, with its ctypes signature.
 _P = ctypes.POINTER
 _vp = ctypes.c_void_p
@@ -134,6 +144,14 @@ SIGNATURES = {
     "ce_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "ce_rms_norm_backward": (ctypes.c_int, [_P(CeNorm), _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp,
                                             ctypes.c_int64, _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]),
+    "ce_token_logprobs_workspace_bytes": (ctypes.c_size_t, [_P(CeLogits), ctypes.c_int32]),
+    "ce_token_logprobs": (ctypes.c_int, [_P(CeLogits), _P(CeLogprobs), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         ctypes.c_size_t, _vp]),
+    "ce_token_logprobs_backward": (ctypes.c_int, [_P(CeLogits), _P(CeLogits), _P(CeLogprobs), _vp, _vp, _vp, _vp, _vp,
+                                                  _vp]),
+    "ce_distill_workspace_bytes": (ctypes.c_size_t, [_P(CeLogits)]),
+    "ce_distill_fwd_bwd": (ctypes.c_int, [_P(CeLogits), _P(CeLogits), _P(CeDistill), ctypes.c_int32, _vp, _vp, _vp,
+                                          _vp, ctypes.c_size_t, _vp]),
     "ce_workspace_check": (ctypes.c_int, [_vp, _vp]),
     "ce_profile_start": (ctypes.c_int, [ctypes.c_int32]),
     "ce_profile_stop": (ctypes.c_int, [_vp, ctypes.c_int32, _P(ctypes.c_int32)]),

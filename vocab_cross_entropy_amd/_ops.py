@@ -1,25 +1,32 @@
-"""The operators around the loss: logit processing, embedding and RMS norm.
+"""The operators around the loss: logit processing, embedding, RMS norm, token log-probabilities and distillation.
 
 Like the rest of the binding, the ``ce_*`` functions marshal torch device
 tensors into the C ABI's descriptors (``include/ce.h`` defines each operator)
 and run on torch's current stream of the tensors' device; ``process_logits``,
-``processed_cross_entropy``, ``embedding``, ``rms_norm`` and
-``norm_linear_cross_entropy`` are their autograd forms.
+``processed_cross_entropy``, ``embedding``, ``rms_norm``,
+``norm_linear_cross_entropy``, ``token_logprobs`` and ``distillation_loss`` are
+their autograd forms.
 """
 from __future__ import annotations
+
+from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
 from . import (CeArgumentError, _check, _device_of, _need, _need_targets, _raw_stream, _workspace,
-               ce_fwd_bwd_fused, ce_scale_grad_inplace, ce_workspace_bytes, lib, linear_cross_entropy, reduction_code)
+               _is_prepared, ce_fwd_bwd_fused, ce_scale_grad_inplace, ce_workspace_bytes, ce_workspace_init, lib,
+               linear_cross_entropy, reduction_code)
 
 __all__ = [
     "ce_logits_process", "ce_logits_process_backward", "logits_signs", "process_logits", "processed_cross_entropy",
     "ce_embedding", "ce_embedding_backward", "ce_embedding_workspace_bytes", "embedding",
     "ce_rms_norm", "ce_rms_norm_quant", "ce_rms_norm_backward", "ce_rms_norm_workspace_bytes", "rms_norm",
     "norm_linear_cross_entropy",
+    "TokenLogprobs", "ce_token_logprobs", "ce_token_logprobs_backward", "ce_token_logprobs_workspace_bytes",
+    "token_logprobs",
+    "ce_distill_fwd_bwd", "ce_distill_workspace_bytes", "distillation_loss",
 ]
 
 
@@ -533,3 +540,256 @@ def norm_linear_cross_entropy(h, norm_weight, weight, target, label_smoothing=0.
     y = rms_norm(h, norm_weight, residual, eps)
     return linear_cross_entropy(y if residual is None else y[0], weight, target, label_smoothing, reduce_loss,
                                 ignore_idx, smoothing=smoothing, chunk_rows=chunk_rows, gemm=gemm)
+
+
+# ---- token log-probabilities -----------------------------------------------------------------------------
+
+
+class TokenLogprobs(NamedTuple):
+    """What ce_token_logprobs and token_logprobs return; None where it was not asked for."""
+
+    logprobs: Optional[torch.Tensor]      # FP32, the shape of ids
+    entropy: Optional[torch.Tensor]       # FP32 (d0, d1)
+    top_ids: Optional[torch.Tensor]       # int64 (d0, d1, top_k)
+    top_logprobs: Optional[torch.Tensor]  # FP32 (d0, d1, top_k)
+    stats: Optional[torch.Tensor]         # FP32 [N, 4], for ce_token_logprobs_backward
+    lse: Optional[torch.Tensor]           # FP32 (d0, d1)
+
+
+def _listed(dev, what, t, d0, d1, dtype):
+    """A (d0, d1, n) companion of the logits, (d0, d1) standing for n = 1: (pointer, s0, s1, n)."""
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype):
+        _need(torch.device("cuda", dev), what, t, dtype, contiguous=False)  # raises
+        _einval(f"{what} is missing")
+    shape, st = t.shape, t.stride()
+    if len(shape) not in (2, 3) or shape[0] != d0 or shape[1] != d1:
+        _einval(f"{what} must be ({d0}, {d1}) or ({d0}, {d1}, n), got {tuple(shape)}")
+    n = shape[2] if len(shape) == 3 else 1
+    if n > 1 and st[2] != 1:
+        _elayout(f"{what} needs a contiguous last dimension")
+    return t.data_ptr(), st[0], st[1], n
+
+
+def _out_logits(dev, x, out):
+    """The descriptor of a tensor like x that a gradient is written to."""
+    if not (isinstance(out, _Tensor) and out.get_device() == dev and out.dtype is x.dtype):
+        _need(torch.device("cuda", dev), "out", out, x.dtype, contiguous=False)  # raises
+    if out.shape != x.shape:
+        _einval(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
+    return _logits(out, "out", 0, None)[0]
+
+
+def _prepared(dev, ws, nbytes, x):
+    """A prepared workspace: the caller's, or a new one of ``nbytes`` bytes."""
+    if ws is None:
+        ws = _workspace(nbytes, x.device)
+    elif not (isinstance(ws, _Tensor) and ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous()):
+        _need(torch.device("cuda", dev), "workspace", ws, torch.uint8)  # raises
+    if not _is_prepared(ws):
+        ce_workspace_init(ws)
+    return ws
+
+
+def ce_token_logprobs_workspace_bytes(x, top_k=0) -> int:
+    """Workspace bytes of ce_token_logprobs for (d0, d1, V) logits (256: it uses none)."""
+    n = lib.ce_token_logprobs_workspace_bytes(_logits(x, "logits", 0, None)[0], int(top_k))
+    if n == 0:
+        _check(_abi.CE_EINVAL)
+    return int(n)
+
+
+def ce_token_logprobs(x, ids=None, *, top_k=0, entropy=False, stats=False, lse=False, ignore_idx=-100, ws=None):
+    """Log-probabilities of given tokens under the softmax of (d0, d1, V) logits, which are left as they are.
+
+    ``ids`` (d0, d1) or (d0, d1, M) int64, M up to 128, any row strides; those equal to ``ignore_idx`` get 0.
+    ``top_k`` (up to 128): the columns of the largest logits, equal ones by the lower column, and their
+    log-probabilities.  ``entropy``, ``lse`` and ``stats`` (what the gradient takes) on request.  ``ws`` is a
+    workspace of ce_token_logprobs_workspace_bytes bytes to keep between calls.  Returns a TokenLogprobs."""
+    dev = _index(x, "logits")
+    xd, d0, d1, V = _logits(x, "logits", 0, None)
+    top_k = int(top_k)
+    f32, device = torch.float32, x.device
+    ids_ptr, s0, s1, M = (None, 0, 0, 0) if ids is None else _listed(dev, "ids", ids, d0, d1, torch.int64)
+    q = _abi.CeLogprobs(ids_ptr, s0, s1, M, top_k, int(ignore_idx))
+    nbytes = lib.ce_token_logprobs_workspace_bytes(xd, top_k)
+    if nbytes == 0:
+        _check(_abi.CE_EINVAL)
+    logp = None if ids is None else torch.empty(ids.shape, dtype=f32, device=device)
+    ent = torch.empty((d0, d1), dtype=f32, device=device) if entropy else None
+    top_ids = top_logp = None
+    if top_k:
+        top_ids = torch.empty((d0, d1, top_k), dtype=torch.int64, device=device)
+        top_logp = torch.empty((d0, d1, top_k), dtype=f32, device=device)
+    st = torch.empty((d0 * d1, 4), dtype=f32, device=device) if stats else None
+    log_sum = torch.empty((d0, d1), dtype=f32, device=device) if lse else None
+    ws_ptr, ws_bytes = None, 0
+    if nbytes > 256:
+        ws = _prepared(dev, ws, nbytes, x)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
+    _call(dev, lib.ce_token_logprobs, xd, q, None if logp is None else logp.data_ptr(),
+          None if ent is None else ent.data_ptr(), None if log_sum is None else log_sum.data_ptr(),
+          None if top_ids is None else top_ids.data_ptr(), None if top_logp is None else top_logp.data_ptr(),
+          None if st is None else st.data_ptr(), ws_ptr, ws_bytes)
+    return TokenLogprobs(logp, ent, top_ids, top_logp, st, log_sum)
+
+
+def ce_token_logprobs_backward(x, stats, ids=None, dlogprobs=None, *, dentropy=None, top_ids=None, dtop=None,
+                               out=None, ignore_idx=-100):
+    """The gradient of ce_token_logprobs with respect to the logits ``x``, from its ``stats`` and the gradients of
+    its log-probabilities (``dlogprobs``, FP32, contiguous, for ``ids``), its entropy (``dentropy``; the forward was
+    asked for it) and its alternatives' log-probabilities (``dtop`` for ``top_ids``).  Into ``out``, which may be
+    ``x`` itself, or a new tensor."""
+    dev = _index(x, "logits")
+    xd, d0, d1, V = _logits(x, "logits", 0, None)
+    N, f32 = d0 * d1, torch.float32
+    ids_ptr, s0, s1, M, K = None, 0, 0, 0, 0
+    if ids is not None:
+        if dlogprobs is None:
+            _einval("ids need dlogprobs")
+        ids_ptr, s0, s1, M = _listed(dev, "ids", ids, d0, d1, torch.int64)
+    elif dlogprobs is not None:
+        _einval("dlogprobs need ids")
+    if (top_ids is None) != (dtop is None):
+        _einval("top_ids and dtop come together")
+    if top_ids is not None:
+        K = _listed(dev, "top_ids", top_ids, d0, d1, torch.int64)[3]
+    if stats is None:
+        _einval("stats is missing")
+    out = torch.empty_like(x) if out is None else out
+    od = xd if out is x else _out_logits(dev, x, out)
+    q = _abi.CeLogprobs(ids_ptr, s0, s1, M, K, int(ignore_idx))
+    _call(dev, lib.ce_token_logprobs_backward, xd, od, q, _flat(dev, "stats", stats, f32, 4 * N),
+          _flat(dev, "dlogprobs", dlogprobs, f32, N * M), _flat(dev, "dentropy", dentropy, f32, N),
+          _flat(dev, "top_ids", top_ids, torch.int64, N * K), _flat(dev, "dtop", dtop, f32, N * K))
+    return out
+
+
+class TokenLogprobsFn(torch.autograd.Function):
+    """Autograd form of ce_token_logprobs: the logits, 16 bytes a row and the ids are kept."""
+
+    @staticmethod
+    def forward(ctx, x, ids, top_k, entropy, ignore_idx, ws):
+        if x.dim() != 3:
+            _einval("logits must be a 3-d (d0, d1, V) tensor")
+        flat = _own_rows(x.detach())
+        r = ce_token_logprobs(flat, ids, top_k=top_k, entropy=entropy, stats=ctx.needs_input_grad[0],
+                              ignore_idx=ignore_idx, ws=ws)
+        ctx.ignore_idx = ignore_idx
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, ids, r.stats, r.top_ids)
+        if r.top_ids is not None:
+            ctx.mark_non_differentiable(r.top_ids)
+        return r.logprobs, r.entropy, r.top_ids, r.top_logprobs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dentropy, _, dtop):
+        x, ids, stats, top_ids = ctx.saved_tensors
+        if dlogp is None and dentropy is None and dtop is None:
+            return (None,) * 6
+
+        def flat(t):
+            return None if t is None else t.float().contiguous()
+
+        x = _own_rows(x)
+        dx = ce_token_logprobs_backward(x, stats, None if dlogp is None else ids, flat(dlogp), dentropy=flat(dentropy),
+                                        top_ids=None if dtop is None else top_ids, dtop=flat(dtop),
+                                        out=torch.empty_like(x), ignore_idx=ctx.ignore_idx)
+        return (dx,) + (None,) * 5
+
+
+def token_logprobs(logits, ids=None, *, top_k=0, entropy=False, ignore_idx=-100, ws=None):
+    """Log-probabilities of ``ids``, the entropy and the ``top_k`` alternatives as ce_token_logprobs gives them, with
+    a gradient: of the log-probabilities, of the entropy and of the alternatives' log-probabilities.  Returns a
+    TokenLogprobs (without stats and lse)."""
+    if ids is None and not top_k and not entropy:
+        _einval("nothing is asked for: ids, top_k or entropy")
+    logp, ent, top_ids, top_logp = TokenLogprobsFn.apply(logits, ids, int(top_k), bool(entropy), int(ignore_idx), ws)
+    return TokenLogprobs(logp, ent, top_ids, top_logp, None, None)
+
+
+# ---- distillation ----------------------------------------------------------------------------------------
+
+_TEACHERS = {"logits": _abi.CE_TEACHER_LOGITS, "logprobs": _abi.CE_TEACHER_LOGPROBS}
+
+
+def ce_distill_workspace_bytes(x) -> int:
+    """Workspace bytes of ce_distill_fwd_bwd for (d0, d1, V) logits."""
+    n = lib.ce_distill_workspace_bytes(_logits(x, "logits", 0, None)[0])
+    if n == 0:
+        _check(_abi.CE_EINVAL)
+    return int(n)
+
+
+def ce_distill_fwd_bwd(x, teacher_ids, teacher_values, temperature=1.0, reduce_loss=False, *, teacher="logits",
+                       teacher_len=None, out=None, want_grad=True, grad_out=None, loss=None, n_valid=None, ws=None):
+    """Distillation of (d0, d1, V) logits from a teacher's top logits: T^2 times the Kullback-Leibler divergence of
+    softmax(x / T) from the teacher's distribution, and its gradient, written over ``x`` or into ``out``.
+
+    ``teacher_ids`` (d0, d1, K) int64 and ``teacher_values`` (d0, d1, K) FP32 or BF16, K up to 128, any row strides:
+    ``teacher="logits"``, the softmax of their values at T is the whole distribution; ``"logprobs"``, they are
+    log-probabilities (at T), and what they leave of 1 goes to all the other columns as one class.  ``teacher_len``
+    [N] int32: how many entries of a row, the first ones, count; a row of none is left out.  ``reduce_loss`` and
+    ``grad_out`` as in ce_fwd_bwd_fused; ``want_grad=False`` computes the loss alone and leaves ``x`` as it is.
+    Returns (loss [N] or [1], n_valid if given or None)."""
+    dev = _index(x, "logits")
+    xd, d0, d1, V = _logits(x, "logits", 0, None)
+    N, f32 = d0 * d1, torch.float32
+    code = reduction_code(reduce_loss)
+    if teacher not in _TEACHERS:
+        _einval(f"teacher {teacher!r} is not one of {sorted(_TEACHERS)}")
+    ids_ptr, is0, is1, K = _listed(dev, "teacher_ids", teacher_ids, d0, d1, torch.int64)
+    if not isinstance(teacher_values, _Tensor):
+        _einval("teacher_values must be a torch tensor")
+    val_ptr, vs0, vs1, Kv = _listed(dev, "teacher_values", teacher_values, d0, d1, teacher_values.dtype)
+    if K != Kv:
+        _einval(f"{K} teacher_ids and {Kv} teacher_values a row")
+    d = _abi.CeDistill(ids_ptr, is0, is1, val_ptr, vs0, vs1, _code(teacher_values.dtype, -1), _TEACHERS[teacher], K,
+                       float(temperature), _flat(dev, "teacher_len", teacher_len, torch.int32, N))
+    od = None
+    if want_grad:
+        od = xd if out is None or out is x else _out_logits(dev, x, out)
+    elif out is not None:
+        _einval("out without want_grad")
+    n_loss = N if code == _abi.CE_REDUCE_NONE else 1
+    loss = torch.empty(n_loss, dtype=f32, device=x.device) if loss is None else loss
+    loss_ptr = _flat(dev, "loss", loss, f32, n_loss)
+    g_ptr = _flat(dev, "grad_out", grad_out, f32, n_loss)
+    n_ptr = _flat(dev, "n_valid", n_valid, torch.int32, 1)
+    nbytes = lib.ce_distill_workspace_bytes(xd)
+    if nbytes == 0:
+        _check(_abi.CE_EINVAL)
+    ws = _prepared(dev, ws, nbytes, x)
+    _call(dev, lib.ce_distill_fwd_bwd, xd, od, d, code, g_ptr, loss_ptr, n_ptr, ws.data_ptr(), ws.numel())
+    return loss, n_valid
+
+
+class DistillationLoss(torch.autograd.Function):
+    """The loss, with the gradient staged in place in ``inp`` for an upstream gradient of 1, which the backward then
+    applies (ce_scale_grad_inplace), as for the cross-entropy.  Without a gradient to give, ``inp`` is left as it is."""
+
+    @staticmethod
+    def forward(ctx, inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws):
+        buf = inp.detach()
+        if buf.dim() != 3:
+            _einval("logits must be a 3-d (d0, d1, V) tensor")
+        loss, _ = ce_distill_fwd_bwd(buf, teacher_ids, teacher_values, temperature, reduce_loss, teacher=teacher,
+                                     teacher_len=teacher_len, want_grad=ctx.needs_input_grad[0], ws=ws)
+        ctx.reduced = reduction_code(reduce_loss) != _abi.CE_REDUCE_NONE
+        ctx.save_for_backward(buf)
+        return loss[0] if ctx.reduced else loss.view(buf.shape[:2])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss):
+        (buf,) = ctx.saved_tensors
+        ce_scale_grad_inplace(buf, grad_loss, per_row=not ctx.reduced)
+        return (buf,) + (None,) * 7
+
+
+def distillation_loss(inp, teacher_ids, teacher_values, temperature=1.0, reduce_loss=False, *, teacher="logits",
+                      teacher_len=None, ws=None):
+    """ce_distill_fwd_bwd through autograd: the loss ((d0, d1), or a scalar with a reduction), whose gradient reaches
+    ``inp`` and is staged in its storage, as parallel_cross_entropy's.  The teacher's values are constants."""
+    _constants(teacher_values=teacher_values)
+    return DistillationLoss.apply(inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws)

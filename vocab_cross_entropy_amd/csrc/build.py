@@ -35,7 +35,7 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
           "-ffp-contract=on"]
 
 SOURCES = ["ce_kernels.hip", "ce_gemm.hip", "ce_stream_ref.hip", "ce_process.hip", "ce_embed.hip", "ce_norm.hip",
-           "ce_api.cpp", "ce_linear.cpp", "ce_ops.cpp"]
+           "ce_logprobs.hip", "ce_distill.hip", "ce_api.cpp", "ce_linear.cpp", "ce_ops.cpp"]
 
 
 def _run(cmd):

@@ -1,0 +1,458 @@
+// Distillation from a teacher's top logits: the loss of every row and its gradient,
+// one read of the student's logits and one write of the gradient.
+//
+// Row of logits x, temperature T, the teacher's K entries (column c_k, value t_k):
+//   q = softmax(x / T)
+//   p_k = softmax_k(t / T), and nothing is left (r = 0), or p_k = exp(t_k), r = max(0, 1 - sum_k p_k)
+//   loss = T^2 (sum_k p_k (log p_k - log q_ck) + r (log r - log q_o)),  q_o = sum of q over unnamed columns
+//   dx_v = s T (q_v S - P_v - [v unnamed] q_v r / q_o),   S = sum_k p_k + r, P_v = sum of p_k with c_k = v
+//
+// The sum of the exponentials is taken over the unnamed columns alone (the named ones
+// are set to -inf in their registers, found by a bitmap of the chunk in LDS), relative to
+// their own maximum; the named ones, a few, are added in 64 bits.  So q_o keeps its digits
+// where the named columns hold nearly everything, and so does q_c - p_c, whose terms
+// are both near 1 there.  All that is per entry or per row is 64-bit, by one wave.
+//
+// Bound: one read and one write of the logits.  A chunk of a row stays in a
+// workgroup's registers between its sums and its gradient, and a row's chunks exchange
+// six words each through the workspace, as in ce_fwd_bwd_fused (whose chunk shapes these are).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ce_internal.h"
+#include "ce_row.h"
+
+namespace vce {
+namespace {
+
+constexpr int kWords = 6;               // per chunk: m2, sum of unnamed, log-sum of named (2), sum of p z (2)
+constexpr int kEntries = kDistillMaxTop / 64;  // entries a lane of the wave that handles them
+constexpr double kLn2d = 0.693147180559945309417;
+
+// a 64-bit value as two FP32 words, and back (an infinity or NaN stands in the first)
+__device__ __forceinline__ void split64(double v, float* hi, float* lo) {
+  *hi = (float)v;
+  const double d = v - (double)*hi;
+  *lo = d == d && fabs(d) != (double)INFINITY ? (float)d : 0.f;
+}
+// log2(2^a + 2^b + ...) over the wave's lanes (-inf: nothing)
+__device__ __forceinline__ double wave_log_sum(double a) {
+  const double m = wave_largest64(a);
+  const double s = wave_sum64(a == -(double)INFINITY ? 0.0 : exp2(a - m));
+  return m == -(double)INFINITY ? (s == s ? m : s) : m + log2(s);
+}
+
+template <int T>
+__device__ void finish_distill(const DistillArgs& a, uint32_t tag, bool ws_ok) {
+  __shared__ double part[T / 64];
+  uint32_t spins = 0;
+  bool ok = true;
+  double acc = 0.0;
+  for (int64_t base = 0; base < a.N; base += 4 * T) {
+    unsigned long long first[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = base + i * T + threadIdx.x;
+      first[i] = peek_word(a.row_words + (at < a.N ? at : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = base + i * T + threadIdx.x;
+      uint32_t w = 0;
+      ok = ok && await_word(a.row_words + (at < a.N ? at : 0), tag, first[i], spins, &w);
+      acc += at < a.N ? (double)__uint_as_float(w) : 0.0;
+    }
+  }
+  if (!ok) atomicOr(&a.hdr->status, 1u);
+  acc = wave_sum64(acc);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
+  ok = __syncthreads_and(ok);
+  if (threadIdx.x != 0) return;
+  if (a.reduce != CE_REDUCE_NONE) {
+    double total = 0.0;
+    for (int i = 0; i < T / 64; ++i) total += part[i];
+    if (a.reduce == CE_REDUCE_MEAN) total /= (double)(a.n ? *a.n : (int32_t)a.N);
+    a.loss[0] = ok && ws_ok ? (float)total : __uint_as_float(0x7fc00000u);
+  }
+  next_epoch(a.hdr);
+}
+
+template <int DT, int T, int P, bool GRAD>
+__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void k_distill(DistillArgs a) {
+  constexpr int E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
+  __shared__ float sh_max[W], sh_sum[W];
+  __shared__ __align__(8) uint8_t named[T * 8];  // byte tid * 8 + j: which columns of slot j's vector are named
+  __shared__ float words[kMaxChunks * kWords];
+  __shared__ float bc[4];  // c_hi, c_lo, the unnamed columns' factor
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
+  const uint32_t C = (uint32_t)a.chunks;
+  const uint32_t in_launch = blockIdx.x / C;
+  const int64_t r = a.row0 + in_launch;
+  const uint32_t k = blockIdx.x - in_launch * C;
+  WsView ws{0u, true, 0ull};
+  if (a.hdr) ws = view_workspace(a.hdr, a.ws_bytes);
+  const bool ends = a.hdr && r == a.N - 1 && k == C - 1;
+  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const char* const row = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
+  char* const out = GRAD ? a.out + (i0 * a.os0 + i1 * a.os1) * EB : nullptr;
+  const uint32_t lo = k * (uint32_t)a.chunk_cols;
+  const uint32_t cols = (uint32_t)a.V - lo < (uint32_t)a.chunk_cols ? (uint32_t)a.V - lo : (uint32_t)a.chunk_cols;
+  int L = a.K;
+  if (a.len) {
+    L = a.len[r];
+    L = L < 0 ? 0 : L > a.K ? a.K : L;
+  }
+  const auto row_loss = [&](float loss) {  // by one thread of the row
+    if (a.reduce == CE_REDUCE_NONE) a.loss[r] = loss;
+    if (a.hdr) put_word(a.row_words + r, ws.tag, __float_as_uint(loss));
+  };
+
+  if (L == 0) {  // left out: loss 0, gradient 0, the logits not read
+    if constexpr (GRAD) {
+      for (uint32_t i = tid; i * E < cols; i += T) store_vec<DT>(out + (size_t)lo * EB, cols, i, u32x4v{0u, 0u, 0u, 0u});
+    }
+    if (k == 0 && tid == 0) row_loss(0.f);
+  } else {
+    // ---- the entries (wave 0), then the chunk
+    int64_t id[kEntries];
+    float tv[kEntries];
+    if (tid < 64) {
+      const int64_t* ids = a.ids + i0 * a.is0 + i1 * a.is1;
+      const char* const t = a.teacher + (i0 * a.ts0 + i1 * a.ts1) * (a.tdtype == CE_BF16 ? 2 : 4);
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        const int at = i * 64 + (int)lane;
+        id[i] = at < L ? ids[at] : -1;
+        tv[i] = at < L ? (a.tdtype == CE_BF16 ? load_logit<CE_BF16>(t, at) : load_logit<CE_F32>(t, at)) : 0.f;
+      }
+    }
+    u32x4v v[P];
+    load_chunk<DT, T, P>(row + (size_t)lo * EB, cols, v);
+    float up = a.g ? a.g[a.reduce == CE_REDUCE_NONE ? r : 0] : 1.f;
+    reinterpret_cast<uint64_t*>(named)[tid] = 0ull;
+    __syncthreads();
+
+    // ---- wave 0: the student's logits of the entries here, the bitmap, the teacher's probabilities
+    bool here[kEntries], first[kEntries];
+    double z[kEntries], p[kEntries], logp[kEntries];
+    double mass = 0.0, plogp = 0.0;
+    bool bad = false;
+    if (tid < 64) {
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        const bool is = i * 64 + (int)lane < L;
+        bad |= is && (id[i] < 0 || id[i] >= a.V);
+        here[i] = is && id[i] >= lo && id[i] < (int64_t)lo + cols;
+        first[i] = false;
+        z[i] = 0.0;
+        if (here[i]) {
+          const uint32_t c = (uint32_t)(id[i] - lo), vec = c / E;
+          const uint32_t at = (vec % T) * 8 + vec / T;  // its byte
+          const uint32_t bit = 1u << (c % E + 8 * (at & 3));
+          first[i] = !(atomicOr(reinterpret_cast<uint32_t*>(named) + (at >> 2), bit) & bit);
+          z[i] = (double)load_logit<DT>(row, id[i]) * (double)a.kb;  // base 2, as the sums' exponents
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < 64) {
+      if (a.kind == CE_TEACHER_LOGITS) {
+        double t[kEntries], top = -(double)INFINITY;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          t[i] = i * 64 + (int)lane < L ? (double)tv[i] * a.inv_t : -(double)INFINITY;
+          top = fmax(top, t[i]);
+        }
+        top = wave_largest64(top);
+        double d = 0.0;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          p[i] = exp(t[i] - top);
+          d += p[i];
+        }
+        d = wave_sum64(d);
+        const double logd = log(d);
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          p[i] /= d;
+          logp[i] = t[i] - top - logd;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          logp[i] = i * 64 + (int)lane < L ? (double)tv[i] : -(double)INFINITY;
+          p[i] = exp(logp[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        mass += p[i];
+        plogp += p[i] == 0.0 ? 0.0 : p[i] * logp[i];
+      }
+      mass = wave_sum64(mass);
+      plogp = wave_sum64(plogp);
+      bad = __any(bad);
+    }
+
+    // ---- the unnamed columns: maximum and sum
+    float m = -INFINITY;
+    const uint64_t flags = reinterpret_cast<const uint64_t*>(named)[tid];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const uint32_t b = (uint32_t)(flags >> (8 * j)) & 0xffu;
+      if (b) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (!(b >> e & 1u)) continue;
+          if constexpr (DT == CE_BF16)
+            v[j][e / 2] = e & 1 ? (v[j][e / 2] & 0xffffu) | 0xff800000u : (v[j][e / 2] & 0xffff0000u) | 0xff80u;
+          else
+            v[j][e] = 0xff800000u;
+        }
+      }
+      m = largest<DT>(v[j], m);
+    }
+    m = wave_largest(m);
+    if (lane == 0) sh_max[tid >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = fmaxf(m, sh_max[i]);
+    const float m2 = m == -INFINITY ? 0.f : m * a.kb;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      relaunch(v[j]);
+      float f[E];
+      unpack_vec<DT>(v[j], f);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        s0 += exp2_hw(__builtin_fmaf(f[e], a.kb, -m2));
+        s1 += exp2_hw(__builtin_fmaf(f[e + 1], a.kb, -m2));
+      }
+    }
+    s0 = wave_sum(s0 + s1);
+    if (lane == 0) sh_sum[tid >> 6] = s0;
+    __syncthreads();
+
+    // ---- wave 0: the row, over the chunks
+    if (tid < 64) {
+      s0 = sh_sum[0];
+#pragma unroll
+      for (int i = 1; i < W; ++i) s0 += sh_sum[i];
+      double named_log = -(double)INFINITY, pz = 0.0;
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) pz += here[i] && p[i] != 0.0 ? p[i] * z[i] : 0.0;
+      {
+        double top = -(double)INFINITY;
+        bool nan = false;  // which the maxima pass over
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          if (first[i]) top = fmax(top, z[i]);
+          nan |= here[i] && z[i] != z[i];
+        }
+        top = wave_largest64(top);
+        if (top != -(double)INFINITY) {
+          double d = 0.0;
+#pragma unroll
+          for (int i = 0; i < kEntries; ++i) d += first[i] ? exp2(z[i] - top) : 0.0;
+          named_log = top + log2(wave_sum64(d));
+        }
+        if (__any(nan)) named_log = __builtin_nan("");
+      }
+      pz = wave_sum64(pz);
+      // lane c: chunk c's unnamed and named columns, as base-2 logarithms of their sums
+      double rest = -(double)INFINITY, most = -(double)INFINITY, cross = 0.0;
+      bool ok = true;
+      float w[kWords];
+      w[0] = m2;
+      w[1] = s0;
+      split64(named_log, &w[2], &w[3]);
+      split64(pz, &w[4], &w[5]);
+      if (C > 1) {
+        unsigned long long* const slots = a.slots + (size_t)r * C * kWords;
+        if (lane < kWords && !withheld(ws, r, (int)k)) {
+          float mine = w[0];
+#pragma unroll
+          for (int q = 1; q < kWords; ++q) mine = (int)lane == q ? w[q] : mine;
+          put_word(slots + k * kWords + lane, ws.tag, __float_as_uint(mine));
+        }
+        uint32_t spins = 0;
+        for (uint32_t i = lane; i < C * kWords; i += 64) {
+          uint32_t got = 0x7fc00000u;
+          ok &= await_word(slots + i, ws.tag, peek_word(slots + i), spins, &got);
+          words[i] = __uint_as_float(got);
+        }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+        if (lane < C) {
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) w[q] = words[lane * kWords + q];
+        }
+        ok = __all(ok);
+      }
+      if (lane < C) {
+        rest = w[1] == 0.f ? -(double)INFINITY : (double)w[0] + log2((double)w[1]);
+        most = (double)w[2] + (double)w[3];
+        cross = (double)w[4] + (double)w[5];
+      }
+      ok = ok && ws.ok;
+      if (!ok && lane == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
+      rest = wave_log_sum(rest);
+      most = wave_log_sum(most);
+      cross = wave_sum64(cross);
+      const double hi = fmax(rest, most);
+      const double lse = rest != rest || most != most ? __builtin_nan("")
+                         : hi == -(double)INFINITY    ? hi
+                                                      : hi + log2(exp2(rest - hi) + exp2(most - hi));
+      // what the teacher leaves, to the unnamed columns; nothing where none of them can take it
+      double left = 0.0;
+      if (a.kind == CE_TEACHER_LOGPROBS && rest != -(double)INFINITY) left = fmax(0.0, 1.0 - mass);
+      if (mass != mass) left = mass;
+      const double S = mass + left;
+      double loss = plogp - (cross - mass * lse) * kLn2d;
+      if (left != 0.0) loss += left * (log(left) - (rest - lse) * kLn2d);
+      loss *= a.t * a.t;
+      double s = (double)up * a.t;
+      if (a.reduce == CE_REDUCE_MEAN) s /= (double)(a.n ? *a.n : (int32_t)a.N);
+      if (bad || !ok) s = loss = __builtin_nan("");
+      if (k == 0 && lane == 0) row_loss((float)loss);
+      if constexpr (GRAD) {
+        const float c_hi = (float)lse;
+        if (lane == 0) {
+          bc[0] = c_hi;
+          bc[1] = DT == CE_F32 ? (float)(lse - (double)c_hi) : 0.f;
+          bc[2] = (float)(s * (S - (left == 0.0 ? 0.0 : left * exp2(lse - rest))));
+        }
+        // the named columns' gradients, into z; entries of the same column add up, in order
+        const bool twice = __any([&] {
+          bool d = false;
+#pragma unroll
+          for (int i = 0; i < kEntries; ++i) d |= here[i] && !first[i];
+          return d;
+        }());
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          double all = p[i];
+          if (twice) {
+            all = 0.0;
+            for (int q = 0; q < L; ++q) {
+              const int64_t other = __shfl(q < 64 ? id[0] : id[kEntries - 1], q & 63);
+              const double add = __shfl(q < 64 ? p[0] : p[kEntries - 1], q & 63);
+              all += other == id[i] ? add : 0.0;
+            }
+          }
+          z[i] = s * (exp2(z[i] - lse) * S - all);
+        }
+      }
+    }
+    if constexpr (GRAD) {
+      __syncthreads();
+      const float c_hi = bc[0], c_lo = bc[1], f_un = bc[2];
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        relaunch(v[j]);
+        float f[E];
+        unpack_vec<DT>(v[j], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float t = __builtin_fmaf(f[e], a.kb, -c_hi);
+          if constexpr (DT == CE_F32) t -= c_lo;
+          f[e] = exp2_hw(t) * f_un;
+        }
+        store_vec<DT>(out + (size_t)lo * EB, cols, j * T + tid, pack_vec<DT>(f));
+      }
+      __syncthreads();
+      if (tid < 64) {  // over the zeros that were written for the named columns
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i)
+          if (here[i]) store_logit<DT>(out, id[i], (float)z[i]);
+      }
+    }
+  }
+  if (ends) finish_distill<T>(a, ws.tag, ws.ok);
+}
+
+// Rows that have an entry.
+__global__ __launch_bounds__(1024) void k_distill_count(const int32_t* len, int64_t N, int32_t K, int32_t* n) {
+  __shared__ int part[16];
+  int c = 0;
+  for (int64_t r = threadIdx.x; r < N; r += 1024) c += len ? len[r] > 0 : K > 0;
+  c = wave_count64(c);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    c = 0;
+    for (int i = 0; i < 16; ++i) c += part[i];
+    *n = c;
+  }
+}
+
+template <int DT, int T, int P>
+void launch_distill_shape(const DistillArgs& a, dim3 grid, hipStream_t stream) {
+  if (a.out) hipLaunchKernelGGL((k_distill<DT, T, P, true>), grid, dim3(T), 0, stream, a);
+  else hipLaunchKernelGGL((k_distill<DT, T, P, false>), grid, dim3(T), 0, stream, a);
+}
+template <int DT>
+void launch_distill_dt(const DistillArgs& a, FusedShape s, dim3 grid, hipStream_t stream) {
+  if (s.threads == 512) launch_distill_shape<DT, 512, 8>(a, grid, stream);
+  else if (s.vecs == 8) launch_distill_shape<DT, 256, 8>(a, grid, stream);
+  else if (s.vecs == 4) launch_distill_shape<DT, 256, 4>(a, grid, stream);
+  else if (s.vecs == 2) launch_distill_shape<DT, 256, 2>(a, grid, stream);
+  else launch_distill_shape<DT, 256, 1>(a, grid, stream);
+}
+
+int64_t vec_cols(int32_t dtype) { return dtype == CE_BF16 ? 8 : 4; }
+
+}  // namespace
+
+int64_t distill_max_cols(int32_t dtype) { return (int64_t)4096 * vec_cols(dtype) * kMaxChunks; }
+
+void distill_plan(int64_t V, int32_t dtype, int64_t* chunks, int64_t* chunk_cols) {
+  const int64_t E = vec_cols(dtype), vecs = (V + E - 1) / E;
+  int64_t n = fused_auto_chunks(dtype, V);
+  while ((vecs + n - 1) / n > 4096) ++n;  // that plan leaves the columns around the whole vectors to other lanes
+  *chunk_cols = (vecs + n - 1) / n * E;
+  *chunks = (V + *chunk_cols - 1) / *chunk_cols;
+}
+
+size_t distill_workspace(int64_t N, int64_t V, int32_t dtype) {
+  int64_t chunks, cols;
+  distill_plan(V, dtype, &chunks, &cols);
+  return kWsHeaderBytes + (size_t)N * 8 + (chunks > 1 ? (size_t)N * chunks * kWords * 8 : 0);
+}
+
+hipError_t launch_distill(DistillArgs a, void* ws, int32_t* n_valid, hipStream_t stream, hipEvent_t ev0,
+                          hipEvent_t ev1) {
+  hipError_t e = hipSuccess;
+  WsHeader* const hdr = static_cast<WsHeader*>(ws);
+  // n is the number of rows without lengths; with them it is counted first
+  if (n_valid || (a.reduce == CE_REDUCE_MEAN && (a.len || a.N == 0))) {
+    int32_t* const n = n_valid ? n_valid : &hdr->n_valid;
+    hipLaunchKernelGGL(k_distill_count, dim3(1), dim3(1024), 0, stream, a.len, a.N, a.K, n);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    a.n = n;
+  }
+  if (a.N == 0)  // the mean of no rows is 0/0
+    return a.reduce == CE_REDUCE_NONE ? hipSuccess
+                                      : launch_mean(nullptr, 0, a.reduce == CE_REDUCE_MEAN ? a.n : nullptr, a.loss, stream);
+  if (ev0 && (e = hipEventRecord(ev0, stream)) != hipSuccess) return e;
+  if (a.chunks > 1 || a.reduce != CE_REDUCE_NONE) {
+    a.hdr = hdr;
+    a.row_words = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + kWsHeaderBytes);
+    a.slots = a.row_words + a.N;
+    a.ws_bytes = distill_workspace(a.N, a.V, a.dtype);
+  }
+  const FusedShape shape = fused_shape_for(a.chunk_cols / vec_cols(a.dtype));
+  const int64_t rows = kMaxGridItems / a.chunks;  // a launch
+  for (a.row0 = 0; a.row0 < a.N; a.row0 += rows) {
+    const int64_t n = a.N - a.row0 < rows ? a.N - a.row0 : rows;
+    const dim3 grid((uint32_t)(n * a.chunks));
+    if (a.dtype == CE_BF16) launch_distill_dt<CE_BF16>(a, shape, grid, stream);
+    else launch_distill_dt<CE_F32>(a, shape, grid, stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (ev1) e = hipEventRecord(ev1, stream);
+  return e;
+}
+
+}  // namespace vce

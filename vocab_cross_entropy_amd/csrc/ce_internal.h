@@ -306,6 +306,92 @@ struct NormGradArgs {
 size_t norm_grad_workspace(int64_t N, int64_t D);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
 
+// Token log-probabilities (ce_logprobs.hip) and distillation (ce_distill.hip): kernels that hold a chunk of a row.
+constexpr int kMaxChunks = 64;                         // of one row
+constexpr int64_t kMaxGridItems = (int64_t)1 << 22;    // workgroups of a launch (a launch holds below 2^32 work-items)
+constexpr int kLogprobMaxList = 128;                   // given tokens, and alternatives, of a row
+constexpr int kLogprobBwdT = 256, kLogprobBwdP = 4;    // threads and vectors a thread of the gradient
+struct LogprobArgs {
+  const char* x;
+  int32_t dtype;
+  int64_t N, d1, V, s0, s1;
+  const int64_t* ids;         // M tokens per row, or NULL
+  int64_t is0, is1;
+  int32_t M, K;
+  int64_t ignore_idx;
+  float* logp;                // [N, M]
+  float* entropy;             // [N] or NULL
+  float* lse;                 // [N] or NULL
+  int64_t* top_ids;           // [N, K]
+  float* top_logp;            // [N, K]
+  float* stats;               // [N][4] or NULL
+  // set by logprob_plan
+  int32_t shape;
+  int64_t chunks, chunk_cols;
+  // set by the launcher
+  int64_t row0;               // the launch's first row
+  WsHeader* hdr;              // with more than one chunk
+  unsigned long long* done;   // [N] tagged words: the row has been brought together
+  unsigned long long* slots;  // [N][chunks] tagged words of a chunk: its sums, then its K keys
+  unsigned long long ws_bytes;
+};
+int64_t logprob_max_cols(int32_t dtype);  // the longest row that kMaxChunks hold
+void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols);
+size_t logprob_workspace(int64_t N, int64_t V, int32_t dtype, int32_t K);  // 0: none is needed
+hipError_t launch_logprobs(LogprobArgs a, void* ws, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
+
+struct LogprobGradArgs {
+  const char* x;
+  char* out;
+  int32_t dtype;
+  int64_t N, d1, V, s0, s1, os0, os1;
+  const int64_t* ids;         // M tokens per row, or NULL
+  int64_t is0, is1;
+  int32_t M, K;
+  int64_t ignore_idx;
+  const float* stats;         // [N][4]
+  const float* dlogp;         // [N, M]
+  const float* dentropy;      // [N] or NULL
+  const int64_t* top_ids;     // [N, K]
+  const float* dtop;          // [N, K]
+  // set by the launcher
+  int64_t chunks, chunk_cols, row0;
+};
+hipError_t launch_logprobs_bwd(LogprobGradArgs a, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
+
+constexpr int kDistillMaxTop = 128;
+struct DistillArgs {
+  const char* x;
+  char* out;                  // or NULL: the loss alone
+  int32_t dtype;
+  int64_t N, d1, V, s0, s1, os0, os1;
+  const int64_t* ids;         // K columns per row
+  int64_t is0, is1;
+  const char* teacher;        // K values per row
+  int64_t ts0, ts1;
+  int32_t tdtype, kind, K;
+  const int32_t* len;         // [N] entries of a row, or NULL: K
+  double t, inv_t;            // the temperature
+  float kb;                   // log2(e) / temperature
+  int32_t reduce;
+  const float* g;             // upstream gradient ([N] or [1]); NULL = 1
+  float* loss;                // [N] or [1]
+  // set by distill_plan
+  int64_t chunks, chunk_cols;
+  // set by the launcher
+  int64_t row0;
+  const int32_t* n;           // rows with an entry; NULL: N
+  WsHeader* hdr;              // with more than one chunk or a reduction
+  unsigned long long* row_words;  // [N] tagged losses
+  unsigned long long* slots;  // [N][chunks][6]
+  unsigned long long ws_bytes;
+};
+int64_t distill_max_cols(int32_t dtype);
+void distill_plan(int64_t V, int32_t dtype, int64_t* chunks, int64_t* chunk_cols);
+size_t distill_workspace(int64_t N, int64_t V, int32_t dtype);
+hipError_t launch_distill(DistillArgs a, void* ws, int32_t* n_valid, hipStream_t stream, hipEvent_t ev0,
+                          hipEvent_t ev1);
+
 // The instrumented build's phase-stamp buffer when it holds `bytes`, else NULL
 // (always NULL in the normal build).
 unsigned long long* phase_buffer(size_t bytes);

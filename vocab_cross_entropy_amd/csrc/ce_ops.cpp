@@ -1,9 +1,11 @@
-// C ABI of the operators around the loss: logit processing, embedding and RMS
-// norm.  Argument checks, then one call of the launcher; every check runs
+// C ABI of the operators around the loss: logit processing, embedding, RMS norm,
+// token log-probabilities and distillation.  Argument checks, then one call of the launcher; every check runs
 // before the first HIP call, so a rejected call enqueues nothing.
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
+
+#include <initializer_list>
 
 #include <hip/hip_runtime_api.h>
 
@@ -166,6 +168,74 @@ ce_status process(const ce_logits* x, const ce_logits* out, const ce_process* p,
   return launched(vce::launch_process(a, backward, stream, e0, e1), backward ? "process backward" : "process");
 }
 
+// ---- token log-probabilities and distillation: whole rows
+ce_status check_whole_rows(const ce_logits* x, int64_t most) {
+  const ce_status st = vce::check_logits_desc(x);
+  if (st) return st;
+  if (x->vocab_start != 0 || x->v_local != x->vocab_total)
+    return ofail(CE_ELAYOUT, "this call needs unsharded logits (vocab_start 0, v_local == vocab_total)");
+  if (x->v_local > most)
+    return ofail(CE_ELAYOUT, "rows of %lld columns exceed %lld", (long long)x->v_local, (long long)most);
+  return CE_OK;
+}
+
+// `out` takes x's rows in place or lies elsewhere
+ce_status check_gradient_rows(const ce_logits* x, const ce_logits* out) {
+  const ce_status st = vce::check_logits_desc(out);
+  if (st) return st;
+  if (x->dtype != out->dtype) return ofail(CE_EDTYPE, "logits and gradient differ in dtype");
+  if (x->d0 != out->d0 || x->d1 != out->d1 || x->v_local != out->v_local || x->vocab_start != out->vocab_start ||
+      x->vocab_total != out->vocab_total)
+    return ofail(CE_ELAYOUT, "logits and gradient differ in shape");
+  const int eb = elem_bytes(x->dtype);
+  if (rows_meet(row_set(x->data, x->d0, x->d1, x->s0, x->s1, x->v_local, eb),
+                row_set(out->data, out->d0, out->d1, out->s0, out->s1, out->v_local, eb), true))
+    return overlap("the gradient", "the logits");
+  return CE_OK;
+}
+
+ce_status check_prepared(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws || ws_bytes < need)
+    return ofail(CE_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+  if ((uintptr_t)ws % 256u) return ofail(CE_EWORKSPACE, "workspace must be 256-byte aligned");
+  return CE_OK;
+}
+
+ce_status check_aligned(std::initializer_list<const void*> ps, unsigned bytes, const char* what) {
+  for (const void* p : ps)
+    if ((uintptr_t)p % bytes) return ofail(CE_ELAYOUT, "%s is not %u-byte aligned", what, bytes);
+  return CE_OK;
+}
+
+ce_status check_logprobs(const ce_logits* x, const ce_logprobs* q) {
+  if (!q) return ofail(CE_EINVAL, "logprobs descriptor is NULL");
+  if (q->M < 0 || q->M > vce::kLogprobMaxList || q->K < 0 || q->K > vce::kLogprobMaxList)
+    return ofail(CE_EINVAL, "M = %d or K = %d outside [0, %d]", q->M, q->K, vce::kLogprobMaxList);
+  if (q->K > x->v_local)
+    return ofail(CE_EINVAL, "%d alternatives of %lld columns", q->K, (long long)x->v_local);
+  if (q->M > 0 && x->d0 > 0 && !q->ids) return ofail(CE_EINVAL, "ids is NULL");
+  if ((uintptr_t)q->ids % 8u || q->ids_s0 < 0 || q->ids_s1 < 0)
+    return ofail(CE_ELAYOUT, "ids misaligned or negative stride");
+  return CE_OK;
+}
+
+ce_status check_distill(const ce_logits* x, const ce_distill* d) {
+  if (!d) return ofail(CE_EINVAL, "distillation descriptor is NULL");
+  if (d->K < 1 || d->K > vce::kDistillMaxTop)
+    return ofail(CE_EINVAL, "%d entries a row outside [1, %d]", d->K, vce::kDistillMaxTop);
+  if (!known(d->values_dtype)) return ofail(CE_EDTYPE, "unsupported dtype %d of the teacher's values", d->values_dtype);
+  if (d->kind != CE_TEACHER_LOGITS && d->kind != CE_TEACHER_LOGPROBS)
+    return ofail(CE_EINVAL, "unknown kind of teacher values %d", d->kind);
+  if (!(d->temperature >= 0x1p-32f && d->temperature <= 0x1p32f))
+    return ofail(CE_EINVAL, "temperature %g outside [2^-32, 2^32]", (double)d->temperature);
+  if (x->d0 > 0 && (!d->ids || !d->values)) return ofail(CE_EINVAL, "the teacher's ids or values are NULL");
+  if ((uintptr_t)d->ids % 8u || d->ids_s0 < 0 || d->ids_s1 < 0)
+    return ofail(CE_ELAYOUT, "ids misaligned or negative stride");
+  if (off(d->values, d->values_dtype) || d->values_s0 < 0 || d->values_s1 < 0)
+    return ofail(CE_ELAYOUT, "the teacher's values are misaligned or have a negative stride");
+  return check_aligned({d->len}, 4, "len");
+}
+
 // ---- embedding
 ce_status check_embedding(const ce_embedding_desc* m, bool table) {
   if (!m) return ofail(CE_EINVAL, "embedding descriptor is NULL");
@@ -252,6 +322,152 @@ ce_status ce_logits_process(const ce_logits* x, const ce_logits* out, const ce_p
 ce_status ce_logits_process_backward(const ce_logits* dz, const ce_logits* out, const ce_process* p,
                                      hipStream_t stream) {
   return process(dz, out, p, true, stream);
+}
+
+size_t ce_token_logprobs_workspace_bytes(const ce_logits* x, int32_t K) {
+  const ce_logprobs q{nullptr, 0, 0, 0, K, 0};
+  if (vce::check_logits_desc(x) || check_whole_rows(x, vce::logprob_max_cols(x->dtype)) || check_logprobs(x, &q))
+    return 0;
+  const size_t need = vce::logprob_workspace(x->d0 * x->d1, x->v_local, x->dtype, K);
+  return need < 256 ? 256 : (need + 255) / 256 * 256;
+}
+
+ce_status ce_token_logprobs(const ce_logits* x, const ce_logprobs* q, float* logp, float* entropy, float* lse,
+                            int64_t* top_ids, float* top_logp, float* stats, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  ce_status st;
+  if ((st = vce::check_logits_desc(x)) || (st = check_whole_rows(x, vce::logprob_max_cols(x->dtype))) ||
+      (st = check_logprobs(x, q)))
+    return st;
+  const int64_t N = x->d0 * x->d1;
+  if (N > 0 && q->M > 0 && !logp) return ofail(CE_EINVAL, "logp is NULL");
+  if (N > 0 && q->K > 0 && (!top_ids || !top_logp)) return ofail(CE_EINVAL, "top_ids or top_logp is NULL");
+  if ((st = check_aligned({logp, entropy, lse, top_logp}, 4, "an output")) ||
+      (st = check_aligned({top_ids}, 8, "top_ids")) || (st = check_aligned({stats}, 16, "stats")))
+    return st;
+  const size_t need = vce::logprob_workspace(N, x->v_local, x->dtype, q->K);
+  if (need && (st = check_prepared(ws, ws_bytes, need))) return st;
+  if (N == 0 || (q->M == 0 && q->K == 0 && !entropy && !lse && !stats)) return CE_OK;
+  vce::LogprobArgs a{};
+  a.x = static_cast<const char*>(x->data);
+  a.dtype = x->dtype;
+  a.N = N;
+  a.d1 = x->d1;
+  a.V = x->v_local;
+  a.s0 = x->s0;
+  a.s1 = x->s1;
+  a.ids = q->M ? q->ids : nullptr;
+  a.is0 = q->ids_s0;
+  a.is1 = q->ids_s1;
+  a.M = q->M;
+  a.K = q->K;
+  a.ignore_idx = q->ignore_idx;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.stats = stats;
+  vce::logprob_plan(N, a.V, a.dtype, &a.shape, &a.chunks, &a.chunk_cols);
+  hipEvent_t e0, e1;
+  vce::profile_next(&e0, &e1);
+  return launched(vce::launch_logprobs(a, ws, stream, e0, e1), "log-probabilities launch");
+}
+
+ce_status ce_token_logprobs_backward(const ce_logits* x, const ce_logits* out, const ce_logprobs* q,
+                                     const float* stats, const float* dlogp, const float* dentropy,
+                                     const int64_t* top_ids, const float* dtop, hipStream_t stream) {
+  ce_status st;
+  if ((st = vce::check_logits_desc(x)) || (st = check_whole_rows(x, vce::logprob_max_cols(x->dtype))) ||
+      (st = check_gradient_rows(x, out)) || (st = check_logprobs(x, q)))
+    return st;
+  const int64_t N = x->d0 * x->d1;
+  if (N > 0 && !stats) return ofail(CE_EINVAL, "stats is NULL");
+  if (N > 0 && q->M > 0 && !dlogp) return ofail(CE_EINVAL, "dlogp is NULL");
+  if (N > 0 && q->K > 0 && (!top_ids || !dtop)) return ofail(CE_EINVAL, "top_ids or dtop is NULL");
+  if ((st = check_aligned({dlogp, dentropy, dtop}, 4, "a gradient")) ||
+      (st = check_aligned({top_ids}, 8, "top_ids")) || (st = check_aligned({stats}, 16, "stats")))
+    return st;
+  if (N == 0) return CE_OK;
+  vce::LogprobGradArgs a{};
+  a.x = static_cast<const char*>(x->data);
+  a.out = static_cast<char*>(out->data);
+  a.dtype = x->dtype;
+  a.N = N;
+  a.d1 = x->d1;
+  a.V = x->v_local;
+  a.s0 = x->s0;
+  a.s1 = x->s1;
+  a.os0 = out->s0;
+  a.os1 = out->s1;
+  a.ids = q->ids;
+  a.is0 = q->ids_s0;
+  a.is1 = q->ids_s1;
+  a.M = q->M;
+  a.K = q->K;
+  a.ignore_idx = q->ignore_idx;
+  a.stats = stats;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  a.top_ids = top_ids;
+  a.dtop = dtop;
+  hipEvent_t e0, e1;
+  vce::profile_next(&e0, &e1);
+  return launched(vce::launch_logprobs_bwd(a, stream, e0, e1), "log-probabilities gradient launch");
+}
+
+size_t ce_distill_workspace_bytes(const ce_logits* x) {
+  if (vce::check_logits_desc(x) || check_whole_rows(x, vce::distill_max_cols(x->dtype))) return 0;
+  return (vce::distill_workspace(x->d0 * x->d1, x->v_local, x->dtype) + 255) / 256 * 256;
+}
+
+ce_status ce_distill_fwd_bwd(const ce_logits* x, const ce_logits* out, const ce_distill* d, int32_t reduce_loss,
+                             const float* grad_out, float* loss, int32_t* n_valid, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  ce_status st;
+  if ((st = vce::check_logits_desc(x)) || (st = check_whole_rows(x, vce::distill_max_cols(x->dtype))) ||
+      (out && (st = check_gradient_rows(x, out))) || (st = check_distill(x, d)))
+    return st;
+  if (reduce_loss != CE_REDUCE_NONE && reduce_loss != CE_REDUCE_MEAN && reduce_loss != CE_REDUCE_SUM)
+    return ofail(CE_EINVAL, "unknown reduction %d", reduce_loss);
+  const int64_t N = x->d0 * x->d1;
+  if (!loss && (N > 0 || reduce_loss != CE_REDUCE_NONE)) return ofail(CE_EINVAL, "loss is NULL");
+  if ((st = check_aligned({grad_out, loss, n_valid}, 4, "grad_out, loss or n_valid")) ||
+      (st = check_prepared(ws, ws_bytes, vce::distill_workspace(N, x->v_local, x->dtype))))
+    return st;
+  vce::DistillArgs a{};
+  a.x = static_cast<const char*>(x->data);
+  a.out = out ? static_cast<char*>(out->data) : nullptr;
+  a.dtype = x->dtype;
+  a.N = N;
+  a.d1 = x->d1;
+  a.V = x->v_local;
+  a.s0 = x->s0;
+  a.s1 = x->s1;
+  if (out) {
+    a.os0 = out->s0;
+    a.os1 = out->s1;
+  }
+  a.ids = d->ids;
+  a.is0 = d->ids_s0;
+  a.is1 = d->ids_s1;
+  a.teacher = static_cast<const char*>(d->values);
+  a.ts0 = d->values_s0;
+  a.ts1 = d->values_s1;
+  a.tdtype = d->values_dtype;
+  a.kind = d->kind;
+  a.K = d->K;
+  a.len = d->len;
+  a.t = (double)d->temperature;
+  a.inv_t = 1.0 / a.t;
+  a.kb = (float)(1.4426950408889634074 / a.t);
+  a.reduce = reduce_loss;
+  a.g = grad_out;
+  a.loss = loss;
+  vce::distill_plan(a.V, a.dtype, &a.chunks, &a.chunk_cols);
+  hipEvent_t e0, e1;
+  vce::profile_next(&e0, &e1);
+  return launched(vce::launch_distill(a, ws, n_valid, stream, e0, e1), "distillation launch");
 }
 
 ce_status ce_embedding(const ce_embedding_desc* m, void* out, int64_t out_ld, hipStream_t stream) {

@@ -1,0 +1,246 @@
+// Device helpers of the kernels that hold a chunk of one row's logits in
+// registers (token log-probabilities, distillation): 16-byte loads at any
+// element alignment, maxima, reductions over a workgroup, and the words that the
+// chunks of a row exchange.
+//
+// The exchange is ce_fwd_bwd_fused's: 64-bit words in the workspace, the call's
+// tag in the high half and a payload in the low one, written and read with
+// relaxed agent-scope atomics.  The tag is the low half of the workspace's epoch,
+// which the last workgroup of a call advances, so that words of earlier calls (or
+// of another entry point on the same workspace) never pass for this call's and
+// nothing is cleared between calls or replays of a captured graph.  Workgroups
+// are dispatched in index order and a row's chunks are consecutive, so a chunk
+// waits only for workgroups that run or start as soon as a running one ends;
+// every wait is bounded.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ce_internal.h"
+#include "ce_vec.h"
+
+namespace vce {
+
+constexpr float kLog2e = 1.44269504088896340736f;  // rounded to FP32
+constexpr float kLn2f = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A 16-byte vector of logits: E columns.
+template <int DT>
+struct LogitT;
+template <>
+struct LogitT<CE_BF16> {
+  static constexpr int E = 8, EB = 2;
+  static constexpr uint32_t kNegInf = 0xff80ff80u;  // a word of -inf
+  typedef u32x4_a2 Word;
+};
+template <>
+struct LogitT<CE_F32> {
+  static constexpr int E = 4, EB = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  typedef u32x4_a4 Word;
+};
+
+template <int DT>
+__device__ __forceinline__ void unpack_vec(const u32x4v& v, float (&f)[LogitT<DT>::E]) {
+  if constexpr (DT == CE_BF16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(v[k] << 16);
+      f[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[k]);
+  }
+}
+template <int DT>
+__device__ __forceinline__ u32x4v pack_vec(const float (&f)[LogitT<DT>::E]) {
+  u32x4v v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == CE_BF16)
+      v[k] = pack2_bf16(f[2 * k], f[2 * k + 1]);
+    else
+      v[k] = __float_as_uint(f[k]);
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ float load_logit(const char* row, int64_t j) {
+  if constexpr (DT == CE_BF16)
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[j] << 16);
+  else
+    return reinterpret_cast<const float*>(row)[j];
+}
+template <int DT>
+__device__ __forceinline__ void store_logit(char* row, int64_t j, float g) {
+  if constexpr (DT == CE_BF16)
+    reinterpret_cast<uint16_t*>(row)[j] = (uint16_t)(pack2_bf16(g, 0.f) & 0xffffu);
+  else
+    reinterpret_cast<float*>(row)[j] = g;
+}
+
+// Register barrier, no instruction: a later sweep unpacks the vector again instead of keeping its floats.
+__device__ __forceinline__ void relaunch(u32x4v& v) { asm volatile("" : "+v"(v)); }
+
+// One v_max3_f32 (fmaxf would quiet each operand first).  A NaN loses; the sums carry it.
+__device__ __forceinline__ float max3_hw(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+// the largest of m and the vector's columns
+template <int DT>
+__device__ __forceinline__ float largest(const u32x4v& v, float m) {
+  float f[LogitT<DT>::E];
+  unpack_vec<DT>(v, f);
+#pragma unroll
+  for (int k = 0; k < LogitT<DT>::E; k += 2) m = max3_hw(m, f[k], f[k + 1]);
+  return m;
+}
+
+// One row's columns [lo, hi) as T x P vectors: vector j * T + tid in slot j of
+// thread tid.  Slots past the chunk, and a last vector's missing columns, hold
+// -inf.  No load stands behind a branch that not all of a wave take: slots past
+// the whole vectors load the chunk's first one and are overwritten.
+template <int DT, int T, int P>
+__device__ __forceinline__ void load_chunk(const char* chunk, uint32_t cols, u32x4v (&v)[P]) {
+  typedef typename LogitT<DT>::Word Word;
+  constexpr int E = LogitT<DT>::E;
+  const uint32_t tid = threadIdx.x;
+  const uint32_t whole = cols / E;
+  if (whole > 0) {
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const uint32_t i = j * T + tid;
+      v[j] = __builtin_nontemporal_load(reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    if ((uint32_t)(j + 1) * T <= whole) continue;  // the same for the whole workgroup
+    const uint32_t i = j * T + tid;
+    if (i >= whole) {
+      v[j] = u32x4v{LogitT<DT>::kNegInf, LogitT<DT>::kNegInf, LogitT<DT>::kNegInf, LogitT<DT>::kNegInf};
+      if (i == whole) {
+#pragma unroll
+        for (int e = 0; e < E - 1; ++e) {
+          if (i * E + e >= cols) continue;
+          if constexpr (DT == CE_BF16) {
+            const uint32_t h = reinterpret_cast<const uint16_t*>(chunk)[i * E + e];
+            v[j][e / 2] = e & 1 ? (v[j][e / 2] & 0xffffu) | h << 16 : (v[j][e / 2] & 0xffff0000u) | h;
+          } else {
+            v[j][e] = reinterpret_cast<const uint32_t*>(chunk)[i * E + e];
+          }
+        }
+      }
+    }
+  }
+}
+
+// Vector i of a chunk of `cols` columns, written non-temporally; columns that are not there are left out.
+template <int DT>
+__device__ __forceinline__ void store_vec(char* chunk, uint32_t cols, uint32_t i, const u32x4v& w) {
+  typedef typename LogitT<DT>::Word Word;
+  constexpr int E = LogitT<DT>::E;
+  if ((i + 1) * E <= cols) {
+    __builtin_nontemporal_store(w, reinterpret_cast<Word*>(chunk + i * 16u));
+  } else if (i * E < cols) {
+#pragma unroll
+    for (int e = 0; e < E - 1; ++e) {
+      if (i * E + e >= cols) continue;
+      if constexpr (DT == CE_BF16)
+        reinterpret_cast<uint16_t*>(chunk)[i * E + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+      else
+        reinterpret_cast<uint32_t*>(chunk)[i * E + e] = w[e];
+    }
+  }
+}
+
+// ---- reductions, in a fixed order
+
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp_or_own(float v) {  // lanes without a source, and rows outside ROWS, read their own
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+// the largest over the wave, of any sign, uniform
+__device__ __forceinline__ float wave_largest(float v) {
+  v = fmaxf(v, dpp_or_own<kSwap1>(v));
+  v = fmaxf(v, dpp_or_own<kSwap2>(v));
+  v = fmaxf(v, dpp_or_own<kHalfMirror>(v));
+  v = fmaxf(v, dpp_or_own<kMirror>(v));
+  v = fmaxf(v, dpp_or_own<kBcast15, 0xa>(v));
+  v = fmaxf(v, dpp_or_own<kBcast31, 0xc>(v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ double wave_largest64(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+  return v;
+}
+__device__ __forceinline__ int wave_count64(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// ---- the exchange
+
+constexpr uint32_t kWaitLimit = 1u << 22;  // polls of one lane, about 128 cycles each
+
+__device__ __forceinline__ void put_word(unsigned long long* p, uint32_t tag, uint32_t payload) {
+  __hip_atomic_store(p, ((unsigned long long)tag << 32) | payload, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long peek_word(const unsigned long long* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The payload of *p once it carries the tag; `w` is a first reading of it.  False
+// where the wait was given up.  `spins` is the lane's over all of its waits.
+__device__ __forceinline__ bool await_word(const unsigned long long* p, uint32_t tag, unsigned long long w,
+                                           uint32_t& spins, uint32_t* payload) {
+  while ((uint32_t)(w >> 32) != tag) {
+    if (++spins > kWaitLimit) return false;
+    __builtin_amdgcn_s_sleep(2);
+    w = peek_word(p);
+  }
+  *payload = (uint32_t)w;
+  return true;
+}
+
+// A call's view of its workspace: the tag, whether ce_workspace_init prepared it
+// for this many bytes, and the test hook (a chunk whose words stay unpublished).
+// Scalar loads: nothing writes the record before the call's last workgroup ends.
+struct WsView {
+  uint32_t tag;
+  bool ok;
+  unsigned long long withhold;
+};
+__device__ __forceinline__ WsView view_workspace(const WsHeader* hdr, unsigned long long bytes) {
+  typedef const __attribute__((address_space(4))) unsigned long long* Const64;
+  const Const64 rec = (Const64)(&hdr->magic);  // magic, init_bytes, epoch, withhold
+  WsView v;
+  v.tag = (uint32_t)rec[2];
+  v.ok = (rec[0] == kWsMagic) & (rec[1] >= bytes);
+  v.withhold = rec[3];
+  return v;
+}
+__device__ __forceinline__ bool withheld(const WsView& ws, int64_t r, int k) {
+  return ws.withhold == ((((unsigned long long)r + 1u) << 8) | (unsigned)k);
+}
+// The next call's tag; the caller has seen a word of every row that this call's
+// workgroups have read the epoch.
+__device__ __forceinline__ void next_epoch(WsHeader* hdr) {
+  unsigned long long next = hdr->epoch + 1;
+  if ((uint32_t)next == 0u) ++next;
+  __hip_atomic_store(&hdr->epoch, next, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+}  // namespace vce
