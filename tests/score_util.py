@@ -86,6 +86,8 @@ class Row64:
             lp = d - self.logd[:, None]
             tol = np.where(np.isfinite(d), self.tol_logd[:, None] + 1.01 * U * (np.abs(d) + np.abs(lp)), 0.0) + TINY
         lp = np.where(inside & self.ok[:, None], lp, np.nan)
+        # the outputs are FP32: what rounds past its largest number, (2 - 2^-23) 2^127, is an infinity there
+        lp = np.where(lp <= -(2 - 2.0 ** -24) * 2.0 ** 127, -np.inf, lp)
         return np.where(ids == ignore_idx, 0.0, lp), tol
 
 

@@ -130,6 +130,10 @@ def _special_rows(V, dtype, seed):
     one[V // 2] = -3.0
     rows["one left"] = one
     rows["lowest value"] = torch.where(torch.isinf(masked), torch.tensor(torch.finfo(dtype).min), masked)
+    rows["lowest values alone"] = torch.full((V,), torch.finfo(dtype).min)
+    huge = torch.full((V,), -2.9e38)
+    huge[::3] = 2.9e38
+    rows["out of range of the exponent"] = huge
     run = base.clone()  # the largest ones side by side, in one lane's vectors
     run[V // 4: V // 4 + min(V - V // 4, 130)] += 50
     rows["a run"] = run

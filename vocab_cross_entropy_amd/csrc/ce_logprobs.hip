@@ -6,25 +6,31 @@
 //   H       = log D - sum_j exp(x_j - m) (x_j - m) / D
 //   dx_v    = sum_i g_i [v = t_i] - p_v (sum_i g_i + dH (log p_v + H))
 //
-// D's largest term is 1, and it is counted apart from the others' sum R: a row with
-// one column at the maximum has log D = log1p(R) and 1 - p_max = R / (1 + R), so
-// log-probabilities and entropies near 0, and the gradient of a token whose
-// probability is near 1, keep their digits.  Exponentials are base 2 on the hardware's
-// v_exp_f32, against m2 = fl(m log2 e); the sums are brought from m2 to the exact m log2 e
-// at the end.
+// One column at the maximum is counted apart, D = 1 + R, so that log D = log1p(R) and
+// 1 - p_max = R / D: log-probabilities and entropies near 0, and the gradient of a token
+// whose probability is near 1, keep their digits.  Every thread sums its columns relative
+// to its own running maximum; the sum of the one thread that owns the row's maximum, which
+// may have lost R's digits beside the 1, is formed again at the end without that column.
+// Exponentials are base 2 on the hardware's v_exp_f32, against m2 = fl(m log2 e); the
+// sums are brought from m2 to the exact m log2 e at the end.
 //
-// Bound: the read of the logits (the gradient: and its write).  A workgroup holds
-// a chunk of one row in registers, loaded at once.  What each chunk finds (m, R, the
-// entropy's sum, its K largest keys) goes to the row's last chunk by tagged words.
+// Bound: the read of the logits (the gradient: and its write).  With many rows a
+// workgroup takes a row; with few, a row is cut into chunks, and what each chunk finds (m, R,
+// the entropy's sum, its K largest keys) goes to the row's last chunk by tagged words.
+// A chunk is read in batches of T x P vectors, each batch a sample of the whole chunk (every
+// nb-th KiB of it), so that what the first one shows holds for the rest.
 //
-// The K largest of a chunk without sorting it: the K-th largest of its threads'
-// maxima, found bit by bit with ballots, is a bound that at least K columns reach and
-// few others do; the columns that reach it are collected in LDS and ranked by counting.
-// Where too many reach it (constant rows, masked ones: all -inf) the exact K-th
-// value is found the same way over all columns, and of its ties the lowest columns are
-// taken.  Keys order by value, then by column, so nothing depends on scheduling.
+// The K largest without sorting: the K-th largest of the threads' running maxima,
+// found with ballots, is a bound that at least K columns reach and few others do (K threads
+// have one each).  Vectors that reach the bound of their time go to LDS; it is raised after
+// the first, second, third, fifth, ninth ... batch.  At the end their columns that reach the
+// last bound, about 1.3 K of them, are ranked by counting.  Where too many reach it (constant
+// rows, runs of equal values) the K-th value is found exactly by further sweeps over the chunk, and of
+// its ties the lowest columns are taken.  Keys order by value, then by column, so nothing
+// depends on scheduling.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "ce_internal.h"
 #include "ce_row.h"
@@ -33,12 +39,11 @@ namespace vce {
 namespace {
 
 constexpr int kTop = kLogprobMaxList;  // most alternatives, and most given tokens, of a row
-constexpr int kCand = 1024;            // candidates of a chunk that LDS holds
-constexpr int kMerge = 1024;           // keys merged at a time
-constexpr int kLocalBits = 15;         // a chunk has at most 2^15 columns
-constexpr uint32_t kLocalMask = (1u << kLocalBits) - 1;
-constexpr int kStatWords = 4;          // m, R, columns at the maximum, the entropy's sum
-static_assert(kMerge / kTop >= 2, "a merge takes the list so far and at least one more");
+constexpr int kStatWords = 4;          // m, R, whether m was counted (1, or 0 of a chunk of -inf), the entropy's sum
+constexpr float kFar = -1000.f;        // 2^kFar is 0; exponents of masked columns (-inf) stop here where they are a factor
+constexpr float kHuge = 2e38f;         // beyond it x log2 e leaves FP32
+typedef unsigned long long Key;        // order << 32 | ~column; 0: none
+typedef Key KeyPair __attribute__((ext_vector_type(2)));
 
 // Values in order as unsigned numbers; +0 and -0 alike, NaN below everything, 0 nothing at all.
 template <int DT>
@@ -56,42 +61,48 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 template <int DT>
 constexpr int kOrderBits = DT == CE_BF16 ? 16 : 32;
+// bits of it that a bound may leave out (FP32: a relative step of 2^-13)
+template <int DT>
+constexpr int kLowBits = DT == CE_BF16 ? 0 : 10;
+__device__ __forceinline__ Key key_of(uint32_t order, uint32_t column) { return (Key)order << 32 | (uint32_t)~column; }
 
-// A chunk's key: order, then the lower column.  BF16's fits 32 bits and one exchange word.
-template <int DT>
-struct KeyT;
-template <>
-struct KeyT<CE_BF16> {
-  typedef uint32_t Key;
-  static constexpr int kWords = 1;
-};
-template <>
-struct KeyT<CE_F32> {
-  typedef unsigned long long Key;
-  static constexpr int kWords = 2;
-};
-template <int DT>
-__device__ __forceinline__ typename KeyT<DT>::Key chunk_key(uint32_t order, uint32_t local) {
-  return (typename KeyT<DT>::Key)order << kLocalBits | (kLocalMask - local);
-}
-// A row's key: order << 32 | ~column.
-template <int DT>
-__device__ __forceinline__ unsigned long long row_key(typename KeyT<DT>::Key k, uint32_t lo) {
-  if (k == 0) return 0ull;
-  const uint32_t local = kLocalMask - ((uint32_t)k & kLocalMask);
-  return (unsigned long long)(k >> kLocalBits) << 32 | (uint32_t)~(lo + local);
-}
-
-// The largest t whose bits are found from the top such that count(t) >= K (0: none).
-template <int BITS, typename Count>
-__device__ __forceinline__ uint32_t kth_largest(uint32_t K, Count count) {
-  uint32_t t = 0;
+// A value that at least K of the wave's 64 G numbers reach and as few as possible more, to within the lowest LOW
+// bits (0 where fewer than K are not 0): found bit by bit, two at a time, below the bits that all of them share.
+template <int LOW, int G>
+__device__ __forceinline__ uint32_t reached_by(uint32_t K, const uint32_t (&g)[G]) {
+  const auto count = [&](uint32_t c) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) n += (uint32_t)__builtin_popcountll(__ballot(g[i] >= c));
+    return n;
+  };
+  const uint32_t one = (uint32_t)__builtin_amdgcn_readfirstlane((int)g[0]);
+  uint32_t differ = 0;
+#pragma unroll
+  for (int i = 0; i < G; ++i) differ |= g[i] ^ one;
+  differ = wave_or(differ);
+  int b = differ ? 32 - __builtin_clz(differ) : 0;  // the numbers differ below bit b only
+  b = (b - LOW + 1) / 2 * 2 + LOW;
+  if (b <= LOW) return one >> LOW << LOW;
+  uint32_t t = b < 32 ? one >> b << b : 0u;
 #pragma unroll 1
-  for (int b = BITS - 1; b >= 0; --b) {
-    const uint32_t c = t | 1u << b;
-    if (count(c) >= K) t = c;
+  for (b -= 2; b >= LOW; b -= 2) {
+    const uint32_t c1 = t + (1u << b), c2 = t + (2u << b), c3 = t + (3u << b);
+    const uint32_t n1 = count(c1), n2 = count(c2), n3 = count(c3);
+    t = n3 >= K ? c3 : n2 >= K ? c2 : n1 >= K ? c1 : t;
   }
   return t;
+}
+
+// The same of 64 G group maxima, G a lane.  Where 64 of them are enough, of each lane's maximum: a few more
+// columns reach that (K = 32: 44 instead of 34), for a G-th of the ballots.
+template <int DT, int G>
+__device__ __forceinline__ uint32_t bound_of(uint32_t K, const uint32_t (&g)[G]) {
+  if (K > 32) return reached_by<kLowBits<DT>, G>(K, g);
+  uint32_t top[1] = {g[0]};
+#pragma unroll
+  for (int i = 1; i < G; ++i) top[0] = g[i] > top[0] ? g[i] : top[0];
+  return reached_by<kLowBits<DT>, 1>(K, top);
 }
 
 template <int T>
@@ -106,145 +117,177 @@ __device__ __forceinline__ uint32_t block_count(uint32_t c, uint32_t* sh) {
   return n;
 }
 
-// The K largest keys of a chunk of at least K columns, exactly, where a bound `t` that
-// `reach` columns reach let too many through, or too few (NaN, which maxima pass over): the
-// K-th largest value over all columns (the bound itself where fewer than K exceed it),
+// The K largest keys of a chunk of at least K columns, exactly, where a bound `t` let
+// too many through, or too few (NaN, which maxima pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it),
 // every column above it, and its ties from the lowest column on.  Leaves K keys in cand[].
-template <int DT, int T, int P>
-__device__ __forceinline__ void exact_largest(const u32x4v (&v)[P], uint32_t cols, uint32_t K, uint32_t t,
-                                              uint32_t reach, typename KeyT<DT>::Key* cand, uint32_t* n_cand,
-                                              uint32_t* sh) {
+// Rare, so it is kept short: every sweep reads the chunk again.  Column 0 of the chunk is the row's column lo.
+template <int DT, int T>
+__device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, uint32_t cols, uint32_t K, uint32_t t,
+                                              Key* cand, uint32_t* n_cand, uint32_t* sh) {
+  typedef typename LogitT<DT>::Word Word;
   constexpr int E = LogitT<DT>::E;
   const uint32_t tid = threadIdx.x;
+  // the orders of vector i's columns, 0 for those that are not there
+  const auto orders = [&](const u32x4v& v, uint32_t i, uint32_t (&o)[E]) {
+    float f[E];
+    unpack_vec<DT>(v, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = i * E + e < cols ? order_of<DT>(f[e]) : 0u;
+  };
+  const uint32_t whole = cols / E;
+  const auto whole_vec = [&](uint32_t i) -> u32x4v { return *reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u); };
+  const u32x4v rest = partial_vec<DT>(chunk, whole * E, cols);
   const auto count = [&](uint32_t at_least) {
     uint32_t c = 0;
+#pragma unroll 1
+    for (uint32_t i = tid; i * E < cols; i += T) {
+      uint32_t o[E];
+      orders(i < whole ? whole_vec(i) : rest, i, o);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      u32x4v w = v[j];
-      relaunch(w);  // the orders are formed again in each round, not kept in registers
-      float f[E];
-      unpack_vec<DT>(w, f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) c += (j * T + tid) * E + e < cols && order_of<DT>(f[e]) >= at_least;
+      for (int e = 0; e < E; ++e) c += o[e] >= at_least;
     }
     return block_count<T>(c, sh);
   };
-  uint32_t above = count(t + 1);
-  if (above >= K || reach < K) {
-    t = kth_largest<kOrderBits<DT>>(K, count);
-    above = count(t + 1);
+  // the bound where at least K columns reach it and fewer are above it; else from the top bit on
+  uint32_t above = 0;
+  bool found = false;
+#pragma unroll 1
+  for (int b = kOrderBits<DT> + 1; b >= -1; --b) {
+    const bool probe = b < 0 || b == kOrderBits<DT>;
+    const uint32_t c = probe ? t + 1 : b > kOrderBits<DT> ? t : t | 1u << b;
+    const uint32_t n = count(c);
+    if (probe) {
+      above = n;
+      if (found && above < K) break;
+      t = b < 0 ? t : 0u;
+    } else if (b > kOrderBits<DT>) {
+      found = n >= K;
+    } else if (n >= K) {
+      t = c;
+    }
   }
   if (tid == 0) *n_cand = 0;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    float f[E];
-    unpack_vec<DT>(v[j], f);
+  uint32_t have = above;
+#pragma unroll 1
+  for (uint32_t base = 0; base * E < cols; base += T) {  // columns rise with base, then with the thread, then within the vector
+    const uint32_t i = base + tid;
+    uint32_t o[E], mine = 0;
+    orders(i < whole ? whole_vec(i) : rest, i, o);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint32_t c = (j * T + tid) * E + e, o = order_of<DT>(f[e]);
-      if (c < cols && o > t) cand[atomicAdd(n_cand, 1u)] = chunk_key<DT>(o, c);
+      mine += o[e] == t;
+      if (o[e] > t) cand[atomicAdd(n_cand, 1u)] = key_of(o[e], lo + i * E + e);
     }
-  }
-  uint32_t have = above;
+    if (have >= K) continue;  // the same for the whole workgroup
+    uint32_t upto = mine;     // inclusive over the wave's lanes
 #pragma unroll
-  for (int j = 0; j < P; ++j) {  // columns rise with j, then with the thread, then within the vector
-    if (have >= K) continue;     // the same for the whole workgroup
-    float f[E];
-    unpack_vec<DT>(v[j], f);
-    uint32_t mine = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) mine += (j * T + tid) * E + e < cols && order_of<DT>(f[e]) == t;
-    uint32_t upto = mine;  // inclusive over the wave's lanes
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t u = (uint32_t)__shfl_up((int)upto, o);
-      upto += (tid & 63) >= (uint32_t)o ? u : 0u;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t u = (uint32_t)__shfl_up((int)upto, d);
+      upto += (tid & 63) >= (uint32_t)d ? u : 0u;
     }
     __syncthreads();
     if ((tid & 63) == 63) sh[tid >> 6] = upto;
     __syncthreads();
-    uint32_t at = have + upto - mine, all = 0;
+    uint32_t at = have + upto - mine;
 #pragma unroll
-    for (int i = 0; i < T / 64; ++i) {
-      at += (uint32_t)i < tid >> 6 ? sh[i] : 0u;
-      all += sh[i];
+    for (int w = 0; w < T / 64; ++w) {
+      at += (uint32_t)w < tid >> 6 ? sh[w] : 0u;
+      have += sh[w];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint32_t c = (j * T + tid) * E + e;
-      if (c < cols && order_of<DT>(f[e]) == t) {
-        if (at < K) cand[at] = chunk_key<DT>(t, c);
-        ++at;
-      }
+      if (o[e] == t && at < K) cand[at] = key_of(t, lo + i * E + e);
+      at += o[e] == t;
     }
-    have += all;
   }
+  __syncthreads();
   if (tid == 0) *n_cand = K;
   __syncthreads();
 }
 
-// Descending lists of K keys (0: none) in `a`, nl of them, merged to one; `b` is room for as many.
-// Returns where it is.  The caller's writes of `a` are visible.
-template <int T>
-__device__ unsigned long long* merge_lists(unsigned long long* a, unsigned long long* b, uint32_t nl, uint32_t K) {
-  while (nl > 1) {
-    for (uint32_t i = threadIdx.x; i < nl * K; i += T) {
-      const uint32_t l = i / K, at = i - l * K, other = l ^ 1u;
-      const unsigned long long key = a[i];
-      uint32_t rank = at;
-      if (other < nl) {
-        const unsigned long long* o = a + other * K;
-        uint32_t lo = 0, hi = K;  // how many of the other list's keys are larger
-        while (lo < hi) {
-          const uint32_t mid = (lo + hi) >> 1;
-          if (o[mid] > key) lo = mid + 1;
-          else hi = mid;
-        }
-        rank += lo;
-      }
-      if (rank < K) b[(l >> 1) * K + rank] = key;
-    }
-    __syncthreads();
-    unsigned long long* const t = a;
-    a = b;
-    b = t;
-    nl = (nl + 1) >> 1;
-  }
-  return a;
+// How many of these lanes come before this one.
+__device__ __forceinline__ uint32_t lanes_below(unsigned long long lanes) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0u));
 }
 
-// What a row comes to, the same in every thread.
-struct RowSum {
-  float m, logd;
-  float rest;    // sum of exp(x - m) but for one column at the maximum
-  float s1;      // sum of exp(x - m) (x - m) log2 e
-  float at_max;  // columns counted as exactly 1
+// Collected keys: each wave's in a segment of its own, in LDS, with zeros behind them: to the next multiple of two, and two more.
+template <int W, int SEG>
+struct Segments {
+  static constexpr int kStride = SEG + 4;
+  Key* keys;
+  uint32_t* n;  // [W]
+
+  // Adds the keys of the lanes that have one; `have` counts the wave's (beyond SEG they are dropped).
+  __device__ __forceinline__ void add(bool mine, Key key, uint32_t& have) const {
+    const unsigned long long lanes = __ballot(mine);
+    if (lanes == 0) return;
+    const uint32_t at = have + lanes_below(lanes);
+    if (mine && at < (uint32_t)SEG) keys[(threadIdx.x >> 6) * kStride + at] = key;
+    have += (uint32_t)__builtin_popcountll(lanes);
+  }
+  __device__ __forceinline__ void close(uint32_t have) const {
+    const uint32_t lane = threadIdx.x & 63, kept = have < (uint32_t)SEG ? have : (uint32_t)SEG;
+    if (lane < 4) keys[(threadIdx.x >> 6) * kStride + kept + lane] = 0;
+    if (lane == 0) n[threadIdx.x >> 6] = have;
+  }
+  // put(rank, key) for each of the keys, by counting the larger ones
+  template <typename Put>
+  __device__ __forceinline__ void rank(Put put) const {
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    uint32_t longest = 0, end[W];  // where a segment's last zeros are
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      end[w] = (n[w] + 1) / 2 * 2;
+      longest = n[w] > longest ? n[w] : longest;
+    }
+#pragma unroll 1
+    for (uint32_t base = 0; base < n[wave]; base += 64) {
+      const uint32_t i = base + lane;
+      const bool mine = i < n[wave];
+      const Key key = mine ? keys[wave * kStride + i] : 0;
+      uint32_t r = 0;
+#pragma unroll 1
+      for (uint32_t q = 0; q < longest; q += 2) {
+        KeyPair o[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) o[w] = *reinterpret_cast<const KeyPair*>(keys + w * kStride + (q < end[w] ? q : end[w]));
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) r += o[w][c] > key;
+      }
+      if (mine) put(r, key);
+    }
+  }
 };
-// (at_max - 1 further columns at the maximum are counted in D beside rest)
-__device__ __forceinline__ float log_of_sum(const RowSum& s) {
-  return s.at_max == 1.f ? log1pf(s.rest) : logf(s.rest + s.at_max);
-}
 
 template <int DT, int T, int P, bool TOP, bool ENT>
 __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
-  typedef typename KeyT<DT>::Key Key;
+  typedef typename LogitT<DT>::Word Word;
   constexpr int E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
-  constexpr int KW = KeyT<DT>::kWords;
   constexpr int TK = (kTop + T - 1) / T;  // given tokens a thread
+  constexpr bool kSplit = W > 1;          // one wave only ever takes a whole row
+  constexpr int kRound = 1024 / T;        // keys a thread takes into one round of merging
+  // A wave's vectors that have reached a bound, and the columns that reach the last one; later the row's keys.  A chunk
+  // of fewer than kTop vectors has no bound; it is one wave's (other shapes' have more), and fits.
+  constexpr int kHits = 128, kSeg = W > 1 ? 256 * 4 / W + 64 : kTop * (E + 1);
+  static_assert(kSeg >= 64 * (kSplit ? kRound : 0) && kHits >= kTop, "what the segments hold");
   __shared__ float sh_max[W];
-  __shared__ float sh_sum[W][4];
-  __shared__ float st[kMaxChunks][kStatWords];
-  __shared__ uint32_t sh_cnt[W];
-  __shared__ uint32_t lane_top[TOP ? T : 1];
-  __shared__ uint32_t n_cand;
-  __shared__ __align__(16) unsigned long long keys[TOP ? 2 * kMerge : 1];  // candidates, later the lists
-  Key* const cand = reinterpret_cast<Key*>(keys);
-  static_assert(kCand * sizeof(Key) <= 2 * kMerge * 8, "candidates fit");
+  __shared__ float sh_sum[W][2];
+  __shared__ uint32_t sh_own[W];
+  __shared__ float st[kSplit ? kMaxChunks : 1][kStatWords];
+  __shared__ uint32_t sh_cnt[W], n_seg[W], n_cand;
+  __shared__ uint32_t thread_top[2][TOP && W > 1 ? T : 1];
+  __shared__ u32x4v hit[TOP ? W : 1][TOP ? kHits : 1];
+  __shared__ uint32_t hit_vec[TOP ? W : 1][TOP ? kHits : 1];
+  __shared__ __align__(32) Key seg_keys[TOP ? W * Segments<W, kSeg>::kStride : 1];
+  __shared__ Key top[TOP ? kTop : 1];  // the row's keys
+  const Segments<W, kSeg> seg{seg_keys, n_seg};
 
-  const uint32_t tid = threadIdx.x, wave = tid >> 6;
-  const uint32_t C = (uint32_t)a.chunks, K = TOP ? (uint32_t)a.K : 0u;
-  const uint32_t in_launch = blockIdx.x / C;
+  const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const uint32_t C = kSplit ? (uint32_t)a.chunks : 1u, K = TOP ? (uint32_t)a.K : 0u;
+  const uint32_t in_launch = kSplit ? blockIdx.x / C : blockIdx.x;
   const int64_t r = a.row0 + in_launch;
   const uint32_t k = blockIdx.x - in_launch * C;
   const bool last = k == C - 1;  // the row's last chunk brings it together
@@ -254,248 +297,391 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   const char* const row = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   const uint32_t lo = k * (uint32_t)a.chunk_cols;
   const uint32_t cols = (uint32_t)a.V - lo < (uint32_t)a.chunk_cols ? (uint32_t)a.V - lo : (uint32_t)a.chunk_cols;
+  const char* const chunk = row + (size_t)lo * EB;
+  // Vectors: `whole` of them, and one of cols % E columns.  Lines of 64 vectors; batch b has every nb-th from the b-th on.
+  const uint32_t whole = cols / E, vecs = (cols + E - 1) / E;
+  const uint32_t nb = (vecs + T * P - 1) / (T * P);
+  const auto vector_at = [&](uint32_t b, uint32_t j, uint32_t w, uint32_t l) { return ((j * W + w) * nb + b) * 64 + l; };
 
-  // ---- the given tokens' ids go out first, then the chunk, then the tokens' logits
+  // ---- the given tokens' ids go out first, and their logits after the first batch
   const int64_t* const ids = a.ids ? a.ids + i0 * a.is0 + i1 * a.is1 : nullptr;
   int64_t id[TK];
-#pragma unroll
-  for (int i = 0; i < TK; ++i) id[i] = last && (int)(i * T + tid) < a.M ? ids[i * T + tid] : -1;
-  u32x4v v[P];
-  load_chunk<DT, T, P>(row + (size_t)lo * EB, cols, v);
   float xt[TK];
 #pragma unroll
-  for (int i = 0; i < TK; ++i) xt[i] = id[i] >= 0 && id[i] < a.V ? load_logit<DT>(row, id[i]) : 0.f;
-  if (TOP && tid == 0) n_cand = 0;
-
-  // ---- maxima
-  float vm[P], m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    vm[j] = largest<DT>(v[j], -INFINITY);
-    m = fmaxf(m, vm[j]);
-  }
-  if constexpr (TOP && W > 1) lane_top[tid] = tid * E < cols ? order_of<DT>(m) : 0u;
-  m = wave_largest(m);
-  if ((tid & 63) == 0) sh_max[wave] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < W; ++i) m = fmaxf(m, sh_max[i]);
-  const float m2 = m == -INFINITY ? 0.f : m * kLog2e;
-
-  // ---- sums: a vector that reaches the maximum leaves one such column out
-  float s0 = 0.f, s1 = 0.f, at_max = 0.f;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    relaunch(v[j]);
-    float f[E], e[E];
-    unpack_vec<DT>(v[j], f);
-    float t = 0.f, h = 0.f;
-    const auto exponent = [&](int c) { return __builtin_fmaf(f[c], kLog2e, -m2); };
-    // (2^-1000 is 0, and 0 times a masked column's -inf would be NaN)
-    const auto bent = [&](int c) { return e[c] * fmaxf(exponent(c), -1000.f); };
-#pragma unroll
-    for (int c = 0; c < E; ++c) {
-      e[c] = exp2_hw(exponent(c));
-      if constexpr (ENT) h += bent(c);
-    }
-#pragma unroll
-    for (int c = 0; c < E; c += 2) t += e[c] + e[c + 1];
-    if (vm[j] == m && m != -INFINITY) {
-      int own = E - 1;
-#pragma unroll
-      for (int c = E - 1; c >= 0; --c) own = f[c] == m ? c : own;
-      t = h = 0.f;
-#pragma unroll
-      for (int c = 0; c < E; ++c) {
-        t += c == own ? 0.f : e[c];
-        if constexpr (ENT) h += c == own ? 0.f : bent(c);
-      }
-      at_max += 1.f;
-    }
-    s0 += t;
-    if constexpr (ENT) s1 += h;
-  }
-  s0 = wave_sum(s0);
-  at_max = wave_sum(at_max);
-  if constexpr (ENT) s1 = wave_sum(s1);
-  if ((tid & 63) == 0) {
-    sh_sum[wave][0] = s0;
-    sh_sum[wave][1] = at_max;
-    sh_sum[wave][2] = s1;
+  for (int i = 0; i < TK; ++i) {
+    id[i] = last && (int)(i * T + tid) < a.M ? ids[i * T + tid] : -1;
+    xt[i] = 0.f;
   }
 
-  // ---- the K largest
-  if constexpr (TOP) {
-    constexpr int G = W > 1 ? W : P;  // group maxima a lane: threads' or, in one wave, vectors'
+  float m = -INFINITY, m2 = -INFINITY;  // this thread's maximum, and m log2 e
+  float s0 = 0.f, s1 = 0.f;             // its sums of 2^u and of 2^u u, u = x log2 e - m2
+  // the sums relative to another m2 (kFar: 2^kFar is 0, and 0 times an infinity would be NaN)
+  const auto move_sums = [&](float to, float& t0, float& t1) {
+    const float d = m2 > -INFINITY && to > -INFINITY ? fmaxf(m2 - to, kFar) : kFar;
+    const float w = exp2_hw(d);
+    if constexpr (ENT) t1 = __builtin_fmaf(d, t0, t1) * w;
+    t0 *= w;
+  };
+  bool low = true;                      // no bound, or -inf
+  float least = -INFINITY;              // the bound
+  uint32_t bound = 0, raised = 0, hits = 0;
+  // from the running maxima of all threads; the two buffers alternate, a barrier each
+  const auto raise_bound = [&] {
+    constexpr int G = W > 1 ? W : P;
     uint32_t g[G];
+    if constexpr (W > 1) {
+      uint32_t* const tops = thread_top[raised++ & 1];
+      tops[tid] = tid < vecs ? order_of<DT>(m) : 0u;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      if constexpr (W > 1) g[i] = lane_top[i * 64 + (tid & 63)];
-      else g[i] = (i * T + tid) * E < cols ? order_of<DT>(vm[i]) : 0u;
+      for (int i = 0; i < G; ++i) g[i] = tops[i * 64 + lane];
+      bound = bound_of<DT>(K, g);
     }
-    const uint32_t bound = kth_largest<kOrderBits<DT>>(K, [&](uint32_t c) {
-      uint32_t n = 0;
+    low = bound <= order_of<DT>(-INFINITY);
+    least = low ? -INFINITY : value_of<DT>(bound);
+  };
+#pragma unroll 1
+  for (uint32_t b = 0; b < nb; ++b) {
+    u32x4v v[P];
+    if (whole > 0) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) n += (uint32_t)__builtin_popcountll(__ballot(g[i] >= c));
-      return n;
-    });
+      for (int j = 0; j < P; ++j) {
+        const uint32_t i = vector_at(b, j, wave, lane);
+        v[j] = __builtin_nontemporal_load(reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u));
+      }
+    }
+    if (b == 0) {
+#pragma unroll
+      for (int i = 0; i < TK; ++i)
+        if (id[i] >= 0 && id[i] < a.V) xt[i] = load_logit<DT>(row, id[i]);
+    }
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      if (order_of<DT>(vm[j]) < bound) continue;
+      constexpr uint32_t kNone = LogitT<DT>::kNegInf;
+      if (vector_at(b, j, wave, 63) < whole) continue;  // the same for the whole wave
+      if (vector_at(b, j, wave, lane) >= whole) v[j] = u32x4v{kNone, kNone, kNone, kNone};
+    }
+    if (vecs > whole && (whole >> 6) % nb == b) {  // the vector that is not whole
+      const uint32_t slot = (whole >> 6) / nb;
+      if (slot % W == wave && (whole & 63) == lane) {
+        const u32x4v w = partial_vec<DT>(chunk, whole * E, cols);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          u32x4v mine = w;
+          relaunch(mine);  // (as in pick)
+          if ((uint32_t)j == slot / W) v[j] = mine;
+        }
+      }
+    }
+
+    // ---- maxima; the sums so far go over to a new one
+    float vm[P], top_m = m;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      vm[j] = largest<DT>(v[j], -INFINITY);
+      top_m = fmaxf(top_m, vm[j]);
+    }
+    if (top_m > m) {
+      const float to = top_m * kLog2e;
+      move_sums(to, s0, s1);
+      m = top_m;
+      m2 = to;
+    }
+    const float from = m2 == -INFINITY ? 0.f : m2;
+    float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      relaunch(v[j]);
       float f[E];
       unpack_vec<DT>(v[j], f);
 #pragma unroll
-      for (int c = 0; c < E; ++c) {
-        const uint32_t o = order_of<DT>(f[c]), local = (j * T + tid) * E + c;
-        if (o >= bound && local < cols) {
-          const uint32_t at = atomicAdd(&n_cand, 1u);
-          if (at < (uint32_t)kCand) cand[at] = chunk_key<DT>(o, local);
+      for (int c = 0; c < E; c += 2) {
+        const float u = __builtin_fmaf(f[c], kLog2e, -from), w = __builtin_fmaf(f[c + 1], kLog2e, -from);
+        const float eu = exp2_hw(u), ew = exp2_hw(w);
+        t0 += eu;
+        t1 += ew;
+        if constexpr (ENT) {
+          s1 = __builtin_fmaf(eu, fmaxf(u, kFar), s1);
+          s1 = __builtin_fmaf(ew, fmaxf(w, kFar), s1);
         }
       }
     }
+    s0 += t0 + t1;
+
+    // ---- vectors that reach the bound
+    if constexpr (TOP) {
+      if constexpr (W > 1) {
+        if ((b & (b - 1)) == 0) raise_bound();  // b = 0, 1, 2, 4, 8 ...
+      } else {  // one batch: of the vectors' maxima
+        uint32_t g[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) g[j] = vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u;
+        bound = bound_of<DT>(K, g);
+        raise_bound();
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        // (under a bound of -inf the columns above it; -inf's own come in at the end)
+        const bool mine = low ? vm[j] > -INFINITY : vm[j] >= least;
+        const unsigned long long lanes = __ballot(mine);
+        if (lanes == 0) continue;
+        const uint32_t at = hits + lanes_below(lanes);
+        if (mine && at < (uint32_t)kHits) {
+          hit[wave][at] = v[j];
+          hit_vec[wave][at] = vector_at(b, j, wave, lane);
+        }
+        hits += (uint32_t)__builtin_popcountll(lanes);
+      }
+    }
+  }
+
+  // ---- the chunk's maximum and the first thread that has it
+  {
+    const float wm = wave_largest(m);
+    const unsigned long long owners = __ballot(m == wm);
+    if (lane == 0) {
+      sh_max[wave] = wm;
+      sh_own[wave] = wave * 64 + (uint32_t)__builtin_ctzll(owners | 1ull << 63);
+    }
+  }
+  if constexpr (TOP && W > 1) {
+    if (nb > 1) raise_bound();
+  }
+  __syncthreads();
+  float M = sh_max[0];
+  uint32_t owner = sh_own[0];
+#pragma unroll
+  for (int i = 1; i < W; ++i) {
+    owner = sh_max[i] > M ? sh_own[i] : owner;
+    M = fmaxf(M, sh_max[i]);
+  }
+  const float M2 = M == -INFINITY ? 0.f : M * kLog2e;
+  move_sums(M2, s0, s1);
+  if (M != -INFINITY && tid == owner) s0 = s1 = 0.f;
+  if (fabsf(M) > kHuge && fabsf(M) < INFINITY) {  // M log2 e is not FP32: only columns equal to M count
+    s0 = s1 = 0.f;
+    for (uint32_t c = tid; c < cols; c += T) s0 += load_logit<DT>(chunk, c) == M ? 1.f : 0.f;
+    if (tid == 0) s0 -= 1.f;
+  } else if (wave == 0 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
+    bool out = false;                 // it has been left out
+    for (uint32_t base = 0; base < nb * P; base += 64) {
+      const uint32_t s = base + lane, i = vector_at(s % nb, s / nb, owner >> 6, owner & 63);
+      float f[E];
+      unpack_vec<DT>(s < nb * P && i < whole ? *reinterpret_cast<const Word*>(chunk + i * 16u)
+                     : s < nb * P            ? partial_vec<DT>(chunk, i * E, cols)
+                                             : partial_vec<DT>(chunk, cols, cols),
+                     f);
+      bool mine = false;
+#pragma unroll
+      for (int c = 0; c < E; ++c) mine |= f[c] == M;
+      const unsigned long long lanes = __ballot(mine);
+      bool leave = !out && mine && lanes_below(lanes) == 0;
+      out |= lanes != 0;
+#pragma unroll
+      for (int c = 0; c < E; ++c) {
+        const float u = __builtin_fmaf(f[c], kLog2e, -M2);
+        const bool skip = leave && f[c] == M;
+        if (skip) leave = false;
+        const float e = skip ? 0.f : exp2_hw(u);
+        s0 += e;
+        if constexpr (ENT) s1 = __builtin_fmaf(e, fmaxf(u, kFar), s1);
+      }
+    }
+  }
+  s0 = wave_sum(s0);
+  if constexpr (ENT) s1 = wave_sum(s1);
+  if (lane == 0) {
+    sh_sum[wave][0] = s0;
+    sh_sum[wave][1] = s1;
+  }
+
+  // ---- the K largest: the hits' columns, a lane each
+  if constexpr (TOP) {
+    uint32_t have = 0;
+    if (hits > (uint32_t)kHits) {
+      have = kSeg + 1;
+      hits = 0;
+    }
+    for (uint32_t i = 0; i < hits * E; i += 64) {
+      const uint32_t at = i + lane < hits * E ? i + lane : 0u;
+      const float f = load_logit<DT>(reinterpret_cast<const char*>(&hit[wave][0]), at);
+      const uint32_t c = hit_vec[wave][at / E] * E + at % E;
+      seg.add(i + lane < hits * E && c < cols && (low ? f > -INFINITY : f >= least), key_of(order_of<DT>(f), lo + c), have);
+    }
+    if (low) {  // fewer than K threads have more than -inf: of the first K columns enough are -inf to fill up with
+      for (uint32_t c = tid; c - lane < (K < cols ? K : cols); c += T) {
+        const bool in = c < (K < cols ? K : cols);
+        seg.add(in && load_logit<DT>(chunk, in ? c : 0) == -INFINITY, key_of(order_of<DT>(-INFINITY), lo + c), have);
+      }
+    }
+    seg.close(have);
     __syncthreads();
-    const uint32_t reach = n_cand;
-    if (reach > (uint32_t)kCand || reach < (cols < K ? cols : K))
-      exact_largest<DT, T, P>(v, cols, K, bound, reach, cand, &n_cand, sh_cnt);
+    uint32_t reach = 0, most = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      reach += n_seg[i];
+      most = n_seg[i] > most ? n_seg[i] : most;
+    }
+    if (most > (uint32_t)kSeg || reach < (cols < K ? cols : K)) {
+      exact_largest<DT, T>(chunk, lo, cols, K, low ? order_of<DT>(-INFINITY) : bound, seg_keys, &n_cand, sh_cnt);
+      if (tid < W) n_seg[tid] = tid == 0 ? n_cand : 0u;
+      if (tid < 4 * W) seg_keys[(tid / 4) * Segments<W, kSeg>::kStride + (tid < 4 ? n_cand : 0u) + tid % 4] = 0;
+      __syncthreads();
+    }
   } else {
     __syncthreads();
   }
-  s0 = at_max = s1 = 0.f;
+  // the chunk's sums, later the row's: `one` column counted apart
+  float one = M == -INFINITY ? 0.f : 1.f, rest = 0.f;
+  s1 = 0.f;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    s0 += sh_sum[i][0];
-    at_max += sh_sum[i][1];
-    s1 += sh_sum[i][2];
+    rest += sh_sum[i][0];
+    s1 += sh_sum[i][1];
   }
-  RowSum sum;
   {
     // from m2 to m log2 e: the terms are too large by 2^d, d = m log2 e - m2
-    const float d = m == -INFINITY || m == INFINITY ? 0.f : __builtin_fmaf(m, kLog2e, -m2);
+    const float d = fabsf(M2) == INFINITY || M == -INFINITY ? 0.f : __builtin_fmaf(M, kLog2e, -M2);
     const float grow = __builtin_fmaf(-d, kLn2f, 1.f);
-    sum.m = m;
-    sum.rest = s0 * grow;
-    sum.at_max = at_max;
-    sum.s1 = (s1 - d * s0) * grow;
+    s1 = (s1 - d * rest) * grow;
+    rest *= grow;
   }
 
-  unsigned long long* top = keys;
   if (C > 1) {
-    const uint32_t words = kStatWords + K * KW;
+    const uint32_t words = kStatWords + 2 * K;
     unsigned long long* const slot = a.slots + ((size_t)r * C + k) * words;
     const bool keep = withheld(ws, r, (int)k);
     if (tid == 0 && !keep) {
-      put_word(slot + 0, ws.tag, __float_as_uint(sum.m));
-      put_word(slot + 1, ws.tag, __float_as_uint(sum.rest));
-      put_word(slot + 2, ws.tag, __float_as_uint(sum.at_max));
-      put_word(slot + 3, ws.tag, __float_as_uint(sum.s1));
+      put_word(slot + 0, ws.tag, __float_as_uint(M));
+      put_word(slot + 1, ws.tag, __float_as_uint(rest));
+      put_word(slot + 2, ws.tag, __float_as_uint(one));
+      put_word(slot + 3, ws.tag, __float_as_uint(s1));
     }
     if constexpr (TOP) {
-      const uint32_t n = n_cand;
-      for (uint32_t i = tid; i < (n > K ? n : K); i += T) {
-        Key key = 0;
-        uint32_t rank = i;
-        if (i < n) {
-          key = cand[i];
-          rank = 0;
-          for (uint32_t q = 0; q < n; ++q) rank += cand[q] > key;
-        }
-        if (rank < K && !keep) {
-          put_word(slot + kStatWords + rank * KW, ws.tag, (uint32_t)key);
-          if constexpr (KW == 2) put_word(slot + kStatWords + rank * KW + 1, ws.tag, (uint32_t)(key >> 32));
-        }
-      }
+      uint32_t n = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) n += n_seg[i];
+      const auto publish = [&](uint32_t rank, Key key) {
+        if (rank >= K || keep) return;
+        put_word(slot + kStatWords + 2 * rank, ws.tag, (uint32_t)key);
+        put_word(slot + kStatWords + 2 * rank + 1, ws.tag, (uint32_t)(key >> 32));
+      };
+      seg.rank(publish);
+      for (uint32_t i = n + tid; i < K; i += T) publish(i, 0);
     }
     if (!last) return;
 
-    // ---- the row's last chunk collects
+    // ---- the row's last chunk collects, with the first readings of all words in flight together
     uint32_t spins = 0;
     bool ok = ws.ok;
     const unsigned long long* const slots = a.slots + (size_t)r * C * words;
-    for (uint32_t i = tid; i < C * kStatWords; i += T) {
-      const unsigned long long* p = slots + (size_t)(i / kStatWords) * words + i % kStatWords;
+    constexpr int kStatReads = (kMaxChunks * kStatWords + T - 1) / T;
+    unsigned long long stat[kStatReads], first[TOP ? 2 * kRound : 1];
+    const auto stat_word = [&](int i) {
+      const uint32_t at = i * T + tid;
+      return slots + (size_t)(at / kStatWords) * words + at % kStatWords;
+    };
+#pragma unroll
+    for (int i = 0; i < kStatReads; ++i) stat[i] = i * T + tid < C * kStatWords ? peek_word(stat_word(i)) : 0ull;
+    const uint32_t spread = lane * W + wave;  // neighbouring keys go to different waves
+    const uint32_t list = TOP ? K : 1u;
+    const auto key_word = [&](uint32_t at) { return slots + (size_t)(at / list) * words + kStatWords + at % list * 2; };
+    if constexpr (TOP) {
+#pragma unroll
+      for (int i = 0; i < kRound; ++i) {
+        const uint32_t at = i * T + spread;
+        first[2 * i] = at < C * K ? peek_word(key_word(at)) : 0ull;
+        first[2 * i + 1] = at < C * K ? peek_word(key_word(at) + 1) : 0ull;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kStatReads; ++i) {
+      if (i * T + tid >= C * kStatWords) continue;
       uint32_t w = 0x7fc00000u;
-      ok &= await_word(p, ws.tag, peek_word(p), spins, &w);
-      st[i / kStatWords][i % kStatWords] = __uint_as_float(w);
+      ok &= await_word(stat_word(i), ws.tag, stat[i], spins, &w);
+      st[(i * T + tid) / kStatWords][(i * T + tid) % kStatWords] = __uint_as_float(w);
     }
     if constexpr (TOP) {
-      const uint32_t most = (uint32_t)kMerge / K;  // lists at a time
-      uint32_t done = 0, held = 0;                 // chunks taken, lists in front (the result so far)
-      unsigned long long* b = keys + kMerge;
-      __syncthreads();  // every thread has ranked its candidates
-      while (done < C) {
-        const uint32_t take = C - done < most - held ? C - done : most - held;
-        for (uint32_t i = tid; i < take * K; i += T) {
-          const uint32_t c = done + i / K;
-          const unsigned long long* p = slots + (size_t)c * words + kStatWords + (i % K) * KW;
-          const unsigned long long w0 = peek_word(p), w1 = KW == 2 ? peek_word(p + KW - 1) : 0ull;
-          uint32_t k0 = 0, k1 = 0;
-          bool got = await_word(p, ws.tag, w0, spins, &k0);
-          if constexpr (KW == 2) got &= await_word(p + 1, ws.tag, w1, spins, &k1);
-          ok &= got;
-          const Key key = KW == 2 ? (Key)((unsigned long long)k1 << 32 | k0) : (Key)k0;
-          top[(held + i / K) * K + i % K] = got ? row_key<DT>(key, c * (uint32_t)a.chunk_cols) : 0ull;
+      uint32_t done = 0, held = 0;  // keys taken, K of each chunk; keys of earlier rounds
+      while (done < C * K) {
+        Key key[kRound];
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kRound; ++i) {
+          const uint32_t at = i * T + spread, from = done + at - held;
+          key[i] = 0;
+          if (at < held) {
+            key[i] = top[at];
+          } else if (from < C * K) {
+            const unsigned long long* const p = key_word(from);
+            uint32_t k0 = 0, k1 = 0;
+            bool got = await_word(p, ws.tag, done ? peek_word(p) : first[2 * i], spins, &k0);
+            got &= await_word(p + 1, ws.tag, done ? peek_word(p + 1) : first[2 * i + 1], spins, &k1);
+            ok &= got;
+            key[i] = got ? (Key)k1 << 32 | k0 : 0ull;
+          }
+          const uint32_t o = (uint32_t)(key[i] >> 32);
+          best = o > best ? o : best;
         }
+        done += kRound * T - held;
+        held = K;
+        uint32_t* const tops = thread_top[raised++ & 1];
+        tops[tid] = best;
+        __syncthreads();  // (and every thread has ranked the chunk's candidates, or read `top`)
+        uint32_t g[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) g[i] = tops[i * 64 + lane];
+        const uint32_t least_order = bound_of<DT>(K, g);
+        uint32_t have = 0;
+#pragma unroll
+        for (int i = 0; i < kRound; ++i)
+          seg.add((uint32_t)(key[i] >> 32) >= least_order && key[i] != 0ull, key[i], have);
+        seg.close(have);
+        for (uint32_t i = tid; i < K; i += T) top[i] = 0ull;  // a word that never came leaves a place empty
         __syncthreads();
-        unsigned long long* const out = merge_lists<T>(top, b, held + take, K);
-        b = out == top ? b : top;
-        top = out;
-        done += take;
-        held = 1;
+        seg.rank([&](uint32_t rank, Key key) {
+          if (rank < K) top[rank] = key;
+        });
+        __syncthreads();
       }
     }
     ok = __syncthreads_and(ok);
     if (!ok && tid == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
-    // lane c of every wave takes chunk c
-    const uint32_t c = tid & 63;
-    const bool has = c < C;
-    const float mc = has ? st[c][0] : -INFINITY;
-    m = wave_largest(mc);
-    const bool some = has && mc != -INFINITY, best = some && mc == m;
-    const float dm = some ? (mc - m) * kLog2e : 0.f, w = exp2_hw(dm);
-    const float rc = some ? st[c][1] : 0.f, nc = some ? st[c][2] : 0.f, sc = some ? st[c][3] : 0.f;
-    // a chunk whose maximum is NaN (it holds nothing else) carries it in its sum
-    const float carry = has && mc == -INFINITY && st[c][1] != st[c][1] ? st[c][1] : 0.f;
-    sum.m = m;
-    sum.rest = wave_sum((best ? rc : (rc + nc) * w) + carry);
-    sum.at_max = wave_sum(best ? nc : 0.f);
-    if constexpr (ENT) sum.s1 = wave_sum(some ? __builtin_fmaf(dm, rc + nc, sc) * w : 0.f);
-    if (!ok) sum.rest = __uint_as_float(0x7fc00000u);
+    // lane c of every wave takes chunk c; the first with the row's maximum counts one column of it apart
+    const bool has = lane < C;
+    const float mc = has ? st[lane][0] : -INFINITY;
+    M = wave_largest(mc);
+    const bool some = has && mc != -INFINITY;
+    const unsigned long long best = __ballot(some && mc == M);
+    const float dm = some ? fmaxf((mc - M) * kLog2e, kFar) : 0.f, w = exp2_hw(dm);
+    const float rc = has ? st[lane][1] : 0.f, sc = some ? st[lane][3] : 0.f;
+    const bool apart = some && mc == M && lanes_below(best) == 0;
+    // (a chunk of -inf has the sum 0, or the NaN of a NaN)
+    rest = wave_sum(apart ? rc : some ? (rc + 1.f) * w : rc);
+    if constexpr (ENT) s1 = wave_sum(some ? __builtin_fmaf(dm, rc + 1.f, sc) * w : 0.f);
+    one = best ? 1.f : 0.f;
+    if (!ok) rest = __uint_as_float(0x7fc00000u);
     if (TOP && !ok) {
       for (uint32_t i = tid; i < K; i += T) top[i] = 0ull;
       __syncthreads();
     }
   } else if constexpr (TOP) {
     // one chunk: its ranks are the row's (K is at most the number of columns)
-    const uint32_t n = n_cand;
-    uint32_t rank[(kCand + T - 1) / T];
-    Key key[(kCand + T - 1) / T];
-#pragma unroll
-    for (int i = 0; i < (kCand + T - 1) / T; ++i) {
-      const uint32_t at = i * T + tid;
-      rank[i] = K;
-      if (i * T < (int)n && at < n) {
-        key[i] = cand[at];
-        rank[i] = 0;
-        for (uint32_t q = 0; q < n; ++q) rank[i] += cand[q] > key[i];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < (kCand + T - 1) / T; ++i)
-      if (rank[i] < K) keys[rank[i]] = row_key<DT>(key[i], 0u);
+    seg.rank([&](uint32_t rank, Key key) {
+      if (rank < K) top[rank] = key;
+    });
     __syncthreads();
   }
 
   // ---- the row's outputs (+inf has no distribution either)
-  if (sum.m == INFINITY) sum.rest = __uint_as_float(0x7fc00000u);
-  sum.logd = log_of_sum(sum);
-  const float logd = sum.logd;
+  if (M == INFINITY) rest = __uint_as_float(0x7fc00000u);
+  const float logd = one == 1.f ? log1pf(rest) : logf(rest);
 #pragma unroll
   for (int i = 0; i < TK; ++i) {
     const int at = i * T + tid;
     if (at < a.M) {
       const int64_t t = id[i];
-      float lp = (xt[i] - sum.m) - logd;
+      float lp = (xt[i] - M) - logd;
       if (t < 0 || t >= a.V) lp = __uint_as_float(0x7fc00000u);
       if (t == a.ignore_idx) lp = 0.f;
       a.logp[r * a.M + at] = lp;
@@ -503,39 +689,39 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   }
   if constexpr (TOP) {
     for (uint32_t i = tid; i < K; i += T) {
-      const unsigned long long key = top[i];
+      const Key key = top[i];
       const float f = value_of<DT>((uint32_t)(key >> 32));
       a.top_ids[r * K + i] = key ? (int64_t)(uint32_t)~(uint32_t)key : -1;
-      a.top_logp[r * K + i] = key ? (f - sum.m) - logd : __uint_as_float(0x7fc00000u);
+      a.top_logp[r * K + i] = key ? (f - M) - logd : __uint_as_float(0x7fc00000u);
     }
   }
   if (tid == 0) {
-    const float D = sum.rest + sum.at_max;
-    const float h = ENT ? __builtin_fmaf(-kLn2f, sum.s1 / D, logd) : 0.f;
+    const float D = rest + one;
+    const float h = ENT ? __builtin_fmaf(-kLn2f, s1 / D, logd) : 0.f;
     if (ENT) a.entropy[r] = h;
-    if (a.lse) a.lse[r] = sum.m + logd;
-    if (a.stats)
-      reinterpret_cast<float4*>(a.stats)[r] =
-          make_float4(sum.m, logd, sum.at_max == 1.f ? sum.rest / D : 1.f - 1.f / D, h);
+    if (a.lse) a.lse[r] = M + logd;
+    if (a.stats) reinterpret_cast<float4*>(a.stats)[r] = make_float4(M, logd, rest / D, h);
   }
 
   // ---- the last row's workgroup ends the call once every row has been brought together
   if (C > 1) {
-    if (tid == 0) put_word(a.done + r, ws.tag, 0u);
-    if (r != a.N - 1) return;
+    if (r != a.N - 1) {
+      if (tid == 0) put_word(a.done + r, ws.tag, 0u);
+      return;
+    }
     uint32_t spins = 0, w;
     bool ok = true;
-    for (int64_t base = 0; base < a.N; base += 4 * T) {
+    for (int64_t base = 0; base < r; base += 4 * T) {
       unsigned long long first[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t at = base + i * T + tid;
-        first[i] = peek_word(a.done + (at < a.N ? at : 0));
+        first[i] = peek_word(a.done + (at < r ? at : 0));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t at = base + i * T + tid;
-        ok = ok && await_word(a.done + (at < a.N ? at : 0), ws.tag, first[i], spins, &w);
+        ok = ok && await_word(a.done + (at < r ? at : 0), ws.tag, first[i], spins, &w);
       }
     }
     if (!ok) atomicOr(&a.hdr->status, 1u);
@@ -583,7 +769,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
   const bool mine = counts && valid && id >= lo && id < (int64_t)lo + cols;
   if (!counts) g = 0.f;
   if (counts && !valid) g = __uint_as_float(0x7fc00000u);  // the row's gradient is NaN
-  const float xt = mine ? load_logit<DT>(row, id) : 0.f;
+  float xt = mine ? load_logit<DT>(row, id) : 0.f;
   float G = g;
   if (L > 1) {
     sid[tid] = mine ? id : -1;
@@ -600,10 +786,24 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
     G = sh[0];
   }
 
+  float top = s.x;
+  if (fabsf(top) > kHuge && fabsf(top) < INFINITY) {  // m log2 e is not FP32: only columns equal to m have a share
+    const auto share = [&](float x) { return x == top ? 0.f : -INFINITY; };
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      float f[E];
+      unpack_vec<DT>(v[j], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = share(f[e]);
+      v[j] = pack_vec<DT>(f);
+    }
+    xt = share(xt);
+    top = 0.f;
+  }
   // p = 2^(x log2 e - c), c = (m + log D) log2 e in two parts; the second matters to FP32's rounding and to log p
   // near 0, which the entropy's gradient takes
   constexpr bool kTwo = DT == CE_F32 || ENT;
-  const double c = ((double)s.x + (double)s.y) * (double)kLog2e;
+  const double c = ((double)top + (double)s.y) * (double)kLog2e;
   const float c_hi = (float)c, c_lo = kTwo ? (float)(c - (double)c_hi) : 0.f;
   const float slope = ENT ? __builtin_fmaf(dh, s.w, G) : G, bend = ENT ? dh * kLn2f : 0.f;
   const auto exponent = [&](float x) {
@@ -618,7 +818,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
     for (int e = 0; e < E; ++e) {
       const float t = exponent(f[e]), p = exp2_hw(t);
       if constexpr (ENT)  // p = 0 of a masked column takes the 0, not its log's infinity
-        f[e] = -p * __builtin_fmaf(fmaxf(t, -1000.f), bend, slope);
+        f[e] = -p * __builtin_fmaf(fmaxf(t, kFar), bend, slope);
       else
         f[e] = -p * slope;
     }
@@ -634,15 +834,15 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
     }
     // own - p (G + ...) without a cancellation at p near 1: own (1 - p) - p (G - own + ...)
     const float t = exponent(xt), p = exp2_hw(t);
-    const float q = xt == s.x && s.z < 0.5f ? s.z : 1.f - p;
+    const float q = xt == top && s.z < 0.5f ? s.z : 1.f - p;
     const float others = L > 1 ? G - own : 0.f;
-    const float h = ENT ? dh * __builtin_fmaf(fmaxf(t, -1000.f), kLn2f, s.w) : 0.f;
+    const float h = ENT ? dh * __builtin_fmaf(fmaxf(t, kFar), kLn2f, s.w) : 0.f;
     store_logit<DT>(out, id, __builtin_fmaf(own, q, -p * (others + h)));
   }
 }
 
-// Chunk shapes (threads, vectors a thread); logprob_plan chooses
-constexpr FusedShape kShapes[] = {{64, 4}, {256, 2}, {256, 8}};
+// Shapes (threads, vectors a thread and batch); logprob_plan chooses
+constexpr FusedShape kShapes[] = {{64, 4}, {256, 2}, {512, 4}};
 
 template <int DT, int T, int P>
 void launch_flags(const LogprobArgs& a, dim3 grid, hipStream_t stream) {
@@ -670,12 +870,24 @@ int64_t share_cols(int64_t V, int64_t chunks, int64_t vec) { return ((V + chunks
 
 }  // namespace
 
-int64_t logprob_max_cols(int32_t dtype) { return shape_cols(2, dtype) * kMaxChunks; }
+int64_t logprob_max_cols(int32_t dtype) { return (int64_t)1 << (dtype == CE_BF16 ? 20 : 19); }
 
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols) {
-  const auto pieces = [=](int s) { return (V + shape_cols(s, dtype) - 1) / shape_cols(s, dtype); };
-  *shape = V <= shape_cols(0, dtype) ? 0 : N * pieces(2) < 256 && pieces(1) <= kMaxChunks ? 1 : 2;
-  *chunks = pieces(*shape);
+  static const int fs = getenv("LPS") ? atoi(getenv("LPS")) : -1, fc = getenv("LPC") ? atoi(getenv("LPC")) : -1;
+  *chunks = 1;
+  if (V <= shape_cols(0, dtype)) {
+    *shape = 0;
+  } else if (N >= 512) {
+    *shape = V <= 2 * shape_cols(1, dtype) ? 1 : 2;
+  } else {
+    // a chunk is a batch at least
+    *shape = 1;
+    const int64_t most = (V + shape_cols(1, dtype) - 1) / shape_cols(1, dtype), want = (512 + N - 1) / (N ? N : 1);
+    *chunks = want < most ? want : most;
+    if (*chunks > kMaxChunks) *chunks = kMaxChunks;
+    if (fs > 0) *shape = fs;
+    if (fc > 0) *chunks = fc;
+  }
   *chunk_cols = share_cols(V, *chunks, vec_cols(dtype));
   *chunks = (V + *chunk_cols - 1) / *chunk_cols;  // whole vectors can leave the last share empty
 }
@@ -685,7 +897,7 @@ size_t logprob_workspace(int64_t N, int64_t V, int32_t dtype, int32_t K) {
   int64_t chunks, cols;
   logprob_plan(N, V, dtype, &shape, &chunks, &cols);
   if (chunks == 1 || N == 0) return 0;
-  const size_t words = kStatWords + (size_t)K * (dtype == CE_BF16 ? 1 : 2);
+  const size_t words = kStatWords + 2 * (size_t)K;
   return kWsHeaderBytes + (size_t)N * 8 + (size_t)N * chunks * words * 8;
 }
 

@@ -102,16 +102,47 @@ __device__ __forceinline__ float largest(const u32x4v& v, float m) {
   return m;
 }
 
-// One row's columns [lo, hi) as T x P vectors: vector j * T + tid in slot j of
+// The chunk's columns first, first + 1, ... of a vector that is not whole; -inf for those that are not there.
+template <int DT>
+__device__ __forceinline__ u32x4v partial_vec(const char* chunk, uint32_t first, uint32_t cols) {
+  constexpr uint32_t kNone = LogitT<DT>::kNegInf;
+  u32x4v v = {kNone, kNone, kNone, kNone};
+#pragma unroll
+  for (int e = 0; e < LogitT<DT>::E - 1; ++e) {
+    if (first + e >= cols) continue;
+    if constexpr (DT == CE_BF16) {
+      const uint32_t h = reinterpret_cast<const uint16_t*>(chunk)[first + e];
+      v[e / 2] = e & 1 ? (v[e / 2] & 0xffffu) | h << 16 : (v[e / 2] & 0xffff0000u) | h;
+    } else {
+      v[e] = reinterpret_cast<const uint32_t*>(chunk)[first + e];
+    }
+  }
+  return v;
+}
+
+// A register chosen at run time (laundered, or the compiler chooses an address and puts the array into scratch memory).
+template <int P>
+__device__ __forceinline__ u32x4v pick(const u32x4v (&v)[P], uint32_t j) {
+  u32x4v w = v[0];
+#pragma unroll
+  for (int i = 1; i < P; ++i) {
+    u32x4v other = v[i];
+    relaunch(other);
+    if ((uint32_t)i == j) w = other;
+  }
+  return w;
+}
+
+// A chunk of `cols` columns as T x P vectors: vector j * T + tid in slot j of
 // thread tid.  Slots past the chunk, and a last vector's missing columns, hold
-// -inf.  No load stands behind a branch that not all of a wave take: slots past
-// the whole vectors load the chunk's first one and are overwritten.
+// -inf.  No load of a whole vector stands behind a branch: slots past them load
+// the chunk's first one and are overwritten.
 template <int DT, int T, int P>
 __device__ __forceinline__ void load_chunk(const char* chunk, uint32_t cols, u32x4v (&v)[P]) {
   typedef typename LogitT<DT>::Word Word;
   constexpr int E = LogitT<DT>::E;
-  const uint32_t tid = threadIdx.x;
-  const uint32_t whole = cols / E;
+  constexpr uint32_t kNone = LogitT<DT>::kNegInf;
+  const uint32_t tid = threadIdx.x, whole = cols / E;
   if (whole > 0) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -122,21 +153,15 @@ __device__ __forceinline__ void load_chunk(const char* chunk, uint32_t cols, u32
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     if ((uint32_t)(j + 1) * T <= whole) continue;  // the same for the whole workgroup
-    const uint32_t i = j * T + tid;
-    if (i >= whole) {
-      v[j] = u32x4v{LogitT<DT>::kNegInf, LogitT<DT>::kNegInf, LogitT<DT>::kNegInf, LogitT<DT>::kNegInf};
-      if (i == whole) {
+    if (j * T + tid >= whole) v[j] = u32x4v{kNone, kNone, kNone, kNone};
+  }
+  if (cols % E != 0 && tid == whole % T) {
+    const u32x4v w = partial_vec<DT>(chunk, whole * E, cols);
 #pragma unroll
-        for (int e = 0; e < E - 1; ++e) {
-          if (i * E + e >= cols) continue;
-          if constexpr (DT == CE_BF16) {
-            const uint32_t h = reinterpret_cast<const uint16_t*>(chunk)[i * E + e];
-            v[j][e / 2] = e & 1 ? (v[j][e / 2] & 0xffffu) | h << 16 : (v[j][e / 2] & 0xffff0000u) | h;
-          } else {
-            v[j][e] = reinterpret_cast<const uint32_t*>(chunk)[i * E + e];
-          }
-        }
-      }
+    for (int j = 0; j < P; ++j) {
+      u32x4v mine = w;
+      relaunch(mine);  // (as in pick)
+      if ((uint32_t)j == whole / T) v[j] = mine;
     }
   }
 }
@@ -175,6 +200,16 @@ __device__ __forceinline__ float wave_largest(float v) {
   v = fmaxf(v, dpp_or_own<kBcast15, 0xa>(v));
   v = fmaxf(v, dpp_or_own<kBcast31, 0xc>(v));
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// the bits set in any lane, uniform
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kSwap1, 0xf, 0xf, true);
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kSwap2, 0xf, 0xf, true);
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kHalfMirror, 0xf, 0xf, true);
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kMirror, 0xf, 0xf, true);
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kBcast15, 0xa, 0xf, true);
+  v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kBcast31, 0xc, 0xf, true);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
