@@ -99,7 +99,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
   const uint32_t cols = (uint32_t)a.V - lo < (uint32_t)a.chunk_cols ? (uint32_t)a.V - lo : (uint32_t)a.chunk_cols;
   int L = a.K;
   if (a.len) {
-    L = a.len[r];
+    L = load_uniform(a.len + r);
     L = L < 0 ? 0 : L > a.K ? a.K : L;
   }
   const auto row_loss = [&](float loss) {  // by one thread of the row
@@ -109,32 +109,36 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
 
   if (L == 0) {  // left out: loss 0, gradient 0, the logits not read
     if constexpr (GRAD) {
-      for (uint32_t i = tid; i * E < cols; i += T) store_vec<DT>(out + (size_t)lo * EB, cols, i, u32x4v{0u, 0u, 0u, 0u});
+      u32x4v v[P] = {};
+      store_chunk<DT, T, P>(out + (size_t)lo * EB, cols, v, [](const u32x4v&) { return u32x4v{0u, 0u, 0u, 0u}; });
     }
     if (k == 0 && tid == 0) row_loss(0.f);
   } else {
-    // ---- the entries (wave 0), then the chunk
+    // ---- wave 0's entries, then the chunk; while it comes in, the bitmap and the teacher's probabilities
+    const float up = a.g ? load_uniform(a.g + (a.reduce == CE_REDUCE_NONE ? r : 0)) : 1.f;
+    const int32_t count = a.reduce == CE_REDUCE_MEAN && a.n ? load_uniform(a.n) : (int32_t)a.N;
     int64_t id[kEntries];
-    float tv[kEntries];
+    float tv[kEntries], xe[kEntries];
     if (tid < 64) {
       const int64_t* ids = a.ids + i0 * a.is0 + i1 * a.is1;
       const char* const t = a.teacher + (i0 * a.ts0 + i1 * a.ts1) * (a.tdtype == CE_BF16 ? 2 : 4);
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         const int at = i * 64 + (int)lane;
-        id[i] = at < L ? ids[at] : -1;
-        tv[i] = at < L ? (a.tdtype == CE_BF16 ? load_logit<CE_BF16>(t, at) : load_logit<CE_F32>(t, at)) : 0.f;
+        id[i] = -1;
+        tv[i] = xe[i] = 0.f;
+        if (at < L) {
+          id[i] = ids[at];
+          tv[i] = a.tdtype == CE_BF16 ? load_logit<CE_BF16>(t, at) : load_logit<CE_F32>(t, at);
+        }
       }
     }
     u32x4v v[P];
     load_chunk<DT, T, P>(row + (size_t)lo * EB, cols, v);
-    float up = a.g ? a.g[a.reduce == CE_REDUCE_NONE ? r : 0] : 1.f;
     reinterpret_cast<uint64_t*>(named)[tid] = 0ull;
     __syncthreads();
-
-    // ---- wave 0: the student's logits of the entries here, the bitmap, the teacher's probabilities
     bool here[kEntries], first[kEntries];
-    double z[kEntries], p[kEntries], logp[kEntries];
+    double p[kEntries];
     double mass = 0.0, plogp = 0.0;
     bool bad = false;
     if (tid < 64) {
@@ -144,18 +148,18 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
         bad |= is && (id[i] < 0 || id[i] >= a.V);
         here[i] = is && id[i] >= lo && id[i] < (int64_t)lo + cols;
         first[i] = false;
-        z[i] = 0.0;
         if (here[i]) {
           const uint32_t c = (uint32_t)(id[i] - lo), vec = c / E;
           const uint32_t at = (vec % T) * 8 + vec / T;  // its byte
           const uint32_t bit = 1u << (c % E + 8 * (at & 3));
           first[i] = !(atomicOr(reinterpret_cast<uint32_t*>(named) + (at >> 2), bit) & bit);
-          z[i] = (double)load_logit<DT>(row, id[i]) * (double)a.kb;  // base 2, as the sums' exponents
+          xe[i] = load_logit<DT>(row, id[i]);
         }
       }
     }
     __syncthreads();
     if (tid < 64) {
+      double logp[kEntries];
       if (a.kind == CE_TEACHER_LOGITS) {
         double t[kEntries], top = -(double)INFINITY;
 #pragma unroll
@@ -193,6 +197,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       plogp = wave_sum64(plogp);
       bad = __any(bad);
     }
+
+    float grad[kEntries];  // of the named columns here
 
     // ---- the unnamed columns: maximum and sum
     float m = -INFINITY;
@@ -239,7 +245,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       s0 = sh_sum[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) s0 += sh_sum[i];
-      double named_log = -(double)INFINITY, pz = 0.0;
+      double named_log = -(double)INFINITY, pz = 0.0, z[kEntries];
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) z[i] = (double)xe[i] * (double)a.kb;  // base 2, as the sums' exponents
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) pz += here[i] && p[i] != 0.0 ? p[i] * z[i] : 0.0;
       {
@@ -313,7 +321,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       if (left != 0.0) loss += left * (log(left) - (rest - lse) * kLn2d);
       loss *= a.t * a.t;
       double s = (double)up * a.t;
-      if (a.reduce == CE_REDUCE_MEAN) s /= (double)(a.n ? *a.n : (int32_t)a.N);
+      if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
       if (k == 0 && lane == 0) row_loss((float)loss);
       if constexpr (GRAD) {
@@ -323,7 +331,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
           bc[1] = DT == CE_F32 ? (float)(lse - (double)c_hi) : 0.f;
           bc[2] = (float)(s * (S - (left == 0.0 ? 0.0 : left * exp2(lse - rest))));
         }
-        // the named columns' gradients, into z; entries of the same column add up, in order
+        // the named columns' gradients; entries of the same column add up, in order
         const bool twice = __any([&] {
           bool d = false;
 #pragma unroll
@@ -341,31 +349,29 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
               all += other == id[i] ? add : 0.0;
             }
           }
-          z[i] = s * (exp2(z[i] - lse) * S - all);
+          grad[i] = (float)(s * (exp2(z[i] - lse) * S - all));
         }
       }
     }
     if constexpr (GRAD) {
       __syncthreads();
       const float c_hi = bc[0], c_lo = bc[1], f_un = bc[2];
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        relaunch(v[j]);
+      store_chunk<DT, T, P>(out + (size_t)lo * EB, cols, v, [&](const u32x4v& x) {
         float f[E];
-        unpack_vec<DT>(v[j], f);
+        unpack_vec<DT>(x, f);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float t = __builtin_fmaf(f[e], a.kb, -c_hi);
           if constexpr (DT == CE_F32) t -= c_lo;
           f[e] = exp2_hw(t) * f_un;
         }
-        store_vec<DT>(out + (size_t)lo * EB, cols, j * T + tid, pack_vec<DT>(f));
-      }
+        return pack_vec<DT>(f);
+      });
       __syncthreads();
       if (tid < 64) {  // over the zeros that were written for the named columns
 #pragma unroll
         for (int i = 0; i < kEntries; ++i)
-          if (here[i]) store_logit<DT>(out, id[i], (float)z[i]);
+          if (here[i]) store_logit<DT>(out, id[i], grad[i]);
       }
     }
   }

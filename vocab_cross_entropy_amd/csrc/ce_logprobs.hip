@@ -30,7 +30,8 @@
 // depends on scheduling.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
+
+#include <type_traits>
 
 #include "ce_internal.h"
 #include "ce_row.h"
@@ -94,15 +95,27 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t K, const uint32_t (&g)[G
   return t;
 }
 
-// The same of 64 G group maxima, G a lane.  Where 64 of them are enough, of each lane's maximum: a few more
-// columns reach that (K = 32: 44 instead of 34), for a G-th of the ballots.
-template <int DT, int G>
-__device__ __forceinline__ uint32_t bound_of(uint32_t K, const uint32_t (&g)[G]) {
-  if (K > 32) return reached_by<kLowBits<DT>, G>(K, g);
-  uint32_t top[1] = {g[0]};
+// The same of group maxima, `g(i)` a lane's i-th of G: of 64, 128 or 256 groups, at least twice K, made of them.  About
+// 1.4 K columns reach it then (K = 32 of 64: 44, 64 of 128: 89); more groups take more ballots than they save.
+template <int DT, int G, typename Group>
+__device__ __forceinline__ uint32_t bound_of(uint32_t K, Group g) {
+  const auto of = [&](auto groups) {
+    constexpr int N = decltype(groups)::value;
+    uint32_t top[N];
 #pragma unroll
-  for (int i = 1; i < G; ++i) top[0] = g[i] > top[0] ? g[i] : top[0];
-  return reached_by<kLowBits<DT>, 1>(K, top);
+    for (int i = 0; i < N; ++i) {
+      top[i] = g(i);
+#pragma unroll
+      for (int k = N; k < G; k += N) {
+        const uint32_t o = g(i + k);
+        top[i] = o > top[i] ? o : top[i];
+      }
+    }
+    return reached_by<kLowBits<DT>, N>(K, top);
+  };
+  if (K <= 32) return of(std::integral_constant<int, 1>{});
+  if (K <= 64) return of(std::integral_constant<int, 2>{});
+  return of(std::integral_constant<int, 4>{});
 }
 
 template <int T>
@@ -216,7 +229,8 @@ template <int W, int SEG>
 struct Segments {
   static constexpr int kStride = SEG + 4;
   Key* keys;
-  uint32_t* n;  // [W]
+  uint32_t* n;      // [W]
+  uint32_t* ranks;  // [W * SEG]
 
   // Adds the keys of the lanes that have one; `have` counts the wave's (beyond SEG they are dropped).
   __device__ __forceinline__ void add(bool mine, Key key, uint32_t& have) const {
@@ -230,35 +244,38 @@ struct Segments {
     const uint32_t lane = threadIdx.x & 63, kept = have < (uint32_t)SEG ? have : (uint32_t)SEG;
     if (lane < 4) keys[(threadIdx.x >> 6) * kStride + kept + lane] = 0;
     if (lane == 0) n[threadIdx.x >> 6] = have;
+    for (uint32_t i = threadIdx.x; i < W * SEG; i += W * 64) ranks[i] = 0;
   }
-  // put(rank, key) for each of the keys, by counting the larger ones
+  // the i-th key of all segments
+  __device__ __forceinline__ Key at(uint32_t i) const {
+    uint32_t base = 0;
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w) {
+      const bool past = i >= n[w] && base == (uint32_t)w * kStride;
+      i -= past ? n[w] : 0u;
+      base += past ? kStride : 0u;
+    }
+    return keys[base + i];
+  }
+  // put(rank, key) for each of the keys: every wave counts, for all keys, the larger ones in its own segment
   template <typename Put>
-  __device__ __forceinline__ void rank(Put put) const {
+  __device__ __forceinline__ void rank(uint32_t total, Put put) const {
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    uint32_t longest = 0, end[W];  // where a segment's last zeros are
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      end[w] = (n[w] + 1) / 2 * 2;
-      longest = n[w] > longest ? n[w] : longest;
-    }
+    const KeyPair* const own = reinterpret_cast<const KeyPair*>(keys + wave * kStride);
 #pragma unroll 1
-    for (uint32_t base = 0; base < n[wave]; base += 64) {
+    for (uint32_t base = 0; base < total; base += 64) {
       const uint32_t i = base + lane;
-      const bool mine = i < n[wave];
-      const Key key = mine ? keys[wave * kStride + i] : 0;
+      const Key key = i < total ? at(i) : ~0ull;
       uint32_t r = 0;
-#pragma unroll 1
-      for (uint32_t q = 0; q < longest; q += 2) {
-        KeyPair o[W];
-#pragma unroll
-        for (int w = 0; w < W; ++w) o[w] = *reinterpret_cast<const KeyPair*>(keys + w * kStride + (q < end[w] ? q : end[w]));
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) r += o[w][c] > key;
+#pragma unroll 2
+      for (uint32_t q = 0; 2 * q < n[wave]; ++q) {
+        const KeyPair o = own[q];
+        r += (o.x > key) + (o.y > key);
       }
-      if (mine) put(r, key);
+      if (r) atomicAdd(&ranks[i], r);
     }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < total; i += W * 64) put(ranks[i], at(i));
   }
 };
 
@@ -269,21 +286,21 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   constexpr int TK = (kTop + T - 1) / T;  // given tokens a thread
   constexpr bool kSplit = W > 1;          // one wave only ever takes a whole row
   constexpr int kRound = 1024 / T;        // keys a thread takes into one round of merging
-  // A wave's vectors that have reached a bound, and the columns that reach the last one; later the row's keys.  A chunk
-  // of fewer than kTop vectors has no bound; it is one wave's (other shapes' have more), and fits.
-  constexpr int kHits = 128, kSeg = W > 1 ? 256 * 4 / W + 64 : kTop * (E + 1);
+  // A wave's vectors that have reached a bound, and the columns that reach the last one; later the row's keys
+  constexpr int kHits = 128, kSeg = W > 1 ? 1024 / W : 320;
   static_assert(kSeg >= 64 * (kSplit ? kRound : 0) && kHits >= kTop, "what the segments hold");
   __shared__ float sh_max[W];
   __shared__ float sh_sum[W][2];
   __shared__ uint32_t sh_own[W];
   __shared__ float st[kSplit ? kMaxChunks : 1][kStatWords];
   __shared__ uint32_t sh_cnt[W], n_seg[W], n_cand;
-  __shared__ uint32_t thread_top[2][TOP && W > 1 ? T : 1];
+  __shared__ uint32_t thread_top[TOP && W > 1 ? T : 1], sh_bound;
+  __shared__ uint32_t ranks[TOP ? W * kSeg : 1];
   __shared__ u32x4v hit[TOP ? W : 1][TOP ? kHits : 1];
   __shared__ uint32_t hit_vec[TOP ? W : 1][TOP ? kHits : 1];
   __shared__ __align__(32) Key seg_keys[TOP ? W * Segments<W, kSeg>::kStride : 1];
   __shared__ Key top[TOP ? kTop : 1];  // the row's keys
-  const Segments<W, kSeg> seg{seg_keys, n_seg};
+  const Segments<W, kSeg> seg{seg_keys, n_seg, ranks};
 
   const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const uint32_t C = kSplit ? (uint32_t)a.chunks : 1u, K = TOP ? (uint32_t)a.K : 0u;
@@ -324,19 +341,20 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   };
   bool low = true;                      // no bound, or -inf
   float least = -INFINITY;              // the bound
-  uint32_t bound = 0, raised = 0, hits = 0;
-  // from the running maxima of all threads; the two buffers alternate, a barrier each
-  const auto raise_bound = [&] {
-    constexpr int G = W > 1 ? W : P;
-    uint32_t g[G];
-    if constexpr (W > 1) {
-      uint32_t* const tops = thread_top[raised++ & 1];
-      tops[tid] = tid < vecs ? order_of<DT>(m) : 0u;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < G; ++i) g[i] = tops[i * 64 + lane];
-      bound = bound_of<DT>(K, g);
+  uint32_t bound = 0, hits = 0;
+  // the bound from the running maxima of all threads, by one wave; two barriers
+  const auto raise_bound = [&](auto meanwhile) {
+    thread_top[tid] = tid < vecs ? order_of<DT>(m) : 0u;
+    __syncthreads();
+    if (wave == 0) {
+      const uint32_t t = bound_of<DT, W>(K, [&](int i) { return thread_top[i * 64 + lane]; });
+      if (lane == 0) sh_bound = t;
     }
+    meanwhile();
+    __syncthreads();
+    bound = sh_bound;
+  };
+  const auto set_least = [&] {
     low = bound <= order_of<DT>(-INFINITY);
     least = low ? -INFINITY : value_of<DT>(bound);
   };
@@ -411,13 +429,13 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     // ---- vectors that reach the bound
     if constexpr (TOP) {
       if constexpr (W > 1) {
-        if ((b & (b - 1)) == 0) raise_bound();  // b = 0, 1, 2, 4, 8 ...
+        if (((b + 2) & (b + 1)) == 0) {  // b = 0, 2, 6, 14 ...
+          raise_bound([] {});
+          set_least();
+        }
       } else {  // one batch: of the vectors' maxima
-        uint32_t g[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) g[j] = vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u;
-        bound = bound_of<DT>(K, g);
-        raise_bound();
+        bound = bound_of<DT, P>(K, [&](int j) { return vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u; });
+        set_least();
       }
 #pragma unroll
       for (int j = 0; j < P; ++j) {
@@ -444,25 +462,23 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       sh_own[wave] = wave * 64 + (uint32_t)__builtin_ctzll(owners | 1ull << 63);
     }
   }
-  if constexpr (TOP && W > 1) {
-    if (nb > 1) raise_bound();
-  }
-  __syncthreads();
-  float M = sh_max[0];
+  float M, M2;
+  const auto sums_of_chunk = [&] {
+  M = sh_max[0];
   uint32_t owner = sh_own[0];
 #pragma unroll
   for (int i = 1; i < W; ++i) {
     owner = sh_max[i] > M ? sh_own[i] : owner;
     M = fmaxf(M, sh_max[i]);
   }
-  const float M2 = M == -INFINITY ? 0.f : M * kLog2e;
+  M2 = M == -INFINITY ? 0.f : M * kLog2e;
   move_sums(M2, s0, s1);
   if (M != -INFINITY && tid == owner) s0 = s1 = 0.f;
   if (fabsf(M) > kHuge && fabsf(M) < INFINITY) {  // M log2 e is not FP32: only columns equal to M count
     s0 = s1 = 0.f;
     for (uint32_t c = tid; c < cols; c += T) s0 += load_logit<DT>(chunk, c) == M ? 1.f : 0.f;
     if (tid == 0) s0 -= 1.f;
-  } else if (wave == 0 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
+  } else if (wave == W - 1 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
     bool out = false;                 // it has been left out
     for (uint32_t base = 0; base < nb * P; base += 64) {
       const uint32_t s = base + lane, i = vector_at(s % nb, s / nb, owner >> 6, owner & 63);
@@ -487,6 +503,19 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         if constexpr (ENT) s1 = __builtin_fmaf(e, fmaxf(u, kFar), s1);
       }
     }
+  }
+  };
+  if constexpr (TOP && W > 1) {
+    if (nb > 1 && ((nb + 1) & nb) != 0) {  // the last batch did not raise it
+      raise_bound(sums_of_chunk);
+      set_least();
+    } else {
+      __syncthreads();
+      sums_of_chunk();
+    }
+  } else {
+    __syncthreads();
+    sums_of_chunk();
   }
   s0 = wave_sum(s0);
   if constexpr (ENT) s1 = wave_sum(s1);
@@ -566,7 +595,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         put_word(slot + kStatWords + 2 * rank, ws.tag, (uint32_t)key);
         put_word(slot + kStatWords + 2 * rank + 1, ws.tag, (uint32_t)(key >> 32));
       };
-      seg.rank(publish);
+      seg.rank(n, publish);
       for (uint32_t i = n + tid; i < K; i += T) publish(i, 0);
     }
     if (!last) return;
@@ -625,13 +654,17 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         }
         done += kRound * T - held;
         held = K;
-        uint32_t* const tops = thread_top[raised++ & 1];
-        tops[tid] = best;
+        thread_top[tid] = best;
         __syncthreads();  // (and every thread has ranked the chunk's candidates, or read `top`)
-        uint32_t g[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) g[i] = tops[i * 64 + lane];
-        const uint32_t least_order = bound_of<DT>(K, g);
+        uint32_t least_order = 0;
+        if (C * K > 192) {  // fewer are ranked sooner than a bound is found
+          if (wave == 0) {
+            const uint32_t t = bound_of<DT, W>(K, [&](int i) { return thread_top[i * 64 + lane]; });
+            if (lane == 0) sh_bound = t;
+          }
+          __syncthreads();
+          least_order = sh_bound;
+        }
         uint32_t have = 0;
 #pragma unroll
         for (int i = 0; i < kRound; ++i)
@@ -639,7 +672,10 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         seg.close(have);
         for (uint32_t i = tid; i < K; i += T) top[i] = 0ull;  // a word that never came leaves a place empty
         __syncthreads();
-        seg.rank([&](uint32_t rank, Key key) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) n += n_seg[i];
+        seg.rank(n, [&](uint32_t rank, Key key) {
           if (rank < K) top[rank] = key;
         });
         __syncthreads();
@@ -667,7 +703,10 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     }
   } else if constexpr (TOP) {
     // one chunk: its ranks are the row's (K is at most the number of columns)
-    seg.rank([&](uint32_t rank, Key key) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) n += n_seg[i];
+    seg.rank(n, [&](uint32_t rank, Key key) {
       if (rank < K) top[rank] = key;
     });
     __syncthreads();
@@ -810,10 +849,9 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
     const float t = __builtin_fmaf(x, kLog2e, -c_hi);
     return kTwo ? t - c_lo : t;
   };
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
+  store_chunk<DT, T, P>(out + (size_t)lo * EB, cols, v, [&](const u32x4v& x) {
     float f[E];
-    unpack_vec<DT>(v[j], f);
+    unpack_vec<DT>(x, f);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float t = exponent(f[e]), p = exp2_hw(t);
@@ -822,8 +860,8 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
       else
         f[e] = -p * slope;
     }
-    store_vec<DT>(out + (size_t)lo * EB, cols, j * T + tid, pack_vec<DT>(f));
-  }
+    return pack_vec<DT>(f);
+  });
   if (L == 0) return;
   __syncthreads();
   if (mine) {
@@ -873,20 +911,25 @@ int64_t share_cols(int64_t V, int64_t chunks, int64_t vec) { return ((V + chunks
 int64_t logprob_max_cols(int32_t dtype) { return (int64_t)1 << (dtype == CE_BF16 ? 20 : 19); }
 
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols) {
-  static const int fs = getenv("LPS") ? atoi(getenv("LPS")) : -1, fc = getenv("LPC") ? atoi(getenv("LPC")) : -1;
+  // Many rows, or short ones: a workgroup a row, a batch of its shape or more.  Few long ones: chunks of a batch at
+  // least, for workgroups enough (64 x 128000 FP32, 5 alternatives: 17 us in 8 chunks by 512 threads, 21 by 256, 25 in 16
+  // chunks; one row of 128000 BF16, 20 alternatives: 12 us in 32 chunks by 256 threads, 14 in 8 to 16 by 512).
+  const auto batches = [=](int s) { return (V + shape_cols(s, dtype) - 1) / shape_cols(s, dtype); };
+  const auto chunks_for = [=](int s, int64_t groups) {
+    const int64_t want = (groups + N - 1) / (N > 0 ? N : 1), most = batches(s) < kMaxChunks ? batches(s) : kMaxChunks;
+    return want < most ? want : most;
+  };
   *chunks = 1;
   if (V <= shape_cols(0, dtype)) {
     *shape = 0;
   } else if (N >= 512) {
-    *shape = V <= 2 * shape_cols(1, dtype) ? 1 : 2;
+    *shape = batches(1) <= 2 ? 1 : 2;
+  } else if (N * batches(2) >= 256) {
+    *shape = 2;
+    *chunks = chunks_for(2, 512);
   } else {
-    // a chunk is a batch at least
     *shape = 1;
-    const int64_t most = (V + shape_cols(1, dtype) - 1) / shape_cols(1, dtype), want = (512 + N - 1) / (N ? N : 1);
-    *chunks = want < most ? want : most;
-    if (*chunks > kMaxChunks) *chunks = kMaxChunks;
-    if (fs > 0) *shape = fs;
-    if (fc > 0) *chunks = fc;
+    *chunks = chunks_for(1, 1024);
   }
   *chunk_cols = share_cols(V, *chunks, vec_cols(dtype));
   *chunks = (V + *chunk_cols - 1) / *chunk_cols;  // whole vectors can leave the last share empty

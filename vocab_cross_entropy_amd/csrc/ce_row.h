@@ -166,21 +166,31 @@ __device__ __forceinline__ void load_chunk(const char* chunk, uint32_t cols, u32
   }
 }
 
-// Vector i of a chunk of `cols` columns, written non-temporally; columns that are not there are left out.
-template <int DT>
-__device__ __forceinline__ void store_vec(char* chunk, uint32_t cols, uint32_t i, const u32x4v& w) {
+// A chunk of `cols` columns from load_chunk's slots, `of(vector)` for each vector, written non-temporally; columns
+// that are not there are left out.
+template <int DT, int T, int P, typename Of>
+__device__ __forceinline__ void store_chunk(char* chunk, uint32_t cols, u32x4v (&v)[P], Of of) {
   typedef typename LogitT<DT>::Word Word;
   constexpr int E = LogitT<DT>::E;
-  if ((i + 1) * E <= cols) {
-    __builtin_nontemporal_store(w, reinterpret_cast<Word*>(chunk + i * 16u));
-  } else if (i * E < cols) {
+  uint32_t tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // the offsets are formed here, not kept from the loads
+  const uint32_t whole = cols / E;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    relaunch(v[j]);
+    const uint32_t i = j * T + tid;
+    const u32x4v w = of(v[j]);
+    if (i < whole) __builtin_nontemporal_store(w, reinterpret_cast<Word*>(chunk + i * 16u));
+  }
+  if (cols % E != 0 && tid == whole % T) {
+    const u32x4v w = of(pick<P>(v, whole / T));
 #pragma unroll
     for (int e = 0; e < E - 1; ++e) {
-      if (i * E + e >= cols) continue;
+      if (whole * E + e >= cols) continue;
       if constexpr (DT == CE_BF16)
-        reinterpret_cast<uint16_t*>(chunk)[i * E + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+        reinterpret_cast<uint16_t*>(chunk)[whole * E + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
       else
-        reinterpret_cast<uint32_t*>(chunk)[i * E + e] = w[e];
+        reinterpret_cast<uint32_t*>(chunk)[whole * E + e] = w[e];
     }
   }
 }
@@ -211,15 +221,38 @@ __device__ __forceinline__ uint32_t wave_or(uint32_t v) {
   v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kBcast31, 0xc, 0xf, true);
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
+// the same of 64-bit values (a shuffle goes through LDS, twice for a double)
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp64(double v, double none) {  // `none` for lanes without a source, and outside ROWS
+  typedef int i2 __attribute__((ext_vector_type(2)));
+  const i2 w = __builtin_bit_cast(i2, v), o = __builtin_bit_cast(i2, none);
+  const i2 r = {__builtin_amdgcn_update_dpp(o.x, w.x, CTRL, ROWS, 0xf, false),
+                __builtin_amdgcn_update_dpp(o.y, w.y, CTRL, ROWS, 0xf, false)};
+  return __builtin_bit_cast(double, r);
+}
+__device__ __forceinline__ double last_lane64(double v) {
+  typedef int i2 __attribute__((ext_vector_type(2)));
+  const i2 w = __builtin_bit_cast(i2, v);
+  const i2 r = {__builtin_amdgcn_readlane(w.x, 63), __builtin_amdgcn_readlane(w.y, 63)};
+  return __builtin_bit_cast(double, r);
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += dpp64<kSwap1>(v, 0.0);
+  v += dpp64<kSwap2>(v, 0.0);
+  v += dpp64<kHalfMirror>(v, 0.0);
+  v += dpp64<kMirror>(v, 0.0);
+  v += dpp64<kBcast15, 0xa>(v, 0.0);
+  v += dpp64<kBcast31, 0xc>(v, 0.0);
+  return last_lane64(v);
 }
 __device__ __forceinline__ double wave_largest64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
-  return v;
+  v = fmax(v, dpp64<kSwap1>(v, v));
+  v = fmax(v, dpp64<kSwap2>(v, v));
+  v = fmax(v, dpp64<kHalfMirror>(v, v));
+  v = fmax(v, dpp64<kMirror>(v, v));
+  v = fmax(v, dpp64<kBcast15, 0xa>(v, v));
+  v = fmax(v, dpp64<kBcast31, 0xc>(v, v));
+  return last_lane64(v);
 }
 __device__ __forceinline__ int wave_count64(int v) {
 #pragma unroll
@@ -250,6 +283,13 @@ __device__ __forceinline__ bool await_word(const unsigned long long* p, uint32_t
   return true;
 }
 
+// A word that nothing writes during the launch, by a scalar load: it takes no place in the order of the vector loads.
+template <typename T>
+__device__ __forceinline__ T load_uniform(const T* p) {
+  typedef const __attribute__((address_space(4))) T* Const;
+  return *(Const)p;
+}
+
 // A call's view of its workspace: the tag, whether ce_workspace_init prepared it
 // for this many bytes, and the test hook (a chunk whose words stay unpublished).
 // Scalar loads: nothing writes the record before the call's last workgroup ends.
@@ -259,12 +299,11 @@ struct WsView {
   unsigned long long withhold;
 };
 __device__ __forceinline__ WsView view_workspace(const WsHeader* hdr, unsigned long long bytes) {
-  typedef const __attribute__((address_space(4))) unsigned long long* Const64;
-  const Const64 rec = (Const64)(&hdr->magic);  // magic, init_bytes, epoch, withhold
+  const unsigned long long* const rec = &hdr->magic;  // magic, init_bytes, epoch, withhold
   WsView v;
-  v.tag = (uint32_t)rec[2];
-  v.ok = (rec[0] == kWsMagic) & (rec[1] >= bytes);
-  v.withhold = rec[3];
+  v.tag = (uint32_t)load_uniform(rec + 2);
+  v.ok = (load_uniform(rec) == kWsMagic) & (load_uniform(rec + 1) >= bytes);
+  v.withhold = load_uniform(rec + 3);
   return v;
 }
 __device__ __forceinline__ bool withheld(const WsView& ws, int64_t r, int k) {
