@@ -152,12 +152,13 @@ def ref_distill(x, ids, t, n_entries, T, logprobs, scale, dtype=torch.float32):
         m = z.max()
         e = np.exp(z - m)
         D = e.sum()
-        lse = m + math.log(D)
+        logD = math.log(D)
+        lse = m + logD
         q = e / D
         q_o = q[~named].sum()
         r = max(0.0, 1.0 - p.sum()) if logprobs and q_o > 0 else 0.0
         with np.errstate(divide="ignore", invalid="ignore"):
-            lq = z - lse
+            lq = (z - m) - logD  # (where m is large, z - lse would leave log D out)
             far = np.where(q > 0, q * np.abs(lq), 0.0).sum()                 # mean distance under q
             zo = z[~named]
             if q_o > 0:
@@ -174,10 +175,11 @@ def ref_distill(x, ids, t, n_entries, T, logprobs, scale, dtype=torch.float32):
         # log2(e) / T is rounded once: as logits scaled by 1 +- U.  rel is the unnamed columns' sum's
         rel = U * (42 + 4 * far_o)
         tl[n] = T * T * (rel * (p.sum() * q_o + r * (1 - q_o) + r) + 2 * U * ((p * (y[c] + far)).sum() + r * (far_o + far + abs(lqo))))
-        # what is 64-bit on either side: z, the log-sums and the differences of them, of a magnitude of at most |z| + |lse|
-        # in units that are 1 or log2 e, are rounded fewer than 8 times by 2^-53 each; so are p and its logarithm
+        # what is 64-bit on either side: z, its difference from the largest and the log-sums, in units that are 1 or
+        # log2 e, are rounded fewer than 8 times by 2^-53 each; so are p and its logarithm.  (Equal z have no difference.)
         with np.errstate(invalid="ignore"):
-            own64 = 8 * 1.45 * 2.0 ** -53 * (abs(lse) + np.abs(np.where(np.isfinite(z), z, 0.0)) + 4)
+            fin = np.where(np.isfinite(z), z, 0.0)
+            own64 = 8 * 1.45 * 2.0 ** -53 * (np.where(fin == m, 0.0, np.abs(fin) + abs(m)) + logD + 4)
         lt64 = np.abs(np.where(p > 0, lt, 0.0))
         tl[n] += T * T * ((p * (own64[c] + 8 * 2.0 ** -53 * (lt64 + 4))).sum() + r * (own64.max() if r > 0 else 0.0))
         loss[n] *= T * T

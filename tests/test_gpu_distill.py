@@ -136,6 +136,10 @@ def test_special_rows(V, dtype):
         "one column only": (base, cols[:1].expand(K), tv),
         "neighbours": (base, torch.arange(K) + V // 2 - 8 if V > 60 else torch.arange(K), tv),
         "lowest value": (put(base, cols[::8], torch.finfo(dtype).min), cols, tv),
+        "lowest values alone": (torch.full((V,), torch.finfo(dtype).min), cols, tv),
+        "masked by -1e9": (torch.full((V,), -1e9), cols, tv),
+        "masked by -1e9 but for some": (torch.full((V,), -1e9).index_copy(0, cols[:5], tv[:5]), cols, tv),
+        "around 1e5": (base + 1e5, cols, tv),
         "a teacher of -inf": (base, cols, torch.full((K,), -inf)),
         "a column outside": (base, put(cols, 7, V), tv),
         "a negative column": (base, put(cols, 7, -1), tv),

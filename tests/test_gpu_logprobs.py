@@ -131,6 +131,10 @@ def _special_rows(V, dtype, seed):
     rows["one left"] = one
     rows["lowest value"] = torch.where(torch.isinf(masked), torch.tensor(torch.finfo(dtype).min), masked)
     rows["lowest values alone"] = torch.full((V,), torch.finfo(dtype).min)
+    rows["masked by -1e9"] = torch.full((V,), -1e9)
+    rows["masked by -1e4 but for one"] = torch.full((V,), -1e4)
+    rows["masked by -1e4 but for one"][V // 2] = 7.0
+    rows["around 1e5"] = base + 1e5
     huge = torch.full((V,), -2.9e38)
     huge[::3] = 2.9e38
     rows["out of range of the exponent"] = huge

@@ -11,11 +11,12 @@
 // are set to -inf in their registers, found by a bitmap of the chunk in LDS), relative to
 // their own maximum; the named ones, a few, are added in 64 bits.  So q_o keeps its digits
 // where the named columns hold nearly everything, and so does q_c - p_c, whose terms
-// are both near 1 there.  All that is per entry or per row is 64-bit, by one wave.
+// are both near 1 there: the largest term of the row is weighted by exactly 1, in q_c and in the sum alike.
+// All that is per entry or per row is 64-bit, by one wave, while the others wait; their loads are under way then.
 //
 // Bound: one read and one write of the logits.  A chunk of a row stays in a
 // workgroup's registers between its sums and its gradient, and a row's chunks exchange
-// six words each through the workspace, as in ce_fwd_bwd_fused (whose chunk shapes these are).
+// eight words each through the workspace, as in ce_fwd_bwd_fused (whose chunk shapes these are).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,21 +26,51 @@
 namespace vce {
 namespace {
 
-constexpr int kWords = 6;               // per chunk: m2, sum of unnamed, log-sum of named (2), sum of p z (2)
+// what a chunk tells: its largest unnamed logit m and the sum of the unnamed columns relative to it; a reference for its
+// named ones (a logit: the largest of all that the chunk has), their sum relative to it (two words), that of
+// p (z - reference) (two words), and that of p
+enum { kMax, kRest, kRef, kSumHi, kSumLo, kCrossHi, kCrossLo, kMass, kWords };
 constexpr int kEntries = kDistillMaxTop / 64;  // entries a lane of the wave that handles them
-constexpr double kLn2d = 0.693147180559945309417;
+constexpr double kLn2d = 0.693147180559945309417, kLog2eD = 1.442695040888963407360;
 
-// a 64-bit value as two FP32 words, and back (an infinity or NaN stands in the first)
+// a 64-bit value as two FP32 words (an infinity or NaN stands in the first)
 __device__ __forceinline__ void split64(double v, float* hi, float* lo) {
   *hi = (float)v;
   const double d = v - (double)*hi;
-  *lo = d == d && fabs(d) != (double)INFINITY ? (float)d : 0.f;
+  *lo = fabs(d) < (double)INFINITY ? (float)d : 0.f;
 }
-// log2(2^a + 2^b + ...) over the wave's lanes (-inf: nothing)
-__device__ __forceinline__ double wave_log_sum(double a) {
-  const double m = wave_largest64(a);
-  const double s = wave_sum64(a == -(double)INFINITY ? 0.0 : exp2(a - m));
-  return m == -(double)INFINITY ? (s == s ? m : s) : m + log2(s);
+
+// 2^x: 2^n times the Taylor series of 2^f, |f| <= 1/2, to (f ln 2)^13 / 13!, 2e-17 of it.  Shorter than the library's,
+// whose code takes longer to fetch than to run.
+__device__ __forceinline__ double exp2_64(double x) {
+  x = x < -1100.0 ? -1100.0 : x;
+  const double n = rint(x), y = (x - n) * kLn2d;
+  double p = 1.0 / 6227020800.0;
+  constexpr double kInv[] = {1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040,
+                             1.0 / 720,       1.0 / 120,      1.0 / 24,      1.0 / 6,      0.5,         1.0, 1.0};
+#pragma unroll
+  for (int i = 0; i < 13; ++i) p = fma(p, y, kInv[i]);
+  return ldexp(p, (int)n);
+}
+// log2 x, x >= 0 and normal: of the mantissa in [sqrt(1/2), sqrt 2), 2 atanh s with s = (m - 1) / (m + 1), |s| < 0.172,
+// to s^21 / 21, 4e-18.
+__device__ __forceinline__ double log2_64(double x) {
+  double m = __builtin_amdgcn_frexp_mant(x);
+  int e = __builtin_amdgcn_frexp_exp(x);
+  const bool small = m < 0.70710678118654752;
+  m = small ? m + m : m;
+  e -= small ? 1 : 0;
+  const double s = (m - 1.0) / (m + 1.0), s2 = s * s;
+  double p = 1.0 / 21.0;
+#pragma unroll
+  for (int k = 19; k >= 1; k -= 2) p = fma(p, s2, 1.0 / k);
+  return x == 0.0 ? -(double)INFINITY : fma(2.0 * kLog2eD * s, p, (double)e);
+}
+__device__ __forceinline__ double lane64(double v, int l) {
+  typedef int i2 __attribute__((ext_vector_type(2)));
+  const i2 w = __builtin_bit_cast(i2, v);
+  const i2 r = {__builtin_amdgcn_readlane(w.x, l), __builtin_amdgcn_readlane(w.y, l)};
+  return __builtin_bit_cast(double, r);
 }
 
 template <int T>
@@ -83,7 +114,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
   __shared__ float sh_max[W], sh_sum[W];
   __shared__ __align__(8) uint8_t named[T * 8];  // byte tid * 8 + j: which columns of slot j's vector are named
   __shared__ float words[kMaxChunks * kWords];
-  __shared__ float bc[4];  // c_hi, c_lo, the unnamed columns' factor
+  __shared__ float bc[3];  // c_hi, c_lo, the unnamed columns' factor
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t C = (uint32_t)a.chunks;
   const uint32_t in_launch = blockIdx.x / C;
@@ -138,8 +169,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
     reinterpret_cast<uint64_t*>(named)[tid] = 0ull;
     __syncthreads();
     bool here[kEntries], first[kEntries];
-    double p[kEntries];
-    double mass = 0.0, plogp = 0.0;
+    double p[kEntries], mass = 0.0, plogp = 0.0;
     bool bad = false;
     if (tid < 64) {
 #pragma unroll
@@ -159,41 +189,31 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
     }
     __syncthreads();
     if (tid < 64) {
-      double logp[kEntries];
-      if (a.kind == CE_TEACHER_LOGITS) {
-        double t[kEntries], top = -(double)INFINITY;
+      double t[kEntries], top = 0.0, logd = 0.0, d = 1.0;
+      const bool logits = a.kind == CE_TEACHER_LOGITS;
+      if (logits) {
+        top = -(double)INFINITY;
 #pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          t[i] = i * 64 + (int)lane < L ? (double)tv[i] * a.inv_t : -(double)INFINITY;
-          top = fmax(top, t[i]);
-        }
+        for (int i = 0; i < kEntries; ++i) top = fmax(top, i * 64 + (int)lane < L ? (double)tv[i] * a.inv_t : top);
         top = wave_largest64(top);
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          p[i] = exp(t[i] - top);
-          d += p[i];
-        }
-        d = wave_sum64(d);
-        const double logd = log(d);
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          p[i] /= d;
-          logp[i] = t[i] - top - logd;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          logp[i] = i * 64 + (int)lane < L ? (double)tv[i] : -(double)INFINITY;
-          p[i] = exp(logp[i]);
-        }
       }
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
+        t[i] = i * 64 + (int)lane < L ? (logits ? (double)tv[i] * a.inv_t : (double)tv[i]) - top : -(double)INFINITY;
+        p[i] = i * 64 < L ? exp2_64(t[i] * kLog2eD) : 0.0;
         mass += p[i];
-        plogp += p[i] == 0.0 ? 0.0 : p[i] * logp[i];
       }
       mass = wave_sum64(mass);
+      if (logits) {
+        d = mass;
+        logd = log2_64(d) * kLn2d;
+        mass = d == d && d > 0.0 ? 1.0 : __builtin_nan("");
+      }
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        p[i] /= d;
+        plogp += p[i] == 0.0 ? 0.0 : p[i] * (t[i] - logd);
+      }
       plogp = wave_sum64(plogp);
       bad = __any(bad);
     }
@@ -201,6 +221,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
     float grad[kEntries];  // of the named columns here
 
     // ---- the unnamed columns: maximum and sum
+    finish_chunk<DT, T, P, true>(row + (size_t)lo * EB, cols, v);
     float m = -INFINITY;
     const uint64_t flags = reinterpret_cast<const uint64_t*>(named)[tid];
 #pragma unroll
@@ -223,7 +244,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < W; ++i) m = fmaxf(m, sh_max[i]);
-    const float m2 = m == -INFINITY ? 0.f : m * a.kb;
+    const bool shifted = fabsf(m * a.kb) > kNear && fabsf(m) < INFINITY;
+    if (shifted) subtract<DT, P>(v, m);
+    const float from = shifted || m == -INFINITY ? 0.f : m * a.kb;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -232,50 +255,53 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       unpack_vec<DT>(v[j], f);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        s0 += exp2_hw(__builtin_fmaf(f[e], a.kb, -m2));
-        s1 += exp2_hw(__builtin_fmaf(f[e + 1], a.kb, -m2));
+        s0 += exp2_hw(__builtin_fmaf(f[e], a.kb, -from));
+        s1 += exp2_hw(__builtin_fmaf(f[e + 1], a.kb, -from));
       }
     }
     s0 = wave_sum(s0 + s1);
     if (lane == 0) sh_sum[tid >> 6] = s0;
     __syncthreads();
 
-    // ---- wave 0: the row, over the chunks
+    // ---- wave 0: the named columns here, then the row over its chunks
     if (tid < 64) {
       s0 = sh_sum[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) s0 += sh_sum[i];
-      double named_log = -(double)INFINITY, pz = 0.0, z[kEntries];
+      if (!shifted && m != -INFINITY) s0 *= exp2_hw(-__builtin_fmaf(m, a.kb, -from));  // from `from` to the exact m kb
+      double z[kEntries], e[kEntries], sum = 0.0, cross = 0.0, own = 0.0;
+      bool odd = false;  // NaN or +inf, which have no sum
+      float ref = m;
 #pragma unroll
-      for (int i = 0; i < kEntries; ++i) z[i] = (double)xe[i] * (double)a.kb;  // base 2, as the sums' exponents
-#pragma unroll
-      for (int i = 0; i < kEntries; ++i) pz += here[i] && p[i] != 0.0 ? p[i] * z[i] : 0.0;
-      {
-        double top = -(double)INFINITY;
-        bool nan = false;  // which the maxima pass over
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          if (first[i]) top = fmax(top, z[i]);
-          nan |= here[i] && z[i] != z[i];
-        }
-        top = wave_largest64(top);
-        if (top != -(double)INFINITY) {
-          double d = 0.0;
-#pragma unroll
-          for (int i = 0; i < kEntries; ++i) d += first[i] ? exp2(z[i] - top) : 0.0;
-          named_log = top + log2(wave_sum64(d));
-        }
-        if (__any(nan)) named_log = __builtin_nan("");
+      for (int i = 0; i < kEntries; ++i) {
+        odd |= here[i] && !(xe[i] < INFINITY);
+        ref = fmaxf(ref, here[i] ? xe[i] : -INFINITY);
       }
-      pz = wave_sum64(pz);
-      // lane c: chunk c's unnamed and named columns, as base-2 logarithms of their sums
-      double rest = -(double)INFINITY, most = -(double)INFINITY, cross = 0.0;
+      ref = wave_largest(ref);
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        const bool some = here[i] && xe[i] != -INFINITY;
+        z[i] = some ? ((double)xe[i] - (double)ref) * (double)a.kb : -(double)INFINITY;
+        e[i] = __any(some) ? exp2_64(z[i]) : 0.0;
+        sum += first[i] ? e[i] : 0.0;
+        if (here[i] && p[i] != 0.0) {
+          cross += p[i] * z[i];
+          own += p[i];
+        }
+      }
+      sum = wave_sum64(sum);
+      cross = wave_sum64(cross);
+      own = wave_sum64(own);
+      if (__any(odd)) sum = __builtin_nan("");
+      // lane c: what chunk c tells
       bool ok = true;
       float w[kWords];
-      w[0] = m2;
-      w[1] = s0;
-      split64(named_log, &w[2], &w[3]);
-      split64(pz, &w[4], &w[5]);
+      w[kMax] = m;
+      w[kRest] = s0;
+      w[kRef] = ref;
+      split64(sum, &w[kSumHi], &w[kSumLo]);
+      split64(cross, &w[kCrossHi], &w[kCrossLo]);
+      w[kMass] = (float)own;
       if (C > 1) {
         unsigned long long* const slots = a.slots + (size_t)r * C * kWords;
         if (lane < kWords && !withheld(ws, r, (int)k)) {
@@ -292,64 +318,62 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
-        if (lane < C) {
 #pragma unroll
-          for (int q = 0; q < kWords; ++q) w[q] = words[lane * kWords + q];
-        }
+        for (int q = 0; q < kWords; ++q) w[q] = words[(lane < C ? lane : 0u) * kWords + q];
         ok = __all(ok);
-      }
-      if (lane < C) {
-        rest = w[1] == 0.f ? -(double)INFINITY : (double)w[0] + log2((double)w[1]);
-        most = (double)w[2] + (double)w[3];
-        cross = (double)w[4] + (double)w[5];
       }
       ok = ok && ws.ok;
       if (!ok && lane == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
-      rest = wave_log_sum(rest);
-      most = wave_log_sum(most);
-      cross = wave_sum64(cross);
-      const double hi = fmax(rest, most);
-      const double lse = rest != rest || most != most ? __builtin_nan("")
-                         : hi == -(double)INFINITY    ? hi
-                                                      : hi + log2(exp2(rest - hi) + exp2(most - hi));
+      // relative to the row's largest logit M: a weight of exactly 1 for whatever holds it
+      const bool has = lane < C;
+      const float M = wave_largest(has ? w[kRef] : -INFINITY);
+      const auto weight = [&](float from) { return from == -INFINITY ? 0.f : exp2_hw((from - M) * a.kb); };
+      const float f_rest = weight(w[kMax]), f_named = weight(w[kRef]);
+      const double rest = wave_sum64(has ? (double)w[kRest] * (double)f_rest : 0.0);
+      const double all = rest + wave_sum64(has ? ((double)w[kSumHi] + (double)w[kSumLo]) * (double)f_named : 0.0);
+      cross = (double)w[kCrossHi] + (double)w[kCrossLo];
+      if (w[kRef] != -INFINITY) cross += (double)w[kMass] * (((double)w[kRef] - (double)M) * (double)a.kb);
+      cross = wave_sum64(has ? cross : 0.0);  // of p (z - M)
       // what the teacher leaves, to the unnamed columns; nothing where none of them can take it
       double left = 0.0;
-      if (a.kind == CE_TEACHER_LOGPROBS && rest != -(double)INFINITY) left = fmax(0.0, 1.0 - mass);
-      if (mass != mass) left = mass;
+      if (a.kind == CE_TEACHER_LOGPROBS && rest != 0.0) left = fmax(0.0, 1.0 - mass);
       const double S = mass + left;
-      double loss = plogp - (cross - mass * lse) * kLn2d;
-      if (left != 0.0) loss += left * (log(left) - (rest - lse) * kLn2d);
+      const double share = rest / all;  // q_o
+      // three logarithms at once: of the sum, of what is left, of q_o
+      const double logs = log2_64(lane == 0 ? all : lane == 1 ? left : share);
+      const double log_all = lane64(logs, 0);
+      double loss = plogp - (cross - mass * log_all) * kLn2d;
+      if (left != 0.0) loss += left * (lane64(logs, 1) - lane64(logs, 2)) * kLn2d;
       loss *= a.t * a.t;
       double s = (double)up * a.t;
       if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
       if (k == 0 && lane == 0) row_loss((float)loss);
       if constexpr (GRAD) {
-        const float c_hi = (float)lse;
+        const double c = (double)a.kb * ((double)M - (shifted ? (double)m : 0.0)) + log_all;
         if (lane == 0) {
-          bc[0] = c_hi;
-          bc[1] = DT == CE_F32 ? (float)(lse - (double)c_hi) : 0.f;
-          bc[2] = (float)(s * (S - (left == 0.0 ? 0.0 : left * exp2(lse - rest))));
+          bc[0] = (float)c;
+          bc[1] = DT == CE_F32 && fabsf((float)c) < INFINITY ? (float)(c - (double)(float)c) : 0.f;
+          bc[2] = (float)(s * (S - (left == 0.0 ? 0.0 : left / share)));
         }
         // the named columns' gradients; entries of the same column add up, in order
-        const bool twice = __any([&] {
-          bool d = false;
+        const double f_own = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(f_named), (int)(C > 1 ? k : 0u)));
+        bool again = false;
 #pragma unroll
-          for (int i = 0; i < kEntries; ++i) d |= here[i] && !first[i];
-          return d;
-        }());
+        for (int i = 0; i < kEntries; ++i) again |= here[i] && !first[i];
+        const bool twice = __any(again);
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) {
-          double all = p[i];
+          double P_i = p[i];
           if (twice) {
-            all = 0.0;
+            P_i = 0.0;
             for (int q = 0; q < L; ++q) {
               const int64_t other = __shfl(q < 64 ? id[0] : id[kEntries - 1], q & 63);
               const double add = __shfl(q < 64 ? p[0] : p[kEntries - 1], q & 63);
-              all += other == id[i] ? add : 0.0;
+              P_i += other == id[i] ? add : 0.0;
             }
           }
-          grad[i] = (float)(s * (exp2(z[i] - lse) * S - all));
+          grad[i] = (float)(s * (e[i] * f_own / all * S - P_i));
         }
       }
     }

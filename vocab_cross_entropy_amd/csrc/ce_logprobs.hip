@@ -11,8 +11,8 @@
 // whose probability is near 1, keep their digits.  Every thread sums its columns relative
 // to its own running maximum; the sum of the one thread that owns the row's maximum, which
 // may have lost R's digits beside the 1, is formed again at the end without that column.
-// Exponentials are base 2 on the hardware's v_exp_f32, against m2 = fl(m log2 e); the
-// sums are brought from m2 to the exact m log2 e at the end.
+// Exponentials are base 2 on the hardware's v_exp_f32, against m2 = fl(m log2 e); each batch's
+// sums are brought from m2 to the exact m log2 e.
 //
 // Bound: the read of the logits (the gradient: and its write).  With many rows a
 // workgroup takes a row; with few, a row is cut into chunks, and what each chunk finds (m, R,
@@ -42,7 +42,6 @@ namespace {
 constexpr int kTop = kLogprobMaxList;  // most alternatives, and most given tokens, of a row
 constexpr int kStatWords = 4;          // m, R, whether m was counted (1, or 0 of a chunk of -inf), the entropy's sum
 constexpr float kFar = -1000.f;        // 2^kFar is 0; exponents of masked columns (-inf) stop here where they are a factor
-constexpr float kHuge = 2e38f;         // beyond it x log2 e leaves FP32
 typedef unsigned long long Key;        // order << 32 | ~column; 0: none
 typedef Key KeyPair __attribute__((ext_vector_type(2)));
 
@@ -330,14 +329,14 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     xt[i] = 0.f;
   }
 
-  float m = -INFINITY, m2 = -INFINITY;  // this thread's maximum, and m log2 e
-  float s0 = 0.f, s1 = 0.f;             // its sums of 2^u and of 2^u u, u = x log2 e - m2
-  // the sums relative to another m2 (kFar: 2^kFar is 0, and 0 times an infinity would be NaN)
-  const auto move_sums = [&](float to, float& t0, float& t1) {
-    const float d = m2 > -INFINITY && to > -INFINITY ? fmaxf(m2 - to, kFar) : kFar;
+  float m = -INFINITY;       // this thread's maximum
+  float s0 = 0.f, s1 = 0.f;  // its sums of 2^u and of 2^u u, u = (x - m) log2 e
+  // the sums relative to a larger maximum (kFar: 2^kFar is 0, and 0 times an infinity would be NaN)
+  const auto move_sums = [&](float to) {
+    const float d = m > -INFINITY ? fmaxf((m - to) * kLog2e, kFar) : kFar;
     const float w = exp2_hw(d);
-    if constexpr (ENT) t1 = __builtin_fmaf(d, t0, t1) * w;
-    t0 *= w;
+    if constexpr (ENT) s1 = __builtin_fmaf(d, s0, s1) * w;
+    s0 *= w;
   };
   bool low = true;                      // no bound, or -inf
   float least = -INFINITY;              // the bound
@@ -400,31 +399,9 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       top_m = fmaxf(top_m, vm[j]);
     }
     if (top_m > m) {
-      const float to = top_m * kLog2e;
-      move_sums(to, s0, s1);
+      move_sums(top_m);
       m = top_m;
-      m2 = to;
     }
-    const float from = m2 == -INFINITY ? 0.f : m2;
-    float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      relaunch(v[j]);
-      float f[E];
-      unpack_vec<DT>(v[j], f);
-#pragma unroll
-      for (int c = 0; c < E; c += 2) {
-        const float u = __builtin_fmaf(f[c], kLog2e, -from), w = __builtin_fmaf(f[c + 1], kLog2e, -from);
-        const float eu = exp2_hw(u), ew = exp2_hw(w);
-        t0 += eu;
-        t1 += ew;
-        if constexpr (ENT) {
-          s1 = __builtin_fmaf(eu, fmaxf(u, kFar), s1);
-          s1 = __builtin_fmaf(ew, fmaxf(w, kFar), s1);
-        }
-      }
-    }
-    s0 += t0 + t1;
 
     // ---- vectors that reach the bound
     if constexpr (TOP) {
@@ -451,6 +428,39 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         hits += (uint32_t)__builtin_popcountll(lanes);
       }
     }
+
+    // ---- sums
+    float from = m == -INFINITY ? 0.f : m * kLog2e;
+    if (fabsf(from) > kNear) {
+      subtract<DT, P>(v, m);
+      from = 0.f;
+    }
+    float t0 = 0.f, t1 = 0.f, h = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      relaunch(v[j]);
+      float f[E];
+      unpack_vec<DT>(v[j], f);
+#pragma unroll
+      for (int c = 0; c < E; c += 2) {
+        const float u = __builtin_fmaf(f[c], kLog2e, -from), w = __builtin_fmaf(f[c + 1], kLog2e, -from);
+        const float eu = exp2_hw(u), ew = exp2_hw(w);
+        t0 += eu;
+        t1 += ew;
+        if constexpr (ENT) {
+          h = __builtin_fmaf(eu, fmaxf(u, kFar), h);
+          h = __builtin_fmaf(ew, fmaxf(w, kFar), h);
+        }
+      }
+    }
+    {
+      // from m2 to m log2 e: the terms are too large by 2^d, d = m log2 e - m2
+      const float d = from != 0.f ? __builtin_fmaf(m, kLog2e, -from) : 0.f, grow = __builtin_fmaf(-d, kLn2f, 1.f);
+      t0 += t1;
+      s0 = __builtin_fmaf(t0, grow, s0);
+      if constexpr (ENT) s1 = __builtin_fmaf(__builtin_fmaf(-d, t0, h), grow, s1);
+    }
+
   }
 
   // ---- the chunk's maximum and the first thread that has it
@@ -462,7 +472,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       sh_own[wave] = wave * 64 + (uint32_t)__builtin_ctzll(owners | 1ull << 63);
     }
   }
-  float M, M2;
+  float M;
   const auto sums_of_chunk = [&] {
   M = sh_max[0];
   uint32_t owner = sh_own[0];
@@ -471,14 +481,9 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     owner = sh_max[i] > M ? sh_own[i] : owner;
     M = fmaxf(M, sh_max[i]);
   }
-  M2 = M == -INFINITY ? 0.f : M * kLog2e;
-  move_sums(M2, s0, s1);
+  move_sums(M);
   if (M != -INFINITY && tid == owner) s0 = s1 = 0.f;
-  if (fabsf(M) > kHuge && fabsf(M) < INFINITY) {  // M log2 e is not FP32: only columns equal to M count
-    s0 = s1 = 0.f;
-    for (uint32_t c = tid; c < cols; c += T) s0 += load_logit<DT>(chunk, c) == M ? 1.f : 0.f;
-    if (tid == 0) s0 -= 1.f;
-  } else if (wave == W - 1 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
+  if (wave == W - 1 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
     bool out = false;                 // it has been left out
     for (uint32_t base = 0; base < nb * P; base += 64) {
       const uint32_t s = base + lane, i = vector_at(s % nb, s / nb, owner >> 6, owner & 63);
@@ -495,7 +500,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       out |= lanes != 0;
 #pragma unroll
       for (int c = 0; c < E; ++c) {
-        const float u = __builtin_fmaf(f[c], kLog2e, -M2);
+        const float u = (f[c] - M) * kLog2e;
         const bool skip = leave && f[c] == M;
         if (skip) leave = false;
         const float e = skip ? 0.f : exp2_hw(u);
@@ -567,13 +572,6 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   for (int i = 0; i < W; ++i) {
     rest += sh_sum[i][0];
     s1 += sh_sum[i][1];
-  }
-  {
-    // from m2 to m log2 e: the terms are too large by 2^d, d = m log2 e - m2
-    const float d = fabsf(M2) == INFINITY || M == -INFINITY ? 0.f : __builtin_fmaf(M, kLog2e, -M2);
-    const float grow = __builtin_fmaf(-d, kLn2f, 1.f);
-    s1 = (s1 - d * rest) * grow;
-    rest *= grow;
   }
 
   if (C > 1) {
@@ -802,6 +800,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
   const float dh = ENT ? a.dentropy[r] : 0.f;
   u32x4v v[P];
   load_chunk<DT, T, P>(row + (size_t)lo * EB, cols, v);
+  finish_chunk<DT, T, P, false>(row + (size_t)lo * EB, cols, v);
 
   const bool counts = tid < L && id != a.ignore_idx;
   const bool valid = id >= 0 && id < a.V;
@@ -826,17 +825,9 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
   }
 
   float top = s.x;
-  if (fabsf(top) > kHuge && fabsf(top) < INFINITY) {  // m log2 e is not FP32: only columns equal to m have a share
-    const auto share = [&](float x) { return x == top ? 0.f : -INFINITY; };
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      float f[E];
-      unpack_vec<DT>(v[j], f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = share(f[e]);
-      v[j] = pack_vec<DT>(f);
-    }
-    xt = share(xt);
+  if (fabsf(top * kLog2e) > kNear && fabsf(top) < INFINITY) {
+    subtract<DT, P>(v, top);
+    xt -= top;
     top = 0.f;
   }
   // p = 2^(x log2 e - c), c = (m + log D) log2 e in two parts; the second matters to FP32's rounding and to log p

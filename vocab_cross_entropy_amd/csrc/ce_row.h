@@ -86,6 +86,25 @@ __device__ __forceinline__ void store_logit(char* row, int64_t j, float g) {
 // Register barrier, no instruction: a later sweep unpacks the vector again instead of keeping its floats.
 __device__ __forceinline__ void relaunch(u32x4v& v) { asm volatile("" : "+v"(v)); }
 
+// Exponents (x - m) log2 e / T come from one fused multiply-add against m2 = fl(m log2 e / T), whose rounding is
+// then taken out of the sums.  Where |m2| exceeds this bound (a row masked with -1e9, or with the type's lowest value) that
+// rounding is too large, or m2 not FP32: the vectors hold x - m instead.  It is exact wherever 2^(x - m) is not 0: BF16
+// logits beyond 2^8 differ by whole numbers of few bits, FP32 ones by what FP32 holds.
+constexpr float kNear = 1024.f;
+template <int DT, int P>
+__device__ __forceinline__ void subtract(u32x4v (&v)[P], float m) {
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    relaunch(v[j]);
+    float f[LogitT<DT>::E];
+    unpack_vec<DT>(v[j], f);
+#pragma unroll
+    for (int e = 0; e < LogitT<DT>::E; ++e) f[e] -= m;
+    v[j] = pack_vec<DT>(f);
+    relaunch(v[j]);
+  }
+}
+
 // One v_max3_f32 (fmaxf would quiet each operand first).  A NaN loses; the sums carry it.
 __device__ __forceinline__ float max3_hw(float a, float b, float c) {
   float d;
@@ -134,26 +153,31 @@ __device__ __forceinline__ u32x4v pick(const u32x4v (&v)[P], uint32_t j) {
 }
 
 // A chunk of `cols` columns as T x P vectors: vector j * T + tid in slot j of
-// thread tid.  Slots past the chunk, and a last vector's missing columns, hold
-// -inf.  No load of a whole vector stands behind a branch: slots past them load
-// the chunk's first one and are overwritten.
+// thread tid.  load_chunk issues the loads of the whole vectors, none behind a
+// branch: slots past them load the chunk's first one.  finish_chunk, the first use of
+// the slots, puts in the columns of a last vector that is not whole, and with FILL -inf where there is no column.
 template <int DT, int T, int P>
 __device__ __forceinline__ void load_chunk(const char* chunk, uint32_t cols, u32x4v (&v)[P]) {
   typedef typename LogitT<DT>::Word Word;
+  const uint32_t whole = cols / LogitT<DT>::E;
+  if (whole == 0) return;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const uint32_t i = j * T + threadIdx.x;
+    v[j] = __builtin_nontemporal_load(reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u));
+  }
+}
+template <int DT, int T, int P, bool FILL>
+__device__ __forceinline__ void finish_chunk(const char* chunk, uint32_t cols, u32x4v (&v)[P]) {
   constexpr int E = LogitT<DT>::E;
   constexpr uint32_t kNone = LogitT<DT>::kNegInf;
   const uint32_t tid = threadIdx.x, whole = cols / E;
-  if (whole > 0) {
+  if constexpr (FILL) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      const uint32_t i = j * T + tid;
-      v[j] = __builtin_nontemporal_load(reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u));
+      if ((uint32_t)(j + 1) * T <= whole) continue;  // the same for the whole workgroup
+      if (j * T + tid >= whole) v[j] = u32x4v{kNone, kNone, kNone, kNone};
     }
-  }
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    if ((uint32_t)(j + 1) * T <= whole) continue;  // the same for the whole workgroup
-    if (j * T + tid >= whole) v[j] = u32x4v{kNone, kNone, kNone, kNone};
   }
   if (cols % E != 0 && tid == whole % T) {
     const u32x4v w = partial_vec<DT>(chunk, whole * E, cols);
