@@ -109,11 +109,13 @@ __device__ void finish_distill(const DistillArgs& a, uint32_t tag, bool ws_ok) {
 }
 
 template <int DT, int T, int P, bool GRAD>
-__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void k_distill(DistillArgs a) {
+__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void k_distill(DistillArgs a) {
   constexpr int E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
   __shared__ float sh_max[W], sh_sum[W];
   __shared__ __align__(8) uint8_t named[T * 8];  // byte tid * 8 + j: which columns of slot j's vector are named
   __shared__ float words[kMaxChunks * kWords];
+  __shared__ double kept_p[kDistillMaxTop], kept_e[kDistillMaxTop];  // the entries', over the exchange
+  __shared__ uint32_t kept_col[kDistillMaxTop];
   __shared__ float bc[3];  // c_hi, c_lo, the unnamed columns' factor
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t C = (uint32_t)a.chunks;
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
   WsView ws{0u, true, 0ull};
   if (a.hdr) ws = view_workspace(a.hdr, a.ws_bytes);
   const bool ends = a.hdr && r == a.N - 1 && k == C - 1;
-  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const int64_t i0 = (uint32_t)r / (uint32_t)a.d1, i1 = (uint32_t)r % (uint32_t)a.d1;
   const char* const row = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   char* const out = GRAD ? a.out + (i0 * a.os0 + i1 * a.os1) * EB : nullptr;
   const uint32_t lo = k * (uint32_t)a.chunk_cols;
@@ -169,6 +171,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
     reinterpret_cast<uint64_t*>(named)[tid] = 0ull;
     __syncthreads();
     bool here[kEntries], first[kEntries];
+    uint32_t col[kEntries];  // of the entries here; others have none
     double p[kEntries], mass = 0.0, plogp = 0.0;
     bool bad = false;
     if (tid < 64) {
@@ -178,8 +181,10 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
         bad |= is && (id[i] < 0 || id[i] >= a.V);
         here[i] = is && id[i] >= lo && id[i] < (int64_t)lo + cols;
         first[i] = false;
+        col[i] = ~0u;
         if (here[i]) {
           const uint32_t c = (uint32_t)(id[i] - lo), vec = c / E;
+          col[i] = c;
           const uint32_t at = (vec % T) * 8 + vec / T;  // its byte
           const uint32_t bit = 1u << (c % E + 8 * (at & 3));
           first[i] = !(atomicOr(reinterpret_cast<uint32_t*>(named) + (at >> 2), bit) & bit);
@@ -289,6 +294,20 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
           own += p[i];
         }
       }
+      if constexpr (GRAD) {
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          kept_p[i * 64 + lane] = p[i];
+          kept_e[i * 64 + lane] = e[i];
+          kept_col[i * 64 + lane] = col[i];
+        }
+      }
+      const bool twice = [&] {
+        bool again = false;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) again |= here[i] && !first[i];
+        return __any(again);
+      }();
       sum = wave_sum64(sum);
       cross = wave_sum64(cross);
       own = wave_sum64(own);
@@ -310,6 +329,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
           for (int q = 1; q < kWords; ++q) mine = (int)lane == q ? w[q] : mine;
           put_word(slots + k * kWords + lane, ws.tag, __float_as_uint(mine));
         }
+        if (!GRAD && k != C - 1) return;  // the last chunk brings the row's loss together; no other needs it
         uint32_t spins = 0;
         for (uint32_t i = lane; i < C * kWords; i += 64) {
           uint32_t got = 0x7fc00000u;
@@ -348,7 +368,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       double s = (double)up * a.t;
       if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
-      if (k == 0 && lane == 0) row_loss((float)loss);
+      if (k == (GRAD ? 0 : C - 1) && lane == 0) row_loss((float)loss);
       if constexpr (GRAD) {
         const double c = (double)a.kb * ((double)M - (shifted ? (double)m : 0.0)) + log_all;
         if (lane == 0) {
@@ -358,22 +378,15 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
         }
         // the named columns' gradients; entries of the same column add up, in order
         const double f_own = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(f_named), (int)(C > 1 ? k : 0u)));
-        bool again = false;
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) again |= here[i] && !first[i];
-        const bool twice = __any(again);
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) {
-          double P_i = p[i];
+          const uint32_t c = kept_col[i * 64 + lane];
+          double P_i = kept_p[i * 64 + lane];
           if (twice) {
             P_i = 0.0;
-            for (int q = 0; q < L; ++q) {
-              const int64_t other = __shfl(q < 64 ? id[0] : id[kEntries - 1], q & 63);
-              const double add = __shfl(q < 64 ? p[0] : p[kEntries - 1], q & 63);
-              P_i += other == id[i] ? add : 0.0;
-            }
+            for (int q = 0; q < L; ++q) P_i += kept_col[q] == c ? kept_p[q] : 0.0;
           }
-          grad[i] = (float)(s * (e[i] * f_own / all * S - P_i));
+          grad[i] = (float)(s * (kept_e[i * 64 + lane] * f_own / all * S - P_i));
         }
       }
     }
@@ -394,8 +407,10 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4, 8))) void 
       __syncthreads();
       if (tid < 64) {  // over the zeros that were written for the named columns
 #pragma unroll
-        for (int i = 0; i < kEntries; ++i)
-          if (here[i]) store_logit<DT>(out, id[i], grad[i]);
+        for (int i = 0; i < kEntries; ++i) {
+          const uint32_t c = kept_col[i * 64 + lane];
+          if (c != ~0u) store_logit<DT>(out, (int64_t)lo + c, grad[i]);
+        }
       }
     }
   }

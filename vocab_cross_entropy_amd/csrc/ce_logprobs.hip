@@ -23,7 +23,7 @@
 // The K largest without sorting: the K-th largest of the threads' running maxima,
 // found with ballots, is a bound that at least K columns reach and few others do (K threads
 // have one each).  Vectors that reach the bound of their time go to LDS; it is raised after
-// the first, second, third, fifth, ninth ... batch.  At the end their columns that reach the
+// the first, second, fourth, eighth ... batch.  At the end their columns that reach the
 // last bound, about 1.3 K of them, are ranked by counting.  Where too many reach it (constant
 // rows, runs of equal values) the K-th value is found exactly by further sweeps over the chunk, and of
 // its ties the lowest columns are taken.  Keys order by value, then by column, so nothing
@@ -149,33 +149,44 @@ __device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, ui
   const uint32_t whole = cols / E;
   const auto whole_vec = [&](uint32_t i) -> u32x4v { return *reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u); };
   const u32x4v rest = partial_vec<DT>(chunk, whole * E, cols);
-  const auto count = [&](uint32_t at_least) {
-    uint32_t c = 0;
-#pragma unroll 1
-    for (uint32_t i = tid; i * E < cols; i += T) {
+  // how many columns reach c, c + step and c + 2 step
+  const auto count = [&](uint32_t c, uint32_t step, uint32_t (&n)[3]) {
+    n[0] = n[1] = n[2] = 0;
+    const auto add = [&](const u32x4v& v, uint32_t i) {
       uint32_t o[E];
-      orders(i < whole ? whole_vec(i) : rest, i, o);
+      orders(v, i, o);
 #pragma unroll
-      for (int e = 0; e < E; ++e) c += o[e] >= at_least;
-    }
-    return block_count<T>(c, sh);
-  };
-  // the bound where at least K columns reach it and fewer are above it; else from the top bit on
-  uint32_t above = 0;
-  bool found = false;
+      for (int e = 0; e < E; ++e) {
+        n[0] += o[e] >= c;
+        n[1] += o[e] >= c + step;
+        n[2] += o[e] >= c + 2 * step;
+      }
+    };
 #pragma unroll 1
-  for (int b = kOrderBits<DT> + 1; b >= -1; --b) {
-    const bool probe = b < 0 || b == kOrderBits<DT>;
-    const uint32_t c = probe ? t + 1 : b > kOrderBits<DT> ? t : t | 1u << b;
-    const uint32_t n = count(c);
-    if (probe) {
-      above = n;
-      if (found && above < K) break;
-      t = b < 0 ? t : 0u;
-    } else if (b > kOrderBits<DT>) {
-      found = n >= K;
-    } else if (n >= K) {
-      t = c;
+    for (uint32_t base = 0; base < whole; base += 4 * T) {
+      u32x4v v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = whole_vec(base + k * T + tid);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (base + k * T + tid < whole) add(v[k], base + k * T + tid);
+    }
+    if (tid == 0) add(rest, whole);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) n[k] = block_count<T>(n[k], sh);
+  };
+  // the bound where at least K columns reach it and fewer are above it; else from the top on, two bits a sweep
+  uint32_t n[3], above = 0;
+#pragma unroll 1
+  for (int b = kOrderBits<DT>; b >= -2; b -= 2) {
+    if (b == kOrderBits<DT> || b < 0) {
+      count(t, 1, n);
+      above = n[1];
+      if (b < 0 || (n[0] >= K && above < K)) break;
+      t = 0;
+    } else {
+      count(t + (1u << b), 1u << b, n);
+      t += n[2] >= K ? 3u << b : n[1] >= K ? 2u << b : n[0] >= K ? 1u << b : 0u;
     }
   }
   if (tid == 0) *n_cand = 0;
@@ -278,6 +289,10 @@ struct Segments {
   }
 };
 
+// Vectors that a wave can keep.  A bound lets 1.4 K of them by over as many batches as it was found from, 45 a wave of
+// four for K = 128, and raising it leaves as many of those before.
+__host__ __device__ constexpr uint32_t hit_room(int32_t K) { return 64u + (uint32_t)K * 5u / 4u; }
+
 template <int DT, int T, int P, bool TOP, bool ENT>
 __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   typedef typename LogitT<DT>::Word Word;
@@ -286,8 +301,8 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   constexpr bool kSplit = W > 1;          // one wave only ever takes a whole row
   constexpr int kRound = 1024 / T;        // keys a thread takes into one round of merging
   // A wave's vectors that have reached a bound, and the columns that reach the last one; later the row's keys
-  constexpr int kHits = 128, kSeg = W > 1 ? 1024 / W : 320;
-  static_assert(kSeg >= 64 * (kSplit ? kRound : 0) && kHits >= kTop, "what the segments hold");
+  constexpr int kSeg = W > 1 ? 1024 / W : 320;
+  static_assert(kSeg >= 64 * (kSplit ? kRound : 0) && kSeg >= kTop, "what the segments hold");
   __shared__ float sh_max[W];
   __shared__ float sh_sum[W][2];
   __shared__ uint32_t sh_own[W];
@@ -295,13 +310,15 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   __shared__ uint32_t sh_cnt[W], n_seg[W], n_cand;
   __shared__ uint32_t thread_top[TOP && W > 1 ? T : 1], sh_bound;
   __shared__ uint32_t ranks[TOP ? W * kSeg : 1];
-  __shared__ u32x4v hit[TOP ? W : 1][TOP ? kHits : 1];
-  __shared__ uint32_t hit_vec[TOP ? W : 1][TOP ? kHits : 1];
+  extern __shared__ __align__(16) char hit_mem[];  // for each wave, hit_room(K) vectors, and where they come from
   __shared__ __align__(32) Key seg_keys[TOP ? W * Segments<W, kSeg>::kStride : 1];
   __shared__ Key top[TOP ? kTop : 1];  // the row's keys
   const Segments<W, kSeg> seg{seg_keys, n_seg, ranks};
 
   const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const uint32_t room = hit_room(a.K);
+  u32x4v* const hit = reinterpret_cast<u32x4v*>(hit_mem) + wave * room;
+  uint32_t* const hit_vec = reinterpret_cast<uint32_t*>(hit_mem + (size_t)W * room * 16) + wave * room;
   const uint32_t C = kSplit ? (uint32_t)a.chunks : 1u, K = TOP ? (uint32_t)a.K : 0u;
   const uint32_t in_launch = kSplit ? blockIdx.x / C : blockIdx.x;
   const int64_t r = a.row0 + in_launch;
@@ -309,7 +326,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   const bool last = k == C - 1;  // the row's last chunk brings it together
   WsView ws{0u, true, 0ull};
   if (C > 1) ws = view_workspace(a.hdr, a.ws_bytes);
-  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const int64_t i0 = (uint32_t)r / (uint32_t)a.d1, i1 = (uint32_t)r % (uint32_t)a.d1;  // (64-bit divisions delay the first load)
   const char* const row = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   const uint32_t lo = k * (uint32_t)a.chunk_cols;
   const uint32_t cols = (uint32_t)a.V - lo < (uint32_t)a.chunk_cols ? (uint32_t)a.V - lo : (uint32_t)a.chunk_cols;
@@ -356,6 +373,24 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   const auto set_least = [&] {
     low = bound <= order_of<DT>(-INFINITY);
     least = low ? -INFINITY : value_of<DT>(bound);
+  };
+  // the wave's hits that still reach the bound, moved up
+  const auto prune = [&] {
+    uint32_t kept = 0;
+    for (uint32_t i = 0; i < hits; i += 64) {
+      const uint32_t at = i + lane < hits ? i + lane : i;
+      const u32x4v v = hit[at];
+      const uint32_t from = hit_vec[at];
+      const float top = largest<DT>(v, -INFINITY);
+      const bool mine = i + lane < hits && (low ? top > -INFINITY : top >= least);
+      const unsigned long long lanes = __ballot(mine);
+      if (mine) {
+        hit[kept + lanes_below(lanes)] = v;
+        hit_vec[kept + lanes_below(lanes)] = from;
+      }
+      kept += (uint32_t)__builtin_popcountll(lanes);
+    }
+    hits = kept;
   };
 #pragma unroll 1
   for (uint32_t b = 0; b < nb; ++b) {
@@ -406,9 +441,10 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     // ---- vectors that reach the bound
     if constexpr (TOP) {
       if constexpr (W > 1) {
-        if (((b + 2) & (b + 1)) == 0) {  // b = 0, 2, 6, 14 ...
+        if (((b + 1) & b) == 0) {  // b = 0, 1, 3, 7 ...
           raise_bound([] {});
           set_least();
+          if (hits > 64 && hits <= room) prune();
         }
       } else {  // one batch: of the vectors' maxima
         bound = bound_of<DT, P>(K, [&](int j) { return vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u; });
@@ -421,9 +457,9 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
         const unsigned long long lanes = __ballot(mine);
         if (lanes == 0) continue;
         const uint32_t at = hits + lanes_below(lanes);
-        if (mine && at < (uint32_t)kHits) {
-          hit[wave][at] = v[j];
-          hit_vec[wave][at] = vector_at(b, j, wave, lane);
+        if (mine && at < room) {
+          hit[at] = v[j];
+          hit_vec[at] = vector_at(b, j, wave, lane);
         }
         hits += (uint32_t)__builtin_popcountll(lanes);
       }
@@ -511,7 +547,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   }
   };
   if constexpr (TOP && W > 1) {
-    if (nb > 1 && ((nb + 1) & nb) != 0) {  // the last batch did not raise it
+    if (((nb - 1) & nb) != 0) {  // the last batch did not raise it
       raise_bound(sums_of_chunk);
       set_least();
     } else {
@@ -532,14 +568,14 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   // ---- the K largest: the hits' columns, a lane each
   if constexpr (TOP) {
     uint32_t have = 0;
-    if (hits > (uint32_t)kHits) {
+    if (hits > room) {
       have = kSeg + 1;
       hits = 0;
     }
     for (uint32_t i = 0; i < hits * E; i += 64) {
       const uint32_t at = i + lane < hits * E ? i + lane : 0u;
-      const float f = load_logit<DT>(reinterpret_cast<const char*>(&hit[wave][0]), at);
-      const uint32_t c = hit_vec[wave][at / E] * E + at % E;
+      const float f = load_logit<DT>(reinterpret_cast<const char*>(hit), at);
+      const uint32_t c = hit_vec[at / E] * E + at % E;
       seg.add(i + lane < hits * E && c < cols && (low ? f > -INFINITY : f >= least), key_of(order_of<DT>(f), lo + c), have);
     }
     if (low) {  // fewer than K threads have more than -inf: of the first K columns enough are -inf to fill up with
@@ -780,7 +816,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
   const uint32_t tid = threadIdx.x, C = (uint32_t)a.chunks;
   const uint32_t in_launch = blockIdx.x / C, k = blockIdx.x - in_launch * C;
   const int64_t r = a.row0 + in_launch;
-  const int64_t i0 = r / a.d1, i1 = r - i0 * a.d1;
+  const int64_t i0 = (uint32_t)r / (uint32_t)a.d1, i1 = (uint32_t)r % (uint32_t)a.d1;  // (64-bit divisions delay the first load)
   const char* const row = a.x + (i0 * a.s0 + i1 * a.s1) * EB;
   char* const out = a.out + (i0 * a.os0 + i1 * a.os1) * EB;
   const uint32_t lo = k * (uint32_t)a.chunk_cols;
@@ -871,11 +907,12 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
 }
 
 // Shapes (threads, vectors a thread and batch); logprob_plan chooses
-constexpr FusedShape kShapes[] = {{64, 4}, {256, 2}, {512, 4}};
+constexpr FusedShape kShapes[] = {{64, 4}, {256, 2}, {256, 8}};
 
 template <int DT, int T, int P>
 void launch_flags(const LogprobArgs& a, dim3 grid, hipStream_t stream) {
-#define VCE_LP(TOP, ENT) hipLaunchKernelGGL((k_logprobs<DT, T, P, TOP, ENT>), grid, dim3(T), 0, stream, a)
+  const uint32_t lds = a.K > 0 ? hit_room(a.K) * (T / 64) * 20u : 0u;
+#define VCE_LP(TOP, ENT) hipLaunchKernelGGL((k_logprobs<DT, T, P, TOP, ENT>), grid, dim3(T), lds, stream, a)
   if (a.K > 0) {
     if (a.entropy) VCE_LP(true, true);
     else VCE_LP(true, false);
