@@ -234,10 +234,10 @@ __device__ __forceinline__ uint32_t lanes_below(unsigned long long lanes) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0u));
 }
 
-// Collected keys: each wave's in a segment of its own, in LDS, with zeros behind them: to the next multiple of two, and two more.
+// Collected keys: each wave's in a segment of its own, in LDS, with zeros behind them to the next multiple of eight.
 template <int W, int SEG>
 struct Segments {
-  static constexpr int kStride = SEG + 4;
+  static constexpr int kStride = SEG + 8;
   Key* keys;
   uint32_t* n;      // [W]
   uint32_t* ranks;  // [W * SEG]
@@ -252,7 +252,7 @@ struct Segments {
   }
   __device__ __forceinline__ void close(uint32_t have) const {
     const uint32_t lane = threadIdx.x & 63, kept = have < (uint32_t)SEG ? have : (uint32_t)SEG;
-    if (lane < 4) keys[(threadIdx.x >> 6) * kStride + kept + lane] = 0;
+    if (lane < 8) keys[(threadIdx.x >> 6) * kStride + kept + lane] = 0;
     if (lane == 0) n[threadIdx.x >> 6] = have;
     for (uint32_t i = threadIdx.x; i < W * SEG; i += W * 64) ranks[i] = 0;
   }
@@ -272,15 +272,19 @@ struct Segments {
   __device__ __forceinline__ void rank(uint32_t total, Put put) const {
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const KeyPair* const own = reinterpret_cast<const KeyPair*>(keys + wave * kStride);
+    const uint32_t count = n[wave];
 #pragma unroll 1
     for (uint32_t base = 0; base < total; base += 64) {
       const uint32_t i = base + lane;
       const Key key = i < total ? at(i) : ~0ull;
       uint32_t r = 0;
-#pragma unroll 2
-      for (uint32_t q = 0; 2 * q < n[wave]; ++q) {
-        const KeyPair o = own[q];
-        r += (o.x > key) + (o.y > key);
+#pragma unroll 1
+      for (uint32_t q = 0; q < count; q += 8) {
+        KeyPair o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = own[q / 2 + c];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) r += (o[c].x > key) + (o[c].y > key);
       }
       if (r) atomicAdd(&ranks[i], r);
     }
@@ -595,7 +599,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
     if (most > (uint32_t)kSeg || reach < (cols < K ? cols : K)) {
       exact_largest<DT, T>(chunk, lo, cols, K, low ? order_of<DT>(-INFINITY) : bound, seg_keys, &n_cand, sh_cnt);
       if (tid < W) n_seg[tid] = tid == 0 ? n_cand : 0u;
-      if (tid < 4 * W) seg_keys[(tid / 4) * Segments<W, kSeg>::kStride + (tid < 4 ? n_cand : 0u) + tid % 4] = 0;
+      if (tid < 8 * W) seg_keys[(tid / 8) * Segments<W, kSeg>::kStride + (tid < 8 ? n_cand : 0u) + tid % 8] = 0;
       __syncthreads();
     }
   } else {
@@ -647,8 +651,8 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
 #pragma unroll
     for (int i = 0; i < kStatReads; ++i) stat[i] = i * T + tid < C * kStatWords ? peek_word(stat_word(i)) : 0ull;
     const uint32_t spread = lane * W + wave;  // neighbouring keys go to different waves
-    const uint32_t list = TOP ? K : 1u;
-    const auto key_word = [&](uint32_t at) { return slots + (size_t)(at / list) * words + kStatWords + at % list * 2; };
+    // the chunks' first keys, then their second ...: the threads' largest are then the T best placed
+    const auto key_word = [&](uint32_t at) { return slots + (size_t)(at % C) * words + kStatWords + at / C * 2; };
     if constexpr (TOP) {
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
@@ -907,7 +911,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
 }
 
 // Shapes (threads, vectors a thread and batch); logprob_plan chooses
-constexpr FusedShape kShapes[] = {{64, 4}, {256, 2}, {256, 8}};
+constexpr FusedShape kShapes[] = {{64, 4}, {64, 8}, {256, 2}, {256, 8}};
 
 template <int DT, int T, int P>
 void launch_flags(const LogprobArgs& a, dim3 grid, hipStream_t stream) {
@@ -926,7 +930,8 @@ template <int DT>
 void launch_shape(const LogprobArgs& a, dim3 grid, hipStream_t stream) {
   if (a.shape == 0) launch_flags<DT, kShapes[0].threads, kShapes[0].vecs>(a, grid, stream);
   else if (a.shape == 1) launch_flags<DT, kShapes[1].threads, kShapes[1].vecs>(a, grid, stream);
-  else launch_flags<DT, kShapes[2].threads, kShapes[2].vecs>(a, grid, stream);
+  else if (a.shape == 2) launch_flags<DT, kShapes[2].threads, kShapes[2].vecs>(a, grid, stream);
+  else launch_flags<DT, kShapes[3].threads, kShapes[3].vecs>(a, grid, stream);
 }
 
 int64_t vec_cols(int32_t dtype) { return dtype == CE_BF16 ? 8 : 4; }
@@ -941,23 +946,24 @@ int64_t logprob_max_cols(int32_t dtype) { return (int64_t)1 << (dtype == CE_BF16
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols) {
   // Many rows, or short ones: a workgroup a row, a batch of its shape or more.  Few long ones: chunks of a batch at
   // least, for workgroups enough (64 x 128000 FP32, 5 alternatives: 17 us in 8 chunks by 512 threads, 21 by 256, 25 in 16
-  // chunks; one row of 128000 BF16, 20 alternatives: 12 us in 32 chunks by 256 threads, 14 in 8 to 16 by 512).
+  // chunks; one row of 128000 BF16, 20 alternatives: 12 us in 32 chunks by 256 threads, 14 in 8 to 16 by 512).  K has no part
+  // in it, so that what is asked for beside changes no log-probability.
   const auto batches = [=](int s) { return (V + shape_cols(s, dtype) - 1) / shape_cols(s, dtype); };
   const auto chunks_for = [=](int s, int64_t groups) {
     const int64_t want = (groups + N - 1) / (N > 0 ? N : 1), most = batches(s) < kMaxChunks ? batches(s) : kMaxChunks;
     return want < most ? want : most;
   };
   *chunks = 1;
-  if (V <= shape_cols(0, dtype)) {
-    *shape = 0;
+  if (batches(1) == 1) {  // a wave a row (22369 x 3000 BF16 with the entropy: 43 us, 72 by 256 threads)
+    *shape = batches(0) == 1 ? 0 : 1;
   } else if (N >= 512) {
-    *shape = batches(1) <= 2 ? 1 : 2;
-  } else if (N * batches(2) >= 256) {
-    *shape = 2;
-    *chunks = chunks_for(2, 512);
+    *shape = batches(2) <= 2 ? 2 : 3;
+  } else if (N * batches(3) >= 256) {
+    *shape = 3;
+    *chunks = chunks_for(3, 512);
   } else {
-    *shape = 1;
-    *chunks = chunks_for(1, 1024);
+    *chunks = chunks_for(2, 1024);
+    *shape = batches(2) <= *chunks ? 2 : 3;
   }
   *chunk_cols = share_cols(V, *chunks, vec_cols(dtype));
   *chunks = (V + *chunk_cols - 1) / *chunk_cols;  // whole vectors can leave the last share empty
