@@ -638,8 +638,10 @@ ce_status ce_token_logprobs_backward(const ce_logits* x, const ce_logits* out, c
  *   loss = T^2 (sum_k p_k (log p_k - log q_ck) + r (log r - log q_o)),   q_o = the unnamed columns' share of q
  *   dx_v = s T (q_v (sum_k p_k + r) - sum of p_k with c_k = v - [v unnamed] q_v r / q_o)
  * with s the upstream gradient, over the number of counted rows for the mean, as in the losses above.  Terms of
- * p_k = 0 or r = 0 are left out (0 log 0 = 0); r is 0 where every unnamed column is masked (-inf), or there is none.
+ * p_k = 0 or r = 0 are left out (0 log 0 = 0); r is 0 where there is no unnamed column, or all of them are masked:
+ * -inf, or so far below the row's largest logit (745 T and more) that q_o is 0 in 64 bits.
  * A masked column that the teacher names with p_k > 0 makes the loss +inf and its gradient -s T p_k.
+ * A teacher's NaN, or logits of +inf or of nothing but -inf, make the row's loss and gradient NaN.
  * A row of no entries counts for nothing: loss 0, gradient 0, not one of the rows of the mean.  A row naming a
  * column outside the vocabulary violates the precondition: nothing is read or written out of bounds, its loss and
  * gradient are NaN, as they are for a row that holds a NaN or +inf, or nothing but -inf.

@@ -168,6 +168,29 @@ def test_special_rows(V, dtype):
             assert_within(f64(out[i]).reshape(1, V), dx[i:i + 1], tol[i:i + 1], f"{name}, tail={tail}: dx")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+@pytest.mark.parametrize("V", [5001, 70001])
+def test_students_sure_by_far(V, dtype):
+    """Unnamed columns whose share of the student is far below FP32's smallest number, and named ones of such a share."""
+    K, gaps, g = 8, (60.0, 100.0, 200.0, 600.0, -100.0, -600.0), _gen(V + 2)
+    N = len(gaps)
+    x = (torch.randn((N, V), generator=g) * 2).view(N, 1, V)
+    ids = torch.stack([torch.randperm(V, generator=g)[:K] for _ in gaps]).view(N, 1, K)
+    t = torch.log_softmax(torch.randn((N, 1, K), generator=g), 2) - 0.4
+    for n, gap in enumerate(gaps):
+        x[n, 0, ids[n, 0, :4 if n % 2 else K]] += gap
+    x = x.to(dtype)
+    for T in (1.0, 1.5):
+        for tail in (True, False):
+            l, tl, dx, tol, _ = _ref(x, ids, t, None, T, tail, "none", None, dtype)
+            out = torch.empty_like(x, device="cuda")
+            say(f"sure by far {NAMES[dtype]} V{V} T{T} tail={tail}")
+            loss, _ = vce.ce_distill_fwd_bwd(x.cuda(), ids.cuda(), t.cuda(), T, teacher="logprobs" if tail else "logits",
+                                             out=out)
+            assert_within(f64(loss), l, tl, f"T={T} tail={tail}: loss")
+            assert_within(f64(out).reshape(N, V), dx, tol, f"T={T} tail={tail}: dx")
+
+
 def test_every_column_named():
     """No column is left for what the teacher leaves: it is left out."""
     V = 24
@@ -256,6 +279,10 @@ def test_autograd_form(reduce):
     with torch.no_grad():
         assert torch.equal(vce.distillation_loss(plain, ids.cuda(), t.cuda(), 2.0, reduce, teacher_len=n.cuda()), loss)
     assert torch.equal(plain.cpu(), x), "without a gradient to give the logits stay"
+    plain.requires_grad_()
+    with torch.no_grad():
+        assert torch.equal(vce.distillation_loss(plain, ids.cuda(), t.cuda(), 2.0, reduce, teacher_len=n.cuda()), loss)
+    assert torch.equal(plain.detach().cpu(), x), "nor where none is recorded"
     with pytest.raises(vce.CeArgumentError):
         vce.distillation_loss(z, ids.cuda(), t.cuda().requires_grad_(), 2.0, reduce)
 

@@ -315,6 +315,26 @@ def test_autograd_forms():
         assert vce.token_logprobs(x.cuda(), ids.cuda()).logprobs.requires_grad is False
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+def test_ignored_column_among_the_alternatives(dtype):
+    """ignore_idx may be a column of the vocabulary: it is left out of the given tokens, not of the alternatives."""
+    N, V, K, pad = 4, 5003, 6, 3
+    x = _logits(1, N, V, dtype, seed=31)
+    x[0, :, pad] = x.amax() + 1
+    ids = torch.tensor([[pad, 7], [7, pad], [pad, pad], [8, 9]]).view(1, N, 2)
+    g = torch.randn((N, 2 + K), generator=_gen(3))
+    xd = x.cuda()
+    r = vce.ce_token_logprobs(xd, ids.cuda(), top_k=K, stats=True, ignore_idx=pad)
+    top = r.top_ids.cpu().view(N, K)
+    assert bool((top[:, 0] == pad).all()) and bool((r.logprobs.cpu() == 0)[ids == pad].all())
+    out = vce.ce_token_logprobs_backward(xd, r.stats, ids.cuda(), g[:, :2].contiguous().cuda(), top_ids=r.top_ids,
+                                         dtop=g[:, 2:].contiguous().cuda(), ignore_idx=pad)
+    # ignored tokens as ones of an index of no meaning, the alternatives as they are
+    lists = torch.cat([torch.where(ids.view(N, 2) == pad, -100, ids.view(N, 2)), top], 1)
+    dx, tol = ref_logprobs_grad(f64(x).reshape(N, V), lists.numpy(), f64(g), None, dtype=dtype)
+    assert_within(f64(out).reshape(N, V), dx, tol, "dx")
+
+
 def test_no_rows_and_nothing_asked():
     x = torch.empty((0, 3, 100), device="cuda")
     r = vce.ce_token_logprobs(x, torch.empty((0, 3), dtype=torch.int64, device="cuda"), top_k=4, entropy=True, stats=True)

@@ -769,12 +769,12 @@ class DistillationLoss(torch.autograd.Function):
     applies (ce_scale_grad_inplace), as for the cross-entropy.  Without a gradient to give, ``inp`` is left as it is."""
 
     @staticmethod
-    def forward(ctx, inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws):
+    def forward(ctx, inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws, want_grad):
         buf = inp.detach()
         if buf.dim() != 3:
             _einval("logits must be a 3-d (d0, d1, V) tensor")
         loss, _ = ce_distill_fwd_bwd(buf, teacher_ids, teacher_values, temperature, reduce_loss, teacher=teacher,
-                                     teacher_len=teacher_len, want_grad=ctx.needs_input_grad[0], ws=ws)
+                                     teacher_len=teacher_len, want_grad=want_grad, ws=ws)
         ctx.reduced = reduction_code(reduce_loss) != _abi.CE_REDUCE_NONE
         ctx.save_for_backward(buf)
         return loss[0] if ctx.reduced else loss.view(buf.shape[:2])
@@ -784,12 +784,14 @@ class DistillationLoss(torch.autograd.Function):
     def backward(ctx, grad_loss):
         (buf,) = ctx.saved_tensors
         ce_scale_grad_inplace(buf, grad_loss, per_row=not ctx.reduced)
-        return (buf,) + (None,) * 7
+        return (buf,) + (None,) * 8
 
 
 def distillation_loss(inp, teacher_ids, teacher_values, temperature=1.0, reduce_loss=False, *, teacher="logits",
                       teacher_len=None, ws=None):
     """ce_distill_fwd_bwd through autograd: the loss ((d0, d1), or a scalar with a reduction), whose gradient reaches
-    ``inp`` and is staged in its storage, as parallel_cross_entropy's.  The teacher's values are constants."""
+    ``inp`` and is staged in its storage, as parallel_cross_entropy's; where none is recorded (no_grad), ``inp`` is left
+    as it is.  The teacher's values are constants."""
     _constants(teacher_values=teacher_values)
-    return DistillationLoss.apply(inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws)
+    return DistillationLoss.apply(inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws,
+                                  inp.requires_grad and torch.is_grad_enabled())

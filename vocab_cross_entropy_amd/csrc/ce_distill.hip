@@ -116,7 +116,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
   __shared__ float words[kMaxChunks * kWords];
   __shared__ double kept_p[kDistillMaxTop], kept_e[kDistillMaxTop];  // the entries', over the exchange
   __shared__ uint32_t kept_col[kDistillMaxTop];
-  __shared__ float bc[3];  // c_hi, c_lo, the unnamed columns' factor
+  __shared__ float bc[2];  // the unnamed columns' exponents' offset, and their factor
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t C = (uint32_t)a.chunks;
   const uint32_t in_launch = blockIdx.x / C;
@@ -344,37 +344,42 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       }
       ok = ok && ws.ok;
       if (!ok && lane == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
-      // relative to the row's largest logit M: a weight of exactly 1 for whatever holds it
+      // the unnamed columns' sum relative to their largest, U, so that it is 0 only where all of them are masked; all of
+      // it relative to the row's largest logit, M: a weight of exactly 1 for whatever holds it
       const bool has = lane < C;
-      const float M = wave_largest(has ? w[kRef] : -INFINITY);
-      const auto weight = [&](float from) { return from == -INFINITY ? 0.f : exp2_hw((from - M) * a.kb); };
-      const float f_rest = weight(w[kMax]), f_named = weight(w[kRef]);
+      const float M = wave_largest(has ? w[kRef] : -INFINITY), U = wave_largest(has ? w[kMax] : -INFINITY);
+      const auto weight = [&](float from, float to) { return from == -INFINITY ? 0.f : exp2_hw((from - to) * a.kb); };
+      const float f_rest = weight(w[kMax], U), f_named = weight(w[kRef], M);
       const double rest = wave_sum64(has ? (double)w[kRest] * (double)f_rest : 0.0);
-      const double all = rest + wave_sum64(has ? ((double)w[kSumHi] + (double)w[kSumLo]) * (double)f_named : 0.0);
+      const double down = U == -INFINITY ? 0.0 : fmax(((double)U - (double)M) * (double)a.kb, -1e30), steps = rint(down);
+      // (FP32's exponential with a 64-bit exponent)
+      const double over = rest * ldexp((double)exp2_hw((float)(down - steps)), (int)fmax(steps, -1100.0));
+      const double all = over + wave_sum64(has ? ((double)w[kSumHi] + (double)w[kSumLo]) * (double)f_named : 0.0);
       cross = (double)w[kCrossHi] + (double)w[kCrossLo];
       if (w[kRef] != -INFINITY) cross += (double)w[kMass] * (((double)w[kRef] - (double)M) * (double)a.kb);
       cross = wave_sum64(has ? cross : 0.0);  // of p (z - M)
-      // what the teacher leaves, to the unnamed columns; nothing where none of them can take it
+      // what the teacher leaves, to the unnamed columns; nothing where none of them can take it: all masked, also by
+      // values such as -1e9, next to which their share is 0 in 64 bits
       double left = 0.0;
-      if (a.kind == CE_TEACHER_LOGPROBS && rest != 0.0) left = fmax(0.0, 1.0 - mass);
+      if (a.kind == CE_TEACHER_LOGPROBS && over != 0.0) left = fmax(0.0, 1.0 - mass);
       const double S = mass + left;
-      const double share = rest / all;  // q_o
-      // three logarithms at once: of the sum, of what is left, of q_o
-      const double logs = log2_64(lane == 0 ? all : lane == 1 ? left : share);
-      const double log_all = lane64(logs, 0);
+      // three logarithms at once: of the sum, of what is left, of the unnamed columns' sum
+      const double logs = log2_64(lane == 0 ? all : lane == 1 ? left : rest);
+      const double log_all = lane64(logs, 0), log_rest = lane64(logs, 2);
       double loss = plogp - (cross - mass * log_all) * kLn2d;
-      if (left != 0.0) loss += left * (lane64(logs, 1) - lane64(logs, 2)) * kLn2d;
+      if (left != 0.0) loss += left * (lane64(logs, 1) - (log_rest + down - log_all)) * kLn2d;
       loss *= a.t * a.t;
       double s = (double)up * a.t;
       if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
       if (k == (GRAD ? 0 : C - 1) && lane == 0) row_loss((float)loss);
       if constexpr (GRAD) {
-        const double c = (double)a.kb * ((double)M - (shifted ? (double)m : 0.0)) + log_all;
+        // of an unnamed column: q_v S - left q_v / q_o = (q_o S - left) 2^(z_v - log2 of their sum)
+        const double c = rest == 0.0 ? 0.0 : (double)a.kb * ((double)U - (shifted ? (double)m : 0.0)) + log_rest;
+        const double c_lo = fabsf((float)c) < INFINITY ? c - (double)(float)c : 0.0;  // 2^-c_lo, a few 2^-14 at most, goes to the factor
         if (lane == 0) {
           bc[0] = (float)c;
-          bc[1] = DT == CE_F32 && fabsf((float)c) < INFINITY ? (float)(c - (double)(float)c) : 0.f;
-          bc[2] = (float)(s * (S - (left == 0.0 ? 0.0 : left / share)));
+          bc[1] = (float)(s * (over / all * S - left) * fma(-kLn2d, c_lo, 1.0));
         }
         // the named columns' gradients; entries of the same column add up, in order
         const double f_own = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(f_named), (int)(C > 1 ? k : 0u)));
@@ -392,16 +397,12 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     }
     if constexpr (GRAD) {
       __syncthreads();
-      const float c_hi = bc[0], c_lo = bc[1], f_un = bc[2];
+      const float c = bc[0], f_un = bc[1];
       store_chunk<DT, T, P>(out + (size_t)lo * EB, cols, v, [&](const u32x4v& x) {
         float f[E];
         unpack_vec<DT>(x, f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float t = __builtin_fmaf(f[e], a.kb, -c_hi);
-          if constexpr (DT == CE_F32) t -= c_lo;
-          f[e] = exp2_hw(t) * f_un;
-        }
+        for (int e = 0; e < E; ++e) f[e] = exp2_hw(__builtin_fmaf(f[e], a.kb, -c)) * f_un;
         return pack_vec<DT>(f);
       });
       __syncthreads();

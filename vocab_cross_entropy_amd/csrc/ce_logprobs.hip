@@ -129,9 +129,9 @@ __device__ __forceinline__ uint32_t block_count(uint32_t c, uint32_t* sh) {
   return n;
 }
 
-// The K largest keys of a chunk of at least K columns, exactly, where a bound `t` let
-// too many through, or too few (NaN, which maxima pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it),
-// every column above it, and its ties from the lowest column on.  Leaves K keys in cand[].
+// The K largest keys of a chunk, exactly, where a bound `t` let too many through, or too few (NaN, which maxima
+// pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it), every column
+// above it, and its ties from the lowest column on.  Leaves K keys in cand[]; a chunk of fewer columns, keys of order 0 too.
 // Rare, so it is kept short: every sweep reads the chunk again.  Column 0 of the chunk is the row's column lo.
 template <int DT, int T>
 __device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, uint32_t cols, uint32_t K, uint32_t t,
@@ -500,7 +500,6 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       s0 = __builtin_fmaf(t0, grow, s0);
       if constexpr (ENT) s1 = __builtin_fmaf(__builtin_fmaf(-d, t0, h), grow, s1);
     }
-
   }
 
   // ---- the chunk's maximum and the first thread that has it
@@ -514,41 +513,41 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
   }
   float M;
   const auto sums_of_chunk = [&] {
-  M = sh_max[0];
-  uint32_t owner = sh_own[0];
+    M = sh_max[0];
+    uint32_t owner = sh_own[0];
 #pragma unroll
-  for (int i = 1; i < W; ++i) {
-    owner = sh_max[i] > M ? sh_own[i] : owner;
-    M = fmaxf(M, sh_max[i]);
-  }
-  move_sums(M);
-  if (M != -INFINITY && tid == owner) s0 = s1 = 0.f;
-  if (wave == W - 1 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
-    bool out = false;                 // it has been left out
-    for (uint32_t base = 0; base < nb * P; base += 64) {
-      const uint32_t s = base + lane, i = vector_at(s % nb, s / nb, owner >> 6, owner & 63);
-      float f[E];
-      unpack_vec<DT>(s < nb * P && i < whole ? *reinterpret_cast<const Word*>(chunk + i * 16u)
-                     : s < nb * P            ? partial_vec<DT>(chunk, i * E, cols)
-                                             : partial_vec<DT>(chunk, cols, cols),
-                     f);
-      bool mine = false;
+    for (int i = 1; i < W; ++i) {
+      owner = sh_max[i] > M ? sh_own[i] : owner;
+      M = fmaxf(M, sh_max[i]);
+    }
+    move_sums(M);
+    if (M != -INFINITY && tid == owner) s0 = s1 = 0.f;
+    if (wave == W - 1 && M != -INFINITY) {  // the owner's vectors again, without one column at the maximum
+      bool out = false;                 // it has been left out
+      for (uint32_t base = 0; base < nb * P; base += 64) {
+        const uint32_t s = base + lane, i = vector_at(s % nb, s / nb, owner >> 6, owner & 63);
+        float f[E];
+        unpack_vec<DT>(s < nb * P && i < whole ? *reinterpret_cast<const Word*>(chunk + i * 16u)
+                       : s < nb * P            ? partial_vec<DT>(chunk, i * E, cols)
+                                               : partial_vec<DT>(chunk, cols, cols),
+                       f);
+        bool mine = false;
 #pragma unroll
-      for (int c = 0; c < E; ++c) mine |= f[c] == M;
-      const unsigned long long lanes = __ballot(mine);
-      bool leave = !out && mine && lanes_below(lanes) == 0;
-      out |= lanes != 0;
+        for (int c = 0; c < E; ++c) mine |= f[c] == M;
+        const unsigned long long lanes = __ballot(mine);
+        bool leave = !out && mine && lanes_below(lanes) == 0;
+        out |= lanes != 0;
 #pragma unroll
-      for (int c = 0; c < E; ++c) {
-        const float u = (f[c] - M) * kLog2e;
-        const bool skip = leave && f[c] == M;
-        if (skip) leave = false;
-        const float e = skip ? 0.f : exp2_hw(u);
-        s0 += e;
-        if constexpr (ENT) s1 = __builtin_fmaf(e, fmaxf(u, kFar), s1);
+        for (int c = 0; c < E; ++c) {
+          const float u = (f[c] - M) * kLog2e;
+          const bool skip = leave && f[c] == M;
+          if (skip) leave = false;
+          const float e = skip ? 0.f : exp2_hw(u);
+          s0 += e;
+          if constexpr (ENT) s1 = __builtin_fmaf(e, fmaxf(u, kFar), s1);
+        }
       }
     }
-  }
   };
   if constexpr (TOP && W > 1) {
     if (((nb - 1) & nb) != 0) {  // the last batch did not raise it
@@ -842,7 +841,7 @@ __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a
   load_chunk<DT, T, P>(row + (size_t)lo * EB, cols, v);
   finish_chunk<DT, T, P, false>(row + (size_t)lo * EB, cols, v);
 
-  const bool counts = tid < L && id != a.ignore_idx;
+  const bool counts = tid < L && (tid >= M || id != a.ignore_idx);  // an alternative may well be that column
   const bool valid = id >= 0 && id < a.V;
   const bool mine = counts && valid && id >= lo && id < (int64_t)lo + cols;
   if (!counts) g = 0.f;
