@@ -94,6 +94,27 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t K, const uint32_t (&g)[G
   return t;
 }
 
+// The same of n numbers in LDS, by the wave that wrote them.  Slower than with a few in registers.
+template <int DT>
+__device__ __forceinline__ uint32_t reached_by(uint32_t K, const uint32_t* g, uint32_t n) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t t = 0;
+#pragma unroll 1
+  for (int b = kOrderBits<DT> - 2; b >= kLowBits<DT>; b -= 2) {
+    const uint32_t step = 1u << b;
+    uint32_t n1 = 0, n2 = 0, n3 = 0;
+#pragma unroll 2
+    for (uint32_t i = 0; i < n; i += 64) {
+      const uint32_t o = i + lane < n ? g[i + lane] : 0u;
+      n1 += (uint32_t)__builtin_popcountll(__ballot(o >= t + step));
+      n2 += (uint32_t)__builtin_popcountll(__ballot(o >= t + 2 * step));
+      n3 += (uint32_t)__builtin_popcountll(__ballot(o >= t + 3 * step));
+    }
+    t += n3 >= K ? 3 * step : n2 >= K ? 2 * step : n1 >= K ? step : 0u;
+  }
+  return t;
+}
+
 // The same of group maxima, `g(i)` a lane's i-th of G: of 64, 128 or 256 groups, at least twice K, made of them.  About
 // 1.4 K columns reach it then (K = 32 of 64: 44, 64 of 128: 89); more groups take more ballots than they save.
 template <int DT, int G, typename Group>
@@ -450,8 +471,26 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
           set_least();
           if (hits > 64 && hits <= room) prune();
         }
-      } else {  // one batch: of the vectors' maxima
-        bound = bound_of<DT, P>(K, [&](int j) { return vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u; });
+      } else {  // one batch: of the vectors' maxima, or of quarter vectors' where K takes nearly all of those (65536 x 1000
+                // BF16, K = 128: 381 us, 778 by sweeps; K = 100, 125 vectors: 293, 322)
+        if (P == 4 && vecs * 4 <= K * 5) {
+          static_assert(kTop * 5 * sizeof(uint32_t) <= sizeof seg_keys, "the quarters' maxima");
+          u32x4v* const quarters = reinterpret_cast<u32x4v*>(seg_keys);
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            const uint32_t i = vector_at(b, j, wave, lane);
+            relaunch(v[j]);
+            float f[E];
+            unpack_vec<DT>(v[j], f);
+            u32x4v o;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = order_of<DT>(fmaxf(f[q * (E / 4)], f[q * (E / 4) + E / 4 - 1]));
+            if (i < vecs) quarters[i] = o;
+          }
+          bound = reached_by<DT>(K, reinterpret_cast<const uint32_t*>(quarters), vecs * 4);
+        } else {
+          bound = bound_of<DT, P>(K, [&](int j) { return vector_at(b, j, wave, lane) < vecs ? order_of<DT>(vm[j]) : 0u; });
+        }
         set_least();
       }
 #pragma unroll
