@@ -161,7 +161,7 @@ def _special_rows(V, dtype, seed):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
-@pytest.mark.parametrize("V", [9, 130, 2000, 4099, 40001, 70000])
+@pytest.mark.parametrize("V", [9, 130, 700, 2000, 4099, 40001, 70000])
 def test_special_rows(V, dtype):
     rows = _special_rows(V, dtype, seed=V)
     x = torch.stack(list(rows.values())).to(dtype).view(len(rows), 1, V)

@@ -16,7 +16,8 @@ and the interface of the TransformerEngineNPU issue #29 page (section 1):
                            dist_process_group=None, ignore_idx=-100)
 
 and, beside the loss (``_ops.py``): logit processing (process_logits,
-processed_cross_entropy), embedding and RMS norm (norm_linear_cross_entropy).
+processed_cross_entropy), embedding, RMS norm (norm_linear_cross_entropy),
+token log-probabilities (token_logprobs) and distillation (distillation_loss).
 
 ``reduce_loss`` is False / True (the page's flag: per-row losses / their mean
 over non-ignored rows) or one of "none", "mean", "sum".  ``smoothing`` (a

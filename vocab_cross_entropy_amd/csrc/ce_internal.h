@@ -383,7 +383,7 @@ struct DistillArgs {
   const int32_t* n;           // rows with an entry; NULL: N
   WsHeader* hdr;              // with more than one chunk or a reduction
   unsigned long long* row_words;  // [N] tagged losses
-  unsigned long long* slots;  // [N][chunks][6]
+  unsigned long long* slots;  // [N][chunks][8] tagged words of a chunk
   unsigned long long ws_bytes;
 };
 int64_t distill_max_cols(int32_t dtype);

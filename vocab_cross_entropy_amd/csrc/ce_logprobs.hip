@@ -28,6 +28,10 @@
 // rows, runs of equal values) the K-th value is found exactly by further sweeps over the chunk, and of
 // its ties the lowest columns are taken.  Keys order by value, then by column, so nothing
 // depends on scheduling.
+//
+// 8192 x 128000 BF16 with the entropy 346 us, 6.06 TB/s; with 1, 20, 64 and 128 alternatives 349, 352, 367 and 402.
+// 2048 x 32000 BF16 with 64: 37 us, where 22 would be its read: five workgroups a CU (by registers; six spill, 45 us)
+// for the eight that each has.  One row of 128000 BF16: 8.5 us, with 20 alternatives 12: latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -848,6 +852,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
 // The gradient: a chunk's vectors, all loaded at once, each written where it was
 // read from or elsewhere; the few columns of given tokens are written again by one
 // thread a token, with every gradient that names the column added up in order.
+// Bound: HBM.  8192 x 128000 BF16 with the entropy's 701 us, 5.99 TB/s; 1024 x 32003 FP32, 5 tokens, 46 us, 5.7 TB/s.
 template <int DT, bool ENT>
 __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a) {
   constexpr int T = kLogprobBwdT, P = kLogprobBwdP, E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
@@ -982,10 +987,14 @@ int64_t share_cols(int64_t V, int64_t chunks, int64_t vec) { return ((V + chunks
 int64_t logprob_max_cols(int32_t dtype) { return (int64_t)1 << (dtype == CE_BF16 ? 20 : 19); }
 
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols) {
-  // Many rows, or short ones: a workgroup a row, a batch of its shape or more.  Few long ones: chunks of a batch at
-  // least, for workgroups enough (64 x 128000 FP32, 5 alternatives: 17 us in 8 chunks by 512 threads, 21 by 256, 25 in 16
-  // chunks; one row of 128000 BF16, 20 alternatives: 12 us in 32 chunks by 256 threads, 14 in 8 to 16 by 512).  K has no part
-  // in it, so that what is asked for beside changes no log-probability.
+  // Many rows, or short ones: a workgroup a row, a batch of its shape or more; few long ones: chunks of a batch at least, for
+  // two workgroups a CU, or four of the smaller shape.  us with the entropy, with 20 and with 128 alternatives:
+  //   64 x 128000 FP32 in 8 chunks 13.4, 22.0, 29.9; in 4: 16.0, 24.0, 32.9; in 16: 13.6, 21.1, 42.4
+  //   700 x 128000 BF16 a row 39.6, 43.8, 53.1; in two 44.1, 54.5, 79.5
+  //   300 x 128000 BF16 in two 25.6, 32.7, 43.2; a row 28.4, 34.4, 42.4
+  //   300 x 32003 FP32, four batches, a row 15.1, 20.3, 26.7; in two 16.4, 23.1, 30.8
+  //   one row of 128000 BF16, 20 alternatives: 12 in 32 chunks of the smaller shape, 14 in 8 to 16 larger ones
+  // K has no part in it, so that what is asked for beside changes no log-probability.
   const auto batches = [=](int s) { return (V + shape_cols(s, dtype) - 1) / shape_cols(s, dtype); };
   const auto chunks_for = [=](int s, int64_t groups) {
     const int64_t want = (groups + N - 1) / (N > 0 ? N : 1), most = batches(s) < kMaxChunks ? batches(s) : kMaxChunks;
@@ -994,7 +1003,7 @@ void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* 
   *chunks = 1;
   if (batches(1) == 1) {  // a wave a row (22369 x 3000 BF16 with the entropy: 43 us, 72 by 256 threads)
     *shape = batches(0) == 1 ? 0 : 1;
-  } else if (N >= 512) {
+  } else if (N >= 512 || (N >= 256 && batches(3) <= 4)) {
     *shape = batches(2) <= 2 ? 2 : 3;
   } else if (N * batches(3) >= 256) {
     *shape = 3;
