@@ -168,6 +168,22 @@ def test_special_rows(V, dtype):
             assert_within(f64(out[i]).reshape(1, V), dx[i:i + 1], tol[i:i + 1], f"{name}, tail={tail}: dx")
 
 
+@pytest.mark.parametrize("N", [2047, 2048, 2049, 5000])
+def test_many_rows_are_counted(N):
+    """The mean's rows, with and without their number asked for; the last row has no entry."""
+    x, ids, t, n = _case(1, N, 37, 3, F32, N, True)
+    n[-1] = 0
+    l, tl, dx, tol, count = _ref(x, ids, t, n, 1.0, True, "mean", None, F32)
+    say(f"distill {N} rows")
+    for nv in (None, torch.zeros(1, dtype=torch.int32, device="cuda")):
+        out = torch.empty_like(x, device="cuda")
+        loss, _ = vce.ce_distill_fwd_bwd(x.cuda(), ids.cuda(), t.cuda(), 1.0, "mean", teacher="logprobs",
+                                         teacher_len=n.cuda(), out=out, n_valid=nv)
+        assert nv is None or int(nv) == count
+        assert_within(f64(loss), l, tl, "loss")
+        assert_within(f64(out).reshape(N, -1), dx, tol, "dx")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
 @pytest.mark.parametrize("V", [5001, 70001])
 def test_students_sure_by_far(V, dtype):
