@@ -711,8 +711,11 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
       st[(i * T + tid) / kStatWords][(i * T + tid) % kStatWords] = __uint_as_float(w);
     }
     if constexpr (TOP) {
+      // Rounds until the last keys taken, one of each chunk, are all behind K others: so are those that follow them.  (One
+      // row of 128000 BF16, 128 alternatives: one round of nine, 21 us; 41 with all.)
       uint32_t done = 0, held = 0;  // keys taken, K of each chunk; keys of earlier rounds
-      while (done < C * K) {
+      bool more = true;
+      while (done < C * K && more) {
         Key key[kRound];
         uint32_t best = 0;
 #pragma unroll
@@ -732,6 +735,7 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
           const uint32_t o = (uint32_t)(key[i] >> 32);
           best = o > best ? o : best;
         }
+        const uint32_t taken = done - held;  // at `at`, key at + taken
         done += kRound * T - held;
         held = K;
         thread_top[tid] = best;
@@ -759,6 +763,12 @@ __global__ __launch_bounds__(T) void k_logprobs(LogprobArgs a) {
           if (rank < K) top[rank] = key;
         });
         __syncthreads();
+        const uint32_t end = done < C * K ? done : C * K;
+        more = false;
+#pragma unroll
+        for (int i = 0; i < kRound; ++i)
+          more |= i * T + spread + taken + C >= end && i * T + spread + taken < end && key[i] != 0ull && key[i] >= top[K - 1];
+        more = __syncthreads_or(more);
       }
     }
     ok = __syncthreads_and(ok);
