@@ -614,14 +614,15 @@ def ce_token_logprobs(x, ids=None, *, top_k=0, entropy=False, stats=False, lse=F
     nbytes = lib.ce_token_logprobs_workspace_bytes(xd, top_k)
     if nbytes == 0:
         _check(_abi.CE_EINVAL)
-    logp = None if ids is None else torch.empty(ids.shape, dtype=f32, device=device)
-    ent = torch.empty((d0, d1), dtype=f32, device=device) if entropy else None
+    # (sizes by themselves: 1.3 us a tensor, 1.65 as a tuple)
+    logp = None if ids is None else torch.empty(*ids.shape, dtype=f32, device=device)
+    ent = torch.empty(d0, d1, dtype=f32, device=device) if entropy else None
     top_ids = top_logp = None
     if top_k:
-        top_ids = torch.empty((d0, d1, top_k), dtype=torch.int64, device=device)
-        top_logp = torch.empty((d0, d1, top_k), dtype=f32, device=device)
-    st = torch.empty((d0 * d1, 4), dtype=f32, device=device) if stats else None
-    log_sum = torch.empty((d0, d1), dtype=f32, device=device) if lse else None
+        top_ids = torch.empty(d0, d1, top_k, dtype=torch.int64, device=device)
+        top_logp = torch.empty(d0, d1, top_k, dtype=f32, device=device)
+    st = torch.empty(d0 * d1, 4, dtype=f32, device=device) if stats else None
+    log_sum = torch.empty(d0, d1, dtype=f32, device=device) if lse else None
     ws_ptr, ws_bytes = None, 0
     if nbytes > 256:
         ws = _prepared(dev, ws, nbytes, x)

@@ -999,7 +999,7 @@ int64_t logprob_max_cols(int32_t dtype) { return (int64_t)1 << (dtype == CE_BF16
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols) {
   // Many rows, or short ones: a workgroup a row, a batch of its shape or more; few long ones: chunks of a batch at least, for
   // two workgroups a CU, or four of the smaller shape.  us with the entropy, with 20 and with 128 alternatives:
-  //   64 x 128000 FP32 in 8 chunks 13.4, 22.0, 29.9; in 4: 16.0, 24.0, 32.9; in 16: 13.6, 21.1, 42.4
+  //   64 x 128000 FP32 in 8 chunks 13.6, 22.2, 30.4; in 4: 15.8, 23.9, 32.9; in 16: 13.9, 21.6, 30.6
   //   700 x 128000 BF16 a row 39.6, 43.8, 53.1; in two 44.1, 54.5, 79.5
   //   300 x 128000 BF16 in two 25.6, 32.7, 43.2; a row 28.4, 34.4, 42.4
   //   300 x 32003 FP32, four batches, a row 15.1, 20.3, 26.7; in two 16.4, 23.1, 30.8
