@@ -116,6 +116,19 @@ def _need_ws(dev: torch.device, ws):
     _need(dev, "workspace", ws, torch.uint8)
 
 
+# torch's version counter of a tensor, raised by the calls that write over logits: the kernels write through raw
+# pointers, and a function that keeps the logits for its backward (token_logprobs) has to see that they are gone.  The
+# public wrapper takes 0.67 us a call, its core 0.28.
+_increment_version = getattr(torch._C, "_increment_version", None)
+if _increment_version is None:
+    _increment_version = torch.autograd.graph.increment_version
+
+
+def _overwritten(*xs: torch.Tensor):
+    """The tensors' values have been replaced (views and detached tensors share the counter)."""
+    _increment_version(xs)
+
+
 def _dtype_code(x: torch.Tensor) -> int:
     if x.dtype == torch.float32:
         return CE_F32
@@ -277,6 +290,7 @@ def ce_backward_inplace_ex(x, t, lse, lse_aux, label_smoothing=0.0, reduce_loss=
     _check(lib.ce_backward_inplace_ex(ctypes.byref(logits_desc(x, vocab_start, vocab_total)),
                                       ctypes.byref(targets_desc(t)), ctypes.byref(p), _ptr(lse), _ptr(lse_aux),
                                       _ptr(grad_out), _ptr(n_valid), _stream(dev)))
+    _overwritten(x)
     return x
 
 
@@ -315,6 +329,7 @@ def ce_fwd_bwd_fused(x, t, label_smoothing=0.0, reduce_loss=False, ignore_idx=-1
         ce_workspace_init(ws)
     _check(lib.ce_fwd_bwd_fused(ctypes.byref(xd), ctypes.byref(targets_desc(t)), ctypes.byref(p), _ptr(grad_out),
                                 _ptr(loss), _ptr(n_valid), _ptr(ws), ws.numel(), _stream(dev)))
+    _overwritten(x)
     return loss, n_valid
 
 
@@ -332,6 +347,7 @@ def ce_fwd_bwd_fused_noalloc(x, t, label_smoothing=0.0, reduce_loss=False, ignor
     _need(dev, "n_valid", n_valid, torch.int32, 1)
     _check(lib.ce_fwd_bwd_fused_noalloc(ctypes.byref(logits_desc(x)), ctypes.byref(targets_desc(t)),
                                         ctypes.byref(p), _ptr(grad_out), _ptr(loss), _ptr(n_valid), _stream(dev)))
+    _overwritten(x)
     return loss, n_valid
 
 
@@ -386,6 +402,7 @@ def ce_shards_fwd_bwd_fused(shards, t, label_smoothing=0.0, reduce_loss=False, i
         ce_workspace_init(ws)
     _check(lib.ce_shards_fwd_bwd_fused(arr, len(shards), ctypes.byref(targets_desc(t)), ctypes.byref(p),
                                        _ptr(grad_out), _ptr(loss), _ptr(n_valid), _ptr(ws), ws.numel(), _stream(dev)))
+    _overwritten(*shards)
     return loss, n_valid
 
 
@@ -618,7 +635,8 @@ class ParallelCrossEntropy(torch.autograd.Function):
     ce_scale_grad_inplace, which leaves rows whose factor is exactly 1
     untouched (no host synchronisation to find them); ``inp``'s storage is
     returned as the gradient.  After the forward, ``inp`` holds the gradient,
-    not the logits.
+    not the logits: its version counter rises, so a function that kept the
+    logits for its own backward raises there.
     """
 
     @staticmethod
@@ -641,7 +659,10 @@ def parallel_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False, 
     """The issue #29 interface: FP32 loss (per row in ``target``'s shape, or
     their mean over non-ignored rows, or with ``reduce_loss="sum"`` their
     sum); the gradient is staged in place in ``inp`` (in its dtype) and
-    reaches autograd through ParallelCrossEntropy.
+    reaches autograd through ParallelCrossEntropy.  So this is the last call
+    on these logits: one that comes before it and keeps them (token_logprobs,
+    another loss staged in them) takes a copy, ``inp.clone()``, or its
+    backward raises, and one that comes after reads the gradient.
 
     ``inp`` is (B, SQ, V) or (SQ, B, V) (any row strides, contiguous
     columns); ``target`` the matching (B, SQ) / (SQ, B) int64 global indices.

@@ -2,7 +2,8 @@
 
 Like the rest of the binding, the ``ce_*`` functions marshal torch device
 tensors into the C ABI's descriptors (``include/ce.h`` defines each operator)
-and run on torch's current stream of the tensors' device; ``process_logits``,
+and run on torch's current stream of the tensors' device; those that write over
+logits raise the tensor's version, as torch's in-place operations do.  ``process_logits``,
 ``processed_cross_entropy``, ``embedding``, ``rms_norm``,
 ``norm_linear_cross_entropy``, ``token_logprobs`` and ``distillation_loss`` are
 their autograd forms.
@@ -16,8 +17,8 @@ from torch.autograd.function import once_differentiable
 
 from . import _abi
 from . import (CeArgumentError, _check, _device_of, _need, _need_targets, _raw_stream, _workspace,
-               _is_prepared, ce_fwd_bwd_fused, ce_scale_grad_inplace, ce_workspace_bytes, ce_workspace_init, lib,
-               linear_cross_entropy, reduction_code)
+               _is_prepared, _overwritten, ce_fwd_bwd_fused, ce_scale_grad_inplace, ce_workspace_bytes,
+               ce_workspace_init, lib, linear_cross_entropy, reduction_code)
 
 __all__ = [
     "ce_logits_process", "ce_logits_process_backward", "logits_signs", "process_logits", "processed_cross_entropy",
@@ -154,6 +155,9 @@ def _process(fn, x, out, vocab_start, vocab_total, history, history_len, prompt_
                        _flat(dev, "temperature", temperature, f32, N), *_side(dev, "bias", bias, d0, d1, V, f32),
                        *_side(dev, "mask", mask, d0, d1, (V + 31) // 32, i32), signs_ptr, signs_ld)
     _call(dev, fn, xd, zd, p)
+    # (a gradient's processing in place writes over no logits: a loss may have staged it, for its backward to return)
+    if zd.data == xd.data and fn is lib.ce_logits_process:
+        _overwritten(x)
     return x if out is None else out
 
 
@@ -278,7 +282,8 @@ def processed_cross_entropy(inp, target, label_smoothing=0.0, reduce_loss=False,
                             frequency=None, bias=None, mask=None, temperature=None):
     """Cross-entropy (the negative log-probability) under the distribution that sampling drew from:
     parallel_cross_entropy of the processed logits, whole rows of the vocabulary, with its options (reduction,
-    smoothing, ignored index) and those of process_logits.  As there, the gradient is staged in place in ``inp``."""
+    smoothing, ignored index) and those of process_logits.  As there, the gradient is staged in place in ``inp``, and what
+    was called on these logits before and keeps them has taken a copy."""
     _constants(repetition=repetition, presence=presence, frequency=frequency, bias=bias, temperature=temperature)
     return ProcessedCrossEntropy.apply(inp, target, label_smoothing, reduce_loss, ignore_idx, smoothing, history,
                                        history_len, prompt_len, repetition, presence, frequency, bias, mask,
@@ -662,6 +667,8 @@ def ce_token_logprobs_backward(x, stats, ids=None, dlogprobs=None, *, dentropy=N
     _call(dev, lib.ce_token_logprobs_backward, xd, od, q, _flat(dev, "stats", stats, f32, 4 * N),
           _flat(dev, "dlogprobs", dlogprobs, f32, N * M), _flat(dev, "dentropy", dentropy, f32, N),
           _flat(dev, "top_ids", top_ids, torch.int64, N * K), _flat(dev, "dtop", dtop, f32, N * K))
+    if od.data == xd.data:
+        _overwritten(x)
     return out
 
 
@@ -702,7 +709,12 @@ class TokenLogprobsFn(torch.autograd.Function):
 def token_logprobs(logits, ids=None, *, top_k=0, entropy=False, ignore_idx=-100, ws=None):
     """Log-probabilities of ``ids``, the entropy and the ``top_k`` alternatives as ce_token_logprobs gives them, with
     a gradient: of the log-probabilities, of the entropy and of the alternatives' log-probabilities.  Returns a
-    TokenLogprobs (without stats and lse)."""
+    TokenLogprobs (without stats and lse).
+
+    The logits are kept for the backward, which raises if something has written over them since.  A loss that stages its
+    gradient in its logits (parallel_cross_entropy, processed_cross_entropy, sharded_cross_entropy, distillation_loss)
+    therefore comes after this call and takes a copy, ``logits.clone()``; called before, it leaves its gradient to be
+    read here."""
     if ids is None and not top_k and not entropy:
         _einval("nothing is asked for: ids, top_k or entropy")
     logp, ent, top_ids, top_logp = TokenLogprobsFn.apply(logits, ids, int(top_k), bool(entropy), int(ignore_idx), ws)
@@ -762,6 +774,8 @@ def ce_distill_fwd_bwd(x, teacher_ids, teacher_values, temperature=1.0, reduce_l
         _check(_abi.CE_EINVAL)
     ws = _prepared(dev, ws, nbytes, x)
     _call(dev, lib.ce_distill_fwd_bwd, xd, od, d, code, g_ptr, loss_ptr, n_ptr, ws.data_ptr(), ws.numel())
+    if want_grad and od.data == xd.data:
+        _overwritten(x)
     return loss, n_valid
 
 
@@ -792,7 +806,10 @@ def distillation_loss(inp, teacher_ids, teacher_values, temperature=1.0, reduce_
                       teacher_len=None, ws=None):
     """ce_distill_fwd_bwd through autograd: the loss ((d0, d1), or a scalar with a reduction), whose gradient reaches
     ``inp`` and is staged in its storage, as parallel_cross_entropy's; where none is recorded (no_grad), ``inp`` is left
-    as it is.  The teacher's values are constants."""
+    as it is.  The teacher's values are constants.
+
+    Beside another loss on the same logits all but the last take a copy: ``distillation_loss(inp.clone(), ...)``, then
+    ``parallel_cross_entropy(inp, ...)``.  Without it the backward of what came before raises."""
     _constants(teacher_values=teacher_values)
     return DistillationLoss.apply(inp, teacher_ids, teacher_values, temperature, reduce_loss, teacher, teacher_len, ws,
                                   inp.requires_grad and torch.is_grad_enabled())
