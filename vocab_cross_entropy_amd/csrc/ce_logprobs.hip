@@ -154,8 +154,8 @@ __device__ __forceinline__ uint32_t block_count(uint32_t c, uint32_t* sh) {
   return n;
 }
 
-// The K largest keys of a chunk, exactly, where a bound `t` let too many through, or too few (NaN, which maxima
-// pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it), every column
+// The K largest keys of a chunk, exactly, where a bound `t` let too many through, or may have let too few (NaN, which
+// maxima pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it), every column
 // above it, and its ties from the lowest column on.  Leaves K keys in cand[]; a chunk of fewer columns, keys of order 0 too.
 // Rare, so it is kept short: every sweep reads the chunk again.  Column 0 of the chunk is the row's column lo.
 template <int DT, int T>
@@ -613,6 +613,17 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 256 && P
     sh_sum[wave][1] = s1;
   }
 
+  // the chunk's sums, later the row's: `one` column counted apart
+  float one = M == -INFINITY ? 0.f : 1.f, rest = 0.f;
+  s1 = 0.f;
+  const auto sums_of_waves = [&] {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      rest += sh_sum[i][0];
+      s1 += sh_sum[i][1];
+    }
+  };
+
   // ---- the K largest: the hits' columns, a lane each
   if constexpr (TOP) {
     uint32_t have = 0;
@@ -640,7 +651,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 256 && P
       reach += n_seg[i];
       most = n_seg[i] > most ? n_seg[i] : most;
     }
-    if (most > (uint32_t)kSeg || reach < (cols < K ? cols : K)) {
+    sums_of_waves();
+    // (a NaN in the sum: a signalling one may have hidden maxima, and with them columns, from the bound)
+    if (most > (uint32_t)kSeg || reach < (cols < K ? cols : K) || rest != rest) {
       exact_largest<DT, T>(chunk, lo, cols, K, low ? order_of<DT>(-INFINITY) : bound, seg_keys, &n_cand, sh_cnt);
       if (tid < W) n_seg[tid] = tid == 0 ? n_cand : 0u;
       if (tid < 8 * W) seg_keys[(tid / 8) * Segments<W, kSeg>::kStride + (tid < 8 ? n_cand : 0u) + tid % 8] = 0;
@@ -648,14 +661,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 256 && P
     }
   } else {
     __syncthreads();
-  }
-  // the chunk's sums, later the row's: `one` column counted apart
-  float one = M == -INFINITY ? 0.f : 1.f, rest = 0.f;
-  s1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    rest += sh_sum[i][0];
-    s1 += sh_sum[i][1];
+    sums_of_waves();
   }
 
   if (C > 1) {

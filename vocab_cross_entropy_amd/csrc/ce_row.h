@@ -105,7 +105,8 @@ __device__ __forceinline__ void subtract(u32x4v (&v)[P], float m) {
   }
 }
 
-// One v_max3_f32 (fmaxf would quiet each operand first).  A NaN loses; the sums carry it.
+// One v_max3_f32 (fmaxf would quiet each operand first).  A quiet NaN loses; a signalling one can take the operands
+// before it along.  The sums carry either: where one is NaN, maxima say nothing.
 __device__ __forceinline__ float max3_hw(float a, float b, float c) {
   float d;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
