@@ -11,7 +11,7 @@
 // are set to -inf in their registers, found by a bitmap of the chunk in LDS), relative to
 // their own maximum; the named ones, a few, are added in 64 bits.  So q_o keeps its digits
 // where the named columns hold nearly everything, and so does q_c - p_c, whose terms
-// are both near 1 there: the largest term of the row is weighted by exactly 1, in q_c and in the sum alike.
+// are both near 1 there: the largest term of the row is the same number in q_c and in the sum.
 // All that is per entry or per row is 64-bit, by one wave, while the others wait; their loads are under way then.
 //
 // Bound: one read and one write of the logits.  A chunk of a row stays in a
@@ -28,19 +28,24 @@
 namespace vce {
 namespace {
 
-// what a chunk tells: its largest unnamed logit m and the sum of the unnamed columns relative to it; a reference for its
-// named ones (a logit: the largest of all that the chunk has), their sum relative to it (two words), that of
-// p (z - reference) (two words), and that of p
-enum { kMax, kRest, kRef, kSumHi, kSumLo, kCrossHi, kCrossLo, kMass, kWords };
+// what a chunk tells: its largest unnamed logit m and the sum of the unnamed columns; a reference for its named ones (a
+// logit: the largest of all that the chunk has), their sum, and that of p times their exponents, both 64-bit, in two words
+// each; sums are relative to powers of two near m and the reference.  (Less would show where a student is near its teacher
+// and the loss is a small difference: log2 e / T in FP32 alone moves a loss of 2e-7 by up to 6e-4 of it and its gradient by
+// 2e-3, one of 2e-9 by 4e-3 and 2e-2.  The eighth word is empty: 64 bytes a chunk, one word a lane for eight chunks.
+// 8192 x 128000 BF16: 695 us; with seven words 702, with nine 721 to 757; weights by 64-bit exponentials instead of powers
+// of two, 705.)
+enum { kMax, kRest, kRef, kSum, kCross = kSum + 2, kEmpty = kCross + 2, kWords };
 constexpr int kEntries = kDistillMaxTop / 64;  // entries a lane of the wave that handles them
 constexpr double kLn2d = 0.693147180559945309417, kLog2eD = 1.442695040888963407360;
 
-// a 64-bit value as two FP32 words (an infinity or NaN stands in the first)
-__device__ __forceinline__ void split64(double v, float* hi, float* lo) {
-  *hi = (float)v;
-  const double d = v - (double)*hi;
-  *lo = fabs(d) < (double)INFINITY ? (float)d : 0.f;
+typedef uint32_t Words2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void put64(uint32_t* w, double v) {
+  const Words2 b = __builtin_bit_cast(Words2, v);
+  w[0] = b.x;
+  w[1] = b.y;
 }
+__device__ __forceinline__ double get64(const uint32_t* w) { return __builtin_bit_cast(double, Words2{w[0], w[1]}); }
 
 // 2^x: 2^n times the Taylor series of 2^f, |f| <= 1/2, to (f ln 2)^13 / 13!, 2e-17 of it.  Shorter than the library's,
 // whose code takes longer to fetch than to run.
@@ -74,6 +79,15 @@ __device__ __forceinline__ double lane64(double v, int l) {
   const i2 r = {__builtin_amdgcn_readlane(w.x, l), __builtin_amdgcn_readlane(w.y, l)};
   return __builtin_bit_cast(double, r);
 }
+
+// References of sums are powers of two, 2^n with n = rint(x log2 e / T) of a chunk's largest logit x: each chunk's is its
+// own, and sums are brought together by exponents alone.  A column's exponent is fma(x, log2 e / T, -n), rounded once.
+// From 2^50 on logits are equal or too far apart to add up, and exponents are their differences from the reference.
+__device__ __forceinline__ double power_of(float x, double kb) { return rint((double)x * kb); }
+__device__ __forceinline__ double above(float x, float ref, double n, double kb) {
+  return fabs(n) < 0x1p50 ? fma((double)x, kb, -n) : ((double)x - (double)ref) * kb;
+}
+__device__ __forceinline__ int steps(double d) { return (int)fmax(d, -2200.0); }  // (d <= 0; NaN is of sums that are 0 or NaN)
 
 template <int T>
 __device__ void finish_distill(const DistillArgs& a, uint32_t tag, bool ws_ok) {
@@ -116,9 +130,10 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
   constexpr int E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
   __shared__ float sh_max[W], sh_sum[W];
   __shared__ __align__(8) uint8_t named[T * 8];  // byte tid * 8 + j: which columns of slot j's vector are named
-  __shared__ float words[kMaxChunks * kWords];
+  __shared__ uint32_t words[kMaxChunks * kWords];
   __shared__ double kept_p[kDistillMaxTop], kept_e[kDistillMaxTop];  // the entries', over the exchange
   __shared__ uint32_t kept_col[kDistillMaxTop];
+  __shared__ uint8_t kept_chunk[kDistillMaxTop];
   __shared__ float bc[2];  // the unnamed columns' exponents' offset, and their factor
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t C = (uint32_t)a.chunks;
@@ -197,14 +212,13 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     }
     __syncthreads();
     if (tid < 64) {
-      double t[kEntries], top = 0.0, logd = 0.0, d = 1.0;
+      double t[kEntries], logd = 0.0, d = 1.0;
       const bool logits = a.kind == CE_TEACHER_LOGITS;
-      if (logits) {
-        top = -(double)INFINITY;
+      float largest_t = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kEntries; ++i) top = fmax(top, i * 64 + (int)lane < L ? (double)tv[i] * a.inv_t : top);
-        top = wave_largest64(top);
-      }
+      for (int i = 0; i < kEntries; ++i) largest_t = fmaxf(largest_t, i * 64 + (int)lane < L ? tv[i] : -INFINITY);
+      largest_t = wave_largest(largest_t);
+      const double top = logits ? (double)largest_t * a.inv_t : 0.0;
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         t[i] = i * 64 + (int)lane < L ? (logits ? (double)tv[i] * a.inv_t : (double)tv[i]) - top : -(double)INFINITY;
@@ -226,6 +240,14 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       bad = __any(bad);
     }
 
+    const bool tells = k == (GRAD ? 0 : C - 1);  // brings the row's loss together
+    if (C > 1 && tells && tid < 64) {
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {  // (bad columns: the row is NaN whichever chunk they are taken for)
+        const uint32_t c = (uint32_t)id[i] / (uint32_t)a.chunk_cols;
+        kept_chunk[i * 64 + lane] = (uint8_t)(c < C ? c : 0u);
+      }
+    }
     float grad[kEntries];  // of the named columns here
 
     // ---- the unnamed columns: maximum and sum
@@ -276,8 +298,11 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       s0 = sh_sum[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) s0 += sh_sum[i];
-      if (!shifted && m != -INFINITY) s0 *= exp2_hw(-__builtin_fmaf(m, a.kb, -from));  // from `from` to the exact m kb
-      double z[kEntries], e[kEntries], sum = 0.0, cross = 0.0, own = 0.0;
+      if (m != -INFINITY) {  // from `from` to the power of two
+        const float d = (float)above(m, m, power_of(m, a.kb64), a.kb64);
+        s0 *= exp2_hw(shifted ? d : d - __builtin_fmaf(m, a.kb, -from));
+      }
+      double e[kEntries], sum = 0.0, cross = 0.0;
       bool odd = false;  // NaN or +inf, which have no sum
       float ref = m;
 #pragma unroll
@@ -286,18 +311,16 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
         ref = fmaxf(ref, here[i] ? xe[i] : -INFINITY);
       }
       ref = wave_largest(ref);
+      const double n_ref = power_of(ref, a.kb64);
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         const bool some = here[i] && xe[i] != -INFINITY;
-        z[i] = some ? ((double)xe[i] - (double)ref) * (double)a.kb : -(double)INFINITY;
-        e[i] = __any(some) ? exp2_64(z[i]) : 0.0;
+        const double z = some ? above(xe[i], ref, n_ref, a.kb64) : -(double)INFINITY;
+        e[i] = __any(some) ? exp2_64(z) : 0.0;
         sum += first[i] ? e[i] : 0.0;
-        if (here[i] && p[i] != 0.0) {
-          cross += p[i] * z[i];
-          own += p[i];
-        }
+        if (here[i] && p[i] != 0.0) cross += p[i] * z;
       }
-      if constexpr (GRAD) {
+      if (GRAD || C > 1) {
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) {
           kept_p[i * 64 + lane] = p[i];
@@ -313,31 +336,30 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       }();
       sum = wave_sum64(sum);
       cross = wave_sum64(cross);
-      own = wave_sum64(own);
       if (__any(odd)) sum = __builtin_nan("");
       // lane c: what chunk c tells
       bool ok = true;
-      float w[kWords];
-      w[kMax] = m;
-      w[kRest] = s0;
-      w[kRef] = ref;
-      split64(sum, &w[kSumHi], &w[kSumLo]);
-      split64(cross, &w[kCrossHi], &w[kCrossLo]);
-      w[kMass] = (float)own;
+      uint32_t w[kWords];
+      w[kMax] = __float_as_uint(m);
+      w[kRest] = __float_as_uint(s0);
+      w[kRef] = __float_as_uint(ref);
+      put64(w + kSum, sum);
+      put64(w + kCross, cross);
+      w[kEmpty] = 0u;
       if (C > 1) {
         unsigned long long* const slots = a.slots + (size_t)r * C * kWords;
         if (lane < kWords && !withheld(ws, r, (int)k)) {
-          float mine = w[0];
+          uint32_t mine = w[0];
 #pragma unroll
           for (int q = 1; q < kWords; ++q) mine = (int)lane == q ? w[q] : mine;
-          put_word(slots + k * kWords + lane, ws.tag, __float_as_uint(mine));
+          put_word(slots + k * kWords + lane, ws.tag, mine);
         }
         if (!GRAD && k != C - 1) return;  // the last chunk brings the row's loss together; no other needs it
         uint32_t spins = 0;
         for (uint32_t i = lane; i < C * kWords; i += 64) {
           uint32_t got = 0x7fc00000u;
           ok &= await_word(slots + i, ws.tag, peek_word(slots + i), spins, &got);
-          words[i] = __uint_as_float(got);
+          words[i] = got;
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
@@ -348,19 +370,29 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       ok = ok && ws.ok;
       if (!ok && lane == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
       // the unnamed columns' sum relative to their largest, U, so that it is 0 only where all of them are masked; all of
-      // it relative to the row's largest logit, M: a weight of exactly 1 for whatever holds it
+      // it relative to the row's largest logit, M
       const bool has = lane < C;
-      const float M = wave_largest(has ? w[kRef] : -INFINITY), U = wave_largest(has ? w[kMax] : -INFINITY);
-      const auto weight = [&](float from, float to) { return from == -INFINITY ? 0.f : exp2_hw((from - to) * a.kb); };
-      const float f_rest = weight(w[kMax], U), f_named = weight(w[kRef], M);
-      const double rest = wave_sum64(has ? (double)w[kRest] * (double)f_rest : 0.0);
-      const double down = U == -INFINITY ? 0.0 : fmax(((double)U - (double)M) * (double)a.kb, -1e30), steps = rint(down);
-      // (FP32's exponential with a 64-bit exponent)
-      const double over = rest * ldexp((double)exp2_hw((float)(down - steps)), (int)fmax(steps, -1100.0));
-      const double all = over + wave_sum64(has ? ((double)w[kSumHi] + (double)w[kSumLo]) * (double)f_named : 0.0);
-      cross = (double)w[kCrossHi] + (double)w[kCrossLo];
-      if (w[kRef] != -INFINITY) cross += (double)w[kMass] * (((double)w[kRef] - (double)M) * (double)a.kb);
-      cross = wave_sum64(has ? cross : 0.0);  // of p (z - M)
+      const float w_max = __uint_as_float(w[kMax]), w_ref = __uint_as_float(w[kRef]);
+      const float M = wave_largest(has ? w_ref : -INFINITY), U = wave_largest(has ? w_max : -INFINITY);
+      const double n_M = power_of(M, a.kb64), n_U = power_of(U, a.kb64);
+      const double rest =
+          wave_sum64(has ? ldexp((double)__uint_as_float(w[kRest]), steps(power_of(w_max, a.kb64) - n_U)) : 0.0);
+      const double down = U == -INFINITY ? 0.0 : n_U - n_M;
+      const double over = ldexp(rest, steps(down));
+      const int up_named = steps(power_of(w_ref, a.kb64) - n_M);
+      const double all = over + wave_sum64(has ? ldexp(get64(w + kSum), up_named) : 0.0);
+      // of p (z - n_M): with each entry's chunk's power (one chunk's is n_M)
+      cross = get64(w + kCross);
+      if (C > 1 && tells) {
+        cross = has ? cross : 0.0;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          const double p_i = kept_p[i * 64 + lane];
+          const float of = __uint_as_float(words[kept_chunk[i * 64 + lane] * kWords + kRef]);
+          if (p_i != 0.0) cross += p_i * (power_of(of, a.kb64) - n_M);
+        }
+        cross = wave_sum64(cross);
+      }
       // what the teacher leaves, to the unnamed columns; nothing where none of them can take it: all masked, also by
       // values such as -1e9, next to which their share is 0 in 64 bits
       double left = 0.0;
@@ -375,17 +407,17 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       double s = (double)up * a.t;
       if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
-      if (k == (GRAD ? 0 : C - 1) && lane == 0) row_loss((float)loss);
+      if (tells && lane == 0) row_loss((float)loss);
       if constexpr (GRAD) {
         // of an unnamed column: q_v S - left q_v / q_o = (q_o S - left) 2^(z_v - log2 of their sum)
-        const double c = rest == 0.0 ? 0.0 : (double)a.kb * ((double)U - (shifted ? (double)m : 0.0)) + log_rest;
+        const double c = rest == 0.0 ? 0.0 : (double)a.kb * ((double)U - (shifted ? (double)m : 0.0)) + (log_rest - above(U, U, n_U, a.kb64));
         const double c_lo = fabsf((float)c) < INFINITY ? c - (double)(float)c : 0.0;  // 2^-c_lo, a few 2^-14 at most, goes to the factor
         if (lane == 0) {
           bc[0] = (float)c;
           bc[1] = (float)(s * (over / all * S - left) * fma(-kLn2d, c_lo, 1.0));
         }
         // the named columns' gradients; entries of the same column add up, in order
-        const double f_own = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(f_named), (int)(C > 1 ? k : 0u)));
+        const int up_own = __builtin_amdgcn_readlane(up_named, (int)(C > 1 ? k : 0u));
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) {
           const uint32_t c = kept_col[i * 64 + lane];
@@ -394,7 +426,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
             P_i = 0.0;
             for (int q = 0; q < L; ++q) P_i += kept_col[q] == c ? kept_p[q] : 0.0;
           }
-          grad[i] = (float)(s * (kept_e[i * 64 + lane] * f_own / all * S - P_i));
+          grad[i] = (float)(s * (ldexp(kept_e[i * 64 + lane], up_own) / all * S - P_i));
         }
       }
     }

@@ -372,7 +372,8 @@ struct DistillArgs {
   int32_t tdtype, kind, K;
   const int32_t* len;         // [N] entries of a row, or NULL: K
   double t, inv_t;            // the temperature
-  float kb;                   // log2(e) / temperature
+  double kb64;                // log2(e) / temperature
+  float kb;                   // the same in FP32, of the unnamed columns' exponents
   int32_t reduce;
   const float* g;             // upstream gradient ([N] or [1]); NULL = 1
   float* loss;                // [N] or [1]

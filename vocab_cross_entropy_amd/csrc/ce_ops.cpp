@@ -460,7 +460,8 @@ ce_status ce_distill_fwd_bwd(const ce_logits* x, const ce_logits* out, const ce_
   a.len = d->len;
   a.t = (double)d->temperature;
   a.inv_t = 1.0 / a.t;
-  a.kb = (float)(1.4426950408889634074 / a.t);
+  a.kb64 = 1.4426950408889634074 / a.t;
+  a.kb = (float)a.kb64;
   a.reduce = reduce_loss;
   a.g = grad_out;
   a.loss = loss;

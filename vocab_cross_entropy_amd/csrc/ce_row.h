@@ -270,15 +270,6 @@ __device__ __forceinline__ double wave_sum64(double v) {
   v += dpp64<kBcast31, 0xc>(v, 0.0);
   return last_lane64(v);
 }
-__device__ __forceinline__ double wave_largest64(double v) {
-  v = fmax(v, dpp64<kSwap1>(v, v));
-  v = fmax(v, dpp64<kSwap2>(v, v));
-  v = fmax(v, dpp64<kHalfMirror>(v, v));
-  v = fmax(v, dpp64<kMirror>(v, v));
-  v = fmax(v, dpp64<kBcast15, 0xa>(v, v));
-  v = fmax(v, dpp64<kBcast31, 0xc>(v, v));
-  return last_lane64(v);
-}
 __device__ __forceinline__ int wave_count64(int v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
