@@ -218,9 +218,11 @@ std::mutex g_prof_mu;
 std::vector<hipEvent_t> g_prof_ev;  // pairs
 int32_t g_prof_cap = 0, g_prof_used = 0;
 
-void prof_next(hipEvent_t* e0, hipEvent_t* e1) {
-  std::lock_guard<std::mutex> lk(g_prof_mu);
+// The next pair of events for a call on `items` rows or bytes: without any there is no kernel between them to time.
+void prof_next(int64_t items, hipEvent_t* e0, hipEvent_t* e1) {
   *e0 = *e1 = nullptr;
+  if (items == 0) return;
+  std::lock_guard<std::mutex> lk(g_prof_mu);
   if (g_prof_used < g_prof_cap) {
     *e0 = g_prof_ev[2 * g_prof_used];
     *e1 = g_prof_ev[2 * g_prof_used + 1];
@@ -241,7 +243,7 @@ unsigned long long* phase_buffer(size_t bytes) { return bytes <= g_phase_bytes ?
 unsigned long long* phase_buffer(size_t) { return nullptr; }
 #endif
 ce_status check_logits_desc(const ce_logits* x) { return check_logits(x, false); }
-void profile_next(hipEvent_t* e0, hipEvent_t* e1) { prof_next(e0, e1); }
+void profile_next(int64_t items, hipEvent_t* e0, hipEvent_t* e1) { prof_next(items, e0, e1); }
 void set_last_error(const char* msg) { snprintf(g_err, sizeof g_err, "%s", msg); }
 size_t fused_workspace_bytes(int64_t N, int32_t dtype, int64_t V, bool reduce) {
   return ws_layout(N, fused_auto_chunks(dtype, V), reduce, true).total;
@@ -325,7 +327,7 @@ ce_status ce_forward_ex(const ce_logits* x, const ce_targets* t, const ce_params
   a.n_out = n_out;  // counted by the stats kernel's workgroup 0
   set_short_rows(&a, x, p);
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(N, &e0, &e1);
   if ((e = vce::launch_stats(a, stream, e0, e1))) return hip_fail(e, "forward launch");
   if (p->reduce_loss && (e = vce::launch_mean(a.row_loss, N, mean_n(p, n_out), loss, stream)))
     return hip_fail(e, "mean launch");
@@ -363,7 +365,7 @@ ce_status ce_backward_inplace_ex(const ce_logits* x, const ce_targets* t, const 
   a.q_o_d = q.q_o;
   a.q_t_d = q.q_t;
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(a.L.N, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_backward(a, stream, e0, e1))) return hip_fail(e, "backward launch");
   return CE_OK;
@@ -475,7 +477,7 @@ ce_status fused_call(const ce_logits* x, const ce_targets* t, const ce_params* p
     return fail(CE_ELAYOUT, "internal: rows of %lld columns planned on a %d x %d workgroup", (long long)x->v_local,
                 shape.threads, shape.vecs);
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(a.L.N, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_fused(a, shape, stream, e0, e1))) return hip_fail(e, "fused launch");
   return CE_OK;
@@ -598,7 +600,7 @@ ce_status ce_shards_fwd_bwd_fused(const ce_logits* shards, int32_t S, const ce_t
   for (int32_t s = 0; s < S; ++s) ss.L[s] = row_layout(&shards[s], t, p);
   a.short_rows = pl.short_rows ? 1 : 0;
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(a.L.N, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_fused_shards(a, ss, pl.shape, stream, e0, e1))) return hip_fail(e, "sharded fused launch");
   return CE_OK;
@@ -627,7 +629,7 @@ ce_status ce_scale_grad_inplace(const ce_logits* x, const float* grad_out, int32
   a.g = grad_out;
   a.per_row = per_row;
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(N, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_scale(a, stream, e0, e1))) return hip_fail(e, "scale launch");
   return CE_OK;
@@ -642,7 +644,7 @@ ce_status ce_stream_reference(const void* src, void* dst, int64_t bytes, hipStre
   if (s0 != d0 && s0 < d0 + (uintptr_t)bytes && d0 < s0 + (uintptr_t)bytes)
     return fail(CE_EINVAL, "src and dst overlap without being the same buffer");
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(bytes, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_stream_ref(src, dst, bytes, s0 == d0 ? 0x80008000u : 0u, stream, e0, e1)))
     return hip_fail(e, "reference stream launch");
@@ -667,7 +669,7 @@ ce_status ce_shard_partial_stats(const ce_logits* shard, const ce_targets* t, co
   a.n_out = nullptr;
   set_short_rows(&a, shard, p);
   hipEvent_t e0, e1;
-  prof_next(&e0, &e1);
+  prof_next(N, &e0, &e1);
   hipError_t e;
   if ((e = vce::launch_stats(a, stream, e0, e1))) return hip_fail(e, "shard stats launch");
   return CE_OK;

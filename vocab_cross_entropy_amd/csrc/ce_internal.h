@@ -401,7 +401,7 @@ unsigned long long* phase_buffer(size_t bytes);
 // and the fused call's workspace need for N whole rows of V columns.
 void set_last_error(const char* msg);
 ce_status check_logits_desc(const ce_logits* x);
-void profile_next(hipEvent_t* e0, hipEvent_t* e1);
+void profile_next(int64_t items, hipEvent_t* e0, hipEvent_t* e1);
 size_t fused_workspace_bytes(int64_t N, int32_t dtype, int64_t V, bool reduce);
 // every check of ce_fwd_bwd_fused that depends on the logits' shape and the
 // parameters (none on buffers), and the plan: chunks per row K, body vectors

@@ -164,7 +164,7 @@ ce_status process(const ce_logits* x, const ce_logits* out, const ce_process* p,
   vce::process_plan(&a);
   if (a.chunks > 0xffffffffLL / a.N) return ofail(CE_EINVAL, "more than 2^32-1 chunks of columns");
   hipEvent_t e0, e1;
-  vce::profile_next(&e0, &e1);
+  vce::profile_next(a.N, &e0, &e1);
   return launched(vce::launch_process(a, backward, stream, e0, e1), backward ? "process backward" : "process");
 }
 
@@ -370,7 +370,7 @@ ce_status ce_token_logprobs(const ce_logits* x, const ce_logprobs* q, float* log
   a.stats = stats;
   vce::logprob_plan(N, a.V, a.dtype, &a.shape, &a.chunks, &a.chunk_cols);
   hipEvent_t e0, e1;
-  vce::profile_next(&e0, &e1);
+  vce::profile_next(N, &e0, &e1);
   return launched(vce::launch_logprobs(a, ws, stream, e0, e1), "log-probabilities launch");
 }
 
@@ -412,7 +412,7 @@ ce_status ce_token_logprobs_backward(const ce_logits* x, const ce_logits* out, c
   a.top_ids = top_ids;
   a.dtop = dtop;
   hipEvent_t e0, e1;
-  vce::profile_next(&e0, &e1);
+  vce::profile_next(N, &e0, &e1);
   return launched(vce::launch_logprobs_bwd(a, stream, e0, e1), "log-probabilities gradient launch");
 }
 
@@ -467,7 +467,7 @@ ce_status ce_distill_fwd_bwd(const ce_logits* x, const ce_logits* out, const ce_
   a.loss = loss;
   vce::distill_plan(a.V, a.dtype, &a.chunks, &a.chunk_cols);
   hipEvent_t e0, e1;
-  vce::profile_next(&e0, &e1);
+  vce::profile_next(N, &e0, &e1);
   return launched(vce::launch_distill(a, ws, n_valid, stream, e0, e1), "distillation launch");
 }
 
