@@ -561,6 +561,11 @@ class TokenLogprobs(NamedTuple):
     lse: Optional[torch.Tensor]           # FP32 (d0, d1)
 
 
+def _too_many(what, n):
+    """Counts are 32-bit in the C interface; ctypes would take this one modulo 2^32."""
+    _einval(f"{what}: {n} a row is out of range")
+
+
 def _listed(dev, what, t, d0, d1, dtype):
     """A (d0, d1, n) companion of the logits, (d0, d1) standing for n = 1: (pointer, s0, s1, n)."""
     if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype):
@@ -572,6 +577,8 @@ def _listed(dev, what, t, d0, d1, dtype):
     n = shape[2] if len(shape) == 3 else 1
     if n > 1 and st[2] != 1:
         _elayout(f"{what} needs a contiguous last dimension")
+    if n >> 31:
+        _too_many(what, n)
     return t.data_ptr(), st[0], st[1], n
 
 
@@ -597,7 +604,10 @@ def _prepared(dev, ws, nbytes, x):
 
 def ce_token_logprobs_workspace_bytes(x, top_k=0) -> int:
     """Workspace bytes of ce_token_logprobs for (d0, d1, V) logits (256: it uses none)."""
-    n = lib.ce_token_logprobs_workspace_bytes(_logits(x, "logits", 0, None)[0], int(top_k))
+    top_k = int(top_k)
+    if top_k >> 31:
+        _too_many("top_k", top_k)
+    n = lib.ce_token_logprobs_workspace_bytes(_logits(x, "logits", 0, None)[0], top_k)
     if n == 0:
         _check(_abi.CE_EINVAL)
     return int(n)
@@ -613,6 +623,8 @@ def ce_token_logprobs(x, ids=None, *, top_k=0, entropy=False, stats=False, lse=F
     dev = _index(x, "logits")
     xd, d0, d1, V = _logits(x, "logits", 0, None)
     top_k = int(top_k)
+    if top_k >> 31:
+        _too_many("top_k", top_k)
     f32, device = torch.float32, x.device
     ids_ptr, s0, s1, M = (None, 0, 0, 0) if ids is None else _listed(dev, "ids", ids, d0, d1, torch.int64)
     q = _abi.CeLogprobs(ids_ptr, s0, s1, M, top_k, int(ignore_idx))
