@@ -599,7 +599,9 @@ typedef struct ce_logprobs {
 } ce_logprobs;
 
 /* Workspace bytes of ce_token_logprobs with K alternatives for logits like `x` (256: none is used); 0 if the
- * arguments are refused.  A prepared workspace (ce_workspace_init) of any call will do that is large enough. */
+ * arguments are refused.  A prepared workspace (ce_workspace_init) of any call will do that is large enough; other calls
+ * on as many rows may share it, while one that ce_linear_cross_entropy, or ce_forward or ce_shard_combine on more rows,
+ * has left its plain values in is prepared again first (a value there could look like a word of this call's). */
 size_t ce_token_logprobs_workspace_bytes(const ce_logits* x, int32_t K);
 
 /*
@@ -661,7 +663,8 @@ typedef struct ce_distill {
   const int32_t* len;        /* [N] entries of row r, the first ones, taken into [0, K]; NULL: K */
 } ce_distill;
 
-/* Workspace bytes of ce_distill_fwd_bwd for logits like `x` with any reduction; 0 if the arguments are refused. */
+/* Workspace bytes of ce_distill_fwd_bwd for logits like `x` with any reduction; 0 if the arguments are refused.
+ * Shared with other calls as ce_token_logprobs' is. */
 size_t ce_distill_workspace_bytes(const ce_logits* x);
 
 /*
@@ -706,7 +709,7 @@ ce_status ce_stream_reference(const void* src, void* dst, int64_t bytes, hipStre
  * the next `capacity` calls of ce_forward(_ex), ce_backward_inplace(_ex),
  * ce_fwd_bwd_fused(_noalloc), ce_shards_fwd_bwd_fused, ce_shard_partial_stats,
  * ce_scale_grad_inplace, ce_logits_process(_backward), ce_token_logprobs(_backward),
- * ce_distill_fwd_bwd or ce_stream_reference that launch work records a pair
+ * ce_distill_fwd_bwd or ce_stream_reference that launch work (have rows) records a pair
  * of HIP events on its stream around its main (bandwidth-dominant) kernel.
  * ce_profile_stop(ms, cap, count) waits for those events, writes up to `cap`
  * durations in milliseconds to host array `ms`, the number recorded to

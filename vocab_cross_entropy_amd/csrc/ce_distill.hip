@@ -499,7 +499,7 @@ void distill_plan(int64_t V, int32_t dtype, int64_t* chunks, int64_t* chunk_cols
 size_t distill_workspace(int64_t N, int64_t V, int32_t dtype) {
   int64_t chunks, cols;
   distill_plan(V, dtype, &chunks, &cols);
-  return kWsHeaderBytes + (size_t)N * 8 + (chunks > 1 ? (size_t)N * chunks * kWords * 8 : 0);
+  return chunks > 1 ? chunk_words_at(N) + (size_t)N * chunks * kWords * 8 : row_words_at(N) + (size_t)N * 8;
 }
 
 hipError_t launch_distill(DistillArgs a, void* ws, int32_t* n_valid, hipStream_t stream, hipEvent_t ev0,
@@ -519,8 +519,8 @@ hipError_t launch_distill(DistillArgs a, void* ws, int32_t* n_valid, hipStream_t
   if (ev0 && (e = hipEventRecord(ev0, stream)) != hipSuccess) return e;
   if (a.chunks > 1 || a.reduce != CE_REDUCE_NONE) {
     a.hdr = hdr;
-    a.row_words = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + kWsHeaderBytes);
-    a.slots = a.row_words + a.N;
+    a.row_words = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + row_words_at(a.N));
+    a.slots = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + chunk_words_at(a.N));
     a.ws_bytes = distill_workspace(a.N, a.V, a.dtype);
   }
   const FusedShape shape = fused_shape_for(a.chunk_cols / vec_cols(a.dtype));

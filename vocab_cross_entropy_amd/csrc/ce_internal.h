@@ -309,6 +309,10 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
 // Token log-probabilities (ce_logprobs.hip) and distillation (ce_distill.hip): kernels that hold a chunk of a row.
 constexpr int kMaxChunks = 64;                         // of one row
 constexpr int64_t kMaxGridItems = (int64_t)1 << 22;    // workgroups of a launch (a launch holds below 2^32 work-items)
+// A workspace of theirs: the header, room for the plain FP32 losses of as many rows that ce_forward and ce_shard_combine
+// keep there (one of which may look like a tag), a tagged word a row, and the chunks' tagged words.
+constexpr size_t row_words_at(int64_t N) { return kWsHeaderBytes + ((size_t)N * 4 + 7) / 8 * 8; }
+constexpr size_t chunk_words_at(int64_t N) { return (row_words_at(N) + (size_t)N * 8 + 63) / 64 * 64; }
 constexpr int kLogprobMaxList = 128;                   // given tokens, and alternatives, of a row
 constexpr int kLogprobBwdT = 256, kLogprobBwdP = 4;    // threads and vectors a thread of the gradient
 struct LogprobArgs {

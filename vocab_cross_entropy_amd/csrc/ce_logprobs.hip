@@ -1036,7 +1036,7 @@ size_t logprob_workspace(int64_t N, int64_t V, int32_t dtype, int32_t K) {
   logprob_plan(N, V, dtype, &shape, &chunks, &cols);
   if (chunks == 1 || N == 0) return 0;
   const size_t words = kStatWords + 2 * (size_t)K;
-  return kWsHeaderBytes + (size_t)N * 8 + (size_t)N * chunks * words * 8;
+  return chunk_words_at(N) + (size_t)N * chunks * words * 8;
 }
 
 hipError_t launch_logprobs(LogprobArgs a, void* ws, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1) {
@@ -1044,8 +1044,8 @@ hipError_t launch_logprobs(LogprobArgs a, void* ws, hipStream_t stream, hipEvent
   if (ev0 && (e = hipEventRecord(ev0, stream)) != hipSuccess) return e;
   if (a.chunks > 1) {
     a.hdr = static_cast<WsHeader*>(ws);
-    a.done = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + kWsHeaderBytes);
-    a.slots = a.done + a.N;
+    a.done = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + row_words_at(a.N));
+    a.slots = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + chunk_words_at(a.N));
     a.ws_bytes = logprob_workspace(a.N, a.V, a.dtype, a.K);
   }
   const int64_t rows = kMaxGridItems / a.chunks;  // a launch
