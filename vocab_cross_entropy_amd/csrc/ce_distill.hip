@@ -33,8 +33,8 @@ namespace {
 // each; sums are relative to powers of two near m and the reference.  (Less would show where a student is near its teacher
 // and the loss is a small difference: log2 e / T in FP32 alone moves a loss of 2e-7 by up to 6e-4 of it and its gradient by
 // 2e-3, one of 2e-9 by 4e-3 and 2e-2.  The eighth word is empty: 64 bytes a chunk, one word a lane for eight chunks.
-// 8192 x 128000 BF16: 695 us; with seven words 702, with nine 721 to 757; weights by 64-bit exponentials instead of powers
-// of two, 705.)
+// 8192 x 128000 BF16, 694 us: with seven words 6 us more, with nine 25 to 60, with weights by 64-bit exponentials in place
+// of powers of two 10.)
 enum { kMax, kRest, kRef, kSum, kCross = kSum + 2, kEmpty = kCross + 2, kWords };
 constexpr int kEntries = kDistillMaxTop / 64;  // entries a lane of the wave that handles them
 constexpr double kLn2d = 0.693147180559945309417, kLog2eD = 1.442695040888963407360;
@@ -80,9 +80,10 @@ __device__ __forceinline__ double lane64(double v, int l) {
   return __builtin_bit_cast(double, r);
 }
 
-// References of sums are powers of two, 2^n with n = rint(x log2 e / T) of a chunk's largest logit x: each chunk's is its
-// own, and sums are brought together by exponents alone.  A column's exponent is fma(x, log2 e / T, -n), rounded once.
-// From 2^50 on logits are equal or too far apart to add up, and exponents are their differences from the reference.
+// In a split row the references of sums are powers of two, 2^n with n = rint(x log2 e / T) of a chunk's largest logit x:
+// each chunk's is its own, and sums are brought together by exponents alone.  A column's exponent is
+// fma(x, log2 e / T, -n), rounded once.  From 2^50 on logits are equal or too far apart to add up, and exponents are their
+// differences from the reference, as they are in a row of one chunk.
 __device__ __forceinline__ double power_of(float x, double kb) { return rint((double)x * kb); }
 __device__ __forceinline__ double above(float x, float ref, double n, double kb) {
   return fabs(n) < 0x1p50 ? fma((double)x, kb, -n) : ((double)x - (double)ref) * kb;
@@ -125,7 +126,8 @@ __device__ void finish_distill(const DistillArgs& a, uint32_t tag, bool ws_ok) {
 }
 
 // (Six waves a SIMD, 80 registers: 515 x 32003 FP32 32 us; left to the compiler, 35.)
-template <int DT, int T, int P, bool GRAD>
+// SPLIT: more than one chunk a row.  (One kernel for both: 65536 x 1000 BF16 with 20 logits 265 us, 215 apart.)
+template <int DT, int T, int P, bool GRAD, bool SPLIT>
 __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void k_distill(DistillArgs a) {
   constexpr int E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
   __shared__ float sh_max[W], sh_sum[W];
@@ -136,8 +138,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
   __shared__ uint8_t kept_chunk[kDistillMaxTop];
   __shared__ float bc[2];  // the unnamed columns' exponents' offset, and their factor
   const uint32_t tid = threadIdx.x, lane = tid & 63;
-  const uint32_t C = (uint32_t)a.chunks;
-  const uint32_t in_launch = blockIdx.x / C;
+  const uint32_t C = SPLIT ? (uint32_t)a.chunks : 1u;
+  const uint32_t in_launch = SPLIT ? blockIdx.x / C : blockIdx.x;
   const int64_t r = a.row0 + in_launch;
   const uint32_t k = blockIdx.x - in_launch * C;
   WsView ws{0u, true, 0ull};
@@ -212,13 +214,14 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     }
     __syncthreads();
     if (tid < 64) {
-      double t[kEntries], logd = 0.0, d = 1.0;
+      double t[kEntries], top = 0.0, logd = 0.0, d = 1.0;
       const bool logits = a.kind == CE_TEACHER_LOGITS;
-      float largest_t = -INFINITY;
+      if (logits) {
+        float largest_t = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kEntries; ++i) largest_t = fmaxf(largest_t, i * 64 + (int)lane < L ? tv[i] : -INFINITY);
-      largest_t = wave_largest(largest_t);
-      const double top = logits ? (double)largest_t * a.inv_t : 0.0;
+        for (int i = 0; i < kEntries; ++i) largest_t = fmaxf(largest_t, i * 64 + (int)lane < L ? tv[i] : -INFINITY);
+        top = (double)wave_largest(largest_t) * a.inv_t;
+      }
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         t[i] = i * 64 + (int)lane < L ? (logits ? (double)tv[i] * a.inv_t : (double)tv[i]) - top : -(double)INFINITY;
@@ -241,7 +244,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     }
 
     const bool tells = k == (GRAD ? 0 : C - 1);  // brings the row's loss together
-    if (C > 1 && tells && tid < 64) {
+    if (SPLIT && tells && tid < 64) {
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {  // (bad columns: the row is NaN whichever chunk they are taken for)
         const uint32_t c = (uint32_t)id[i] / (uint32_t)a.chunk_cols;
@@ -277,6 +280,11 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     const bool shifted = fabsf(m * a.kb) > kNear && fabsf(m) < INFINITY;
     if (shifted) subtract<DT, P>(v, m);
     const float from = shifted || m == -INFINITY ? 0.f : m * a.kb;
+    float grow = 1.f;
+    if (tid < 64 && m != -INFINITY) {  // from `from` to the exact m kb, or to the power of two
+      const float d = SPLIT ? (float)above(m, m, power_of(m, a.kb64), a.kb64) : 0.f;
+      grow = exp2_hw(shifted ? d : d - __builtin_fmaf(m, a.kb, -from));
+    }
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -293,15 +301,13 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
     if (lane == 0) sh_sum[tid >> 6] = s0;
     __syncthreads();
 
+    double loss = 0.0, power = 0.0;
     // ---- wave 0: the named columns here, then the row over its chunks
     if (tid < 64) {
       s0 = sh_sum[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) s0 += sh_sum[i];
-      if (m != -INFINITY) {  // from `from` to the power of two
-        const float d = (float)above(m, m, power_of(m, a.kb64), a.kb64);
-        s0 *= exp2_hw(shifted ? d : d - __builtin_fmaf(m, a.kb, -from));
-      }
+      s0 *= grow;
       double e[kEntries], sum = 0.0, cross = 0.0;
       bool odd = false;  // NaN or +inf, which have no sum
       float ref = m;
@@ -311,7 +317,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
         ref = fmaxf(ref, here[i] ? xe[i] : -INFINITY);
       }
       ref = wave_largest(ref);
-      const double n_ref = power_of(ref, a.kb64);
+      const double n_ref = SPLIT ? power_of(ref, a.kb64) : INFINITY;  // (one chunk's exponents are differences from M)
 #pragma unroll
       for (int i = 0; i < kEntries; ++i) {
         const bool some = here[i] && xe[i] != -INFINITY;
@@ -319,14 +325,6 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
         e[i] = __any(some) ? exp2_64(z) : 0.0;
         sum += first[i] ? e[i] : 0.0;
         if (here[i] && p[i] != 0.0) cross += p[i] * z;
-      }
-      if (GRAD || C > 1) {
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          kept_p[i * 64 + lane] = p[i];
-          kept_e[i * 64 + lane] = e[i];
-          kept_col[i * 64 + lane] = col[i];
-        }
       }
       const bool twice = [&] {
         bool again = false;
@@ -346,7 +344,16 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       put64(w + kSum, sum);
       put64(w + kCross, cross);
       w[kEmpty] = 0u;
-      if (C > 1) {
+      const auto keep = [&] {
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          kept_p[i * 64 + lane] = p[i];
+          kept_e[i * 64 + lane] = e[i];
+          kept_col[i * 64 + lane] = col[i];
+        }
+      };
+      if (GRAD && !SPLIT) keep();
+      if (SPLIT) {
         unsigned long long* const slots = a.slots + (size_t)r * C * kWords;
         if (lane < kWords && !withheld(ws, r, (int)k)) {
           uint32_t mine = w[0];
@@ -354,7 +361,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
           for (int q = 1; q < kWords; ++q) mine = (int)lane == q ? w[q] : mine;
           put_word(slots + k * kWords + lane, ws.tag, mine);
         }
-        if (!GRAD && k != C - 1) return;  // the last chunk brings the row's loss together; no other needs it
+        if (!GRAD && k != C - 1) return;
+        keep();  // the last chunk brings the row's loss together; no other needs it
         uint32_t spins = 0;
         for (uint32_t i = lane; i < C * kWords; i += 64) {
           uint32_t got = 0x7fc00000u;
@@ -371,53 +379,54 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
       if (!ok && lane == 0) atomicOr(&a.hdr->status, ws.ok ? 1u : 2u);
       // the unnamed columns' sum relative to their largest, U, so that it is 0 only where all of them are masked; all of
       // it relative to the row's largest logit, M
-      const bool has = lane < C;
-      const float w_max = __uint_as_float(w[kMax]), w_ref = __uint_as_float(w[kRef]);
-      const float M = wave_largest(has ? w_ref : -INFINITY), U = wave_largest(has ? w_max : -INFINITY);
-      const double n_M = power_of(M, a.kb64), n_U = power_of(U, a.kb64);
-      const double rest =
-          wave_sum64(has ? ldexp((double)__uint_as_float(w[kRest]), steps(power_of(w_max, a.kb64) - n_U)) : 0.0);
-      const double down = U == -INFINITY ? 0.0 : n_U - n_M;
-      const double over = ldexp(rest, steps(down));
-      const int up_named = steps(power_of(w_ref, a.kb64) - n_M);
-      const double all = over + wave_sum64(has ? ldexp(get64(w + kSum), up_named) : 0.0);
-      // of p (z - n_M): with each entry's chunk's power (one chunk's is n_M)
-      cross = get64(w + kCross);
-      if (C > 1 && tells) {
-        cross = has ? cross : 0.0;
-#pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          const double p_i = kept_p[i * 64 + lane];
-          const float of = __uint_as_float(words[kept_chunk[i * 64 + lane] * kWords + kRef]);
-          if (p_i != 0.0) cross += p_i * (power_of(of, a.kb64) - n_M);
-        }
-        cross = wave_sum64(cross);
+      float M = ref, U = m;
+      double rest = (double)s0, down = ((double)U - (double)M) * a.kb64, n_M = 0.0, n_U = 0.0, all = sum;
+      int up_named = 0;
+      if (SPLIT) {
+        const bool has = lane < C;
+        const float w_max = __uint_as_float(w[kMax]), w_ref = __uint_as_float(w[kRef]);
+        M = wave_largest(has ? w_ref : -INFINITY);
+        U = wave_largest(has ? w_max : -INFINITY);
+        n_M = power_of(M, a.kb64);
+        n_U = power_of(U, a.kb64);
+        down = n_U - n_M;
+        rest = wave_sum64(has ? ldexp((double)__uint_as_float(w[kRest]), steps(power_of(w_max, a.kb64) - n_U)) : 0.0);
+        up_named = steps(power_of(w_ref, a.kb64) - n_M);
+        all = wave_sum64(has ? ldexp(get64(w + kSum), up_named) : 0.0);
       }
+      // their sum and its logarithm are made of the same three factors: of `rest`, 2^whole, and of an FP32 exponential
+      down = U == -INFINITY ? 0.0 : fmax(down, -1e30);
+      const double whole = rint(down), part = (double)exp2_hw((float)(down - whole));
+      const double over = rest * ldexp(part, steps(whole));
+      all += over;
       // what the teacher leaves, to the unnamed columns; nothing where none of them can take it: all masked, also by
       // values such as -1e9, next to which their share is 0 in 64 bits
       double left = 0.0;
       if (a.kind == CE_TEACHER_LOGPROBS && over != 0.0) left = fmax(0.0, 1.0 - mass);
       const double S = mass + left;
-      // three logarithms at once: of the sum, of what is left, of the unnamed columns' sum
-      const double logs = log2_64(lane == 0 ? all : lane == 1 ? left : rest);
+      // four logarithms at once: of the sum, of what is left, of the unnamed columns' sum's factors
+      const double logs = log2_64(lane == 0 ? all : lane == 1 ? left : lane == 2 ? rest : part);
       const double log_all = lane64(logs, 0), log_rest = lane64(logs, 2);
-      double loss = plogp - (cross - mass * log_all) * kLn2d;
-      if (left != 0.0) loss += left * (lane64(logs, 1) - (log_rest + down - log_all)) * kLn2d;
-      loss *= a.t * a.t;
+      // the loss but for the named columns' exponents
+      loss = plogp + mass * log_all * kLn2d;
+      if (left != 0.0) loss += left * (lane64(logs, 1) - (log_rest + (whole + lane64(logs, 3)) - log_all)) * kLn2d;
+      if constexpr (!SPLIT) loss -= cross * kLn2d;
       double s = (double)up * a.t;
       if (a.reduce == CE_REDUCE_MEAN) s /= (double)count;
       if (bad || !ok) s = loss = __builtin_nan("");
-      if (tells && lane == 0) row_loss((float)loss);
+      if (!SPLIT && lane == 0) row_loss((float)(loss * a.t * a.t));
+      power = n_M;
       if constexpr (GRAD) {
         // of an unnamed column: q_v S - left q_v / q_o = (q_o S - left) 2^(z_v - log2 of their sum)
-        const double c = rest == 0.0 ? 0.0 : (double)a.kb * ((double)U - (shifted ? (double)m : 0.0)) + (log_rest - above(U, U, n_U, a.kb64));
+        const double near_u = SPLIT ? log_rest - above(U, U, n_U, a.kb64) : log_rest;
+        const double c = rest == 0.0 ? 0.0 : (double)a.kb * ((double)U - (shifted ? (double)m : 0.0)) + near_u;
         const double c_lo = fabsf((float)c) < INFINITY ? c - (double)(float)c : 0.0;  // 2^-c_lo, a few 2^-14 at most, goes to the factor
         if (lane == 0) {
           bc[0] = (float)c;
           bc[1] = (float)(s * (over / all * S - left) * fma(-kLn2d, c_lo, 1.0));
         }
         // the named columns' gradients; entries of the same column add up, in order
-        const int up_own = __builtin_amdgcn_readlane(up_named, (int)(C > 1 ? k : 0u));
+        const int up_own = __builtin_amdgcn_readlane(up_named, (int)k);
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) {
           const uint32_t c = kept_col[i * 64 + lane];
@@ -430,9 +439,26 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
         }
       }
     }
+    // of p (z - n_M), with the power of each entry's chunk; the other waves write their part of the gradient meanwhile
+    const auto tell_loss = [&] {
+      const bool has = lane < C;
+      double cross = has ? get64(words + lane * kWords + kCross) : 0.0;
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) {
+        const double p_i = kept_p[i * 64 + lane];
+        const float of = __uint_as_float(words[kept_chunk[i * 64 + lane] * kWords + kRef]);
+        if (p_i != 0.0) cross += p_i * (power_of(of, a.kb64) - power);
+      }
+      loss = (loss - wave_sum64(cross) * kLn2d) * (a.t * a.t);
+      if (lane == 0) row_loss((float)loss);
+    };
+    if constexpr (SPLIT && !GRAD) {
+      if (tid < 64) tell_loss();
+    }
     if constexpr (GRAD) {
       __syncthreads();
       const float c = bc[0], f_un = bc[1];
+      if (SPLIT && tells && tid < 64) tell_loss();
       store_chunk<DT, T, P>(out + (size_t)lo * EB, cols, v, [&](const u32x4v& x) {
         float f[E];
         unpack_vec<DT>(x, f);
@@ -468,10 +494,20 @@ __global__ __launch_bounds__(1024) void k_distill_count(const int32_t* len, int6
   }
 }
 
+template <int DT, int T, int P, bool GRAD>
+void launch_distill_chunks(const DistillArgs& a, dim3 grid, hipStream_t stream) {
+  if constexpr (P == 8) {  // (a split row's chunks have more than 1365 vectors, and the smaller shapes hold 1024)
+    if (a.chunks > 1) {
+      hipLaunchKernelGGL((k_distill<DT, T, P, GRAD, true>), grid, dim3(T), 0, stream, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_distill<DT, T, P, GRAD, false>), grid, dim3(T), 0, stream, a);
+}
 template <int DT, int T, int P>
 void launch_distill_shape(const DistillArgs& a, dim3 grid, hipStream_t stream) {
-  if (a.out) hipLaunchKernelGGL((k_distill<DT, T, P, true>), grid, dim3(T), 0, stream, a);
-  else hipLaunchKernelGGL((k_distill<DT, T, P, false>), grid, dim3(T), 0, stream, a);
+  if (a.out) launch_distill_chunks<DT, T, P, true>(a, grid, stream);
+  else launch_distill_chunks<DT, T, P, false>(a, grid, stream);
 }
 template <int DT>
 void launch_distill_dt(const DistillArgs& a, FusedShape s, dim3 grid, hipStream_t stream) {
@@ -524,6 +560,7 @@ hipError_t launch_distill(DistillArgs a, void* ws, int32_t* n_valid, hipStream_t
     a.ws_bytes = distill_workspace(a.N, a.V, a.dtype);
   }
   const FusedShape shape = fused_shape_for(a.chunk_cols / vec_cols(a.dtype));
+  if (a.chunks > 1 && shape.vecs != 8) return hipErrorInvalidConfiguration;
   const int64_t rows = kMaxGridItems / a.chunks;  // a launch
   for (a.row0 = 0; a.row0 < a.N; a.row0 += rows) {
     const int64_t n = a.N - a.row0 < rows ? a.N - a.row0 : rows;
