@@ -613,8 +613,10 @@ size_t ce_token_logprobs_workspace_bytes(const ce_logits* x, int32_t K);
  *            column leaves to the others), and the entropy (0 where `entropy` is not asked for)
  *   ws       as for ce_fwd_bwd_fused: ce_token_logprobs_workspace_bytes bytes, prepared by ce_workspace_init; NULL
  *            where that is 256.  Not prepared: results NaN, top_ids -1, and ce_workspace_check tells
- * Rows of at most 1,048,576 BF16 or 524,288 FP32 columns (CE_ELAYOUT).
- * Results do not depend on scheduling: repeats are equal bit for bit.
+ * Rows of at most 1,048,576 BF16 or 524,288 FP32 columns (CE_ELAYOUT): the longest that are tested; the kernels' own
+ * limits are further off.
+ * Results do not depend on scheduling: repeats are equal bit for bit.  The order of a row's sums goes by the columns, the
+ * dtype and the number of rows of the call, so a row by itself and among others may differ in the last bits.
  */
 ce_status ce_token_logprobs(const ce_logits* x, const ce_logprobs* q, float* logp, float* entropy, float* lse,
                             int64_t* top_ids, float* top_logp, float* stats, void* ws, size_t ws_bytes,

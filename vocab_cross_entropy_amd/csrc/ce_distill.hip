@@ -17,8 +17,9 @@
 // Bound: one read and one write of the logits.  A chunk of a row stays in a
 // workgroup's registers between its sums and its gradient, and a row's chunks exchange
 // eight words each through the workspace, as in ce_fwd_bwd_fused (whose chunk shapes these are).
-// The loss alone is brought together by a row's last chunk, and no other waits.  8192 x 128000 BF16 with 64 entries: 696 us,
-// 6.03 TB/s of the logits' bytes; 2048 x 32000 BF16 with 20: 49 us, 5.4 TB/s; the loss alone of 1024 x 128000 BF16, 57 us.
+// The loss alone is brought together by a row's last chunk, and no other waits.  A call among others, 8192 x 128000
+// BF16 with 64 entries: 696 us, 6.03 TB/s of the logits' bytes; 2048 x 32000 BF16 with 20 and lengths: 56 us, 4.7 TB/s, two
+// of them the rows' count; the loss alone of 1024 x 128000 BF16, 56 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,7 +34,7 @@ namespace {
 // each; sums are relative to powers of two near m and the reference.  (Less would show where a student is near its teacher
 // and the loss is a small difference: log2 e / T in FP32 alone moves a loss of 2e-7 by up to 6e-4 of it and its gradient by
 // 2e-3, one of 2e-9 by 4e-3 and 2e-2.  The eighth word is empty: 64 bytes a chunk, one word a lane for eight chunks.
-// 8192 x 128000 BF16, 694 us: with seven words 6 us more, with nine 25 to 60, with weights by 64-bit exponentials in place
+// 8192 x 128000 BF16, 696 us: with seven words 6 us more, with nine 25 to 60, with weights by 64-bit exponentials in place
 // of powers of two 10.)
 enum { kMax, kRest, kRef, kSum, kCross = kSum + 2, kEmpty = kCross + 2, kWords };
 constexpr int kEntries = kDistillMaxTop / 64;  // entries a lane of the wave that handles them
@@ -479,7 +480,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(6, 8))) void 
   if (ends) finish_distill<T>(a, ws.tag, ws.ok);
 }
 
-// Rows that have an entry: every row's gradient is over their number.  3 us of 2048 rows, mostly the launch.
+// Rows that have an entry: every row's gradient is over their number.  2048 rows: 2.4 us and more by itself, mostly the
+// launch; 1 to 2 of a call.
 __global__ __launch_bounds__(1024) void k_distill_count(const int32_t* len, int64_t N, int32_t K, int32_t* n) {
   __shared__ int part[16];
   int c = 0;

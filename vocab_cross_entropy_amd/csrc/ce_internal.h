@@ -339,7 +339,7 @@ struct LogprobArgs {
   unsigned long long* slots;  // [N][chunks] tagged words of a chunk: its sums, then its K keys
   unsigned long long ws_bytes;
 };
-int64_t logprob_max_cols(int32_t dtype);  // the longest row that kMaxChunks hold
+int64_t logprob_max_cols(int32_t dtype);  // the longest row that is tested: kMaxChunks batches of the larger shape
 void logprob_plan(int64_t N, int64_t V, int32_t dtype, int32_t* shape, int64_t* chunks, int64_t* chunk_cols);
 size_t logprob_workspace(int64_t N, int64_t V, int32_t dtype, int32_t K);  // 0: none is needed
 hipError_t launch_logprobs(LogprobArgs a, void* ws, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);

@@ -29,9 +29,9 @@
 // its ties the lowest columns are taken.  Keys order by value, then by column, so nothing
 // depends on scheduling.
 //
-// 8192 x 128000 BF16 with the entropy 346 us, 6.06 TB/s; with 1, 20, 64 and 128 alternatives 349, 352, 367 and 402.
-// 2048 x 32000 BF16 with 64: 37 us, where 22 would be its read: five workgroups a CU (by registers; six spill, 45 us)
-// for the eight that each has.  One row of 128000 BF16: 8.5 us, with 20 alternatives 12: latency.
+// 8192 x 128000 BF16 with the entropy 343 us, 6.11 TB/s; with 1, 20, 64 and 128 alternatives 344, 352, 367 and 398.
+// 2048 x 32000 BF16 with 64: 37 us, where 22 would be its read: five workgroups a CU (93 registers, 27 KB of LDS each;
+// held to the registers of six they spill, 45 us) for the eight that each has.  One row of 128000 BF16: 8.8 us, with 20 alternatives 12: latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -866,7 +866,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 256 && P
 // The gradient: a chunk's vectors, all loaded at once, each written where it was
 // read from or elsewhere; the few columns of given tokens are written again by one
 // thread a token, with every gradient that names the column added up in order.
-// Bound: HBM.  8192 x 128000 BF16 with the entropy's 701 us, 5.99 TB/s; 1024 x 32003 FP32, 5 tokens, 46 us, 5.7 TB/s.
+// Bound: HBM.  8192 x 128000 BF16 with the entropy's 706 us, 5.94 TB/s; 1024 x 32003 FP32, 5 tokens, 46 us, 5.7 TB/s.
 template <int DT, bool ENT>
 __global__ __launch_bounds__(kLogprobBwdT) void k_logprobs_bwd(LogprobGradArgs a) {
   constexpr int T = kLogprobBwdT, P = kLogprobBwdP, E = LogitT<DT>::E, EB = LogitT<DT>::EB, W = T / 64;
