@@ -158,9 +158,11 @@ __device__ __forceinline__ uint32_t block_count(uint32_t c, uint32_t* sh) {
 // maxima pass over): the K-th largest value over all columns (the bound itself where fewer than K exceed it), every column
 // above it, and its ties from the lowest column on.  Leaves K keys in cand[]; a chunk of fewer columns, keys of order 0 too.
 // Rare, so it is kept short: every sweep reads the chunk again.  Column 0 of the chunk is the row's column lo.
+// With `if_signalling` nothing is done, and false returned, for a chunk without a signalling NaN.  (64 x 128000 FP32 with a
+// NaN in every row, 5 alternatives: 24 us, 17 without any; 152 where every NaN is answered by the search.)
 template <int DT, int T>
-__device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, uint32_t cols, uint32_t K, uint32_t t,
-                                              Key* cand, uint32_t* n_cand, uint32_t* sh) {
+__device__ __forceinline__ bool exact_largest(const char* chunk, uint32_t lo, uint32_t cols, uint32_t K, uint32_t t,
+                                              bool if_signalling, Key* cand, uint32_t* n_cand, uint32_t* sh) {
   typedef typename LogitT<DT>::Word Word;
   constexpr int E = LogitT<DT>::E;
   const uint32_t tid = threadIdx.x;
@@ -174,6 +176,20 @@ __device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, ui
   const uint32_t whole = cols / E;
   const auto whole_vec = [&](uint32_t i) -> u32x4v { return *reinterpret_cast<const Word*>(chunk + (i < whole ? i : 0u) * 16u); };
   const u32x4v rest = partial_vec<DT>(chunk, whole * E, cols);
+  if (if_signalling) {
+    uint32_t found = 0;
+#pragma unroll 1
+    for (uint32_t i = tid; i <= whole; i += T) {
+      float f[E];
+      unpack_vec<DT>(i < whole ? whole_vec(i) : rest, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t bits = __float_as_uint(f[e]);
+        found |= (bits & 0x7fc00000u) == 0x7f800000u && (bits & 0x3fffffu);
+      }
+    }
+    if (block_count<T>(found, sh) == 0) return false;
+  }
   // how many columns reach c, c + step and c + 2 step
   const auto count = [&](uint32_t c, uint32_t step, uint32_t (&n)[3]) {
     n[0] = n[1] = n[2] = 0;
@@ -252,6 +268,7 @@ __device__ __forceinline__ void exact_largest(const char* chunk, uint32_t lo, ui
   __syncthreads();
   if (tid == 0) *n_cand = K;
   __syncthreads();
+  return true;
 }
 
 // How many of these lanes come before this one.
@@ -652,12 +669,13 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 256 && P
       most = n_seg[i] > most ? n_seg[i] : most;
     }
     sums_of_waves();
-    // (a NaN in the sum: a signalling one may have hidden maxima, and with them columns, from the bound)
-    if (most > (uint32_t)kSeg || reach < (cols < K ? cols : K) || rest != rest) {
-      exact_largest<DT, T>(chunk, lo, cols, K, low ? order_of<DT>(-INFINITY) : bound, seg_keys, &n_cand, sh_cnt);
-      if (tid < W) n_seg[tid] = tid == 0 ? n_cand : 0u;
-      if (tid < 8 * W) seg_keys[(tid / 8) * Segments<W, kSeg>::kStride + (tid < 8 ? n_cand : 0u) + tid % 8] = 0;
-      __syncthreads();
+    const bool missed = most > (uint32_t)kSeg || reach < (cols < K ? cols : K);
+    if (missed || rest != rest) {  // (a signalling NaN may have hidden maxima, and with them columns, from the bound)
+      if (exact_largest<DT, T>(chunk, lo, cols, K, low ? order_of<DT>(-INFINITY) : bound, !missed, seg_keys, &n_cand, sh_cnt)) {
+        if (tid < W) n_seg[tid] = tid == 0 ? n_cand : 0u;
+        if (tid < 8 * W) seg_keys[(tid / 8) * Segments<W, kSeg>::kStride + (tid < 8 ? n_cand : 0u) + tid % 8] = 0;
+        __syncthreads();
+      }
     }
   } else {
     __syncthreads();
